@@ -25,6 +25,7 @@ __all__ = [
     "gemm_workspace_bytes", "linear_workspace_bytes", "linear_host_workspace_bytes", "linear_kernels",
     "last_device_error",
     "swiglu_gemm", "ffn", "moe_permute", "moe_workspace_bytes", "moe_grouped_gemm", "moe_gate", "moe_route",
+    "mla_absorb", "mla_append", "mla_attention", "mla_attention_workspace_bytes",
 ]
 
 SCALE_FP32 = 0
@@ -355,6 +356,108 @@ def mla_absorb(inp: torch.Tensor, wkv_b: torch.Tensor, wkv_b_s: torch.Tensor, mo
     name = "fp8blk_mla_absorb_qk" if mode == "qk" else "fp8blk_mla_absorb_v"
     f = _set_types(name, [vp] * 4 + [i64] * 5 + [vp])
     _check(f(_ptr(inp), _ptr(wkv_b), _ptr(wkv_b_s), _ptr(out), T, H, dn, dv, C, _stream(inp.device)), name)
+    return out
+
+
+MLA_LATENT, MLA_ROPE, MLA_NOPE = 512, 64, 128   # kv_lora_rank, qk_rope_head_dim, qk_nope_head_dim of every config
+
+
+def mla_append(kv: torch.Tensor, norm_w: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor,
+               slots: torch.Tensor, cache: torch.Tensor, q: torch.Tensor | None = None, eps: float = 1e-6,
+               q_nope: torch.Tensor | None = None, q_pe: torch.Tensor | None = None):
+    """Writes each token's cache row: kv bf16 [T, 576] -> RMS-normed latent (norm_w fp32 [512]) and rotated key
+    (rope fp32 [max_pos, 32, 2], positions int64 [T]) at row slots[t] (int64 [T], negative: not written) of
+    cache bf16 [pages, page_size, 576]. With q bf16 [T, H, 192] returns (q_nope [T, H, 128], rotated q_pe
+    [T, H, 64]), else None. kv and q may have strided rows (inner dimensions contiguous)."""
+    if not kv.is_cuda or kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != MLA_LATENT + MLA_ROPE:
+        raise Fp8BlkError("kv must be a CUDA bfloat16 tensor [T, 576]")
+    T = kv.shape[0]
+    if kv.stride(1) != 1:
+        raise Fp8BlkError("kv: the columns of a row must be contiguous")
+    _need(norm_w, torch.float32, "norm_w", ndim=1)
+    _need(rope, torch.float32, "rope", ndim=3)
+    _need(positions, torch.int64, "positions", ndim=1)
+    _need(slots, torch.int64, "slots", ndim=1)
+    _need(cache, torch.bfloat16, "cache", ndim=3)
+    if norm_w.shape[0] != MLA_LATENT or tuple(rope.shape[1:]) != (MLA_ROPE // 2, 2) or cache.shape[2] != kv.shape[1]:
+        raise Fp8BlkError("norm_w must be [512], rope [max_pos, 32, 2], cache [pages, page_size, 576]")
+    if positions.shape[0] != T or slots.shape[0] != T:
+        raise Fp8BlkError("positions and slots must be [T]")
+    H, q_stride = 0, 0
+    if q is not None:
+        if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != T or \
+                q.shape[2] != MLA_NOPE + MLA_ROPE:
+            raise Fp8BlkError("q must be a CUDA bfloat16 tensor [T, H, 192]")
+        H = q.shape[1]
+        if q.stride(2) != 1 or (H > 1 and q.stride(1) != MLA_NOPE + MLA_ROPE):
+            raise Fp8BlkError("q: the heads of a token must be contiguous")
+        q_stride = q.stride(0) if T > 1 else H * (MLA_NOPE + MLA_ROPE)
+        if q_nope is None:
+            q_nope = torch.empty((T, H, MLA_NOPE), dtype=torch.bfloat16, device=q.device)
+        if q_pe is None:
+            q_pe = torch.empty((T, H, MLA_ROPE), dtype=torch.bfloat16, device=q.device)
+        _need(q_nope, torch.bfloat16, "q_nope", ndim=3)
+        _need(q_pe, torch.bfloat16, "q_pe", ndim=3)
+        if tuple(q_nope.shape) != (T, H, MLA_NOPE) or tuple(q_pe.shape) != (T, H, MLA_ROPE):
+            raise Fp8BlkError("q_nope must be [T, H, 128] and q_pe [T, H, 64]")
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    f = _set_types("fp8blk_mla_append", [vp, i64, vp, ctypes.c_float, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64,
+                                         vp, vp, vp])
+    _check(f(_ptr(kv), kv.stride(0) if T > 1 else kv.shape[1], _ptr(norm_w), float(eps), _ptr(q), q_stride, H,
+             _ptr(rope), rope.shape[0], _ptr(positions), _ptr(slots), T, _ptr(cache), cache.shape[0] * cache.shape[1],
+             _ptr(q_nope if q is not None else None), _ptr(q_pe if q is not None else None), _stream(kv.device)),
+           "mla_append")
+    return None if q is None else (q_nope, q_pe)
+
+
+def mla_attention_workspace_bytes(B: int, H: int, prefix_len: int = 0) -> int:
+    i64 = ctypes.c_int64
+    return int(_set_types("fp8blk_mla_attention_workspace_bytes", [i64] * 3, ctypes.c_size_t)(B, H, prefix_len))
+
+
+def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                  lens: torch.Tensor, scale: float, prefix_pages: torch.Tensor | None = None, prefix_len: int = 0,
+                  out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Latent attention of one query token per request: q bf16 [B, H, 512] (mla_absorb "qk" output), q_pe bf16
+    [B, H, 64], cache bf16 [pages, page_size, 576], block_table int32 [B, max_pages] and lens int32 [B] (a
+    request's own keys), after prefix_len keys of prefix_pages (int32) that every request shares
+    -> bf16 [B, H, 512]; lse fp32 [B, H] is written where given."""
+    _need(q, torch.bfloat16, "q", ndim=3)
+    _need(q_pe, torch.bfloat16, "q_pe", ndim=3)
+    _need(cache, torch.bfloat16, "cache", ndim=3)
+    _need(block_table, torch.int32, "block_table")
+    _need(lens, torch.int32, "lens", ndim=1)
+    B, H = q.shape[0], q.shape[1]
+    if q.shape[2] != MLA_LATENT or tuple(q_pe.shape) != (B, H, MLA_ROPE) or \
+            cache.shape[2] != MLA_LATENT + MLA_ROPE:
+        raise Fp8BlkError("q must be [B, H, 512], q_pe [B, H, 64], cache [pages, page_size, 576]")
+    if block_table.shape[0] != B or lens.shape[0] != B:
+        raise Fp8BlkError("block_table must be [B, max_pages] and lens [B]")
+    pages, page_size = cache.shape[0], cache.shape[1]
+    if prefix_len:
+        if prefix_pages is None:
+            raise Fp8BlkError("prefix_len needs prefix_pages")
+        _need(prefix_pages, torch.int32, "prefix_pages", ndim=1)
+        if prefix_len > prefix_pages.shape[0] * page_size:
+            raise Fp8BlkError("prefix_pages has fewer than prefix_len keys")
+    if out is None:
+        out = torch.empty((B, H, MLA_LATENT), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out", ndim=3)
+    if tuple(out.shape) != (B, H, MLA_LATENT):
+        raise Fp8BlkError("out must be [B, H, 512]")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (B, H):
+            raise Fp8BlkError("lse must be [B, H]")
+    if ws is None:
+        ws = workspace(mla_attention_workspace_bytes(B, H, prefix_len), q.device, "mla_attention")
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    f = _set_types("fp8blk_mla_attention", [vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp,
+                                            vp, vp, ctypes.c_size_t, vp])
+    _check(f(_ptr(q), _ptr(q_pe), B, H, _ptr(cache), pages, page_size, _ptr(prefix_pages if prefix_len else None),
+             prefix_len, _ptr(block_table), block_table.shape[1], _ptr(lens), float(scale), _ptr(out), _ptr(lse),
+             _ptr(ws), ws.numel(), _stream(q.device)), "mla_attention")
     return out
 
 

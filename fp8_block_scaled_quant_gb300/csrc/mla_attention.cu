@@ -1,0 +1,1027 @@
+// Attention of single query tokens over a paged latent cache whose first
+// `prefix_len` keys are shared by the whole batch ("Administrator & Developer
+// Guide", 8.3, attn_impl "absorb": scores are q_nope' c + q_pe k_pe on the
+// latent cache, the output stays in the latent space for wkv_b's v rows).
+// Per request b and head h, with x = [q[b, h], q_pe[b, h]] (576 columns) and
+// cache rows c_j over the prefix's keys and then the request's own:
+//
+//   s_j = scale * <x, c_j>,   a = softmax(s),   out = sum_j a_j c_j[0:512].
+//
+// Rows and keys. A tile is 128 query rows (rows are (b, h) flattened) against
+// 128 keys. The prefix is the same for all rows, so its tiles hold rows of
+// any requests: it is read once per 128 rows instead of once per request. A
+// request's own keys meet that request's rows alone. Where H is a multiple
+// of 128 a row tile belongs to one request and prefix and own keys form one
+// item, one running softmax over both; otherwise prefix row tiles and the
+// requests' own keys are items of their own, joined at the end (a row never
+// meets another request's keys: 0 * Inf in the product would leak them).
+//
+// Work split. The items' key tiles, laid end to end, are cut into equal
+// ranges, one per CTA pair: one long sequence and a ragged batch fill the GPU
+// alike. Where a range cuts an item, each part leaves its unnormalised sum,
+// maximum and weight sum in the workspace, and a second kernel joins each
+// row's parts in key order: no atomics, the same bits every run. Lengths are
+// read on the device.
+//
+// The pair. The fp32 output of 128 rows x 512 columns would fill an SM's whole
+// tensor memory, so two SMs share a tile (cta_group::2, M = 128): each holds
+// 64 rows, as 128 lanes x 256 columns (lanes 64-127 hold the upper half of
+// each MMA's columns), and two 64-column score buffers beside it. Each SM's
+// shared memory holds its 64 query rows, half the tile's keys (all 576
+// columns) as the B operand of the scores, half the columns of all 128 keys
+// as the MN-major B operand of the output, and its rows' weights P in bf16.
+// The tensor cores run this M = 128 pair shape at their full rate (measured:
+// 4090 multiply-adds per clock and SM; a single SM's M = 64 runs at half).
+//
+// Softmax. Four warps per CTA, a thread per (row, key half): base-2 exponents
+// in fp32, the running maximum raised only when a tile's maximum passes it by
+// more than 8 (weights stay below 2^8, so the fp32 sums lose nothing and the
+// output is rescaled in tensor memory on few tiles). P is rounded to bf16, the
+// type the tensor cores take next to bf16 keys; the weight sum adds the
+// rounded weights, so equal keys give exactly their mean. Keys past the end
+// are masked by position, not by value, and their rows enter the output
+// product as zeros (out-of-range TMA rows), so whatever an unused cache row
+// holds, NaN included, stays out. The logarithm of the sum, where asked for,
+// comes from a second sum of the weights before their rounding.
+//
+// Every wait is bounded (2 s): on expiry roles leave their loops, in-flight
+// copies are waited for (bounded), tensor memory is freed, an error bit set.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "fp8blk.h"
+#include "host.cuh"
+#include "ptx.cuh"
+
+namespace fp8blk {
+namespace {
+
+constexpr int kC = 512, kR = 64, kRow = kC + kR;
+constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr int kSlab = 64 * 128;             // 64 rows x 64 bf16, 128-byte swizzled
+constexpr int kQSlabs = kRow / 64;          // 9 slabs of 64 columns
+constexpr int kKGroups = 3;                 // key slabs signalled three at a time
+constexpr int kGroupBytes = 3 * kSlab;
+constexpr int kVChunks = 4;                 // 32 keys x 256 columns each
+constexpr int kVSlab = 32 * 128;            // 32 keys x 64 columns
+constexpr int kVChunk = 4 * kVSlab;
+constexpr int kOffQ = 0;
+constexpr int kOffP = kOffQ + kQSlabs * kSlab;
+constexpr int kOffK = kOffP + 2 * kSlab;
+constexpr int kOffV = kOffK + kQSlabs * kSlab;
+constexpr int kOffRed = kOffV + kVChunks * kVChunk;  // [2][2][64] row maxima, then sums
+constexpr int kOffBar = kOffRed + 2 * 2 * 64 * 4;
+constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 1;
+constexpr int kAttnSmem = 1024 + kOffBar + kNumBars * 8 + 32;
+static_assert(kAttnSmem <= 232448, "shared memory per CTA");
+
+// Warps: 0-3 softmax (warp w: tensor-memory lanes 32 w ..), 4 queries and
+// keys, 5 values, 6 MMA.
+constexpr int kAttnThreads = 224;
+constexpr int kMaxPairs = 96;
+constexpr uint32_t kTmemS = 256;            // columns 0-255: output; 256-383: two score buffers
+constexpr float kRaise = 8.0f;              // log2 by which a tile's maximum must pass the running one
+constexpr unsigned kDevErrTimeoutMla = 1u << 6;
+constexpr unsigned kDevErrBadSlot = 1u << 8;
+
+struct AttnParams {
+  const int* prefix_pages;
+  const int* table;        // [B][table_stride]
+  const int* lens;         // [B]
+  __nv_bfloat16* out;      // [B H][512]
+  float* lse;              // [B H] or null
+  float* part_o;           // [part rows][512]
+  float4* part_ml;         // [part rows] (maximum in log2 units, sum of the rounded weights, of the fp32 weights)
+  int* plan;               // [0] units, [1] pairs in use, [2 + i] first unit of item i (items + 1 entries)
+  unsigned* err;
+  int B, H, P, page, page_shift, num_pages, table_stride, max_own;
+  int total_rows;          // cache rows: the out-of-range row coordinate
+  int prefix_tiles, prefix_items, items, own_rows;
+  int merged;              // H % 128 == 0: prefix and own keys in one item
+  int kbox, vbox;          // rows of a TMA box of keys / values
+  float scale_log2;
+};
+
+struct Item {
+  int row0, nrows;   // flattened query rows
+  int pt, tiles;     // prefix tiles, all tiles
+  int b, len;        // the request whose own keys follow the prefix tiles
+};
+
+__device__ __forceinline__ int own_len(const AttnParams& p, int b) {
+  return min(max(__ldg(p.lens + b), 0), p.max_own);
+}
+
+__device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
+  Item it;
+  if (p.merged) {
+    it.row0 = i * kTileRows;
+    it.nrows = kTileRows;
+    it.b = it.row0 / p.H;
+    it.pt = p.prefix_tiles;
+  } else if (i < p.prefix_items) {
+    it.row0 = i * kTileRows;
+    it.nrows = min(kTileRows, p.B * p.H - it.row0);
+    it.b = -1;
+    it.pt = p.prefix_tiles;
+  } else {
+    const int per = (p.H + kTileRows - 1) / kTileRows;
+    const int k = i - p.prefix_items;
+    it.b = k / per;
+    it.row0 = it.b * p.H + (k % per) * kTileRows;
+    it.nrows = min(kTileRows, (it.b + 1) * p.H - it.row0);
+    it.pt = 0;
+  }
+  it.len = it.b >= 0 ? own_len(p, it.b) : 0;
+  it.tiles = it.pt + (it.len + kTileKeys - 1) / kTileKeys;
+  return it;
+}
+
+// First row of the parts of item i written by pair q: item-major, 128 rows
+// apart from one pair to the next, so parts never overlap.
+__host__ __device__ __forceinline__ int64_t part_row(int merged, int prefix_items, int own_rows, int i, int q) {
+  const int64_t base = merged || i < prefix_items
+                           ? static_cast<int64_t>(i) * kTileRows
+                           : static_cast<int64_t>(prefix_items) * kTileRows +
+                                 static_cast<int64_t>(i - prefix_items) * own_rows;
+  return base + static_cast<int64_t>(q) * kTileRows;
+}
+
+__device__ __forceinline__ int64_t unit_of_pair(int64_t units, int pairs, int q) { return units * q / pairs; }
+
+// ---- instructions of the CTA pair ----------------------------------------------
+
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// Arrives on an mbarrier of any CTA of the cluster (shared::cluster address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Waits with acquire at cluster scope for what the peer CTA's threads wrote
+// before arriving; otherwise as mbar_wait.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
+                                                  unsigned code) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 63u) {
+      if (*abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *abort = 1;
+        atomicOr(err, code);
+        return false;
+      }
+    }
+  }
+}
+
+// 2-D tiled load into this CTA's shared memory; the bytes complete on the
+// mbarrier at shared::cluster address `bar`, in this CTA or its pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// D (+)= A B^T over the pair for one K = 16 slice; issued by one thread of CTA 0.
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Arrives on `bar` in both CTAs when the MMAs issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// bf16 x bf16 -> f32, A K-major, B K-major or MN-major, M x N over the pair.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The cache row of key `key` of a page list, or the out-of-range row where the
+// page id is not one of the cache's pages.
+__device__ __forceinline__ int key_row(const AttnParams& p, const int* pages, int key) {
+  const int pg = __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
+  if (pg < 0 || pg >= p.num_pages) {
+    atomicOr(p.err, kDevErrBadSlot);
+    return p.total_rows;
+  }
+  return pg * p.page + (p.page_shift >= 0 ? key & (p.page - 1) : key % p.page);
+}
+
+// Items [lo, hi) of thread `tid` of `n`.
+__device__ __forceinline__ int split(int items, int tid, int n) {
+  return static_cast<int>(static_cast<int64_t>(items) * tid / n);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
+    mla_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qpe,
+                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_row, const AttnParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;
+  uint64_t* k_empty = k_full + kKGroups;
+  uint64_t* v_full = k_empty + kKGroups;
+  uint64_t* v_empty = v_full + kVChunks;
+  uint64_t* s_full = v_empty + kVChunks;  // [2]
+  uint64_t* s_empty = s_full + 2;         // [2]
+  uint64_t* p_full = s_empty + 2;
+  uint64_t* pv_done = p_full + 1;
+  uint64_t* o_empty = pv_done + 1;
+  uint64_t* red_bar = o_empty + 1;
+  uint64_t* drain = red_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* start = reinterpret_cast<int*>(tmem_slot + 2);  // first item, its first tile, unit count
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x) >> 1;
+  const int npairs_max = static_cast<int>(gridDim.x) >> 1;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < kKGroups; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kVChunks; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 8);  // four softmax warps of each CTA
+    }
+    mbar_init(p_full, 8);
+    mbar_init(pv_done, 1);
+    mbar_init(o_empty, 8);
+    mbar_init(red_bar, 4);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 6) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 128) {
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_qpe);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_row);
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // The plan: every CTA sums the items' tiles (thread-contiguous ranges, then
+  // a scan over the threads) and finds the item its range starts in.
+  {
+    int* sums = reinterpret_cast<int*>(smem);  // the query slabs are not loaded yet
+    const int lo = split(p.items, tid, kAttnThreads), hi = split(p.items, tid + 1, kAttnThreads);
+    int own = 0;
+    for (int i = lo; i < hi; ++i) own += get_item(p, i).tiles;
+    sums[tid] = own;
+    __syncthreads();
+    int before = 0, units = 0;
+    for (int i = 0; i < kAttnThreads; ++i) {
+      const int v = sums[i];
+      before += i < tid ? v : 0;
+      units += v;
+    }
+    const int pairs = max(1, min(npairs_max, units));
+    const int64_t u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
+    const int64_t u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
+    int at = before;
+    for (int i = lo; i < hi; ++i) {
+      const int n = get_item(p, i).tiles;
+      if (u0 < u1 && u0 >= at && u0 < at + n) {
+        start[0] = i;
+        start[1] = static_cast<int>(u0 - at);
+      }
+      if (blockIdx.x == 0) p.plan[2 + i] = at;
+      at += n;
+    }
+    if (tid == 0) start[2] = static_cast<int>(u1 - u0);
+    if (blockIdx.x == 0 && tid == 0) {
+      p.plan[0] = units;
+      p.plan[1] = pairs;
+      p.plan[2 + p.items] = units;
+    }
+  }
+  fence_proxy_async_smem();  // the scan's use of the query slabs, before TMA writes them
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int nunits = start[2];
+  const int item0 = nunits ? start[0] : 0, tile0 = nunits ? start[1] : 0;
+
+  if (warp == 4 || warp == 5) {
+    // ---- loads: queries and keys (warp 4), values (warp 5) -------------------
+    const bool is_k = warp == 4;
+    uint32_t n = 0, seg = 0;
+    int left = nunits, i = item0, t0 = tile0;
+    bool ok = true;
+    while (ok && left > 0 && i < p.items) {
+      const Item it = get_item(p, i);
+      const int t1 = min(it.tiles, t0 + left);
+      left -= t1 - t0;
+      if (is_k && t1 > t0) {
+        if (seg > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (seg - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        if (!ok) break;
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kQSlabs * kSlab);
+          const uint32_t bar = map_to_cta(smem_u32(q_full), 0);
+          const int y = it.row0 + static_cast<int>(rank) * 64;
+          for (int s = 0; s < kQSlabs; ++s)
+            tma_load_2d_pair(smem_u32(smem + kOffQ + s * kSlab), s < kC / 64 ? &map_q : &map_qpe, bar,
+                             s < kC / 64 ? s * 64 : 0, y);
+        }
+        __syncwarp();
+        ++seg;
+      }
+      for (int t = t0; ok && t < t1; ++t, ++n) {
+        const bool pre = t < it.pt;
+        const int key0 = (pre ? t : t - it.pt) * kTileKeys;
+        const int limit = pre ? p.P : it.len;
+        const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
+        if (is_k) {
+          // This CTA's 64 keys; lane l loads box l of every slab.
+          const int nbox = 64 / p.kbox;
+          const int key = key0 + static_cast<int>(rank) * 64 + lane * p.kbox;
+          const int y = lane < nbox && key < limit ? key_row(p, pages, key) : p.total_rows;
+          for (int g = 0; g < kKGroups; ++g) {
+            if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[g], (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            if (!ok) break;
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
+            const uint32_t bar = map_to_cta(smem_u32(&k_full[g]), 0);
+            if (lane < nbox)
+              for (int s = 3 * g; s < 3 * g + 3; ++s)
+                tma_load_2d_pair(smem_u32(smem + kOffK + s * kSlab + lane * p.kbox * 128), &map_k, bar, s * 64, y);
+            __syncwarp();
+          }
+        } else {
+          // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
+          // the half 128 rank .. + 128, as slabs 2 j and 2 j + 1 of each chunk.
+          for (int c = 0; c < kVChunks; ++c) {
+            const int kc = key0 + c * 32;
+            const bool whole = kc + 32 <= limit || kc >= limit;
+            const int nbox = whole ? 32 / p.vbox : 32;
+            const int key = kc + lane * (whole ? p.vbox : 1);
+            const int y = lane < nbox && key < limit ? key_row(p, pages, key) : p.total_rows;
+            if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[c], (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            if (!ok) break;
+            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
+            const uint32_t bar = map_to_cta(smem_u32(&v_full[c]), 0);
+            if (lane < nbox) {
+              const uint32_t dst = smem_u32(smem + kOffV + c * kVChunk) + lane * (whole ? p.vbox : 1) * 128;
+              for (int s = 0; s < 4; ++s)
+                tma_load_2d_pair(dst + s * kVSlab, whole ? &map_v : &map_row, bar,
+                                 (s >> 1) * 256 + static_cast<int>(rank) * 128 + (s & 1) * 64, y);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      ++i;
+      t0 = 0;
+    }
+    if (*abort_flag && rank == 0) {
+      // Copies of both CTAs complete on this CTA's barriers: wait for the last
+      // phase each was armed for.
+      if (is_k) {
+        if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+        for (int g = 0; g < kKGroups; ++g)
+          if (n > 0) mbar_wait(&k_full[g], (n - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+      } else {
+        for (int c = 0; c < kVChunks; ++c)
+          if (n > 0) mbar_wait(&v_full[c], (n - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+      }
+    }
+  } else if (warp == 6) {
+    // ---- MMA (CTA 0 issues for the pair) -------------------------------------
+    if (rank == 0) {
+      constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 256, true);
+      const uint32_t qa = smem_u32(smem + kOffQ), pa = smem_u32(smem + kOffP);
+      const uint32_t ka = smem_u32(smem + kOffK), va = smem_u32(smem + kOffV);
+      uint32_t n = 0, seg = 0;
+      int left = nunits, i = item0, t0 = tile0;
+      bool ok = true;
+      bool prev_first = false;
+      uint32_t prev_seg = 0;
+      // The output product of tile k (whose weights the softmax warps publish
+      // while the scores of tile k + 1 are formed).
+      auto output = [&](uint32_t k, bool first, uint32_t sg) {
+        if (first && sg > 0)
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(o_empty, (sg - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_full, k & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        for (int c = 0; ok && c < kVChunks; ++c) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&v_full[c], k & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one_sync()) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int ks = 2 * c + h;  // 16 keys
+              const uint64_t ad = sdesc_kmajor_sw128(pa + (ks >> 2) * kSlab) + 2 * (ks & 3);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_bf16_pair(tmem + j * 128, ad, sdesc_mn_sw128(va + c * kVChunk + j * 2 * kVSlab + h * 2048, kVSlab),
+                              kIdO, first && ks == 0 ? 0u : 1u);
+            }
+            mma_commit_pair(&v_empty[c]);
+            if (c == kVChunks - 1) mma_commit_pair(pv_done);
+          }
+          __syncwarp();
+        }
+      };
+      while (ok && left > 0 && i < p.items) {
+        const Item it = get_item(p, i);
+        const int t1 = min(it.tiles, t0 + left);
+        left -= t1 - t0;
+        for (int t = t0; ok && t < t1; ++t) {
+          const uint32_t buf = n & 1;
+          if (t == t0) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(q_full, seg & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          if (n > 1)
+            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err,
+                                                                 kDevErrTimeoutMla));
+          for (int g = 0; ok && g < kKGroups; ++g) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&k_full[g], n & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (elect_one_sync()) {
+#pragma unroll
+              for (int s = 3 * g; s < 3 * g + 3; ++s) {
+                const uint64_t ad = sdesc_kmajor_sw128(qa + s * kSlab), bd = sdesc_kmajor_sw128(ka + s * kSlab);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16_pair(tmem + kTmemS + buf * 64, ad + 2 * k, bd + 2 * k, kIdS, s > 0 || k > 0 ? 1u : 0u);
+              }
+              mma_commit_pair(&k_empty[g]);
+              if (g == kKGroups - 1) {
+                mma_commit_pair(&s_full[buf]);
+                if (t == t1 - 1) mma_commit_pair(q_empty);
+              }
+            }
+            __syncwarp();
+          }
+          if (ok && n > 0) output(n - 1, prev_first, prev_seg);
+          prev_first = t == t0;
+          prev_seg = seg;
+          ++n;
+        }
+        if (t1 > t0) ++seg;
+        ++i;
+        t0 = 0;
+      }
+      if (ok && n > 0) output(n - 1, prev_first, prev_seg);
+      if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
+        if (elect_one_sync()) mma_commit_pair(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, nullptr, p.err, kDevErrTimeoutMla);
+      }
+    }
+  } else {
+    // ---- softmax and stores ---------------------------------------------------
+    const int row = (warp & 1) * 32 + lane;   // of this CTA's 64
+    const int kh = warp >> 1;                 // key half of the scores, column half of the output
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t leader_p = map_to_cta(smem_u32(p_full), 0), leader_o = map_to_cta(smem_u32(o_empty), 0);
+    uint8_t* prow = smem + kOffP + kh * kSlab + row * 128;
+    uint32_t n = 0, nred = 0;
+    int left = nunits, i = item0, t0 = tile0;
+    bool ok = true;
+    // Both threads of a row give a value; returns the partner's (bounded wait:
+    // the four warps meet on an mbarrier).
+    auto exchange = [&](float v) {
+      float* r = red + (nred & 1) * 128;
+      r[kh * 64 + row] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(red_bar);
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(red_bar, nred & 1, abort_flag, p.err, kDevErrTimeoutMla));
+      ++nred;
+      return r[(kh ^ 1) * 64 + row];
+    };
+    while (ok && left > 0 && i < p.items) {
+      const Item it = get_item(p, i);
+      const int t1 = min(it.tiles, t0 + left);
+      left -= t1 - t0;
+      const int rt = static_cast<int>(rank) * 64 + row;  // row of the tile
+      const bool have = rt < it.nrows;
+      float m = -INFINITY, l = 0.f, lx = 0.f;  // running maximum, sums of rounded and of fp32 weights
+      for (int t = t0; ok && t < t1; ++t, ++n) {
+        const bool pre = t < it.pt;
+        const int key0 = (pre ? t : t - it.pt) * kTileKeys;
+        const int valid = have ? (pre ? p.P : it.len) - key0 - kh * 64 : 0;  // keys of this half that count
+        const uint32_t buf = n & 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[buf], (n >> 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        if (!ok) break;
+        tc_fence_after_sync();
+        uint32_t s[64];
+        tmem_ld_32x32b_x64(t_lane + kTmemS + buf * 64, s);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&s_empty[buf]), 0));
+        if (valid < 64) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j >= valid) s[j] = 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        mt = fmaxf(mt, exchange(mt)) * p.scale_log2;
+        if (!ok) break;
+        float fix = 1.f;
+        bool raised = false;
+        if (mt > m + kRaise) {
+          raised = m != -INFINITY;  // a row without keys so far has no output to rescale
+          fix = ex2(m - mt);
+          m = mt;
+        }
+        const bool rescale = __any_sync(0xFFFFFFFFu, raised);
+        l *= fix;
+        lx *= fix;
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint32_t w[32];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f}, sx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float a = ex2(fmaf(__uint_as_float(s[2 * j]), p.scale_log2, -mu));
+          const float b = ex2(fmaf(__uint_as_float(s[2 * j + 1]), p.scale_log2, -mu));
+          const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+          w[j] = *reinterpret_cast<const uint32_t*>(&r);
+          sum[2 * (j & 1)] += __uint_as_float(w[j] << 16);
+          sum[2 * (j & 1) + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+          sx[2 * (j & 1)] += a;
+          sx[2 * (j & 1) + 1] += b;
+        }
+        lx += (sx[0] + sx[1]) + (sx[2] + sx[3]);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // The previous tile's output product has read P and written the output.
+        if (n > 0) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done, (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
+        if (rescale && t > t0) {
+          tc_fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_lane + c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * fix);
+            tmem_st_32x32b_x32(t_lane + c, o);
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_p);
+      }
+      if (ok && t1 > t0) {
+        const float lt = l + exchange(l);
+        const float lxt = lx + exchange(lx);
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(pv_done, (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const bool cut = t0 > 0 || t1 < it.tiles || (!p.merged && p.prefix_tiles > 0);
+        const int64_t r = it.row0 + rt;
+        if (!cut) {
+          const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;  // NaN stays NaN
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_lane + c, o);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + r * kC + (c >> 7) * 256 + kh * 128 + (c & 127));
+            if (have) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * g + 2 * e]) * inv,
+                                                                  __uint_as_float(o[8 * g + 2 * e + 1]) * inv);
+                  v[e] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                dst[g] = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+          if (have && kh == 0 && p.lse) p.lse[r] = m * 0.69314718055994531f + logf(lxt);
+        } else {
+          const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, i, pair) + rt;
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_lane + c, o);
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + pr * kC + (c >> 7) * 256 + kh * 128 + (c & 127));
+            if (have) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) dst[g] = make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+            }
+          }
+          if (have && kh == 0) p.part_ml[pr] = make_float4(m, lt, lxt, 0.f);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_o);
+      }
+      ++i;
+      t0 = 0;
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 6) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Joins the parts of each query row, in item and key order: with weights
+// 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k. One CTA per row: four
+// warps take the parts round robin (a lane has 16 of the 512 columns), then
+// add up in shared memory in warp order. Rows whose one item was not cut were
+// stored by the attention kernel; rows without any key become zeros.
+__global__ void __launch_bounds__(128) mla_join_kernel(const AttnParams p) {
+  __shared__ float4 acc_s[3][128];
+  __shared__ float ml_s[4][3];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t r = blockIdx.x;
+  const int b = static_cast<int>(r / p.H), h = static_cast<int>(r % p.H);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.plan[0], pairs = p.plan[1];
+  // Up to two items hold the row's keys: (item, row of the item).
+  int item[2], local[2], n_items = 0;
+  if (p.merged) {
+    item[0] = static_cast<int>(r / kTileRows);
+    local[0] = static_cast<int>(r % kTileRows);
+    n_items = 1;
+  } else {
+    if (p.prefix_tiles > 0) {
+      item[0] = static_cast<int>(r / kTileRows);
+      local[0] = static_cast<int>(r % kTileRows);
+      n_items = 1;
+    }
+    item[n_items] = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
+    local[n_items] = h % kTileRows;
+    ++n_items;
+  }
+  // Pairs [q0, q1] hold the units [a, e) of an item.
+  int q0[2], q1[2], parts = 0;
+  bool any_cut = !p.merged && p.prefix_tiles > 0;
+  for (int k = 0; k < n_items; ++k) {
+    const int64_t a = p.plan[2 + item[k]], e = p.plan[3 + item[k]];
+    q0[k] = 0;
+    q1[k] = -1;
+    if (e > a) {
+      // pair q owns [units q / pairs, units (q + 1) / pairs): the pair of unit u
+      // is the largest q with units q / pairs <= u.
+      q0[k] = static_cast<int>(((a + 1) * pairs - 1) / units);
+      q1[k] = static_cast<int>((e * pairs - 1) / units);
+      if (q1[k] > q0[k]) any_cut = true;
+    }
+    parts += q1[k] - q0[k] + 1;
+  }
+  if (parts == 1 && !any_cut) return;
+  float m = -INFINITY, l = 0.f, lx = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n0 = q1[0] - q0[0] + 1;
+  for (int k = warp; k < parts; k += 4) {
+    const int which = k < n0 ? 0 : 1;
+    const int q = which == 0 ? q0[0] + k : q0[1] + k - n0;
+    const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, item[which], q) + local[which];
+    const float4 ml = p.part_ml[pr];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + pr * kC) + lane;
+    float4 v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = __ldcs(src + c * 32);
+    const float mn = fmaxf(m, ml.x);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float wo = ex2(m - mu), wn = ex2(ml.x - mu);
+    m = mn;
+    l = l * wo + ml.y * wn;
+    lx = lx * wo + ml.z * wn;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      acc[c].x = acc[c].x * wo + v[c].x * wn;
+      acc[c].y = acc[c].y * wo + v[c].y * wn;
+      acc[c].z = acc[c].z * wo + v[c].z * wn;
+      acc[c].w = acc[c].w * wo + v[c].w * wn;
+    }
+  }
+  if (lane == 0) {
+    ml_s[warp][0] = m;
+    ml_s[warp][1] = l;
+    ml_s[warp][2] = lx;
+  }
+  __syncthreads();
+  const float mm = fmaxf(fmaxf(ml_s[0][0], ml_s[1][0]), fmaxf(ml_s[2][0], ml_s[3][0]));
+  const float mu = mm == -INFINITY ? 0.f : mm;
+  float lt = 0.f, lxt = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float wk = ex2(ml_s[k][0] - mu);
+    lt += ml_s[k][1] * wk;
+    lxt += ml_s[k][2] * wk;
+  }
+  // Column vector c of warp 0's lane: the four warps' sums, through shared memory.
+  const float wgt = ex2(m - mu);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    acc[c].x *= wgt;
+    acc[c].y *= wgt;
+    acc[c].z *= wgt;
+    acc[c].w *= wgt;
+    if (warp > 0) acc_s[warp - 1][c * 32 + lane] = acc[c];
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float4 a = acc[c];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const float4 o = acc_s[k][c * 32 + lane];
+      a.x += o.x;
+      a.y += o.y;
+      a.z += o.z;
+      a.w += o.w;
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+    reinterpret_cast<uint2*>(p.out + r * kC)[c * 32 + lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  if (lane == 0 && p.lse) p.lse[r] = lt == 0.f ? -INFINITY : mm * 0.69314718055994531f + logf(lxt);
+}
+
+// ---- host --------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn attention_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* q = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &st) == cudaSuccess &&
+        st == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(q);
+  });
+  return fn;
+}
+
+// bf16 rows x cols, boxes of 64 columns x box_rows, 128-byte swizzled.
+bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  EncodeTiledFn enc = attention_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
+
+struct AttnSizes {
+  bool merged;
+  int64_t prefix_items, items, own_rows, part_rows;
+  size_t plan_bytes, ml_bytes, o_bytes;
+};
+
+AttnSizes attention_sizes(int64_t B, int64_t H, int64_t P) {
+  AttnSizes z{};
+  z.merged = H % kTileRows == 0;
+  z.own_rows = H < kTileRows ? H : kTileRows;
+  const int64_t per = (H + kTileRows - 1) / kTileRows;
+  z.prefix_items = !z.merged && P > 0 ? (B * H + kTileRows - 1) / kTileRows : 0;
+  z.items = z.merged ? B * per : z.prefix_items + B * per;
+  z.part_rows = part_row(z.merged, static_cast<int>(z.prefix_items), static_cast<int>(z.own_rows),
+                         static_cast<int>(z.items), kMaxPairs);
+  z.plan_bytes = align256(static_cast<size_t>(z.items + 3) * 4);
+  z.ml_bytes = align256(static_cast<size_t>(z.part_rows) * 16);
+  z.o_bytes = static_cast<size_t>(z.part_rows) * kC * 4;
+  return z;
+}
+
+bool attention_shape_ok(int64_t B, int64_t H, int64_t P) {
+  return B >= 0 && H >= 1 && H <= 1024 && P >= 0 && P <= (int64_t{1} << 30) && B <= (int64_t{1} << 20) &&
+         B * H <= (int64_t{1} << 24);
+}
+
+// CTA pairs that run at once (one CTA per SM).
+int resident_pairs(const DevInfo* d) {
+  static int cached[64] = {};
+  if (d->device < 64 && cached[d->device]) return cached[d->device];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(d->sm_count / 2 * 2));
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kAttnSmem;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, mla_attention_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = d->sm_count / 2;
+  }
+  if (n > kMaxPairs) n = kMaxPairs;
+  if (d->device < 64) cached[d->device] = n;
+  return n;
+}
+
+}  // namespace
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" size_t fp8blk_mla_attention_workspace_bytes(int64_t B, int64_t H, int64_t prefix_len) {
+  if (!attention_shape_ok(B, H, prefix_len)) return 0;
+  const AttnSizes z = attention_sizes(B, H, prefix_len);
+  return z.plan_bytes + z.ml_bytes + z.o_bytes;
+}
+
+extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, int64_t B, int64_t H,
+                                    const void* cache_bf16, int64_t num_pages, int64_t page_size,
+                                    const int32_t* prefix_pages, int64_t prefix_len, const int32_t* block_table,
+                                    int64_t table_stride, const int32_t* lens, float scale, void* out_bf16, float* lse,
+                                    void* workspace, size_t workspace_bytes, fp8blk_stream_t stream) {
+  if (!attention_shape_ok(B, H, prefix_len)) return FP8BLK_ERR_SHAPE;
+  if (page_size < 16 || page_size % 16 || num_pages < 0 || table_stride < 0 ||
+      num_pages * page_size > (int64_t{1} << 31) - 129 || table_stride * page_size > (int64_t{1} << 30) ||
+      page_size > (int64_t{1} << 20))
+    return FP8BLK_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 1e30f) return FP8BLK_ERR_ARG;
+  if (B == 0) return FP8BLK_OK;
+  if (!q_bf16 || !q_pe_bf16 || !lens || !out_bf16 || (num_pages > 0 && !cache_bf16) ||
+      (prefix_len > 0 && !prefix_pages) || (table_stride > 0 && !block_table))
+    return FP8BLK_ERR_NULL;
+  if (!is_aligned(q_bf16, 16) || !is_aligned(q_pe_bf16, 16) || !is_aligned(cache_bf16, 16) ||
+      !is_aligned(out_bf16, 16) || !is_aligned(lens, 4) || !is_aligned(prefix_pages, 4) ||
+      !is_aligned(block_table, 4) || !is_aligned(lse, 4))
+    return FP8BLK_ERR_ALIGN;
+  if (!workspace) return FP8BLK_ERR_WORKSPACE;
+  if (!is_aligned(workspace, 256)) return FP8BLK_ERR_ALIGN;
+  const AttnSizes z = attention_sizes(B, H, prefix_len);
+  if (workspace_bytes < z.plan_bytes + z.ml_bytes + z.o_bytes) return FP8BLK_ERR_WORKSPACE;
+  // The tile counts are summed in 32 bits.
+  const int64_t most = (prefix_len + kTileKeys - 1) / kTileKeys * (z.merged ? z.items : z.prefix_items) +
+                       (table_stride * page_size / kTileKeys + 1) * (z.items - z.prefix_items);
+  if (most > (int64_t{1} << 31) - 1) return FP8BLK_ERR_SHAPE;
+  const DevInfo* d;
+  if (int st = current_device(&d)) return st;
+  static bool attr_done[64] = {};
+  if (d->device >= 64 || !attr_done[d->device]) {
+    if (cudaFuncSetAttribute(mla_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem) !=
+        cudaSuccess)
+      return FP8BLK_ERR_CUDA;
+    if (d->device < 64) attr_done[d->device] = true;
+  }
+  AttnParams p{};
+  p.prefix_pages = prefix_pages;
+  p.table = block_table;
+  p.lens = lens;
+  p.out = static_cast<__nv_bfloat16*>(out_bf16);
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.plan = reinterpret_cast<int*>(ws);
+  p.part_ml = reinterpret_cast<float4*>(ws + z.plan_bytes);
+  p.part_o = reinterpret_cast<float*>(ws + z.plan_bytes + z.ml_bytes);
+  p.err = d->err_word;
+  p.B = static_cast<int>(B);
+  p.H = static_cast<int>(H);
+  p.P = static_cast<int>(prefix_len);
+  p.page = static_cast<int>(page_size);
+  p.page_shift = -1;
+  for (int s = 0; s < 21; ++s)
+    if ((int64_t{1} << s) == page_size) p.page_shift = s;
+  p.num_pages = static_cast<int>(num_pages);
+  p.table_stride = static_cast<int>(table_stride);
+  p.max_own = static_cast<int>(table_stride * page_size);
+  p.total_rows = static_cast<int>(num_pages * page_size);
+  p.prefix_tiles = static_cast<int>((prefix_len + kTileKeys - 1) / kTileKeys);
+  p.prefix_items = static_cast<int>(z.prefix_items);
+  p.items = static_cast<int>(z.items);
+  p.own_rows = static_cast<int>(z.own_rows);
+  p.merged = z.merged ? 1 : 0;
+  p.kbox = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  p.vbox = page_size % 32 == 0 ? 32 : 16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  // A cache without pages is never read: its maps describe one row of q.
+  const void* cbase = num_pages > 0 ? cache_bf16 : q_bf16;
+  const uint64_t crows = num_pages > 0 ? static_cast<uint64_t>(num_pages * page_size) : 1;
+  const uint64_t ccols = num_pages > 0 ? kRow : kC;
+  CUtensorMap mq, mqp, mk, mv, mr;
+  if (!make_bf16_map(&mq, q_bf16, static_cast<uint64_t>(B * H), kC, 64) ||
+      !make_bf16_map(&mqp, q_pe_bf16, static_cast<uint64_t>(B * H), kR, 64) ||
+      !make_bf16_map(&mk, cbase, crows, ccols, static_cast<uint32_t>(p.kbox)) ||
+      !make_bf16_map(&mv, cbase, crows, ccols, static_cast<uint32_t>(p.vbox)) ||
+      !make_bf16_map(&mr, cbase, crows, ccols, 1))
+    return FP8BLK_ERR_CUDA;
+  if (num_pages == 0) p.total_rows = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * resident_pairs(d)));
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kAttnSmem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, mr, p))) return st;
+  cudaLaunchConfig_t join = {};
+  join.gridDim = dim3(static_cast<unsigned>(B * H));
+  join.blockDim = dim3(128);
+  join.stream = cfg.stream;
+  join.attrs = attr;
+  join.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&join, mla_join_kernel, p));
+}

@@ -277,6 +277,67 @@ FP8BLK_API int fp8blk_mla_absorb_v(const void *x_bf16, const void *wkv_b_e4m3, c
                                    int64_t T, int64_t H, int64_t dn, int64_t dv, int64_t C, fp8blk_stream_t stream);
 
 /*
+ * Latent cache append ("Administrator & Developer Guide", 8.3: the MLA layer
+ * caches the normalised latent and the rotated key part; 1.2: RMSNorm, rotary
+ * embedding). For token t with position p = positions[t]:
+ *     cache[slots[t], 0:512]   = bf16( kv[t, 0:512] / sqrt(mean of kv[t, 0:512]^2 + eps) * norm_w )
+ *     cache[slots[t], 512:576] = bf16( rot_p(kv[t, 512:576]) )
+ * and, with q given, per head h:
+ *     q_nope[t, h] = q[t, h, 0:128]  (the operand of fp8blk_mla_absorb_qk)
+ *     q_pe[t, h]   = bf16( rot_p(q[t, h, 128:192]) )
+ * where rot_p turns the pairs (v[2i], v[2i + 1]) to (v[2i] c - v[2i+1] s,
+ * v[2i] s + v[2i+1] c), (c, s) = rope[p, i]. fp32 arithmetic, one rounding.
+ * kv: bf16 [T, 576], rows kv_stride elements apart. q: bf16 [T, H, 192] or
+ * NULL, tokens q_stride elements apart (a head's 192 columns and the heads
+ * contiguous). norm_w: fp32 [512]. rope: fp32 [max_pos, 32, 2]. positions and
+ * slots: int64 [T]. cache: bf16 [num_slots, 576], slot = page * page_size +
+ * offset of a paged cache. A negative slot marks a padding token: its cache
+ * row is not written (its queries are). Two tokens of one call must not name
+ * the same slot. A slot >= num_slots is not written and a position outside
+ * [0, max_pos) is taken as 0; both set device error bit 0x100.
+ * 1 <= H <= 1024, kv_stride >= 576, q_stride >= 192 H, strides multiples of 8
+ * (FP8BLK_ERR_ALIGN), eps >= 0. kv, q, norm_w, rope, cache, q_nope, q_pe
+ * 16-byte aligned. T == 0 launches nothing. No workspace.
+ */
+FP8BLK_API int fp8blk_mla_append(const void *kv_bf16, int64_t kv_stride, const float *norm_w, float eps,
+                                 const void *q_bf16, int64_t q_stride, int64_t H, const float *rope, int64_t max_pos,
+                                 const int64_t *positions, const int64_t *slots, int64_t T, void *cache_bf16,
+                                 int64_t num_slots, void *q_nope_bf16, void *q_pe_bf16, fp8blk_stream_t stream);
+
+/*
+ * Attention of one query token per request over the paged latent cache, with
+ * a prefix that the whole batch shares ("Administrator & Developer Guide",
+ * 8.3, attn_impl "absorb"). Request b's keys are the prefix_len rows that
+ * prefix_pages names, then the lens[b] rows that block_table[b] names; key j
+ * of a page list is row j % page_size of page list[j / page_size]. With
+ * x[b, h] = [q[b, h] (512), q_pe[b, h] (64)] and cache rows c_j (576):
+ *     a = softmax over the request's keys of scale * <x[b, h], c_j>,
+ *     out[b, h] = bf16( sum_j a_j c_j[0:512] ),
+ *     lse[b, h] = log( sum_j exp(scale * <x[b, h], c_j>) )   (lse may be NULL).
+ * Products of bf16 numbers summed in fp32 on the tensor cores; maxima, sums
+ * and the output accumulate in fp32; the weights are rounded to bf16 for the
+ * second product. A row without any key gives zeros and lse = -inf. Cache rows
+ * past a length, and table entries past a request's pages, may hold anything.
+ * q: bf16 [B, H, 512] (fp8blk_mla_absorb_qk's output), q_pe: bf16 [B, H, 64],
+ * cache: bf16 [num_pages, page_size, 576], prefix_pages: int32
+ * [ceil(prefix_len / page_size)], block_table: int32 [B, table_stride],
+ * lens: int32 [B] on the device (outside [0, table_stride * page_size]: taken
+ * as the nearer end), out: bf16 [B, H, 512], lse: fp32 [B, H]. A page id
+ * outside [0, num_pages) reads as zeros and sets device error bit 0x100.
+ * page_size a multiple of 16; 1 <= H <= 1024, B * H <= 2^24, num_pages *
+ * page_size < 2^31 - 128; scale > 0 (FP8BLK_ERR_ARG). bf16 tensors 16-byte
+ * aligned. Two launches; the result does not vary from run to run.
+ * Workspace: fp8blk_mla_attention_workspace_bytes(B, H, prefix_len), 256-byte
+ * aligned, any contents.
+ */
+FP8BLK_API size_t fp8blk_mla_attention_workspace_bytes(int64_t B, int64_t H, int64_t prefix_len);
+FP8BLK_API int fp8blk_mla_attention(const void *q_bf16, const void *q_pe_bf16, int64_t B, int64_t H,
+                                    const void *cache_bf16, int64_t num_pages, int64_t page_size,
+                                    const int32_t *prefix_pages, int64_t prefix_len, const int32_t *block_table,
+                                    int64_t table_stride, const int32_t *lens, float scale, void *out_bf16, float *lse,
+                                    void *workspace, size_t workspace_bytes, fp8blk_stream_t stream);
+
+/*
  * MoE gate ("Administrator & Developer Guide", 8.4 the Gate and 3.3 per-config
  * fields; "Repository overview" page, MoE data flow: scores, optional group
  * masking, top-k indices, the original scores, normalize, route_scale).
@@ -398,7 +459,7 @@ FP8BLK_API int fp8blk_gemm_noalloc(const void *a_e4m3, const float *a_s, const v
  * 0x01-0x08: a GEMM role gave up waiting (producer, MMA, epilogue, drain);
  * 0x20: an expert id outside [0, E) (MoE); 0x40: an MLA kernel gave up
  * waiting; 0x80: a UE8M0-format scale that is not a positive normal power of
- * two. After a wait gave up, that kernel returned early: its outputs are
+ * two; 0x100: a cache slot, page id or position out of range. After a wait gave up, that kernel returned early: its outputs are
  * undefined and the workspace's first 64 KB must be zero-filled again before
  * reuse. The function returns FP8BLK_ERR_TIMEOUT when any bit is set.
  */
