@@ -26,6 +26,7 @@ __all__ = [
     "last_device_error",
     "swiglu_gemm", "ffn", "moe_permute", "moe_workspace_bytes", "moe_grouped_gemm", "moe_gate", "moe_route",
     "mla_absorb", "mla_append", "mla_attention", "mla_attention_workspace_bytes",
+    "moe_layer", "moe_layer_workspace_bytes", "SCORE_SOFTMAX", "SCORE_SIGMOID",
 ]
 
 SCALE_FP32 = 0
@@ -542,4 +543,61 @@ def moe_grouped_gemm(x: torch.Tensor, x_s: torch.Tensor, topk_idx: torch.Tensor,
     _check(f(_ptr(x), _ptr(x_s), _ptr(topk_idx), _ptr(topk_w), _ptr(w1), _ptr(w1_s), _ptr(w3), _ptr(w3_s),
              _ptr(w2), _ptr(w2_s), _ptr(out), T, k, E, dim, inter, n_shared, scale_fmt, _ptr(ws), ws.numel(),
              _stream(x.device)), "moe_grouped_gemm")
+    return out
+
+
+MOE_LAYER_MAX_TOKENS = 32
+
+
+def moe_layer_workspace_bytes(T: int, topk: int, E: int, dim: int, inter: int, n_shared: int = 0) -> int:
+    i64 = ctypes.c_int64
+    return int(_set_types("fp8blk_moe_layer_workspace_bytes", [i64] * 6, ctypes.c_size_t)(T, topk, E, dim, inter,
+                                                                                          n_shared))
+
+
+def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_s, topk: int,
+              gate_bias: torch.Tensor | None = None, n_groups: int = 1, topk_groups: int = 1,
+              score_func: int = SCORE_SIGMOID, route_scale: float = 1.0, normalize: bool = True, n_shared: int = 0,
+              scale_fmt: int = SCALE_FP32, out: torch.Tensor | None = None, idx: torch.Tensor | None = None,
+              w: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """A whole MoE layer for up to 32 tokens in one kernel: gate product and gate (x bf16 [T, dim], gate_w bf16
+    [E, dim], gate_bias fp32 [E]), routed and shared experts (stacked e4m3 weights and block scales as for
+    moe_grouped_gemm) and their sum -> bf16 [T, dim]. idx int32 / w fp32 [T, topk] receive the routing where given."""
+    _need(x, torch.bfloat16, "x")
+    _need(gate_w, torch.bfloat16, "gate_w")
+    for t, n, dt in ((w1, "w1", torch.float8_e4m3fn), (w3, "w3", torch.float8_e4m3fn), (w2, "w2", torch.float8_e4m3fn),
+                     (w1_s, "w1_s", torch.float32), (w3_s, "w3_s", torch.float32), (w2_s, "w2_s", torch.float32)):
+        _need(t, dt, n)
+    T, dim = x.shape
+    E, inter = gate_w.shape[0], w2.shape[1]
+    K = E + n_shared
+    if gate_w.shape[1] != dim or tuple(w1.shape) != (K * inter, dim) or tuple(w3.shape) != (K * inter, dim) or \
+            w2.shape[0] != K * dim:
+        raise Fp8BlkError("gate_w must be [E, dim], w1 and w3 [(E + n_shared) * inter, dim], "
+                          "w2 [(E + n_shared) * dim, inter]")
+    s13, s2 = (K * inter // BLOCK, dim // BLOCK), (K * dim // BLOCK, inter // BLOCK)
+    if tuple(w1_s.shape) != s13 or tuple(w3_s.shape) != s13 or tuple(w2_s.shape) != s2:
+        raise Fp8BlkError("block scales must have one entry per 128x128 block")
+    if gate_bias is not None:
+        _need(gate_bias, torch.float32, "gate_bias", ndim=1)
+        if gate_bias.shape[0] != E:
+            raise Fp8BlkError("gate_bias must be [E]")
+    if out is None:
+        out = torch.empty((T, dim), dtype=torch.bfloat16, device=x.device)
+    _need(out, torch.bfloat16, "out")
+    if tuple(out.shape) != (T, dim):
+        raise Fp8BlkError("out must be [T, dim]")
+    for t, n, dt in ((idx, "idx", torch.int32), (w, "w", torch.float32)):
+        if t is not None:
+            _need(t, dt, n)
+            if tuple(t.shape) != (T, topk):
+                raise Fp8BlkError(f"{n} must be [T, topk]")
+    if ws is None:
+        ws = workspace(moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared), x.device, "moe_layer")
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    f = _set_types("fp8blk_moe_layer", [vp] * 10 + [i64] * 8 + [i32, f32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp])
+    _check(f(_ptr(x), _ptr(gate_w), _ptr(gate_bias), _ptr(w1), _ptr(w1_s), _ptr(w3), _ptr(w3_s), _ptr(w2), _ptr(w2_s),
+             _ptr(out), T, topk, E, dim, inter, n_shared, n_groups, topk_groups, score_func, float(route_scale),
+             int(bool(normalize)), scale_fmt, _ptr(idx), _ptr(w), _ptr(ws), ws.numel(), _stream(x.device)),
+           "moe_layer")
     return out

@@ -1,0 +1,143 @@
+// The MoE gate of one token, by one warp: shared by the gate and route
+// kernels and the few-token layer.
+// Per token ("Administrator & Developer Guide", 8.4 and 3.3; "Repository
+// overview" MoE data flow): scores s from the logits (sigmoid, or softmax over
+// the E experts), selection keys z = s + bias (z = s without a bias); with G > 1
+// groups of E/G consecutive experts a group scores its largest z (no bias) or
+// the sum of its two largest (bias), and only the TG best groups' experts stay
+// eligible; the K best eligible z give the experts in descending order (ties:
+// lower index); the weights are their s, divided by the sum of the K when
+// `normalize`, times route_scale.
+//
+// One warp per token. Lane l holds experts [l V, l V + V) (E = 32 V), so a
+// group is a run of 32 / G whole lanes: group maxima and top-two pairs merge
+// with shuffles inside that run. Each top-k round is a warp argmax over 64-bit
+// keys (order-preserving bits of z, then the complement of the index).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+namespace fp8blk {
+
+__device__ __forceinline__ uint64_t gate_key(float z, int e) {
+  const uint32_t u = __float_as_uint(z);
+  const uint32_t ord = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<uint64_t>(ord) << 32) | static_cast<uint32_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
+}
+
+__device__ __forceinline__ uint64_t warp_max_u64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = w > v ? w : v;
+  }
+  return v;
+}
+
+// The gate of one token, computed by one warp from its logits: lane l holds
+// x[i] = logit of expert l v + i for i < v <= V (E = 32 v experts; v = V where
+// the caller knows it at compile time), and the experts' biases likewise. Lane
+// j < K ends with the expert of slot j in *out_idx and its weight (normalised,
+// times route_scale) in *out_w.
+template <int V>
+__device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V], bool has_bias, int v, int G, int TG,
+                                          int K, int sigmoid, float route_scale, int normalize, int lane, int* out_idx,
+                                          float* out_w) {
+  float s[V], z[V];
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < v) s[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x[i])));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < v) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < v) {
+        x[i] = expf(__fsub_rn(x[i], m));
+        sum = __fadd_rn(sum, x[i]);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < v) s[i] = __fdiv_rn(x[i], sum);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < v) z[i] = has_bias ? __fadd_rn(s[i], bias[i]) : s[i];
+
+  // Group selection: a lane is eligible while its group is kept.
+  bool eligible = true;
+  if (G > 1) {
+    const int lpg = 32 / G;  // lanes per group
+    float a = -INFINITY, b = -INFINITY;  // this lane's two largest z
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i >= v) continue;
+      if (z[i] > a) {
+        b = a;
+        a = z[i];
+      } else if (z[i] > b) {
+        b = z[i];
+      }
+    }
+    for (int o = lpg >> 1; o > 0; o >>= 1) {  // merge the pairs of the group's lanes
+      const float a2 = __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      const float b2 = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+      const float hi = fmaxf(a, a2);
+      b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+      a = hi;
+    }
+    const float gscore = has_bias ? __fadd_rn(a, b) : a;
+    const int g = lane / lpg;
+    bool kept = false;
+    for (int r = 0; r < TG; ++r) {
+      const uint64_t best = warp_max_u64(kept ? 0ull : gate_key(gscore, g));
+      if (static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best)) == g) kept = true;
+    }
+    eligible = kept;
+  }
+
+  // Top-k experts among the eligible lanes' z.
+  uint32_t taken = 0;
+  int my_idx = 0;
+  float my_s = 0.0f, sum = 0.0f;
+  for (int j = 0; j < K; ++j) {
+    uint64_t key = 0;
+    if (eligible) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint64_t k = i >= v || ((taken >> i) & 1u) ? 0ull : gate_key(z[i], lane * v + i);
+        key = k > key ? k : key;
+      }
+    }
+    key = warp_max_u64(key);
+    const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    const int owner = e / v;
+    float se = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane == owner && i < v && e - lane * v == i) {
+        se = s[i];
+        taken |= 1u << i;
+      }
+    se = __shfl_sync(0xFFFFFFFFu, se, owner);
+    sum = __fadd_rn(sum, se);
+    if (lane == j) {
+      my_idx = e;
+      my_s = se;
+    }
+  }
+  *out_idx = my_idx;
+  *out_w = __fmul_rn(normalize ? __fdiv_rn(my_s, sum) : my_s, route_scale);
+}
+
+}  // namespace fp8blk

@@ -424,6 +424,45 @@ FP8BLK_API int fp8blk_moe_grouped_gemm(const void *x_e4m3, const float *x_s, con
                                        size_t workspace_bytes, fp8blk_stream_t stream);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens, in one kernel
+ * ("Administrator & Developer Guide", 8.4 and 6.3): the gate product, the
+ * gate, the routed and the shared experts and their weighted sum. Per token t:
+ *     logits[t, e] = sum_i x[t, i] * gate_w[e, i]                    (fp32)
+ *     (topk_idx, topk_w)[t] = fp8blk_moe_gate of logits[t] with gate_bias
+ *     xq = act_quant(x),   h1 = w1_e xq,  h3 = w3_e xq   (block-scaled, fp32)
+ *     uq = act_quant(silu(h1) * h3)                      (fp32 until here)
+ *     y[t] = bf16( sum over j of topk_w[t, j] * (w2_e uq)  with e = topk_idx[t, j]
+ *                  + sum over shared experts s of w2_s uq )
+ * with fp32 sums and one rounding of y. (The chain of fp8blk_moe_gate and
+ * fp8blk_moe_grouped_gemm rounds h1, h3, silu, u, each expert's output and the
+ * two sums to bf16; the results differ by those roundings.) UE8M0 in scale_fmt
+ * rounds the activation scales up to powers of two; weight scales are fp32 of
+ * any value, as in fp8blk_gemm.
+ * x: bf16 [T, dim], gate_w: bf16 [E, dim], gate_bias: fp32 [E] or NULL; stacked
+ * weights as in fp8blk_moe_grouped_gemm (E routed experts, then n_shared shared
+ * ones); y: bf16 [T, dim]. topk_idx int32 / topk_w fp32 [T, topk] are written
+ * where not NULL. T <= 32 (more tokens: fp8blk_moe_grouped_gemm), dim and
+ * inter multiples of 128, dim <= 8192, inter <= 16384, n_shared <= 8, dim / 8 <=
+ * 8 * SMs, and the rules of fp8blk_moe_gate for E, topk and the groups; else
+ * FP8BLK_ERR_SHAPE. bf16 and e4m3 inputs 16-byte aligned. An expert without a
+ * token reads none of its weights. One cooperative launch of one CTA per SM;
+ * the result does not vary from run to run.
+ * Workspace: fp8blk_moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared),
+ * 256-byte aligned; its first 256 bytes hold counters: ZERO-FILLED before the
+ * first use, and every call leaves them at zero. One workspace serves layers of
+ * any shape, one stream at a time.
+ */
+FP8BLK_API size_t fp8blk_moe_layer_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t dim, int64_t inter,
+                                                   int64_t n_shared);
+FP8BLK_API int fp8blk_moe_layer(const void *x_bf16, const void *gate_w_bf16, const float *gate_bias,
+                                const void *w1_e4m3, const float *w1_s, const void *w3_e4m3, const float *w3_s,
+                                const void *w2_e4m3, const float *w2_s, void *y_bf16, int64_t T, int64_t topk,
+                                int64_t E, int64_t dim, int64_t inter, int64_t n_shared, int64_t n_groups,
+                                int64_t topk_groups, int score_func, float route_scale, int normalize, int scale_fmt,
+                                int32_t *topk_idx, float *topk_w, void *workspace, size_t workspace_bytes,
+                                fp8blk_stream_t stream);
+
+/*
  * fp8_gemm with no workspace argument and no device allocation: the same
  * computation, result and argument rules as fp8blk_gemm, but its scratch
  * (tile counters and stream-K partial sums) lives in a buffer of
@@ -459,7 +498,8 @@ FP8BLK_API int fp8blk_gemm_noalloc(const void *a_e4m3, const float *a_s, const v
  * 0x01-0x08: a GEMM role gave up waiting (producer, MMA, epilogue, drain);
  * 0x20: an expert id outside [0, E) (MoE); 0x40: an MLA kernel gave up
  * waiting; 0x80: a UE8M0-format scale that is not a positive normal power of
- * two; 0x100: a cache slot, page id or position out of range. After a wait gave up, that kernel returned early: its outputs are
+ * two; 0x100: a cache slot, page id or position out of range;
+ * 0x200: the few-token MoE layer gave up waiting. After a wait gave up, that kernel returned early: its outputs are
  * undefined and the workspace's first 64 KB must be zero-filled again before
  * reuse. The function returns FP8BLK_ERR_TIMEOUT when any bit is set.
  */
