@@ -117,7 +117,7 @@ __device__ __forceinline__ int own_len(const AttnParams& p, int b) {
   return min(max(__ldg(p.lens + b), 0), p.max_own);
 }
 
-__device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
+__device__ __noinline__ Item get_item(const AttnParams& p, int i) {
   Item it;
   if (p.merged) {
     it.row0 = i * kTileRows;
@@ -163,37 +163,45 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
 }
 
 // Arrives on an mbarrier of any CTA of the cluster (shared::cluster address).
+// What it orders for the MMA thread are tensor-memory accesses, by the
+// tcgen05 fences around it, and shared-memory writes that the tensor cores read
+// through the async proxy, by the proxy fence before it; the waiting thread
+// itself reads none of that memory, and a release of cluster scope would stall
+// the warp for more than 1000 cycles here.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// Waits with acquire at cluster scope for what the peer CTA's threads wrote
-// before arriving; otherwise as mbar_wait.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
-                                                  unsigned code) {
-  const uint32_t a = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 63u) {
-      if (*abort) return false;
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) {
-        *abort = 1;
-        atomicOr(err, code);
-        return false;
+// The bounded wait of every role, out of line: the roles' loops have to stay
+// in the instruction cache together (with inlined waits and unrolled tile loops
+// the kernel was 131 KB, and every role ran five times slower on fetches).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint64_t t0 = global_timer_ns();
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) {
+      ok = true;
+      break;
+    }
+    if ((i & 63u) == 0) {
+      if (abort && *abort) break;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (abort) *abort = 1;
+        atomicOr(err, kDevErrTimeoutMla);
+        break;
       }
     }
   }
+  return ok;
+}
+
+// The same for a whole warp: true in all lanes or in none.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint32_t a = smem_u32(bar);
+  bool ok = mbar_try_wait(a, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) ok = __all_sync(0xFFFFFFFFu, ok || wait_slow(a, parity, abort, err));
+  return ok;
 }
 
 // 2-D tiled load into this CTA's shared memory; the bytes complete on the
@@ -261,7 +269,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // The cache row of key `key` of a page list, or the out-of-range row where the
 // page id is not one of the cache's pages.
-__device__ __forceinline__ int key_row(const AttnParams& p, const int* pages, int key) {
+__device__ __noinline__ int key_row(const AttnParams& p, const int* pages, int key) {
   const int pg = __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
   if (pg < 0 || pg >= p.num_pages) {
     atomicOr(p.err, kDevErrBadSlot);
@@ -340,7 +348,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_desc(&map_v);
     tma_prefetch_desc(&map_row);
   }
-  griddep_launch_dependents();
   griddep_wait();
 
   // The plan: every CTA sums the items' tiles (thread-contiguous ranges, then
@@ -349,10 +356,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     int* sums = reinterpret_cast<int*>(smem);  // the query slabs are not loaded yet
     const int lo = split(p.items, tid, kAttnThreads), hi = split(p.items, tid + 1, kAttnThreads);
     int own = 0;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) own += get_item(p, i).tiles;
     sums[tid] = own;
     __syncthreads();
     int before = 0, units = 0;
+#pragma unroll 1
     for (int i = 0; i < kAttnThreads; ++i) {
       const int v = sums[i];
       before += i < tid ? v : 0;
@@ -362,6 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int64_t u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
     const int64_t u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
     int at = before;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       const int n = get_item(p, i).tiles;
       if (u0 < u1 && u0 >= at && u0 < at + n) {
@@ -393,17 +403,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     uint32_t n = 0, seg = 0;
     int left = nunits, i = item0, t0 = tile0;
     bool ok = true;
+#pragma unroll 1
     while (ok && left > 0 && i < p.items) {
       const Item it = get_item(p, i);
       const int t1 = min(it.tiles, t0 + left);
       left -= t1 - t0;
       if (is_k && t1 > t0) {
-        if (seg > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (seg - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        if (seg > 0) ok = wait_warp(q_empty, (seg - 1) & 1, abort_flag, p.err);
         if (!ok) break;
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kQSlabs * kSlab);
           const uint32_t bar = map_to_cta(smem_u32(q_full), 0);
           const int y = it.row0 + static_cast<int>(rank) * 64;
+#pragma unroll 1
           for (int s = 0; s < kQSlabs; ++s)
             tma_load_2d_pair(smem_u32(smem + kOffQ + s * kSlab), s < kC / 64 ? &map_q : &map_qpe, bar,
                              s < kC / 64 ? s * 64 : 0, y);
@@ -411,6 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         ++seg;
       }
+#pragma unroll 1
       for (int t = t0; ok && t < t1; ++t, ++n) {
         const bool pre = t < it.pt;
         const int key0 = (pre ? t : t - it.pt) * kTileKeys;
@@ -421,12 +434,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           const int nbox = 64 / p.kbox;
           const int key = key0 + static_cast<int>(rank) * 64 + lane * p.kbox;
           const int y = lane < nbox && key < limit ? key_row(p, pages, key) : p.total_rows;
+#pragma unroll 1
           for (int g = 0; g < kKGroups; ++g) {
-            if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&k_empty[g], (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            if (n > 0) ok = wait_warp(&k_empty[g], (n - 1) & 1, abort_flag, p.err);
             if (!ok) break;
             if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
             const uint32_t bar = map_to_cta(smem_u32(&k_full[g]), 0);
             if (lane < nbox)
+#pragma unroll 1
               for (int s = 3 * g; s < 3 * g + 3; ++s)
                 tma_load_2d_pair(smem_u32(smem + kOffK + s * kSlab + lane * p.kbox * 128), &map_k, bar, s * 64, y);
             __syncwarp();
@@ -434,18 +449,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         } else {
           // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
           // the half 128 rank .. + 128, as slabs 2 j and 2 j + 1 of each chunk.
+          // Lane l < 8 looks up the l-th 16 keys; boxes of a chunk without the
+          // end take their row from there, the chunk with the end goes row by
+          // row, chunks past it are zeros.
+          const int key = key0 + lane * 16;
+          const int y16 = lane < 8 && key < limit ? key_row(p, pages, key) : p.total_rows;
+#pragma unroll 1
           for (int c = 0; c < kVChunks; ++c) {
             const int kc = key0 + c * 32;
             const bool whole = kc + 32 <= limit || kc >= limit;
-            const int nbox = whole ? 32 / p.vbox : 32;
-            const int key = kc + lane * (whole ? p.vbox : 1);
-            const int y = lane < nbox && key < limit ? key_row(p, pages, key) : p.total_rows;
-            if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&v_empty[c], (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            const int step = whole ? p.vbox : 1;
+            int y = __shfl_sync(0xFFFFFFFFu, y16, (2 * c + lane * (step >> 4)) & 7);
+            if (!whole) y = kc + lane < limit ? key_row(p, pages, kc + lane) : p.total_rows;
+            if (n > 0) ok = wait_warp(&v_empty[c], (n - 1) & 1, abort_flag, p.err);
             if (!ok) break;
             if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
             const uint32_t bar = map_to_cta(smem_u32(&v_full[c]), 0);
-            if (lane < nbox) {
-              const uint32_t dst = smem_u32(smem + kOffV + c * kVChunk) + lane * (whole ? p.vbox : 1) * 128;
+            if (lane * step < 32) {
+              const uint32_t dst = smem_u32(smem + kOffV + c * kVChunk) + lane * step * 128;
+#pragma unroll 1
               for (int s = 0; s < 4; ++s)
                 tma_load_2d_pair(dst + s * kVSlab, whole ? &map_v : &map_row, bar,
                                  (s >> 1) * 256 + static_cast<int>(rank) * 128 + (s & 1) * 64, y);
@@ -461,12 +483,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       // Copies of both CTAs complete on this CTA's barriers: wait for the last
       // phase each was armed for.
       if (is_k) {
-        if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+        if (seg > 0) wait_slow(smem_u32(q_full), (seg - 1) & 1, nullptr, p.err);
+#pragma unroll 1
         for (int g = 0; g < kKGroups; ++g)
-          if (n > 0) mbar_wait(&k_full[g], (n - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+          if (n > 0) wait_slow(smem_u32(&k_full[g]), (n - 1) & 1, nullptr, p.err);
       } else {
+#pragma unroll 1
         for (int c = 0; c < kVChunks; ++c)
-          if (n > 0) mbar_wait(&v_full[c], (n - 1) & 1, nullptr, p.err, kDevErrTimeoutMla);
+          if (n > 0) wait_slow(smem_u32(&v_full[c]), (n - 1) & 1, nullptr, p.err);
       }
     }
   } else if (warp == 6) {
@@ -484,10 +508,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       // while the scores of tile k + 1 are formed).
       auto output = [&](uint32_t k, bool first, uint32_t sg) {
         if (first && sg > 0)
-          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(o_empty, (sg - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_full, k & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          ok = ok && wait_warp(o_empty, (sg - 1) & 1, abort_flag, p.err);
+        ok = ok && wait_warp(p_full, k & 1, abort_flag, p.err);
+#pragma unroll 1
         for (int c = 0; ok && c < kVChunks; ++c) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&v_full[c], k & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          ok = wait_warp(&v_full[c], k & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one_sync()) {
@@ -506,18 +531,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
         }
       };
+#pragma unroll 1
       while (ok && left > 0 && i < p.items) {
         const Item it = get_item(p, i);
         const int t1 = min(it.tiles, t0 + left);
         left -= t1 - t0;
+#pragma unroll 1
         for (int t = t0; ok && t < t1; ++t) {
           const uint32_t buf = n & 1;
-          if (t == t0) ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(q_full, seg & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          if (t == t0) ok = wait_warp(q_full, seg & 1, abort_flag, p.err);
           if (n > 1)
-            ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err,
-                                                                 kDevErrTimeoutMla));
+            ok = ok && wait_warp(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
+#pragma unroll 1
           for (int g = 0; ok && g < kKGroups; ++g) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&k_full[g], n & 1, abort_flag, p.err, kDevErrTimeoutMla));
+            ok = wait_warp(&k_full[g], n & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one_sync()) {
@@ -549,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
         if (elect_one_sync()) mma_commit_pair(drain);
         __syncwarp();
-        mbar_wait(drain, 0, nullptr, p.err, kDevErrTimeoutMla);
+        wait_slow(smem_u32(drain), 0, nullptr, p.err);
       }
     }
   } else {
@@ -569,10 +596,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       r[kh * 64 + row] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(red_bar);
-      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(red_bar, nred & 1, abort_flag, p.err, kDevErrTimeoutMla));
+      ok = ok && wait_warp(red_bar, nred & 1, abort_flag, p.err);
       ++nred;
       return r[(kh ^ 1) * 64 + row];
     };
+#pragma unroll 1
     while (ok && left > 0 && i < p.items) {
       const Item it = get_item(p, i);
       const int t1 = min(it.tiles, t0 + left);
@@ -580,12 +608,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const int rt = static_cast<int>(rank) * 64 + row;  // row of the tile
       const bool have = rt < it.nrows;
       float m = -INFINITY, l = 0.f, lx = 0.f;  // running maximum, sums of rounded and of fp32 weights
+#pragma unroll 1
       for (int t = t0; ok && t < t1; ++t, ++n) {
         const bool pre = t < it.pt;
         const int key0 = (pre ? t : t - it.pt) * kTileKeys;
         const int valid = have ? (pre ? p.P : it.len) - key0 - kh * 64 : 0;  // keys of this half that count
         const uint32_t buf = n & 1;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[buf], (n >> 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        ok = wait_warp(&s_full[buf], (n >> 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after_sync();
         uint32_t s[64];
@@ -632,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // The previous tile's output product has read P and written the output.
         if (n > 0) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(pv_done, (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+          ok = wait_warp(pv_done, (n - 1) & 1, abort_flag, p.err);
           if (!ok) break;
         }
 #pragma unroll
@@ -659,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (ok && t1 > t0) {
         const float lt = l + exchange(l);
         const float lxt = lx + exchange(lx);
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(pv_done, (n - 1) & 1, abort_flag, p.err, kDevErrTimeoutMla));
+        ok = ok && wait_warp(pv_done, (n - 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after_sync();
         const bool cut = t0 > 0 || t1 < it.tiles || (!p.merged && p.prefix_tiles > 0);
@@ -709,6 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     }
   }
 
+  griddep_launch_dependents();  // not earlier: the join's waiting CTAs would share the SMs
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();
