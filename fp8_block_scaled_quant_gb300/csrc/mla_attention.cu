@@ -267,10 +267,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The cache row of key `key` of a page list, or the out-of-range row where the
-// page id is not one of the cache's pages.
-__device__ __noinline__ int key_row(const AttnParams& p, const int* pages, int key) {
-  const int pg = __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
+// The cache row of key `key`, whose page is `pg`, or the out-of-range row
+// where that is not one of the cache's pages.
+__device__ __forceinline__ int entry_row(const AttnParams& p, int pg, int key) {
   if (pg < 0 || pg >= p.num_pages) {
     atomicOr(p.err, kDevErrBadSlot);
     return p.total_rows;
@@ -403,6 +402,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     uint32_t n = 0, seg = 0;
     int left = nunits, i = item0, t0 = tile0;
     bool ok = true;
+    const uint32_t bars = map_to_cta(smem_u32(is_k ? k_full : v_full), 0);
+    const uint32_t dst0 = smem_u32(smem + (is_k ? kOffK : kOffV));
+    const int rows = is_k ? p.kbox : 16;   // keys per looked-up page entry
+    const int mine = is_k ? static_cast<int>(rank) * 64 : 0;
+    const bool looks = lane * rows < (is_k ? 64 : kTileKeys);
 #pragma unroll 1
     while (ok && left > 0 && i < p.items) {
       const Item it = get_item(p, i);
@@ -411,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (is_k && t1 > t0) {
         if (seg > 0) ok = wait_warp(q_empty, (seg - 1) & 1, abort_flag, p.err);
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one_sync()) {
           if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kQSlabs * kSlab);
           const uint32_t bar = map_to_cta(smem_u32(q_full), 0);
           const int y = it.row0 + static_cast<int>(rank) * 64;
@@ -423,56 +427,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         ++seg;
       }
+      // Lane l's page entry of tile t: that of its l-th `rows` keys. It is
+      // loaded a tile ahead and becomes a cache row when the tile comes.
+      auto first_key = [&](int t) { return (t < it.pt ? t : t - it.pt) * kTileKeys; };
+      auto page_entry = [&](int t) {
+        const bool pre = t < it.pt;
+        const int key = first_key(t) + mine + lane * rows;
+        const int limit = pre ? p.P : it.len;
+        if (t >= t1 || !looks || key >= limit) return -1;
+        const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
+        return __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
+      };
+      int entry = page_entry(t0);
 #pragma unroll 1
       for (int t = t0; ok && t < t1; ++t, ++n) {
         const bool pre = t < it.pt;
-        const int key0 = (pre ? t : t - it.pt) * kTileKeys;
+        const int key0 = first_key(t);
         const int limit = pre ? p.P : it.len;
-        const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
+        const int key = key0 + mine + lane * rows;
+        const int y16 = looks && key < limit ? entry_row(p, entry, key) : p.total_rows;
+        entry = page_entry(t + 1);
         if (is_k) {
-          // This CTA's 64 keys; lane l loads box l of every slab.
+          // This CTA's 64 keys, in boxes of kbox keys x 64 columns.
           const int nbox = 64 / p.kbox;
-          const int key = key0 + static_cast<int>(rank) * 64 + lane * p.kbox;
-          const int y = lane < nbox && key < limit ? key_row(p, pages, key) : p.total_rows;
 #pragma unroll 1
           for (int g = 0; g < kKGroups; ++g) {
             if (n > 0) ok = wait_warp(&k_empty[g], (n - 1) & 1, abort_flag, p.err);
             if (!ok) break;
-            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
-            const uint32_t bar = map_to_cta(smem_u32(&k_full[g]), 0);
-            if (lane < nbox)
+            if (rank == 0 && elect_one_sync()) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
 #pragma unroll 1
-              for (int s = 3 * g; s < 3 * g + 3; ++s)
-                tma_load_2d_pair(smem_u32(smem + kOffK + s * kSlab + lane * p.kbox * 128), &map_k, bar, s * 64, y);
-            __syncwarp();
+            for (int q = 0; q < nbox; ++q) {
+              const int y = __shfl_sync(0xFFFFFFFFu, y16, q);
+              const uint32_t dst = dst0 + g * kGroupBytes + q * p.kbox * 128;
+              if (elect_one_sync()) {
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                  tma_load_2d_pair(dst + s * kSlab, &map_k, bars + g * 8, (3 * g + s) * 64, y);
+              }
+              __syncwarp();
+            }
           }
         } else {
           // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
           // the half 128 rank .. + 128, as slabs 2 j and 2 j + 1 of each chunk.
-          // Lane l < 8 looks up the l-th 16 keys; boxes of a chunk without the
-          // end take their row from there, the chunk with the end goes row by
-          // row, chunks past it are zeros.
-          const int key = key0 + lane * 16;
-          const int y16 = lane < 8 && key < limit ? key_row(p, pages, key) : p.total_rows;
+          // The chunk that holds the end goes row by row, those past it are zeros.
+          const int x0 = static_cast<int>(rank) * 128;
 #pragma unroll 1
           for (int c = 0; c < kVChunks; ++c) {
             const int kc = key0 + c * 32;
-            const bool whole = kc + 32 <= limit || kc >= limit;
-            const int step = whole ? p.vbox : 1;
-            int y = __shfl_sync(0xFFFFFFFFu, y16, (2 * c + lane * (step >> 4)) & 7);
-            if (!whole) y = kc + lane < limit ? key_row(p, pages, kc + lane) : p.total_rows;
+            const uint32_t dst = dst0 + c * kVChunk;
             if (n > 0) ok = wait_warp(&v_empty[c], (n - 1) & 1, abort_flag, p.err);
             if (!ok) break;
-            if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
-            const uint32_t bar = map_to_cta(smem_u32(&v_full[c]), 0);
-            if (lane * step < 32) {
-              const uint32_t dst = smem_u32(smem + kOffV + c * kVChunk) + lane * step * 128;
+            if (rank == 0 && elect_one_sync()) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
+            if (kc + 32 <= limit || kc >= limit) {
+#pragma unroll 1
+              for (int q = 0; q < 32; q += p.vbox) {
+                const int y = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (q >> 4));
+                if (elect_one_sync()) {
+#pragma unroll
+                  for (int s = 0; s < 4; ++s)
+                    tma_load_2d_pair(dst + s * kVSlab + q * 128, &map_v, bars + c * 8,
+                                     (s >> 1) * 256 + x0 + (s & 1) * 64, y);
+                }
+                __syncwarp();
+              }
+            } else {
+              const int y0 = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (lane >> 4));
+              const int y = kc + lane < limit && y0 < p.total_rows ? y0 + (lane & 15) : p.total_rows;
 #pragma unroll 1
               for (int s = 0; s < 4; ++s)
-                tma_load_2d_pair(dst + s * kVSlab, whole ? &map_v : &map_row, bar,
-                                 (s >> 1) * 256 + static_cast<int>(rank) * 128 + (s & 1) * 64, y);
+                tma_load_2d_pair(dst + s * kVSlab + lane * 128, &map_row, bars + c * 8,
+                                 (s >> 1) * 256 + x0 + (s & 1) * 64, y);
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
       }
@@ -497,8 +524,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     // ---- MMA (CTA 0 issues for the pair) -------------------------------------
     if (rank == 0) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 256, true);
-      const uint32_t qa = smem_u32(smem + kOffQ), pa = smem_u32(smem + kOffP);
-      const uint32_t ka = smem_u32(smem + kOffK), va = smem_u32(smem + kOffV);
+      const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + kOffQ)), kd = sdesc_kmajor_sw128(smem_u32(smem + kOffK));
+      const uint64_t pd = sdesc_kmajor_sw128(smem_u32(smem + kOffP));
+      const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + kOffV), kVSlab);
       uint32_t n = 0, seg = 0;
       int left = nunits, i = item0, t0 = tile0;
       bool ok = true;
@@ -516,15 +544,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one_sync()) {
+            const uint64_t ad = pd + static_cast<uint32_t>(c >> 1) * (kSlab >> 4) + 4 * (c & 1);
+            const uint64_t bd = vd + static_cast<uint32_t>(c) * (kVChunk >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int ks = 2 * c + h;  // 16 keys
-              const uint64_t ad = sdesc_kmajor_sw128(pa + (ks >> 2) * kSlab) + 2 * (ks & 3);
+            for (int h = 0; h < 2; ++h)  // 16 keys
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                mma_bf16_pair(tmem + j * 128, ad, sdesc_mn_sw128(va + c * kVChunk + j * 2 * kVSlab + h * 2048, kVSlab),
-                              kIdO, first && ks == 0 ? 0u : 1u);
-            }
+                mma_bf16_pair(tmem + j * 128, ad + 2 * h, bd + j * (2 * kVSlab >> 4) + h * (2048 >> 4), kIdO,
+                              first && c == 0 && h == 0 ? 0u : 1u);
             mma_commit_pair(&v_empty[c]);
             if (c == kVChunks - 1) mma_commit_pair(pv_done);
           }
@@ -538,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         left -= t1 - t0;
 #pragma unroll 1
         for (int t = t0; ok && t < t1; ++t) {
-          const uint32_t buf = n & 1;
+          const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
           if (t == t0) ok = wait_warp(q_full, seg & 1, abort_flag, p.err);
           if (n > 1)
             ok = ok && wait_warp(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
@@ -548,13 +575,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             if (!ok) break;
             tc_fence_after_sync();
             if (elect_one_sync()) {
+              const uint64_t ad = qd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
+              const uint64_t bd = kd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
 #pragma unroll
-              for (int s = 3 * g; s < 3 * g + 3; ++s) {
-                const uint64_t ad = sdesc_kmajor_sw128(qa + s * kSlab), bd = sdesc_kmajor_sw128(ka + s * kSlab);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_bf16_pair(tmem + kTmemS + buf * 64, ad + 2 * k, bd + 2 * k, kIdS, s > 0 || k > 0 ? 1u : 0u);
-              }
+              for (int k = 0; k < 12; ++k)
+                mma_bf16_pair(d, ad + (k >> 2) * (kSlab >> 4) + 2 * (k & 3), bd + (k >> 2) * (kSlab >> 4) + 2 * (k & 3),
+                              kIdS, g > 0 || k > 0 ? 1u : 0u);
               mma_commit_pair(&k_empty[g]);
               if (g == kKGroups - 1) {
                 mma_commit_pair(&s_full[buf]);
