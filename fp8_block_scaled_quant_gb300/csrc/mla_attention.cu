@@ -104,6 +104,8 @@ struct AttnParams {
   int prefix_tiles, prefix_items, items, own_rows;
   int merged;              // H % 128 == 0: prefix and own keys in one item
   int kbox, vbox;          // rows of a TMA box of keys / values
+  int lone_prefix;         // few row tiles: the prefix's keys come from HBM too
+  int direct;              // no item can be cut or share a row: no join
   float scale_log2;
 };
 
@@ -140,6 +142,13 @@ __device__ __noinline__ Item get_item(const AttnParams& p, int i) {
   it.len = it.b >= 0 ? own_len(p, it.b) : 0;
   it.tiles = it.pt + (it.len + kTileKeys - 1) / kTileKeys;
   return it;
+}
+
+__device__ __forceinline__ int item_tiles(const AttnParams& p, int i) {
+  if (!p.merged && i < p.prefix_items) return p.prefix_tiles;
+  const int per = (p.H + kTileRows - 1) / kTileRows;
+  const int len = own_len(p, (i - p.prefix_items) / per);
+  return (p.merged ? p.prefix_tiles : 0) + (len + kTileKeys - 1) / kTileKeys;
 }
 
 // First row of the parts of item i written by pair q: item-major, 128 rows
@@ -285,7 +294,8 @@ __device__ __forceinline__ int split(int items, int tid, int n) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     mla_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qpe,
                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                         const __grid_constant__ CUtensorMap map_row, const AttnParams p) {
+                         const __grid_constant__ CUtensorMap map_four, const __grid_constant__ CUtensorMap map_row,
+                         const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   float* red = reinterpret_cast<float*>(smem + kOffRed);
@@ -345,34 +355,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_desc(&map_qpe);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
-    tma_prefetch_desc(&map_row);
   }
   griddep_wait();
 
   // The plan: every CTA sums the items' tiles (thread-contiguous ranges, then
   // a scan over the threads) and finds the item its range starts in.
   {
-    int* sums = reinterpret_cast<int*>(smem);  // the query slabs are not loaded yet
+    int* sums = reinterpret_cast<int*>(red);
     const int lo = split(p.items, tid, kAttnThreads), hi = split(p.items, tid + 1, kAttnThreads);
     int own = 0;
 #pragma unroll 1
-    for (int i = lo; i < hi; ++i) own += get_item(p, i).tiles;
-    sums[tid] = own;
+    for (int i = lo; i < hi; ++i) own += item_tiles(p, i);
+    int upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    int before = 0, units = 0;
-#pragma unroll 1
-    for (int i = 0; i < kAttnThreads; ++i) {
-      const int v = sums[i];
-      before += i < tid ? v : 0;
+    int at = upto - own, units = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+      const int v = sums[w];
+      at += w < warp ? v : 0;
       units += v;
     }
     const int pairs = max(1, min(npairs_max, units));
     const int64_t u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
     const int64_t u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
-    int at = before;
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
-      const int n = get_item(p, i).tiles;
+      const int n = hi - lo == 1 ? own : item_tiles(p, i);
       if (u0 < u1 && u0 >= at && u0 < at + n) {
         start[0] = i;
         start[1] = static_cast<int>(u0 - at);
@@ -387,7 +401,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       p.plan[2 + p.items] = units;
     }
   }
-  fence_proxy_async_smem();  // the scan's use of the query slabs, before TMA writes them
   tc_fence_before_sync();
   __syncthreads();
   cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
@@ -412,6 +425,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const Item it = get_item(p, i);
       const int t1 = min(it.tiles, t0 + left);
       left -= t1 - t0;
+      // Lane l's page entry of tile t: that of its l-th `rows` keys. Entries are
+      // loaded two tiles ahead and become cache rows when they are needed.
+      auto first_key = [&](int t) { return (t < it.pt ? t : t - it.pt) * kTileKeys; };
+      auto page_entry = [&](int t) {
+        const bool pre = t < it.pt;
+        const int key = first_key(t) + mine + lane * rows;
+        const int limit = pre ? p.P : it.len;
+        if (t >= t1 || !looks || key >= limit) return -1;
+        const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
+        return __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
+      };
+      auto row_of = [&](int t, int entry) {
+        const int key = first_key(t) + mine + lane * rows;
+        return looks && t < t1 && key < (t < it.pt ? p.P : it.len) ? entry_row(p, entry, key) : p.total_rows;
+      };
+      int entry1 = page_entry(t0), entry2 = page_entry(t0 + 1);
       if (is_k && t1 > t0) {
         if (seg > 0) ok = wait_warp(q_empty, (seg - 1) & 1, abort_flag, p.err);
         if (!ok) break;
@@ -427,26 +456,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         ++seg;
       }
-      // Lane l's page entry of tile t: that of its l-th `rows` keys. It is
-      // loaded a tile ahead and becomes a cache row when the tile comes.
-      auto first_key = [&](int t) { return (t < it.pt ? t : t - it.pt) * kTileKeys; };
-      auto page_entry = [&](int t) {
-        const bool pre = t < it.pt;
-        const int key = first_key(t) + mine + lane * rows;
-        const int limit = pre ? p.P : it.len;
-        if (t >= t1 || !looks || key >= limit) return -1;
-        const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
-        return __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
-      };
-      int entry = page_entry(t0);
+      int y_next = row_of(t0, entry1);
+      entry1 = entry2;
 #pragma unroll 1
       for (int t = t0; ok && t < t1; ++t, ++n) {
         const bool pre = t < it.pt;
         const int key0 = first_key(t);
         const int limit = pre ? p.P : it.len;
-        const int key = key0 + mine + lane * rows;
-        const int y16 = looks && key < limit ? entry_row(p, entry, key) : p.total_rows;
-        entry = page_entry(t + 1);
+        const int y16 = y_next;
+        y_next = row_of(t + 1, entry1);
+        entry1 = page_entry(t + 2);
+        if (is_k && (t + 1 >= it.pt || p.lone_prefix)) {
+          // Keys that no other pair reads come from HBM: ask for the next
+          // tile's while this one is loaded.
+#pragma unroll 1
+          for (int q = 0; q < 64 / p.kbox; ++q) {
+            const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
+            if (y < p.total_rows && elect_one_sync()) {
+#pragma unroll 1
+              for (int x = 0; x < kRow; x += 64) tma_prefetch_l2_2d(&map_k, x, y);
+            }
+            __syncwarp();
+          }
+        }
         if (is_k) {
           // This CTA's 64 keys, in boxes of kbox keys x 64 columns.
           const int nbox = 64 / p.kbox;
@@ -492,13 +524,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 __syncwarp();
               }
             } else {
-              const int y0 = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (lane >> 4));
-              const int y = kc + lane < limit && y0 < p.total_rows ? y0 + (lane & 15) : p.total_rows;
+              // Four rows at a time, the four with the end one by one.
 #pragma unroll 1
-              for (int s = 0; s < 4; ++s)
-                tma_load_2d_pair(dst + s * kVSlab + lane * 128, &map_row, bars + c * 8,
-                                 (s >> 1) * 256 + x0 + (s & 1) * 64, y);
-              __syncwarp();
+              for (int r = 0; r < 32;) {
+                const int y0 = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (r >> 4));
+                const int left = limit - kc - r;
+                const bool four = left <= 0 || left >= 4 ? (r & 3) == 0 : false;
+                const int y = left > 0 && y0 < p.total_rows ? y0 + (r & 15) : p.total_rows;
+                if (elect_one_sync()) {
+#pragma unroll
+                  for (int s = 0; s < 4; ++s)
+                    tma_load_2d_pair(dst + s * kVSlab + r * 128, four ? &map_four : &map_row, bars + c * 8,
+                                     (s >> 1) * 256 + x0 + (s & 1) * 64, y);
+                }
+                __syncwarp();
+                r += four ? 4 : 1;
+              }
             }
           }
         }
@@ -607,6 +648,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     // ---- softmax and stores ---------------------------------------------------
+    if (p.direct && rank == 0) {
+      // Nothing joins the rows later: those without any key become zeros here.
+#pragma unroll 1
+      for (int e = pair; e < p.items; e += npairs_max) {
+        if (item_tiles(p, e)) continue;
+        const Item z = get_item(p, e);
+#pragma unroll 1
+        for (int k = tid; k < z.nrows * (kC / 8); k += 128)
+          reinterpret_cast<uint4*>(p.out + z.row0 * static_cast<int64_t>(kC))[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse)
+          for (int k = tid; k < z.nrows; k += 128) p.lse[z.row0 + k] = -INFINITY;
+      }
+    }
     const int row = (warp & 1) * 32 + lane;   // of this CTA's 64
     const int kh = warp >> 1;                 // key half of the scores, column half of the output
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -719,41 +773,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         tc_fence_after_sync();
         const bool cut = t0 > 0 || t1 < it.tiles || (!p.merged && p.prefix_tiles > 0);
         const int64_t r = it.row0 + rt;
+        // Rows leave through this warp's quarter of the P buffer (its readers are
+        // done), 128 bytes of 32 rows at a time, so that stores cover whole
+        // lines: 16-byte chunk j of row r sits at chunk j ^ (r % 8).
+        uint8_t* stage = smem + kOffP + warp * 4096;
+        const int r0 = static_cast<int>(rank) * 64 + (warp & 1) * 32;  // tile row of lane 0
+        auto store_rows = [&](const uint32_t (&v)[32], uint8_t* dst, int64_t pitch) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int rr = q * 4 + (lane >> 3);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane ^ rr) & 7) << 4));
+            if (r0 + rr < it.nrows) *reinterpret_cast<uint4*>(dst + rr * pitch + (lane & 7) * 16) = x;
+          }
+          __syncwarp();
+        };
         if (!cut) {
           const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;  // NaN stays NaN
+          uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + (it.row0 + r0) * static_cast<int64_t>(kC) + kh * 128);
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_lane + c, o);
-            uint4* dst = reinterpret_cast<uint4*>(p.out + r * kC + (c >> 7) * 256 + kh * 128 + (c & 127));
-            if (have) {
+          for (int c = 0; c < 256; c += 64) {
+            uint32_t o[64], v[32];
+            tmem_ld_32x32b_x64(t_lane + c, o);
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                uint32_t v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * g + 2 * e]) * inv,
-                                                                  __uint_as_float(o[8 * g + 2 * e + 1]) * inv);
-                  v[e] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-                dst[g] = make_uint4(v[0], v[1], v[2], v[3]);
-              }
+            for (int e = 0; e < 32; ++e) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
+                                                              __uint_as_float(o[2 * e + 1]) * inv);
+              v[e] = *reinterpret_cast<const uint32_t*>(&b2);
             }
+            store_rows(v, dst + ((c >> 7) * 256 + (c & 127)) * 2, kC * 2);
           }
           if (have && kh == 0 && p.lse) p.lse[r] = m * 0.69314718055994531f + logf(lxt);
         } else {
-          const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, i, pair) + rt;
+          const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, i, pair);
+          uint8_t* dst = reinterpret_cast<uint8_t*>(p.part_o + (pr + r0) * kC + kh * 128);
 #pragma unroll 1
           for (int c = 0; c < 256; c += 32) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_lane + c, o);
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + pr * kC + (c >> 7) * 256 + kh * 128 + (c & 127));
-            if (have) {
-#pragma unroll
-              for (int g = 0; g < 8; ++g) dst[g] = make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
-            }
+            store_rows(o, dst + ((c >> 7) * 256 + (c & 127)) * 4, kC * 4);
           }
-          if (have && kh == 0) p.part_ml[pr] = make_float4(m, lt, lxt, 0.f);
+          if (have && kh == 0) p.part_ml[pr + rt] = make_float4(m, lt, lxt, 0.f);
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -775,124 +839,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the parts of each query row, in item and key order: with weights
-// 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k. One CTA per row: four
-// warps take the parts round robin (a lane has 16 of the 512 columns), then
-// add up in shared memory in warp order. Rows whose one item was not cut were
-// stored by the attention kernel; rows without any key become zeros.
+// 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k. CTA (row, column part): the
+// weights first (a thread per part), then four warps add the parts round robin,
+// their loads independent of each other, and the four sums meet in shared
+// memory in warp order. With few rows the 512 columns are spread over four
+// CTAs (128 rows of 76 parts: 20 us in one). Rows whose one item was not cut
+// were stored by the attention kernel; rows without any key become zeros.
+template <int V>  // vectors of four columns per lane
 __global__ void __launch_bounds__(128) mla_join_kernel(const AttnParams p) {
-  __shared__ float4 acc_s[3][128];
-  __shared__ float ml_s[4][3];
+  __shared__ float4 acc_s[3][V][32];
+  __shared__ float w_s[2 * kMaxPairs];
+  __shared__ float red_s[3][4];
   griddep_launch_dependents();
   griddep_wait();
   const int64_t r = blockIdx.x;
   const int b = static_cast<int>(r / p.H), h = static_cast<int>(r % p.H);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int units = p.plan[0], pairs = p.plan[1];
-  // Up to two items hold the row's keys: (item, row of the item).
-  int item[2], local[2], n_items = 0;
-  if (p.merged) {
-    item[0] = static_cast<int>(r / kTileRows);
-    local[0] = static_cast<int>(r % kTileRows);
-    n_items = 1;
-  } else {
-    if (p.prefix_tiles > 0) {
-      item[0] = static_cast<int>(r / kTileRows);
-      local[0] = static_cast<int>(r % kTileRows);
-      n_items = 1;
-    }
-    item[n_items] = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
-    local[n_items] = h % kTileRows;
-    ++n_items;
+  // Up to two items hold the row's keys. Item, row of the item and pairs of the
+  // first (the prefix's, or both together) and of the second (its own keys).
+  int first_item = -1, own_item = -1;
+  if (p.merged || p.prefix_tiles > 0) first_item = static_cast<int>(r / kTileRows);
+  if (!p.merged) own_item = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
+  auto pairs_of = [&](int item, int* q0) {
+    if (item < 0) return 0;
+    const int64_t a = p.plan[2 + item], e = p.plan[3 + item];
+    if (e <= a) return 0;
+    // Pair q has the units [units q / pairs, units (q + 1) / pairs): that of unit
+    // u is the largest q with units q / pairs <= u.
+    *q0 = static_cast<int>(((a + 1) * pairs - 1) / units);
+    return static_cast<int>((e * pairs - 1) / units) - *q0 + 1;
+  };
+  int qa = 0, qb = 0;
+  const int na = pairs_of(first_item, &qa), nb = pairs_of(own_item, &qb);
+  const int parts = na + nb;
+  if (parts == 1 && (p.merged || p.prefix_tiles == 0)) return;
+  auto part_of = [&](int k) {
+    return k < na ? part_row(p.merged, p.prefix_items, p.own_rows, first_item, qa + k) + r % kTileRows
+                  : part_row(p.merged, p.prefix_items, p.own_rows, own_item, qb + k - na) + h % kTileRows;
+  };
+  float m = -INFINITY;
+  for (int k = tid; k < parts; k += 128) m = fmaxf(m, p.part_ml[part_of(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (lane == 0) red_s[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red_s[0][0], red_s[0][1]), fmaxf(red_s[0][2], red_s[0][3]));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f, lx = 0.f;
+  for (int k = tid; k < parts; k += 128) {
+    const float4 ml = p.part_ml[part_of(k)];
+    const float w = ex2(ml.x - mu);
+    w_s[k] = w;
+    l += ml.y * w;
+    lx += ml.z * w;
   }
-  // Pairs [q0, q1] hold the units [a, e) of an item.
-  int q0[2], q1[2], parts = 0;
-  bool any_cut = !p.merged && p.prefix_tiles > 0;
-  for (int k = 0; k < n_items; ++k) {
-    const int64_t a = p.plan[2 + item[k]], e = p.plan[3 + item[k]];
-    q0[k] = 0;
-    q1[k] = -1;
-    if (e > a) {
-      // pair q owns [units q / pairs, units (q + 1) / pairs): the pair of unit u
-      // is the largest q with units q / pairs <= u.
-      q0[k] = static_cast<int>(((a + 1) * pairs - 1) / units);
-      q1[k] = static_cast<int>((e * pairs - 1) / units);
-      if (q1[k] > q0[k]) any_cut = true;
-    }
-    parts += q1[k] - q0[k] + 1;
-  }
-  if (parts == 1 && !any_cut) return;
-  float m = -INFINITY, l = 0.f, lx = 0.f;
-  float4 acc[4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int n0 = q1[0] - q0[0] + 1;
-  for (int k = warp; k < parts; k += 4) {
-    const int which = k < n0 ? 0 : 1;
-    const int q = which == 0 ? q0[0] + k : q0[1] + k - n0;
-    const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, item[which], q) + local[which];
-    const float4 ml = p.part_ml[pr];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + pr * kC) + lane;
-    float4 v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = __ldcs(src + c * 32);
-    const float mn = fmaxf(m, ml.x);
-    const float mu = mn == -INFINITY ? 0.f : mn;
-    const float wo = ex2(m - mu), wn = ex2(ml.x - mu);
-    m = mn;
-    l = l * wo + ml.y * wn;
-    lx = lx * wo + ml.z * wn;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[c].x = acc[c].x * wo + v[c].x * wn;
-      acc[c].y = acc[c].y * wo + v[c].y * wn;
-      acc[c].z = acc[c].z * wo + v[c].z * wn;
-      acc[c].w = acc[c].w * wo + v[c].w * wn;
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    lx += __shfl_xor_sync(0xFFFFFFFFu, lx, o);
   }
   if (lane == 0) {
-    ml_s[warp][0] = m;
-    ml_s[warp][1] = l;
-    ml_s[warp][2] = lx;
+    red_s[1][warp] = l;
+    red_s[2][warp] = lx;
   }
   __syncthreads();
-  const float mm = fmaxf(fmaxf(ml_s[0][0], ml_s[1][0]), fmaxf(ml_s[2][0], ml_s[3][0]));
-  const float mu = mm == -INFINITY ? 0.f : mm;
-  float lt = 0.f, lxt = 0.f;
+  l = (red_s[1][0] + red_s[1][1]) + (red_s[1][2] + red_s[1][3]);
+  lx = (red_s[2][0] + red_s[2][1]) + (red_s[2][2] + red_s[2][3]);
+  const int col0 = static_cast<int>(blockIdx.y) * (V * 32);  // in vectors of four
+  float4 acc[V];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float wk = ex2(ml_s[k][0] - mu);
-    lt += ml_s[k][1] * wk;
-    lxt += ml_s[k][2] * wk;
-  }
-  // Column vector c of warp 0's lane: the four warps' sums, through shared memory.
-  const float wgt = ex2(m - mu);
+  for (int c = 0; c < V; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = warp; k < parts; k += 4) {
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + part_of(k) * kC) + col0 + lane;
+    const float w = w_s[k];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    acc[c].x *= wgt;
-    acc[c].y *= wgt;
-    acc[c].z *= wgt;
-    acc[c].w *= wgt;
-    if (warp > 0) acc_s[warp - 1][c * 32 + lane] = acc[c];
+    for (int c = 0; c < V; ++c) {
+      const float4 v = __ldcs(src + c * 32);
+      acc[c].x = fmaf(v.x, w, acc[c].x);
+      acc[c].y = fmaf(v.y, w, acc[c].y);
+      acc[c].z = fmaf(v.z, w, acc[c].z);
+      acc[c].w = fmaf(v.w, w, acc[c].w);
+    }
   }
+  if (warp > 0)
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc_s[warp - 1][c][lane] = acc[c];
   __syncthreads();
   if (warp > 0) return;
-  const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < V; ++c) {
     float4 a = acc[c];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const float4 o = acc_s[k][c * 32 + lane];
+      const float4 o = acc_s[k][c][lane];
       a.x += o.x;
       a.y += o.y;
       a.z += o.z;
       a.w += o.w;
     }
     const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-    reinterpret_cast<uint2*>(p.out + r * kC)[c * 32 + lane] =
+    reinterpret_cast<uint2*>(p.out + r * kC)[col0 + c * 32 + lane] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (lane == 0 && p.lse) p.lse[r] = lt == 0.f ? -INFINITY : mm * 0.69314718055994531f + logf(lxt);
+  if (lane == 0 && blockIdx.y == 0 && p.lse)
+    p.lse[r] = l == 0.f ? -INFINITY : mu * 0.69314718055994531f + logf(lx);
 }
 
 // ---- host --------------------------------------------------------------------------
@@ -1050,16 +1103,18 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   p.kbox = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   p.vbox = page_size % 32 == 0 ? 32 : 16;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.lone_prefix = B * H <= 2 * kTileRows;
+  p.direct = (z.merged || p.prefix_tiles == 0) && p.prefix_tiles + (p.max_own + kTileKeys - 1) / kTileKeys <= 1;
   // A cache without pages is never read: its maps describe one row of q.
   const void* cbase = num_pages > 0 ? cache_bf16 : q_bf16;
   const uint64_t crows = num_pages > 0 ? static_cast<uint64_t>(num_pages * page_size) : 1;
   const uint64_t ccols = num_pages > 0 ? kRow : kC;
-  CUtensorMap mq, mqp, mk, mv, mr;
+  CUtensorMap mq, mqp, mk, mv, m4, mr;
   if (!make_bf16_map(&mq, q_bf16, static_cast<uint64_t>(B * H), kC, 64) ||
       !make_bf16_map(&mqp, q_pe_bf16, static_cast<uint64_t>(B * H), kR, 64) ||
       !make_bf16_map(&mk, cbase, crows, ccols, static_cast<uint32_t>(p.kbox)) ||
       !make_bf16_map(&mv, cbase, crows, ccols, static_cast<uint32_t>(p.vbox)) ||
-      !make_bf16_map(&mr, cbase, crows, ccols, 1))
+      !make_bf16_map(&m4, cbase, crows, ccols, 4) || !make_bf16_map(&mr, cbase, crows, ccols, 1))
     return FP8BLK_ERR_CUDA;
   if (num_pages == 0) p.total_rows = 1;
   cudaLaunchConfig_t cfg = {};
@@ -1072,12 +1127,15 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, mr, p))) return st;
+  if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, m4, mr, p))) return st;
+  if (p.direct) return FP8BLK_OK;
+  const bool few = B * H <= 4 * d->sm_count;
   cudaLaunchConfig_t join = {};
-  join.gridDim = dim3(static_cast<unsigned>(B * H));
+  join.gridDim = dim3(static_cast<unsigned>(B * H), few ? 4 : 1);
   join.blockDim = dim3(128);
   join.stream = cfg.stream;
   join.attrs = attr;
   join.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&join, mla_join_kernel, p));
+  return cuda_status(few ? cudaLaunchKernelEx(&join, mla_join_kernel<1>, p)
+                         : cudaLaunchKernelEx(&join, mla_join_kernel<4>, p));
 }
