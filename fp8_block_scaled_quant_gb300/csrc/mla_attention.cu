@@ -95,7 +95,7 @@ struct AttnParams {
   const int* lens;         // [B]
   __nv_bfloat16* out;      // [B H][512]
   float* lse;              // [B H] or null
-  float* part_o;           // [part rows][512]
+  float4* part_o;          // per part [128 column quads][rows of the item]: a warp's rows are contiguous
   float4* part_ml;         // [part rows] (maximum in log2 units, sum of the rounded weights, of the fp32 weights)
   int* plan;               // [0] units, [1] pairs in use, [2 + i] first unit of item i (items + 1 entries)
   unsigned* err;
@@ -810,12 +810,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (have && kh == 0 && p.lse) p.lse[r] = m * 0.69314718055994531f + logf(lxt);
         } else {
           const int64_t pr = part_row(p.merged, p.prefix_items, p.own_rows, i, pair);
-          uint8_t* dst = reinterpret_cast<uint8_t*>(p.part_o + (pr + r0) * kC + kh * 128);
+          const int pitch = it.b >= 0 && !p.merged ? p.own_rows : kTileRows;
+          float4* dst = p.part_o + pr * (kC / 4) + rt;
 #pragma unroll 1
           for (int c = 0; c < 256; c += 32) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_lane + c, o);
-            store_rows(o, dst + ((c >> 7) * 256 + (c & 127)) * 4, kC * 4);
+            if (have) {
+              float4* q = dst + ((c >> 7) * 64 + kh * 32 + (c & 127) / 4) * pitch;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                q[j * pitch] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                           __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+            }
           }
           if (have && kh == 0) p.part_ml[pr + rt] = make_float4(m, lt, lxt, 0.f);
         }
@@ -839,113 +846,149 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the parts of each query row, in item and key order: with weights
-// 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k. CTA (row, column part): the
-// weights first (a thread per part), then four warps add the parts round robin,
-// their loads independent of each other, and the four sums meet in shared
-// memory in warp order. With few rows the 512 columns are spread over four
-// CTAs (128 rows of 76 parts: 20 us in one). Rows whose one item was not cut
-// were stored by the attention kernel; rows without any key become zeros.
-template <int V>  // vectors of four columns per lane
-__global__ void __launch_bounds__(128) mla_join_kernel(const AttnParams p) {
-  __shared__ float4 acc_s[3][V][32];
-  __shared__ float w_s[2 * kMaxPairs];
-  __shared__ float red_s[3][4];
+// 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k. A lane has one row and Q
+// quads of columns (a warp's 32 rows of a quad are contiguous in a part); U
+// parts are loaded together, then added under a running maximum. S warps share
+// a row's parts and meet in shared memory in warp order. The fewer the rows,
+// the more parts each has: Q = 1, S = 8 keeps all of 128 rows x 76 parts in
+// flight, Q = 4, S = 1 suits thousands of rows of two or three parts. Rows whose one
+// item was not cut were stored by the attention kernel; rows without any key
+// become zeros.
+template <int Q, int S, int U>
+__global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const AttnParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t r = blockIdx.x;
-  const int b = static_cast<int>(r / p.H), h = static_cast<int>(r % p.H);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.H;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int quad = (S > 1 ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) * 4 + warp) * Q;
+  const int slot = S > 1 ? warp : 0;
+  const int b = static_cast<int>(min(r, rows - 1) / p.H), h = static_cast<int>(min(r, rows - 1) % p.H);
   const int units = p.plan[0], pairs = p.plan[1];
-  // Up to two items hold the row's keys. Item, row of the item and pairs of the
-  // first (the prefix's, or both together) and of the second (its own keys).
-  int first_item = -1, own_item = -1;
-  if (p.merged || p.prefix_tiles > 0) first_item = static_cast<int>(r / kTileRows);
-  if (!p.merged) own_item = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
-  auto pairs_of = [&](int item, int* q0) {
-    if (item < 0) return 0;
+  // Up to two items hold the row's keys: the prefix's (or both together) and
+  // its own. Per item: parts, first part's row and quad-0 address, quad pitch.
+  int n[2] = {0, 0};
+  int64_t at[2] = {0, 0};
+  int local[2], pitch[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int item = -1;
+    if (k == 0 && (p.merged || p.prefix_tiles > 0)) item = static_cast<int>(min(r, rows - 1) / kTileRows);
+    if (k == 1 && !p.merged) item = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
+    local[k] = k == 0 ? static_cast<int>(r % kTileRows) : h % kTileRows;
+    pitch[k] = k == 0 ? kTileRows : p.own_rows;
+    if (item < 0) continue;
     const int64_t a = p.plan[2 + item], e = p.plan[3 + item];
-    if (e <= a) return 0;
+    if (e <= a) continue;
     // Pair q has the units [units q / pairs, units (q + 1) / pairs): that of unit
     // u is the largest q with units q / pairs <= u.
-    *q0 = static_cast<int>(((a + 1) * pairs - 1) / units);
-    return static_cast<int>((e * pairs - 1) / units) - *q0 + 1;
-  };
-  int qa = 0, qb = 0;
-  const int na = pairs_of(first_item, &qa), nb = pairs_of(own_item, &qb);
-  const int parts = na + nb;
-  if (parts == 1 && (p.merged || p.prefix_tiles == 0)) return;
-  auto part_of = [&](int k) {
-    return k < na ? part_row(p.merged, p.prefix_items, p.own_rows, first_item, qa + k) + r % kTileRows
-                  : part_row(p.merged, p.prefix_items, p.own_rows, own_item, qb + k - na) + h % kTileRows;
-  };
-  float m = -INFINITY;
-  for (int k = tid; k < parts; k += 128) m = fmaxf(m, p.part_ml[part_of(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if (lane == 0) red_s[0][warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red_s[0][0], red_s[0][1]), fmaxf(red_s[0][2], red_s[0][3]));
-  const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, lx = 0.f;
-  for (int k = tid; k < parts; k += 128) {
-    const float4 ml = p.part_ml[part_of(k)];
-    const float w = ex2(ml.x - mu);
-    w_s[k] = w;
-    l += ml.y * w;
-    lx += ml.z * w;
+    const int q0 = static_cast<int>(((a + 1) * pairs - 1) / units);
+    n[k] = static_cast<int>((e * pairs - 1) / units) - q0 + 1;
+    at[k] = part_row(p.merged, p.prefix_items, p.own_rows, item, q0);
   }
+  const int parts = r < rows ? n[0] + n[1] : 0;
+  const bool stored = r >= rows || (parts == 1 && (p.merged || p.prefix_tiles == 0));
+  if (__all_sync(0xFFFFFFFFu, stored) && S == 1) return;
+  const int todo = stored ? 0 : parts;
+  constexpr int kStride = kTileRows * (kC / 4);  // from a part to the next pair's, in vectors
+  float m = -INFINITY, l = 0.f, lx = 0.f;
+  float4 acc[Q];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    lx += __shfl_xor_sync(0xFFFFFFFFu, lx, o);
-  }
-  if (lane == 0) {
-    red_s[1][warp] = l;
-    red_s[2][warp] = lx;
-  }
-  __syncthreads();
-  l = (red_s[1][0] + red_s[1][1]) + (red_s[1][2] + red_s[1][3]);
-  lx = (red_s[2][0] + red_s[2][1]) + (red_s[2][2] + red_s[2][3]);
-  const int col0 = static_cast<int>(blockIdx.y) * (V * 32);  // in vectors of four
-  float4 acc[V];
+  for (int c = 0; c < Q; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k0 = slot; k0 < todo; k0 += S * U) {
+    float4 ml[U], v[U][Q];
 #pragma unroll
-  for (int c = 0; c < V; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = warp; k < parts; k += 4) {
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + part_of(k) * kC) + col0 + lane;
-    const float w = w_s[k];
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * S, g = k < n[0] ? 0 : 1, kk = k - (g ? n[0] : 0);
+      ml[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float4 v = __ldcs(src + c * 32);
-      acc[c].x = fmaf(v.x, w, acc[c].x);
-      acc[c].y = fmaf(v.y, w, acc[c].y);
-      acc[c].z = fmaf(v.z, w, acc[c].z);
-      acc[c].w = fmaf(v.w, w, acc[c].w);
+      for (int c = 0; c < Q; ++c) v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < todo) {
+        ml[u] = p.part_ml[at[g] + static_cast<int64_t>(kk) * kTileRows + local[g]];
+        const float4* src = p.part_o + at[g] * (kC / 4) + static_cast<int64_t>(kk) * kStride +
+                            static_cast<int64_t>(quad) * pitch[g] + local[g];
+#pragma unroll
+        for (int c = 0; c < Q; ++c) v[u][c] = __ldcs(src + c * pitch[g]);
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float w0 = ex2(m - mu);
+    m = mn;
+    l *= w0;
+    lx *= w0;
+#pragma unroll
+    for (int c = 0; c < Q; ++c) acc[c] = make_float4(acc[c].x * w0, acc[c].y * w0, acc[c].z * w0, acc[c].w * w0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = ex2(ml[u].x - mu);
+      l = fmaf(ml[u].y, w, l);
+      lx = fmaf(ml[u].z, w, lx);
+#pragma unroll
+      for (int c = 0; c < Q; ++c) {
+        acc[c].x = fmaf(v[u][c].x, w, acc[c].x);
+        acc[c].y = fmaf(v[u][c].y, w, acc[c].y);
+        acc[c].z = fmaf(v[u][c].z, w, acc[c].z);
+        acc[c].w = fmaf(v[u][c].w, w, acc[c].w);
+      }
     }
   }
-  if (warp > 0)
+  float mm = m;
+  if constexpr (S > 1) {
+    __shared__ float red_s[S][3][32];
+    __shared__ float4 acc_s[S - 1][Q][32];
+    red_s[warp][0][lane] = m;
+    red_s[warp][1][lane] = l;
+    red_s[warp][2][lane] = lx;
+    if (warp > 0)
 #pragma unroll
-    for (int c = 0; c < V; ++c) acc_s[warp - 1][c][lane] = acc[c];
-  __syncthreads();
-  if (warp > 0) return;
+      for (int c = 0; c < Q; ++c) acc_s[warp - 1][c][lane] = acc[c];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 1; k < S; ++k) mm = fmaxf(mm, red_s[k][0][lane]);
+    const float mz = mm == -INFINITY ? 0.f : mm;
+    const float w0 = ex2(m - mz);
+    l *= w0;
+    lx *= w0;
+#pragma unroll
+    for (int c = 0; c < Q; ++c) acc[c] = make_float4(acc[c].x * w0, acc[c].y * w0, acc[c].z * w0, acc[c].w * w0);
+#pragma unroll
+    for (int k = 1; k < S; ++k) {
+      const float w = ex2(red_s[k][0][lane] - mz);
+      l = fmaf(red_s[k][1][lane], w, l);
+      lx = fmaf(red_s[k][2][lane], w, lx);
+#pragma unroll
+      for (int c = 0; c < Q; ++c) {
+        const float4 o = acc_s[k - 1][c][lane];
+        acc[c] = make_float4(fmaf(o.x, w, acc[c].x), fmaf(o.y, w, acc[c].y), fmaf(o.z, w, acc[c].z),
+                             fmaf(o.w, w, acc[c].w));
+      }
+    }
+  }
+  if (stored) return;
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // NaN stays NaN
+  uint2 o[Q];
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    float4 a = acc[c];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const float4 o = acc_s[k][c][lane];
-      a.x += o.x;
-      a.y += o.y;
-      a.z += o.z;
-      a.w += o.w;
-    }
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv), y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-    reinterpret_cast<uint2*>(p.out + r * kC)[col0 + c * 32 + lane] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  for (int c = 0; c < Q; ++c) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c].x * inv, acc[c].y * inv),
+                         y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
+    o[c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (lane == 0 && blockIdx.y == 0 && p.lse)
-    p.lse[r] = l == 0.f ? -INFINITY : mu * 0.69314718055994531f + logf(lx);
+  uint2* dst = reinterpret_cast<uint2*>(p.out + r * kC) + quad;
+  if constexpr (Q % 2 == 0) {
+#pragma unroll
+    for (int c = 0; c < Q; c += 2)
+      *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[c].x, o[c].y, o[c + 1].x, o[c + 1].y);
+  } else {
+#pragma unroll
+    for (int c = 0; c < Q; ++c) dst[c] = o[c];
+  }
+  if (quad == 0 && p.lse)
+    p.lse[r] = l == 0.f ? -INFINITY : mm * 0.69314718055994531f + logf(lx);
 }
 
 // ---- host --------------------------------------------------------------------------
@@ -1082,7 +1125,7 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.plan = reinterpret_cast<int*>(ws);
   p.part_ml = reinterpret_cast<float4*>(ws + z.plan_bytes);
-  p.part_o = reinterpret_cast<float*>(ws + z.plan_bytes + z.ml_bytes);
+  p.part_o = reinterpret_cast<float4*>(ws + z.plan_bytes + z.ml_bytes);
   p.err = d->err_word;
   p.B = static_cast<int>(B);
   p.H = static_cast<int>(H);
@@ -1129,13 +1172,15 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   cfg.numAttrs = 1;
   if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, m4, mr, p))) return st;
   if (p.direct) return FP8BLK_OK;
-  const bool few = B * H <= 4 * d->sm_count;
+  const int64_t rows = B * H;
+  const int variant = rows <= 256 ? 0 : rows <= 2048 ? 1 : 2;
   cudaLaunchConfig_t join = {};
-  join.gridDim = dim3(static_cast<unsigned>(B * H), few ? 4 : 1);
-  join.blockDim = dim3(128);
+  join.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32), variant == 0 ? kC / 4 : variant == 1 ? kC / 8 : kC / 64);
+  join.blockDim = dim3(variant == 0 ? 256 : 128);
   join.stream = cfg.stream;
   join.attrs = attr;
   join.numAttrs = 1;
-  return cuda_status(few ? cudaLaunchKernelEx(&join, mla_join_kernel<1>, p)
-                         : cudaLaunchKernelEx(&join, mla_join_kernel<4>, p));
+  return cuda_status(variant == 0   ? cudaLaunchKernelEx(&join, mla_join_kernel<1, 8, 5>, p)
+                     : variant == 1 ? cudaLaunchKernelEx(&join, mla_join_kernel<2, 4, 2>, p)
+                                    : cudaLaunchKernelEx(&join, mla_join_kernel<4, 1, 2>, p));
 }
