@@ -286,6 +286,9 @@ __device__ __forceinline__ int entry_row(const AttnParams& p, int pg, int key) {
   return pg * p.page + (p.page_shift >= 0 ? key & (p.page - 1) : key % p.page);
 }
 
+// Value chunks of a tile that hold keys.
+__device__ __forceinline__ int chunks_of(int key0, int limit) { return min(kVChunks, (limit - key0 + 31) / 32); }
+
 // Items [lo, hi) of thread `tid` of `n`.
 __device__ __forceinline__ int split(int items, int tid, int n) {
   return static_cast<int>(static_cast<int64_t>(items) * tid / n);
@@ -356,6 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_wait();
 
   // The plan: every CTA sums the items' tiles (thread-contiguous ranges, then
@@ -403,7 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   }
   tc_fence_before_sync();
   __syncthreads();
-  cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
+  // Barriers initialised and tensor memory allocated in both CTAs.
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int nunits = start[2];
@@ -418,6 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const uint32_t bars = map_to_cta(smem_u32(is_k ? k_full : v_full), 0);
     const uint32_t dst0 = smem_u32(smem + (is_k ? kOffK : kOffV));
     const int rows = is_k ? p.kbox : 16;   // keys per looked-up page entry
+    uint32_t vphase = 0;                   // bit c: phase of value chunk c
     const int mine = is_k ? static_cast<int>(rank) * 64 : 0;
     const bool looks = lane * rows < (is_k ? 64 : kTileKeys);
 #pragma unroll 1
@@ -502,16 +509,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         } else {
           // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
           // the half 128 rank .. + 128, as slabs 2 j and 2 j + 1 of each chunk.
-          // The chunk that holds the end goes row by row, those past it are zeros.
+          // The rows past the end in the chunk that holds it are zeros; chunks past
+          // it are neither loaded nor multiplied.
           const int x0 = static_cast<int>(rank) * 128;
 #pragma unroll 1
-          for (int c = 0; c < kVChunks; ++c) {
+          for (int c = 0; c < chunks_of(key0, limit); ++c) {
             const int kc = key0 + c * 32;
             const uint32_t dst = dst0 + c * kVChunk;
-            if (n > 0) ok = wait_warp(&v_empty[c], (n - 1) & 1, abort_flag, p.err);
+            ok = wait_warp(&v_empty[c], ((vphase >> c) & 1) ^ 1, abort_flag, p.err);
             if (!ok) break;
+            vphase ^= 1u << c;
             if (rank == 0 && elect_one_sync()) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
-            if (kc + 32 <= limit || kc >= limit) {
+            if (kc + 32 <= limit) {
 #pragma unroll 1
               for (int q = 0; q < 32; q += p.vbox) {
                 const int y = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (q >> 4));
@@ -558,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       } else {
 #pragma unroll 1
         for (int c = 0; c < kVChunks; ++c)
-          if (n > 0) wait_slow(smem_u32(&v_full[c]), (n - 1) & 1, nullptr, p.err);
+          if (n > 0) wait_slow(smem_u32(&v_full[c]), ((vphase >> c) & 1) ^ 1, nullptr, p.err);
       }
     }
   } else if (warp == 6) {
@@ -573,15 +582,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       bool ok = true;
       bool prev_first = false;
       uint32_t prev_seg = 0;
+      int prev_chunks = 0;
       // The output product of tile k (whose weights the softmax warps publish
       // while the scores of tile k + 1 are formed).
-      auto output = [&](uint32_t k, bool first, uint32_t sg) {
+      uint32_t vphase = 0;
+      auto output = [&](uint32_t k, bool first, uint32_t sg, int chunks) {
         if (first && sg > 0)
           ok = ok && wait_warp(o_empty, (sg - 1) & 1, abort_flag, p.err);
         ok = ok && wait_warp(p_full, k & 1, abort_flag, p.err);
 #pragma unroll 1
-        for (int c = 0; ok && c < kVChunks; ++c) {
-          ok = wait_warp(&v_full[c], k & 1, abort_flag, p.err);
+        for (int c = 0; ok && c < chunks; ++c) {
+          ok = wait_warp(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after_sync();
           if (elect_one_sync()) {
@@ -594,9 +605,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 mma_bf16_pair(tmem + j * 128, ad + 2 * h, bd + j * (2 * kVSlab >> 4) + h * (2048 >> 4), kIdO,
                               first && c == 0 && h == 0 ? 0u : 1u);
             mma_commit_pair(&v_empty[c]);
-            if (c == kVChunks - 1) mma_commit_pair(pv_done);
+            if (c == chunks - 1) mma_commit_pair(pv_done);
           }
           __syncwarp();
+          vphase ^= 1u << c;
         }
       };
 #pragma unroll 1
@@ -630,16 +642,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             }
             __syncwarp();
           }
-          if (ok && n > 0) output(n - 1, prev_first, prev_seg);
+          if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
           prev_first = t == t0;
           prev_seg = seg;
+          const bool pre = t < it.pt;
+          prev_chunks = chunks_of((pre ? t : t - it.pt) * kTileKeys, pre ? p.P : it.len);
           ++n;
         }
         if (t1 > t0) ++seg;
         ++i;
         t0 = 0;
       }
-      if (ok && n > 0) output(n - 1, prev_first, prev_seg);
+      if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
       if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
         if (elect_one_sync()) mma_commit_pair(drain);
         __syncwarp();

@@ -132,6 +132,29 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The bounded wait, its slow part out of line (the loops that call it stay
+// small enough for the instruction cache).
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 63u) == 0) {
+      if (abort && *abort) return;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (abort) *abort = 1;
+        atomicOr(err, kDevErrTimeoutLayer);
+        return;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint32_t a = smem_u32(bar);
+  if (!mbar_try_wait(a, parity)) wait_slow(a, parity, abort, err);
+}
+
 // Quantises one 128-element block, four elements per lane; lane 0 stores the scale.
 __device__ __forceinline__ void quant_block(const float (&v)[4], bool ue8m0, int lane, uint8_t* q, float* s) {
   float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
@@ -196,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     *abort_flag = 0;
+#pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
@@ -215,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map2);
       auto issue = [&](const CUtensorMap* mlo, int ylo, const CUtensorMap* mhi, int yhi, int z, int nkb) {
         const int s = n % kStages;
-        if (n >= kStages) mbar_wait(&empty[s], ((n / kStages) - 1) & 1, abort_flag, p.err, kDevErrTimeoutLayer);
+        if (n >= kStages) wait(&empty[s], ((n / kStages) - 1) & 1, abort_flag, p.err);
         if (*abort_flag) return;
         uint8_t* dst = ring + s * kStageBytes;
         const uint32_t bytes = static_cast<uint32_t>(nkb) * 1024;
@@ -225,27 +249,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       };
       auto units = [&](int u0, int u1, bool shared) {
+#pragma unroll 1
         for (int u = u0; u < u1; ++u) {
           const int e = shared ? p.E + u / upe : act[p.ns + u / upe];
           const int y = e * p.inter + (u % upe) * 8;
+#pragma unroll 1
           for (int st = 0; st < p.st1; ++st) issue(&map1, y, &map3, y, st * p.kb1, p.kb1);
         }
       };
       units(even(shared_units, c, G), even(shared_units, c + 1, G), true);
-      mbar_wait(routed, 0, abort_flag, p.err, kDevErrTimeoutLayer);
+      wait(routed, 0, abort_flag, p.err);
       if (!*abort_flag) {
         const int nact = misc[0], ur = (nact - p.ns) * upe;
         units(routed_start(shared_units, ur, c, G), routed_start(shared_units, ur, c + 1, G), false);
+#pragma unroll 1
         for (int a = 0; a < nact; ++a)
+#pragma unroll 1
           for (int st = 0; st < p.st2; ++st)
+#pragma unroll 1
             for (int g = 0; g < ngroups; ++g) {
               const int y = act[a] * p.dim + d0 + g * 16;
               issue(&map2, y, d0 + g * 16 + 8 < d1 ? &map2 : nullptr, y + 8, st * p.kb2, p.kb2);
             }
       }
       // No copy may be in flight when the CTA exits.
+#pragma unroll 1
       for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        mbar_wait(&full[i % kStages], (i / kStages) & 1, nullptr, p.err, kDevErrTimeoutLayer);
+        wait(&full[i % kStages], (i / kStages) & 1, nullptr, p.err);
     }
     __syncwarp();
   } else {
@@ -278,17 +308,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // Phase 0: x quantised and the logits formed, both spread over the grid.
+#pragma unroll 1
     for (int i = c * kWarps + warp; i < p.T * Kb1; i += G * kWarps) {
       const uint2 raw = reinterpret_cast<const uint2*>(p.x)[static_cast<size_t>(i) * 32 + lane];
       const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
                           __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
       quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
     }
+#pragma unroll 1
     for (int e = c; e < p.E; e += G) {
       float acc[kCols];
 #pragma unroll
       for (int m = 0; m < kCols; ++m) acc[m] = 0.f;
       const uint4* wv = reinterpret_cast<const uint4*>(p.gate_w + static_cast<size_t>(e) * p.dim);
+#pragma unroll 1
       for (int v = tid; v < p.dim / 8; v += kWarps * 32) {
         const uint4 a = __ldg(wv + v);
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
@@ -325,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // part buffer until they are sorted by expert.
     int* sel_e = reinterpret_cast<int*>(part);
     float* sel_w = part + kMaxTokens * 32;
+#pragma unroll 1
     for (int m = warp; m < p.T; m += kWarps) {
       const int v = p.E / 32;
       float xl[8], bl[8];
@@ -350,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scan over the 8 warps that hold experts.
     uint32_t my_mask = 0;
     if (tid < p.E)
+#pragma unroll 1
       for (int i = 0; i < p.T * p.k; ++i)
         if (sel_e[i] == tid) my_mask |= 1u << (i / p.k);
     const unsigned have = __ballot_sync(0xFFFFFFFFu, my_mask != 0);
@@ -369,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mask[tid] = all_tokens;
       base[tid] = tid * p.T;
     }
+#pragma unroll 1
     for (int i = tid; i < p.ns * p.T; i += kWarps * 32) wrow[i] = 1.0f;
     sync_warps();
     int a0 = p.ns, r0 = p.ns * p.T;
@@ -382,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       act[a] = tid;
       mask[a] = my_mask;
       base[a] = r;
+#pragma unroll 1
       for (int i = 0; i < p.T * p.k; ++i)
         if (sel_e[i] == tid) wrow[r + __popc(my_mask & ((1u << (i / p.k)) - 1u))] = sel_w[i];
     }
@@ -427,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One stage: this warp's K block (the warp-th) of 16 rows, promoted into acc.
     auto multiply = [&](const Frag<NT>& f, uint32_t mk, int nkb, bool mine, float (&acc)[NT][4]) {
       const int s = n % kStages;
-      mbar_wait(&full[s], (n / kStages) & 1, abort_flag, p.err, kDevErrTimeoutLayer);
+      wait(&full[s], (n / kStages) & 1, abort_flag, p.err);
       if (mine) {
         const uint8_t* lo = ring + s * kStageBytes + warp * 1024 + g * 128;
         const uint8_t* hi = lo + nkb * 1024;
@@ -468,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Phase 1: u = silu(w1 x) (w3 x), unit by unit (8 rows of an expert).
     int nb = 0;  // units so far: which part buffer
     auto phase1 = [&](int u0, int u1, int first) {
+#pragma unroll 1
       for (int u = u0; u < u1; ++u) {
         const int a = first + u / upe, e = act[a], rb = u % upe;
         const uint32_t mk = mask[a];
@@ -475,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float acc[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll 1
         for (int st = 0; st < p.st1; ++st) {
           const int kb = st * p.kb1 + warp;
           const bool mine = warp < p.kb1 && kb < Kb1;
@@ -511,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ur = (nact - p.ns) * upe;
     phase1(routed_start(shared_units, ur, c, G), routed_start(shared_units, ur, c + 1, G), p.ns);
     grid_barrier(1);
+#pragma unroll 1
     for (int i = c * kWarps + warp; i < nrows * Kb2; i += G * kWarps) {
       const float4 raw = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
       const float v[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -525,9 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < kMaxGroups; ++q)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
+#pragma unroll 1
     for (int a = 0; a < nact; ++a) {
       const uint32_t mk = mask[a];
       const int e = act[a];
+#pragma unroll 1
       for (int st = 0; st < p.st2; ++st) {
         const int kb = st * p.kb2 + warp;
         const bool mine = warp < p.kb2 && kb < Kb2;
