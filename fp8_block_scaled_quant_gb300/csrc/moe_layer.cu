@@ -17,22 +17,26 @@
 // floor is those bytes at HBM rate. The kernel is built to keep that stream
 // from stopping:
 //   - One CTA per SM, one launch (cooperative: CTAs meet at three barriers).
-//     A producer warp feeds a ring of 32 KB stages by TMA; sixteen warps
-//     multiply.
+//     Each of the CTA's sixteen warps owns 12 KB of shared memory and streams
+//     and multiplies its own share of the weights: nothing but the phases'
+//     ends makes warps wait for one another, so one warp's latencies hide
+//     behind fifteen others. (A producer warp with stages that all sixteen
+//     warps multiplied together, then met to add up, ran at 3.9 TB/s.)
 //   - The gate decides what the routed weights are, but not the shared ones:
-//     the producer starts on its share of the shared experts while the other
-//     warps quantise x, form the logits and run the gate.
-//   - w2 does not depend on u, only its use does: the ring fills with w2
-//     tiles while the CTAs wait for the last u and quantise it.
+//     every warp asks for its share of the shared experts first, then x is
+//     quantised and the gate computed.
+//   - w2 does not depend on u, only its use does: a warp that is done with
+//     its part of phase 1 asks for its first w2 tiles before the barriers.
 //   - Phase 1 splits (expert, 8 rows of w1 and the same 8 of w3) evenly over
-//     the CTAs, phase 2 gives each CTA the same rows of every expert's w2: the
-//     sum over experts stays in its registers, without atomics or partial
-//     outputs, in one order.
+//     the CTAs, and a CTA's units, K laid end to end, evenly over its warps; a
+//     unit cut between warps is added up in warp order. Phase 2 gives each CTA
+//     the same rows of every expert's w2, and its (expert, K block) pairs round
+//     robin to the warps: the sum over experts stays in registers. No atomics
+//     on values, one order of every sum.
 //
 // The products are warp-level FP8 MMAs (m16n8k32): tokens are the 8 columns,
-// so one MMA serves an expert's up to 8 tokens at the cost of one, and a stage
-// of 16 rows x 16 K blocks gives every warp one K block. In phase 1 rows 0-7
-// of an MMA tile are w1's and rows 8-15 w3's, so one lane ends with h1 and h3 of
+// so one MMA serves up to 8 tokens at the cost of one. In phase 1 rows 0-7 of
+// an MMA tile are w1's and rows 8-15 w3's, so one lane ends with h1 and h3 of
 // the same element. Each K block's product is promoted as acc += D * (a_s w_s).
 // A tcgen05.mma with so few columns takes about 130 cycles for 4 KB of weights,
 // 31 bytes a cycle, hardly the HBM rate of one SM (23); the warp MMAs take 64.
@@ -40,9 +44,10 @@
 // 32) of a K block for row g, MMA j of the block takes bytes [8 j, 8 j + 8) of
 // those, the same for both operands.
 //
-// Token columns are tokens 0-7, 8-15, ... themselves (a tile of 8 columns
-// without any token of the expert is skipped): no gathering, and in phase 2 the
-// columns mean the same token for every expert.
+// Columns. In phase 1 they are an expert's tokens, closely packed (one tile of 8
+// columns serves nearly every routed expert). In phase 2, whose accumulators
+// run over the experts, they are the tokens 0-7, 8-15, ... themselves, and a
+// tile without any token of the expert is skipped.
 //
 // Every wait is bounded (2 s): on expiry an error bit is set, waits return at
 // once from then on, and the control flow, whose loops are finite, runs out.
@@ -71,22 +76,27 @@ constexpr int kMaxTokens = 32;
 constexpr int kMaxShared = 8;
 constexpr int kMaxActive = 256 + kMaxShared;
 constexpr int kMaxRows = kMaxTokens * (32 + kMaxShared);  // (token, expert) pairs
-constexpr int kWarps = 16;                                // multiplying warps
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kStageBytes = 2 * 8 * 128 * kWarps;         // two boxes of 8 rows x 16 K blocks
+constexpr int kWarps = 16;
+constexpr int kMaxCtas = 192;                             // SMs a device may have
+constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroups = 4;                             // 16-row groups of w2 per CTA
 constexpr int kMaxDim = 8192, kMaxInter = 16384;
+constexpr int kWarpRing = 12288;                          // a warp's weight tiles
+constexpr int kSlots = 3;                                 // at most
+constexpr int kChunk = 2;                                 // K blocks of a phase-1 slot
+constexpr int kSlot1 = kChunk * 2 * 1024;                 // 8 rows of w1 and of w3
 
-constexpr int kTables = kMaxActive * 12 + kMaxRows * 4 + 64;
-constexpr int kLayerSmemLimit = 232448;
-
-// Partial sums of a 16-row tile: [warp][row][columns], padded so that a warp's
-// stores of 8 rows hit different banks.
-__host__ __device__ constexpr int part_width(int nt) { return 8 * nt + (nt > 1 ? 8 : 0); }
-__host__ __device__ constexpr int part_floats(int nt) { return kWarps * 16 * part_width(nt); }
-__host__ __device__ constexpr int ring_stages(int nt) {
-  return (kLayerSmemLimit - 1024 - kTables - 2 * part_floats(nt) * 4 - 256) / kStageBytes;
-}
+// Shared memory: rings, barriers, then the routing tables.
+constexpr int kOffBar = kWarps * kWarpRing;
+constexpr int kOffAct = kOffBar + kWarps * kSlots * 8 + 16;
+constexpr int kOffMask = kOffAct + kMaxActive * 4;
+constexpr int kOffBase = kOffMask + kMaxActive * 4;
+constexpr int kOffRowW = kOffBase + (kMaxActive + 1) * 4;
+constexpr int kOffRowT = kOffRowW + kMaxRows * 4;
+constexpr int kOffSel = kOffRowT + kMaxRows;              // ids, weights of the pairs; scratch before
+constexpr int kOffScan = kOffSel + 2 * kMaxTokens * 32 * 4;
+constexpr int kLayerSmem = 1024 + kOffScan + 48 * 4;
+static_assert(kLayerSmem <= 232448, "shared memory per CTA");
 
 struct LayerParams {
   const __nv_bfloat16* x;
@@ -105,11 +115,11 @@ struct LayerParams {
   float* u;           // [rows][inter]
   uint8_t* uq;        // [rows][inter]
   float* us;          // [rows][inter / 128]
+  float* part;        // [CTA][warp][4][16 rows x columns] sums of units cut between warps
   unsigned* err;
   int T, dim, inter, E, ns, k, groups, kept, sigmoid, normalize, ue8m0;
   float route_scale;
-  int kb1, st1;  // K blocks per stage and stages per unit, phase 1
-  int kb2, st2;  // the same, phase 2
+  int r2, slots2;  // rows of w2 per CTA at most, ring slots of that size
 };
 
 constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
@@ -167,9 +177,10 @@ __device__ __forceinline__ void quant_block(const float (&v)[4], bool ue8m0, int
   if (lane == 0) *s = sc;
 }
 
-// First unit of CTA c of G when n units are split evenly.
+// First unit of part c of G when n units are split evenly (n * c stays below
+// 2^31: at most 264 experts x 2048 units x 192 CTAs).
 __device__ __forceinline__ int even(int n, int c, int G) {
-  return static_cast<int>(static_cast<int64_t>(n) * c / G);
+  return static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint32_t>(c) / static_cast<uint32_t>(G));
 }
 
 // First routed unit of CTA c, such that shared and routed units together are
@@ -179,434 +190,517 @@ __device__ __forceinline__ int routed_start(int us, int ur, int c, int G) {
   return even(us + ur, c, G) - even(us, c, G);
 }
 
-// The B fragments of one K block for NT column tiles, its activation scales,
-// and the weight scales of the low and high rows.
-template <int NT>
+// The B fragment of one K block for 8 columns and the columns' scales.
 struct Frag {
-  uint4 b[NT][2];
-  float s[NT][2];
-  float wlo, whi;
+  uint4 b0, b1;
+  float s0, s1;
 };
+
+// One K block of a 16-row tile: rows g of `lo` and of `hi` (128-byte swizzled
+// rows of 128 bytes), promoted into acc with the rows' weight scales.
+__device__ __forceinline__ void block_product(const uint8_t* lo, const uint8_t* hi, const Frag& f, float wlo, float whi,
+                                              int g, int t4, float (&acc)[4]) {
+  uint4 al[2], ah[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = g * 128 + (((2 * t4 + h) ^ g) << 4);
+    al[h] = *reinterpret_cast<const uint4*>(lo + at);
+    ah[h] = *reinterpret_cast<const uint4*>(hi + at);
+  }
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  mma_16x8x32(d, al[0].x, ah[0].x, al[0].y, ah[0].y, f.b0.x, f.b0.y);
+  mma_16x8x32(d, al[0].z, ah[0].z, al[0].w, ah[0].w, f.b0.z, f.b0.w);
+  mma_16x8x32(d, al[1].x, ah[1].x, al[1].y, ah[1].y, f.b1.x, f.b1.y);
+  mma_16x8x32(d, al[1].z, ah[1].z, al[1].w, ah[1].w, f.b1.z, f.b1.w);
+  acc[0] = fmaf(d[0], f.s0 * wlo, acc[0]);
+  acc[1] = fmaf(d[1], f.s1 * wlo, acc[1]);
+  acc[2] = fmaf(d[2], f.s0 * whi, acc[2]);
+  acc[3] = fmaf(d[3], f.s1 * whi, acc[3]);
+}
+
+__device__ __forceinline__ float silu_mul(float h1, float h3) { return h1 / (1.0f + expf(-h1)) * h3; }
+
+// Ids and weights of token m by one warp, into the pair tables.
+__device__ __noinline__ void gate_of_token(const LayerParams& p, int m, int lane, bool store, int* sel_e, float* sel_w) {
+  const int v = p.E / 32;
+  float xl[8], bl[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    xl[i] = i < v ? __ldcg(p.logits + static_cast<size_t>(m) * p.E + lane * v + i) : 0.f;
+    bl[i] = i < v && p.gate_bias ? __ldg(p.gate_bias + lane * v + i) : 0.f;
+  }
+  int e;
+  float w;
+  gate_warp<8>(xl, bl, p.gate_bias != nullptr, v, p.groups, p.kept, p.k, p.sigmoid, p.route_scale, p.normalize, lane,
+               &e, &w);
+  if (lane < p.k) {
+    e = min(max(e, 0), p.E - 1);
+    sel_e[m * p.k + lane] = e;
+    sel_w[m * p.k + lane] = w;
+    if (store && p.topk_idx) p.topk_idx[m * p.k + lane] = e;
+    if (store && p.topk_w) p.topk_w[m * p.k + lane] = w;
+  }
+}
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map3,
-                     const __grid_constant__ CUtensorMap map2, const LayerParams p) {
-  constexpr int kStages = ring_stages(NT);
-  constexpr int W = part_width(NT);
+                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ LayerParams p) {
   constexpr int kCols = 8 * NT;
+  constexpr int kTile = 16 * kCols;  // sums of a 16-row tile
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  float* part = reinterpret_cast<float*>(ring + kStages * kStageBytes);  // [2][part_floats]
-  int* act = reinterpret_cast<int*>(part + 2 * part_floats(NT));         // active experts, shared ones first
-  uint32_t* mask = reinterpret_cast<uint32_t*>(act + kMaxActive);        // their tokens
-  int* base = reinterpret_cast<int*>(mask + kMaxActive);                 // their first (token, expert) row
-  float* wrow = reinterpret_cast<float*>(base + kMaxActive);             // gate weight of each row
-  int* misc = reinterpret_cast<int*>(wrow + kMaxRows);                   // active experts, rows
-  uint64_t* full = reinterpret_cast<uint64_t*>(misc + 16);
-  uint64_t* empty = full + kStages;
-  uint64_t* routed = empty + kStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(routed + 1);
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + kWarps * kSlots * 8);
+  int* act = reinterpret_cast<int*>(smem + kOffAct);             // active experts, shared ones first
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kOffMask);  // tokens; by expert id until sorted
+  int* base = reinterpret_cast<int*>(smem + kOffBase);           // first (token, expert) row; one past the last
+  float* row_w = reinterpret_cast<float*>(smem + kOffRowW);      // gate weight of each row
+  uint8_t* row_t = smem + kOffRowT;                              // token of each row
+  int* sel_e = reinterpret_cast<int*>(smem + kOffSel);
+  float* sel_w = reinterpret_cast<float*>(sel_e + kMaxTokens * 32);
+  int* scan = reinterpret_cast<int*>(smem + kOffScan);  // [16] active, [16] rows, active experts, rows
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
   const int G = gridDim.x, c = blockIdx.x;
   const int Kb1 = p.dim / 128, Kb2 = p.inter / 128;
-  const int upe = p.inter / 8;  // phase-1 units of an expert
-  const int shared_units = p.ns * upe;
+  const int chunks = (Kb1 + kChunk - 1) / kChunk;  // phase-1 slots of a unit
+  const int upe = p.inter / 8;                     // units of an expert
   const int d0 = even(p.dim / 8, c, G) * 8, d1 = even(p.dim / 8, c + 1, G) * 8;  // this CTA's rows of w2
   const int ngroups = (d1 - d0 + 15) / 16;
   const uint32_t all_tokens = p.T == 32 ? 0xFFFFFFFFu : (1u << p.T) - 1u;
+  uint8_t* ring = smem + warp * kWarpRing;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar) + warp * kSlots;
+  uint32_t phase = 0;  // bit s: phase of slot s
 
-  if (tid == 0) {
-    *abort_flag = 0;
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
-    mbar_init(routed, 1);
+  if (lane == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
   }
-  __syncthreads();
+  if (tid == 0) *abort_flag = 0;
+  __syncwarp();
 
-  if (warp == kWarps) {
-    // ---- producer ---------------------------------------------------------------
-    int n = 0;  // stages issued
-    if (lane == 0) {
-      const uint64_t policy = l2_policy_evict_first();  // weights are read once
-      tma_prefetch_desc(&map1);
-      tma_prefetch_desc(&map3);
-      tma_prefetch_desc(&map2);
-      auto issue = [&](const CUtensorMap* mlo, int ylo, const CUtensorMap* mhi, int yhi, int z, int nkb) {
-        const int s = n % kStages;
-        if (n >= kStages) wait(&empty[s], ((n / kStages) - 1) & 1, abort_flag, p.err);
-        if (*abort_flag) return;
-        uint8_t* dst = ring + s * kStageBytes;
-        const uint32_t bytes = static_cast<uint32_t>(nkb) * 1024;
-        mbar_arrive_expect_tx(&full[s], mhi ? 2 * bytes : bytes);
-        tma_load_3d_hint(dst, mlo, &full[s], 0, ylo, z, policy);
-        if (mhi) tma_load_3d_hint(dst + bytes, mhi, &full[s], 0, yhi, z, policy);
-        ++n;
-      };
-      auto units = [&](int u0, int u1, bool shared) {
-#pragma unroll 1
-        for (int u = u0; u < u1; ++u) {
-          const int e = shared ? p.E + u / upe : act[p.ns + u / upe];
-          const int y = e * p.inter + (u % upe) * 8;
-#pragma unroll 1
-          for (int st = 0; st < p.st1; ++st) issue(&map1, y, &map3, y, st * p.kb1, p.kb1);
-        }
-      };
-      units(even(shared_units, c, G), even(shared_units, c + 1, G), true);
-      wait(routed, 0, abort_flag, p.err);
-      if (!*abort_flag) {
-        const int nact = misc[0], ur = (nact - p.ns) * upe;
-        units(routed_start(shared_units, ur, c, G), routed_start(shared_units, ur, c + 1, G), false);
-#pragma unroll 1
-        for (int a = 0; a < nact; ++a)
-#pragma unroll 1
-          for (int st = 0; st < p.st2; ++st)
-#pragma unroll 1
-            for (int g = 0; g < ngroups; ++g) {
-              const int y = act[a] * p.dim + d0 + g * 16;
-              issue(&map2, y, d0 + g * 16 + 8 < d1 ? &map2 : nullptr, y + 8, st * p.kb2, p.kb2);
-            }
-      }
-      // No copy may be in flight when the CTA exits.
-#pragma unroll 1
-      for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
-        wait(&full[i % kStages], (i / kStages) & 1, nullptr, p.err);
+  // This warp's phase-1 slots: first of the shared units, then of the routed
+  // ones, each a range of chunks of the CTA's units.
+  const int us0 = even(p.ns * upe, c, G), us1 = even(p.ns * upe, c + 1, G);
+  const int sq0 = even((us1 - us0) * chunks, warp, kWarps), sq1 = even((us1 - us0) * chunks, warp + 1, kWarps);
+  int ur0 = 0, ur1 = 0, rq0 = 0, rq1 = 0;  // routed: known after the gate
+  const uint64_t policy = l2_policy_evict_first();  // weights are read once
+  auto issue1 = [&](int q) {  // slot q of this warp
+    const bool shared = q < sq1 - sq0;
+    const int at = shared ? sq0 + q : rq0 + q - (sq1 - sq0);
+    const int u = (shared ? us0 : ur0) + at / chunks;
+    const int e = shared ? p.E + u / upe : act[p.ns + u / upe];
+    if (elect_one_sync()) {
+      const int y = e * p.inter + u % upe * 8, z = at % chunks * kChunk;
+      uint64_t* bar = &full[q % kSlots];
+      uint8_t* dst = ring + q % kSlots * kSlot1;
+      mbar_arrive_expect_tx(bar, kSlot1);
+      tma_load_3d_hint(dst, &map1, bar, 0, y, z, policy);
+      tma_load_3d_hint(dst + kSlot1 / 2, &map3, bar, 0, y, z, policy);
     }
     __syncwarp();
-  } else {
-    // ---- the multiplying warps ----------------------------------------------------
-    const int g = lane >> 2, t4 = lane & 3;
-    auto sync_warps = [&] { named_barrier_sync(1, kWarps * 32); };
-    // Grid barrier i: every CTA's warps have arrived, their global writes are visible.
-    auto grid_barrier = [&](int i) {
-      __threadfence();
-      sync_warps();
-      if (tid == 0) {
-        atomicAdd(p.counters + i, 1u);
-        const uint64_t t0 = global_timer_ns();
-        for (uint32_t spin = 0;; ++spin) {
-          unsigned v;
-          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters + i) : "memory");
-          if (v >= static_cast<unsigned>(G)) break;
-          if ((spin & 63u) == 63u) {
-            if (*abort_flag) break;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-              *abort_flag = 1;
-              atomicOr(p.err, kDevErrTimeoutLayer);
-              break;
-            }
+  };
+  const int early = min(kSlots, sq1 - sq0);
+#pragma unroll 1
+  for (int q = 0; q < early; ++q) issue1(q);
+
+  // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
+  auto grid_barrier = [&](int i) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      atomicAdd(p.counters + i, 1u);
+      const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+      for (uint32_t spin = 0;; ++spin) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters + i) : "memory");
+        if (v >= static_cast<unsigned>(G)) break;
+        if ((spin & 63u) == 63u) {
+          if (*abort_flag) break;
+          if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(p.err, kDevErrTimeoutLayer);
+            break;
           }
         }
-        __threadfence();
       }
-      sync_warps();
-    };
-
-    // Phase 0: x quantised and the logits formed, both spread over the grid.
-#pragma unroll 1
-    for (int i = c * kWarps + warp; i < p.T * Kb1; i += G * kWarps) {
-      const uint2 raw = reinterpret_cast<const uint2*>(p.x)[static_cast<size_t>(i) * 32 + lane];
-      const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
-      quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
+      __threadfence();
     }
+    __syncthreads();
+  };
+
+  // Phase 0: x quantised and the logits formed, both spread over the grid. A
+  // CTA's experts share its warps, each with a slice of K.
 #pragma unroll 1
-    for (int e = c; e < p.E; e += G) {
+  for (int i = c * kWarps + warp; i < p.T * Kb1; i += G * kWarps) {
+    const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x) + static_cast<size_t>(i) * 32 + lane);
+    const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                        __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
+    quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
+  }
+  {
+    const int per_cta = min((p.E + G - 1) / G, kWarps);  // experts at a time
+    const int wpe = kWarps / per_cta;                    // warps of an expert
+    float* sums = sel_w;                                 // [warp][columns]
+#pragma unroll 1
+    for (int e0 = c; e0 < p.E; e0 += per_cta * G) {
+      const int e = e0 + warp / wpe * G;
       float acc[kCols];
 #pragma unroll
       for (int m = 0; m < kCols; ++m) acc[m] = 0.f;
-      const uint4* wv = reinterpret_cast<const uint4*>(p.gate_w + static_cast<size_t>(e) * p.dim);
+      if (warp < per_cta * wpe && e < p.E) {
+        const uint4* wv = reinterpret_cast<const uint4*>(p.gate_w + static_cast<size_t>(e) * p.dim);
+        const int n = p.dim / 8, step = wpe * 32;
+        // Two vectors of the gate row a pass, their loads and x's in flight together.
 #pragma unroll 1
-      for (int v = tid; v < p.dim / 8; v += kWarps * 32) {
-        const uint4 a = __ldg(wv + v);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+        for (int v = warp % wpe * 32 + lane; v < n; v += 2 * step) {
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 a[2] = {__ldg(wv + v), v + step < n ? __ldg(wv + v + step) : zero};
 #pragma unroll
-        for (int m = 0; m < kCols; ++m) {
-          if (m < p.T) {
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim) + v);
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+          for (int m = 0; m < kCols; ++m) {
+            if (m < p.T) {
+              const uint4* xv = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim);
+              const uint4 b[2] = {__ldg(xv + v), v + step < n ? __ldg(xv + v + step) : zero};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
-              acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t aw[4] = {a[h].x, a[h].y, a[h].z, a[h].w}, bw[4] = {b[h].x, b[h].y, b[h].z, b[h].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
+                  acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
+                }
+              }
             }
           }
         }
       }
 #pragma unroll
       for (int m = 0; m < kCols; ++m) {
+        if (m < p.T) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
-        if (lane == 0) part[warp * kCols + m] = acc[m];
+          for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
+          if (lane == 0) sums[warp * kCols + m] = acc[m];
+        }
       }
-      sync_warps();
-      if (tid < p.T) {
-        float s = 0.f;
-        for (int w = 0; w < kWarps; ++w) s += part[w * kCols + tid];
-        p.logits[static_cast<size_t>(tid) * p.E + e] = s;
+      __syncthreads();
+      for (int i = tid; i < per_cta * p.T; i += kThreads) {
+        const int k = i / p.T, m = i % p.T;
+        float v = 0.f;
+        for (int w = 0; w < wpe; ++w) v += sums[(k * wpe + w) * kCols + m];
+        if (e0 + k * G < p.E) p.logits[static_cast<size_t>(m) * p.E + e0 + k * G] = v;
       }
-      sync_warps();
+      __syncthreads();
     }
-    grid_barrier(0);
+  }
+  grid_barrier(0);
 
-    // The gate, by every CTA for itself: ids and weights of all tokens, in the
-    // part buffer until they are sorted by expert.
-    int* sel_e = reinterpret_cast<int*>(part);
-    float* sel_w = part + kMaxTokens * 32;
+  // The gate, by every CTA for itself, then the tables: tokens of each expert,
+  // active experts in order (shared ones first), their rows.
 #pragma unroll 1
-    for (int m = warp; m < p.T; m += kWarps) {
-      const int v = p.E / 32;
-      float xl[8], bl[8];
+  for (int m = warp; m < p.T; m += kWarps) gate_of_token(p, m, lane, c == 0, sel_e, sel_w);
+  uint32_t* tokens_of = reinterpret_cast<uint32_t*>(base);  // by expert id, until the scan
+  for (int e = tid; e < p.E; e += kThreads) tokens_of[e] = 0;
+  __syncthreads();
+  const int pairs = p.T * p.k;
+  for (int i = tid; i < pairs; i += kThreads) atomicOr(&tokens_of[sel_e[i]], 1u << (i / p.k));
+  __syncthreads();
+  const uint32_t my_tokens = tid < p.E ? tokens_of[tid] : 0;
+  const unsigned have = __ballot_sync(0xFFFFFFFFu, my_tokens != 0);
+  int upto = __popc(my_tokens);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xl[i] = i < v ? __ldcg(p.logits + static_cast<size_t>(m) * p.E + lane * v + i) : 0.f;
-        bl[i] = i < v && p.gate_bias ? __ldg(p.gate_bias + lane * v + i) : 0.f;
-      }
-      int e;
-      float w;
-      gate_warp<8>(xl, bl, p.gate_bias != nullptr, v, p.groups, p.kept, p.k, p.sigmoid, p.route_scale, p.normalize,
-                   lane, &e, &w);
-      if (lane < p.k) {
-        e = min(max(e, 0), p.E - 1);
-        sel_e[m * p.k + lane] = e;
-        sel_w[m * p.k + lane] = w;
-        if (c == 0 && p.topk_idx) p.topk_idx[m * p.k + lane] = e;
-        if (c == 0 && p.topk_w) p.topk_w[m * p.k + lane] = w;
-      }
-    }
-    sync_warps();
-    // Experts' token masks (thread e for expert e), then the active list by a
-    // scan over the 8 warps that hold experts.
-    uint32_t my_mask = 0;
-    if (tid < p.E)
-#pragma unroll 1
-      for (int i = 0; i < p.T * p.k; ++i)
-        if (sel_e[i] == tid) my_mask |= 1u << (i / p.k);
-    const unsigned have = __ballot_sync(0xFFFFFFFFu, my_mask != 0);
-    int rows = __popc(my_mask);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) {
+    scan[warp] = __popc(have);
+    scan[16 + warp] = upto;
+  }
+  __syncthreads();  // every thread has its tokens: base may be written
+  int a0 = p.ns, r0 = p.ns * p.T;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, rows, o);
-      if (lane >= o) rows += v;
+  for (int w = 0; w < kWarps; ++w) {
+    a0 += w < warp ? scan[w] : 0;
+    r0 += w < warp ? scan[16 + w] : 0;
+  }
+  if (tid < p.ns) {
+    act[tid] = p.E + tid;
+    mask[tid] = all_tokens;
+    base[tid] = tid * p.T;
+  }
+  for (int i = tid; i < p.ns * p.T; i += kThreads) {
+    row_w[i] = 1.0f;
+    row_t[i] = static_cast<uint8_t>(i % p.T);
+  }
+  if (my_tokens) {
+    const int a = a0 + __popc(have & ((1u << lane) - 1u));
+    const int r = r0 + upto - __popc(my_tokens);
+    act[a] = tid;
+    mask[a] = my_tokens;
+    base[a] = r;
+    int k = r;
+    for (uint32_t left = my_tokens; left; left &= left - 1, ++k) {
+      const int m = __ffs(left) - 1;
+      row_t[k] = static_cast<uint8_t>(m);
+      float w = 0.f;
+      for (int j = 0; j < p.k; ++j)
+        if (sel_e[m * p.k + j] == tid) w = sel_w[m * p.k + j];
+      row_w[k] = w;
     }
-    int* wsum = reinterpret_cast<int*>(part) + 2 * kMaxTokens * 32;  // [16] active, [16] rows
-    if (lane == 31) {
-      wsum[warp] = __popc(have);
-      wsum[16 + warp] = rows;
-    }
-    if (tid < p.ns) {
-      act[tid] = p.E + tid;
-      mask[tid] = all_tokens;
-      base[tid] = tid * p.T;
-    }
+  }
+  if (tid == kThreads - 1) {
+    scan[32] = a0 + __popc(have);
+    scan[33] = r0 + upto;
+  }
+  __syncthreads();
+  const int nact = scan[32], nrows = scan[33];
+  {
+    const int n = (nact - p.ns) * upe;
+    ur0 = routed_start(p.ns * upe, n, c, G);
+    ur1 = routed_start(p.ns * upe, n, c + 1, G);
+    rq0 = even((ur1 - ur0) * chunks, warp, kWarps);
+    rq1 = even((ur1 - ur0) * chunks, warp + 1, kWarps);
+  }
+  const int nq = (sq1 - sq0) + (rq1 - rq0);
 #pragma unroll 1
-    for (int i = tid; i < p.ns * p.T; i += kWarps * 32) wrow[i] = 1.0f;
-    sync_warps();
-    int a0 = p.ns, r0 = p.ns * p.T;
-    for (int w = 0; w < warp; ++w) {
-      a0 += wsum[w];
-      r0 += wsum[16 + w];
-    }
-    if (my_mask) {
-      const int a = a0 + __popc(have & ((1u << lane) - 1u));
-      const int r = r0 + rows - __popc(my_mask);
-      act[a] = tid;
-      mask[a] = my_mask;
-      base[a] = r;
-#pragma unroll 1
-      for (int i = 0; i < p.T * p.k; ++i)
-        if (sel_e[i] == tid) wrow[r + __popc(my_mask & ((1u << (i / p.k)) - 1u))] = sel_w[i];
-    }
-    if (tid == kWarps * 32 - 1) {
-      misc[0] = a0 + __popc(have);
-      misc[1] = r0 + rows;
-    }
-    sync_warps();
-    const int nact = misc[0], nrows = misc[1];
-    if (tid == 0) mbar_arrive(routed);
+  for (int q = early; q < min(kSlots, nq); ++q) issue1(q);
 
-    int n = 0;  // stages consumed
-    // The fragments of K block kb for active expert a; `rows` maps a token to
-    // its row of the quantised activations.
-    auto load_frag = [&](Frag<NT>& f, const uint8_t* q, const float* s, int K, int Kb, int a, int kb, bool by_row,
-                         const float* slo, const float* shi) {
-      const uint32_t mk = mask[a];
-      const int bs = base[a];
-      auto row_of = [&](int m) { return by_row ? bs + __popc(mk & ((1u << m) - 1u)) : m; };
+  // Phase 1: u = silu(w1 x) (w3 x).
+  auto count_of = [&](int a) { return __popc(mask[a]); };
+  auto store_u = [&](int a, int u, int col, int r, float h1, float h3) {
+    p.u[static_cast<size_t>(base[a] + col) * p.inter + u % upe * 8 + r] = silu_mul(h1, h3);
+  };
+  float* my_part = p.part + (static_cast<size_t>(c) * kWarps + warp) * 4 * kTile;
+  {
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    int first = 0;  // the slot of this unit's first chunk here
+#pragma unroll 1
+    for (int q = 0; q < nq; ++q) {
+      const bool shared = q < sq1 - sq0;
+      const int at = shared ? sq0 + q : rq0 + q - (sq1 - sq0);
+      const int u = (shared ? us0 : ur0) + at / chunks, ck = at % chunks;
+      const int a = (shared ? 0 : p.ns) + u / upe;
+      const int cnt = count_of(a), r_base = base[a];
+      const size_t srow = static_cast<size_t>((static_cast<int64_t>(act[a]) * p.inter + u % upe * 8) / 128) * Kb1;
+      const int s = q % kSlots;
+      const uint8_t* w = ring + s * kSlot1;
+      // The first column tile's fragments are asked for before the wait.
+      auto frag = [&](int nt, int kb) {
+        Frag f;
+        const int col = nt * 8 + g, c2 = nt * 8 + 2 * t4;
+        f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
+        f.s0 = f.s1 = 0.f;
+        if (col < cnt) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.xq + static_cast<size_t>(row_t[r_base + col]) * p.dim +
+                                                            kb * 128 + t4 * 32);
+          f.b0 = __ldcg(src);
+          f.b1 = __ldcg(src + 1);
+        }
+        if (c2 < cnt) f.s0 = __ldcg(p.xs + row_t[r_base + c2] * Kb1 + kb);
+        if (c2 + 1 < cnt) f.s1 = __ldcg(p.xs + row_t[r_base + c2 + 1] * Kb1 + kb);
+        return f;
+      };
+      Frag f[kChunk];
+      float wlo[kChunk], whi[kChunk];
+#pragma unroll
+      for (int h = 0; h < kChunk; ++h) {
+        const int kb = min(ck * kChunk + h, Kb1 - 1);  // past K: the weights are zeros
+        f[h] = frag(0, kb);
+        wlo[h] = __ldg(p.w1_s + srow + kb);
+        whi[h] = __ldg(p.w3_s + srow + kb);
+      }
+      wait(&full[s], (phase >> s) & 1, abort_flag, p.err);
+      phase ^= 1u << s;
+      __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        if ((mk >> m) & 1u) {
-          const uint4* src = reinterpret_cast<const uint4*>(q + static_cast<size_t>(row_of(m)) * K + kb * 128 + t4 * 32);
-          f.b[nt][0] = __ldcg(src);
-          f.b[nt][1] = __ldcg(src + 1);
-        } else {
-          f.b[nt][0] = f.b[nt][1] = zero;
-        }
+        if (nt * 8 >= cnt) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f.s[nt][i] = 0.f;
-          if ((mk >> (m2 + i)) & 1u) {
-            const int r = row_of(m2 + i);
-            f.s[nt][i] = __ldcg(s + static_cast<size_t>(r) * Kb + kb) * (by_row ? wrow[r] : 1.0f);
-          }
-        }
-      }
-      f.wlo = __ldg(slo);
-      f.whi = __ldg(shi);
-    };
-    // One stage: this warp's K block (the warp-th) of 16 rows, promoted into acc.
-    auto multiply = [&](const Frag<NT>& f, uint32_t mk, int nkb, bool mine, float (&acc)[NT][4]) {
-      const int s = n % kStages;
-      wait(&full[s], (n / kStages) & 1, abort_flag, p.err);
-      if (mine) {
-        const uint8_t* lo = ring + s * kStageBytes + warp * 1024 + g * 128;
-        const uint8_t* hi = lo + nkb * 1024;
-        uint4 al[2], ah[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          al[h] = *reinterpret_cast<const uint4*>(lo + (((2 * t4 + h) ^ g) << 4));
-          ah[h] = *reinterpret_cast<const uint4*>(hi + (((2 * t4 + h) ^ g) << 4));
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16x8x32(d, al[0].x, ah[0].x, al[0].y, ah[0].y, f.b[nt][0].x, f.b[nt][0].y);
-          mma_16x8x32(d, al[0].z, ah[0].z, al[0].w, ah[0].w, f.b[nt][0].z, f.b[nt][0].w);
-          mma_16x8x32(d, al[1].x, ah[1].x, al[1].y, ah[1].y, f.b[nt][1].x, f.b[nt][1].y);
-          mma_16x8x32(d, al[1].z, ah[1].z, al[1].w, ah[1].w, f.b[nt][1].z, f.b[nt][1].w);
-          acc[nt][0] = fmaf(d[0], f.s[nt][0] * f.wlo, acc[nt][0]);
-          acc[nt][1] = fmaf(d[1], f.s[nt][1] * f.wlo, acc[nt][1]);
-          acc[nt][2] = fmaf(d[2], f.s[nt][0] * f.whi, acc[nt][2]);
-          acc[nt][3] = fmaf(d[3], f.s[nt][1] * f.whi, acc[nt][3]);
+        for (int h = 0; h < kChunk; ++h) {
+          const Frag x = nt == 0 ? f[h] : frag(nt, min(ck * kChunk + h, Kb1 - 1));
+          block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, x, wlo[h], whi[h], g, t4, acc[nt]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
-      ++n;
-    };
-    // This warp's sums of a 16-row tile into part buffer `buf`.
-    auto put = [&](const float (&acc)[NT][4], float* buf) {
+      if (q + kSlots < nq && !*abort_flag) issue1(q + kSlots);
+      const bool last = q + 1 == nq || q + 1 == sq1 - sq0;  // of the shared or of the routed range
+      if (ck + 1 == chunks || last) {
+        const int ck0 = ck - (q - first);
+        if (ck0 == 0 && ck + 1 == chunks) {
+          // The whole unit: lane (g, t4) has columns 2 t4, 2 t4 + 1 of row g, h1 and h3.
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float* q = buf + (warp * 16 + g) * W + nt * 8 + 2 * t4;
-        *reinterpret_cast<float2*>(q) = make_float2(acc[nt][0], acc[nt][1]);
-        *reinterpret_cast<float2*>(q + 8 * W) = make_float2(acc[nt][2], acc[nt][3]);
-      }
-    };
-
-    // Phase 1: u = silu(w1 x) (w3 x), unit by unit (8 rows of an expert).
-    int nb = 0;  // units so far: which part buffer
-    auto phase1 = [&](int u0, int u1, int first) {
-#pragma unroll 1
-      for (int u = u0; u < u1; ++u) {
-        const int a = first + u / upe, e = act[a], rb = u % upe;
-        const uint32_t mk = mask[a];
-        const size_t srow = static_cast<size_t>((static_cast<int64_t>(e) * p.inter + rb * 8) / 128) * Kb1;
-        float acc[NT][4];
+          for (int nt = 0; nt < NT; ++nt) {
+            const int col = nt * 8 + 2 * t4;
+            if (col < cnt) store_u(a, u, col, g, acc[nt][0], acc[nt][2]);
+            if (col + 1 < cnt) store_u(a, u, col + 1, g, acc[nt][1], acc[nt][3]);
+          }
+        } else {
+          float* t = my_part + ((shared ? 0 : 2) + (ck0 == 0 ? 1 : 0)) * kTile;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (nt * 8 < cnt)
+              *reinterpret_cast<float4*>(t + (nt * 32 + lane) * 4) =
+                  make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll 1
-        for (int st = 0; st < p.st1; ++st) {
-          const int kb = st * p.kb1 + warp;
-          const bool mine = warp < p.kb1 && kb < Kb1;
-          Frag<NT> f;
-          if (mine) load_frag(f, p.xq, p.xs, p.dim, Kb1, a, kb, false, p.w1_s + srow + kb, p.w3_s + srow + kb);
-          multiply(f, mk, p.kb1, mine, acc);
-        }
-        float* buf = part + (nb & 1) * part_floats(NT);
-        ++nb;
-        put(acc, buf);
-        sync_warps();
-        // kCols x 8 elements, 8 / NT threads each, summed in warp order within a
-        // thread and then across the threads.
-        constexpr int kTpo = 8 / NT;
-        const int o = tid / kTpo, q = tid % kTpo;
-        const int m = o / 8, r = o % 8;
-        float h1 = 0.f, h3 = 0.f;
-        for (int w = q; w < p.kb1; w += kTpo) {
-          h1 += buf[(w * 16 + r) * W + m];
-          h3 += buf[(w * 16 + r + 8) * W + m];
-        }
-#pragma unroll
-        for (int of = kTpo / 2; of > 0; of >>= 1) {
-          h1 += __shfl_xor_sync(0xFFFFFFFFu, h1, of);
-          h3 += __shfl_xor_sync(0xFFFFFFFFu, h3, of);
-        }
-        if (q == 0 && ((mk >> m) & 1u)) {
-          const int row = base[a] + __popc(mk & ((1u << m) - 1u));
-          p.u[static_cast<size_t>(row) * p.inter + rb * 8 + r] = h1 / (1.0f + expf(-h1)) * h3;
-        }
-      }
-    };
-    phase1(even(shared_units, c, G), even(shared_units, c + 1, G), 0);
-    const int ur = (nact - p.ns) * upe;
-    phase1(routed_start(shared_units, ur, c, G), routed_start(shared_units, ur, c + 1, G), p.ns);
-    grid_barrier(1);
-#pragma unroll 1
-    for (int i = c * kWarps + warp; i < nrows * Kb2; i += G * kWarps) {
-      const float4 raw = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
-      const float v[4] = {raw.x, raw.y, raw.z, raw.w};
-      quant_block(v, p.ue8m0 != 0, lane, p.uq + static_cast<size_t>(i) * 128, p.us + i);
-    }
-    grid_barrier(2);
-
-    // Phase 2: this CTA's rows of every active expert's w2, weighted and summed
-    // over the experts in the accumulators.
-    float acc[kMaxGroups][NT][4];
-#pragma unroll
-    for (int q = 0; q < kMaxGroups; ++q)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
-#pragma unroll 1
-    for (int a = 0; a < nact; ++a) {
-      const uint32_t mk = mask[a];
-      const int e = act[a];
-#pragma unroll 1
-      for (int st = 0; st < p.st2; ++st) {
-        const int kb = st * p.kb2 + warp;
-        const bool mine = warp < p.kb2 && kb < Kb2;
-        Frag<NT> f;
-        if (mine) load_frag(f, p.uq, p.us, p.inter, Kb2, a, kb, true, p.w2_s, p.w2_s);
-#pragma unroll
-        for (int q = 0; q < kMaxGroups; ++q) {
-          if (q < ngroups) {
-            if (mine) {
-              const int64_t row = static_cast<int64_t>(e) * p.dim + d0 + q * 16;
-              const int64_t last = static_cast<int64_t>(e) * p.dim + d1 - 1;
-              f.wlo = __ldg(p.w2_s + row / 128 * Kb2 + kb);
-              f.whi = __ldg(p.w2_s + (row + 8 < last ? row + 8 : last) / 128 * Kb2 + kb);
-            }
-            multiply(f, mk, p.kb2, mine, acc[q]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kMaxGroups; ++q) {
-      if (q < ngroups) {
-        float* buf = part + (nb & 1) * part_floats(NT);
-        ++nb;
-        put(acc[q], buf);
-        sync_warps();
-        if (tid < 16 * kCols) {
-          const int m = tid / 16, r = tid % 16;
-          float s = 0.f;
-          for (int w = 0; w < p.kb2; ++w) s += buf[(w * 16 + r) * W + m];
-          if (m < p.T && d0 + q * 16 + r < d1)
-            p.y[static_cast<size_t>(m) * p.dim + d0 + q * 16 + r] = __float2bfloat16_rn(s);
-        }
+        first = q + 1;
       }
     }
   }
+
+  // The first w2 tiles: item i is K block i % Kb2 of active expert i / Kb2.
+  const int items = nact * Kb2;
+  auto issue2 = [&](int i) {
+    const int n = (i - warp) / kWarps, s = n % p.slots2;
+    if (elect_one_sync()) {
+      uint64_t* bar = &full[s];
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.r2) * 128);
+      tma_load_3d_hint(ring + s * p.r2 * 128, &map2, bar, 0, act[i / Kb2] * p.dim + d0, i % Kb2, policy);
+    }
+    __syncwarp();
+  };
+  if (!*abort_flag)
+#pragma unroll 1
+    for (int n = 0; n < p.slots2 && warp + n * kWarps < items; ++n) issue2(warp + n * kWarps);
+
+  // Units cut between warps: warp w adds up units w, w + 16, ... of the CTA.
   __syncthreads();
+#pragma unroll 1
+  for (int range = 0; range < 2; ++range) {
+    const int u0 = range ? ur0 : us0, n = (range ? ur1 : us1) - u0, total = n * chunks;
+#pragma unroll 1
+    for (int k = warp; k < n; k += kWarps) {
+      // The warp of chunk x is the largest w with even(total, w) <= x.
+      const int w0 = ((k * chunks + 1) * kWarps - 1) / total;
+      const int w1 = ((k + 1) * chunks * kWarps - 1) / total;
+      if (w0 == w1) continue;
+      const int u = u0 + k, a = (range ? p.ns : 0) + u / upe, cnt = count_of(a);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt * 8 >= cnt) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = w0; w <= w1; ++w) {
+          const int from = even(total, w, kWarps);
+          if (from == even(total, w + 1, kWarps)) continue;  // fewer chunks than warps: this one has none
+          const bool starts = from <= k * chunks;
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(
+                                      p.part + ((static_cast<size_t>(c) * kWarps + w) * 4 + range * 2 + (starts ? 1 : 0)) *
+                                                   kTile) +
+                                  nt * 32 + lane);
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
+        const int col = nt * 8 + 2 * t4;
+        if (col < cnt) store_u(a, u, col, g, v.x, v.z);
+        if (col + 1 < cnt) store_u(a, u, col + 1, g, v.y, v.w);
+      }
+    }
+  }
+  grid_barrier(1);
+#pragma unroll 1
+  for (int i = c * kWarps + warp; i < nrows * Kb2; i += G * kWarps) {
+    const float4 raw = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
+    const float v[4] = {raw.x, raw.y, raw.z, raw.w};
+    quant_block(v, p.ue8m0 != 0, lane, p.uq + static_cast<size_t>(i) * 128, p.us + i);
+  }
+  grid_barrier(2);
+
+  // Phase 2: this CTA's rows of every active expert's w2, weighted and summed
+  // over the experts in the accumulators.
+  float acc[kMaxGroups][NT][4];
+#pragma unroll
+  for (int q = 0; q < kMaxGroups; ++q)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
+  int n2 = 0;
+#pragma unroll 1
+  for (int i = warp; i < items; i += kWarps, ++n2) {
+    const int a = i / Kb2, kb = i % Kb2, s = n2 % p.slots2;
+    const uint32_t mk = mask[a];
+    const int r_base = base[a];
+    auto frag = [&](int nt) {
+      Frag f;
+      f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
+      f.s0 = f.s1 = 0.f;
+      auto row_of = [&](int m) { return r_base + __popc(mk & ((1u << m) - 1u)); };
+      const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
+      if ((mk >> m) & 1u) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(row_of(m)) * p.inter + kb * 128 + t4 * 32);
+        f.b0 = __ldcg(src);
+        f.b1 = __ldcg(src + 1);
+      }
+      if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + row_of(m2) * Kb2 + kb) * row_w[row_of(m2)];
+      if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + row_of(m2 + 1) * Kb2 + kb) * row_w[row_of(m2 + 1)];
+      return f;
+    };
+    // Weight scales of the groups' low and high rows, and the lowest tile's fragment, before the wait.
+    float wlo[kMaxGroups], whi[kMaxGroups];
+#pragma unroll
+    for (int q = 0; q < kMaxGroups; ++q) {
+      wlo[q] = whi[q] = 0.f;
+      if (q < ngroups) {
+        const int64_t row = static_cast<int64_t>(act[a]) * p.dim + d0 + q * 16;
+        wlo[q] = __ldg(p.w2_s + row / 128 * Kb2 + kb);
+        if (d0 + q * 16 + 8 < d1) whi[q] = __ldg(p.w2_s + (row + 8) / 128 * Kb2 + kb);
+      }
+    }
+    Frag f0;
+    if (NT == 1) f0 = frag(0);
+    wait(&full[s], (phase >> s) & 1, abort_flag, p.err);
+    phase ^= 1u << s;
+    __syncwarp();
+    const uint8_t* w = ring + s * p.r2 * 128;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
+      const Frag f = NT == 1 ? f0 : frag(nt);
+#pragma unroll
+      for (int q = 0; q < kMaxGroups; ++q)
+        if (q < ngroups) {
+          // A last group of 8 rows takes them twice; the second copy has scale 0.
+          const uint8_t* lo = w + q * 2048;
+          block_product(lo, d0 + q * 16 + 8 < d1 ? lo + 1024 : lo, f, wlo[q], whi[q], g, t4, acc[q][nt]);
+        }
+    }
+    __syncwarp();
+    if (i + p.slots2 * kWarps < items && !*abort_flag) issue2(i + p.slots2 * kWarps);
+  }
+  __syncthreads();
+  // Every warp's copies have landed and are used: the rings hold the warps'
+  // sums [warp][row][columns] now (a copy still in flight after a wait that
+  // gave up is waited for first).
+  if (*abort_flag) {
+    for (int i = 0; i < kSlots; ++i) wait(&full[i], (phase >> i) & 1, nullptr, p.err);
+    __syncthreads();
+  }
+  float* sums = reinterpret_cast<float*>(smem);
+  const int rows2 = ngroups * 16;
+#pragma unroll
+  for (int q = 0; q < kMaxGroups; ++q)
+    if (q < ngroups)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* t = sums + (warp * rows2 + q * 16 + g) * kCols + nt * 8 + 2 * t4;
+        *reinterpret_cast<float2*>(t) = make_float2(acc[q][nt][0], acc[q][nt][1]);
+        *reinterpret_cast<float2*>(t + 8 * kCols) = make_float2(acc[q][nt][2], acc[q][nt][3]);
+      }
+  __syncthreads();
+  for (int i = tid; i < (d1 - d0) * p.T; i += kThreads) {
+    const int m = i / (d1 - d0), r = i % (d1 - d0);
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += sums[(w * rows2 + r) * kCols + m];
+    p.y[static_cast<size_t>(m) * p.dim + d0 + r] = __float2bfloat16_rn(v);
+  }
   // The last CTA to leave zeroes the counters for the next call.
   if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u) {
     p.counters[0] = p.counters[1] = p.counters[2] = 0;
@@ -632,13 +726,13 @@ EncodeTiledFn layer_map_encoder() {
 }
 
 // An e4m3 weight [N, K] as (128 bytes of a K block, row, K block), read in
-// boxes of 8 rows x kb blocks, 128-byte swizzled; blocks past K read as zeros.
-bool make_weight_map(CUtensorMap* map, const void* w, uint64_t N, uint64_t K, uint32_t kb) {
+// boxes of `rows` x kb blocks, 128-byte swizzled; blocks past K read as zeros.
+bool make_weight_map(CUtensorMap* map, const void* w, uint64_t N, uint64_t K, uint32_t rows, uint32_t kb) {
   EncodeTiledFn enc = layer_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {128, N, K / 128};
   const cuuint64_t strides[2] = {K, 128};
-  const cuuint32_t box[3] = {128, 8, kb};
+  const cuuint32_t box[3] = {128, rows, kb};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -648,7 +742,7 @@ bool make_weight_map(CUtensorMap* map, const void* w, uint64_t N, uint64_t K, ui
 size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 
 struct LayerSizes {
-  size_t logits, xq, xs, u, uq, us, total;
+  size_t logits, xq, xs, u, uq, us, part, total;
 };
 
 LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t topk, int64_t ns) {
@@ -660,7 +754,9 @@ LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t
   z.u = z.xs + align256(static_cast<size_t>(T) * (dim / 128) * 4);
   z.uq = z.u + align256(rows * inter * 4);
   z.us = z.uq + align256(rows * inter);
-  z.total = z.us + align256(rows * (inter / 128) * 4);
+  z.part = z.us + align256(rows * (inter / 128) * 4);
+  const size_t cols = T <= 8 ? 8 : T <= 16 ? 16 : 32;
+  z.total = z.part + static_cast<size_t>(kMaxCtas) * kWarps * 4 * 16 * cols * 4;
   return z;
 }
 
@@ -673,21 +769,17 @@ bool layer_shape_ok(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t to
 template <int NT>
 int layer_launch(const DevInfo* d, const CUtensorMap& m1, const CUtensorMap& m3, const CUtensorMap& m2,
                  const LayerParams& p, cudaStream_t stream) {
-  static_assert(ring_stages(NT) >= 3, "ring depth");
-  constexpr int kSmem = 1024 + ring_stages(NT) * kStageBytes + 2 * part_floats(NT) * 4 + kTables +
-                        (2 * ring_stages(NT) + 1) * 8 + 16;
-  static_assert(kSmem <= kLayerSmemLimit, "shared memory per CTA");
   static bool attr_done[64] = {};
   auto kern = moe_layer_kernel<NT>;
   if (d->device >= 64 || !attr_done[d->device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLayerSmem) != cudaSuccess)
       return FP8BLK_ERR_CUDA;
     if (d->device < 64) attr_done[d->device] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(d->sm_count));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = kLayerSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
@@ -733,7 +825,7 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
   // Phase 2 keeps a CTA's rows of w2 in its accumulators.
-  if ((dim / 8 + d->sm_count - 1) / d->sm_count > 2 * kMaxGroups) return FP8BLK_ERR_SHAPE;
+  if ((dim / 8 + d->sm_count - 1) / d->sm_count > 2 * kMaxGroups || d->sm_count > kMaxCtas) return FP8BLK_ERR_SHAPE;
   LayerParams p{};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.x = static_cast<const __nv_bfloat16*>(x_bf16);
@@ -752,6 +844,7 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.u = reinterpret_cast<float*>(ws + z.u);
   p.uq = ws + z.uq;
   p.us = reinterpret_cast<float*>(ws + z.us);
+  p.part = reinterpret_cast<float*>(ws + z.part);
   p.err = d->err_word;
   p.T = static_cast<int>(T);
   p.dim = static_cast<int>(dim);
@@ -765,16 +858,14 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.normalize = normalize != 0;
   p.ue8m0 = scale_fmt_ue8m0(scale_fmt);
   p.route_scale = route_scale;
-  // Stages of at most 16 K blocks, as even as they divide.
-  const int Kb1 = p.dim / 128, Kb2 = p.inter / 128;
-  p.st1 = (Kb1 + kWarps - 1) / kWarps;
-  p.kb1 = (Kb1 + p.st1 - 1) / p.st1;
-  p.st2 = (Kb2 + kWarps - 1) / kWarps;
-  p.kb2 = (Kb2 + p.st2 - 1) / p.st2;
+  p.r2 = static_cast<int>((dim / 8 + d->sm_count - 1) / d->sm_count) * 8;
+  p.slots2 = kWarpRing / (p.r2 * 128);
+  if (p.slots2 > kSlots) p.slots2 = kSlots;
   const uint64_t K = static_cast<uint64_t>(E + n_shared);
   CUtensorMap m1, m3, m2;
-  if (!make_weight_map(&m1, w1_e4m3, K * inter, dim, p.kb1) || !make_weight_map(&m3, w3_e4m3, K * inter, dim, p.kb1) ||
-      !make_weight_map(&m2, w2_e4m3, K * dim, inter, p.kb2))
+  if (!make_weight_map(&m1, w1_e4m3, K * inter, dim, 8, kChunk) ||
+      !make_weight_map(&m3, w3_e4m3, K * inter, dim, 8, kChunk) ||
+      !make_weight_map(&m2, w2_e4m3, K * dim, inter, static_cast<uint32_t>(p.r2), 1))
     return FP8BLK_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return T <= 8    ? layer_launch<1>(d, m1, m3, m2, p, cs)
