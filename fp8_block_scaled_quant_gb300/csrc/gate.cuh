@@ -11,8 +11,8 @@
 //
 // One warp per token. Lane l holds experts [l V, l V + V) (E = 32 V), so a
 // group is a run of 32 / G whole lanes: group maxima and top-two pairs merge
-// with shuffles inside that run. Each top-k round is a warp argmax over 64-bit
-// keys (order-preserving bits of z, then the complement of the index).
+// with shuffles inside that run. Each top-k round is a warp argmax: the largest
+// order-preserving bits of z, then the lowest index that has them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,19 +21,16 @@
 
 namespace fp8blk {
 
-__device__ __forceinline__ uint64_t gate_key(float z, int e) {
+// Order-preserving bits of a float.
+__device__ __forceinline__ uint32_t gate_order(float z) {
   const uint32_t u = __float_as_uint(z);
-  const uint32_t ord = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  return (static_cast<uint64_t>(ord) << 32) | static_cast<uint32_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ uint64_t warp_max_u64(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = w > v ? w : v;
-  }
-  return v;
+// The index of the largest key over the warp, ties to the lower index.
+__device__ __forceinline__ uint32_t warp_argmax(uint32_t key, uint32_t index) {
+  const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key);
+  return __reduce_min_sync(0xFFFFFFFFu, key == best ? index : 0xFFFFFFFFu);
 }
 
 // The gate of one token, computed by one warp from its logits: lane l holds
@@ -49,7 +46,7 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
   if (sigmoid) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i < v) s[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x[i])));
+      if (i < v) s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-x[i])));
   } else {
     float m = -INFINITY;
 #pragma unroll
@@ -100,27 +97,32 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
     const int g = lane / lpg;
     bool kept = false;
     for (int r = 0; r < TG; ++r) {
-      const uint64_t best = warp_max_u64(kept ? 0ull : gate_key(gscore, g));
-      if (static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best)) == g) kept = true;
+      if (warp_argmax(kept ? 0u : gate_order(gscore), kept ? 0xFFFFFFFFu : static_cast<uint32_t>(g)) ==
+          static_cast<uint32_t>(g))
+        kept = true;
     }
     eligible = kept;
   }
 
-  // Top-k experts among the eligible lanes' z.
+  // Top-k experts among the eligible lanes' z: each lane offers its largest, the
+  // lane that wins looks for its next.
   uint32_t taken = 0;
   int my_idx = 0;
   float my_s = 0.0f, sum = 0.0f;
+#pragma unroll 1
   for (int j = 0; j < K; ++j) {
-    uint64_t key = 0;
+    uint32_t key = 0, index = 0xFFFFFFFFu;
     if (eligible) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint64_t k = i >= v || ((taken >> i) & 1u) ? 0ull : gate_key(z[i], lane * v + i);
-        key = k > key ? k : key;
+        const uint32_t k = gate_order(z[i]);
+        if (i < v && !((taken >> i) & 1u) && (index == 0xFFFFFFFFu || k > key)) {
+          key = k;
+          index = static_cast<uint32_t>(lane * v + i);
+        }
       }
     }
-    key = warp_max_u64(key);
-    const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    const int e = static_cast<int>(warp_argmax(key, index));
     const int owner = e / v;
     float se = 0.0f;
 #pragma unroll

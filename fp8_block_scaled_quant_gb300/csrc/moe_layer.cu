@@ -85,6 +85,7 @@ constexpr int kWarpRing = 12288;                          // a warp's weight til
 constexpr int kSlots = 3;                                 // at most
 constexpr int kChunk = 2;                                 // K blocks of a phase-1 slot
 constexpr int kSlot1 = kChunk * 2 * 1024;                 // 8 rows of w1 and of w3
+constexpr int kGateVecs = 4;                              // 16-byte vectors of a gate row per thread
 
 // Shared memory: rings, barriers, then the routing tables.
 constexpr int kOffBar = kWarps * kWarpRing;
@@ -280,30 +281,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) *abort_flag = 0;
   __syncwarp();
 
+  // The gate rows of this CTA's experts, asked for before the weight stream
+  // fills the memory's queues. The experts share the warps, each with a slice of
+  // K: warp's vectors v0, v0 + step, ... of its expert's row.
+  const int per_cta = min((p.E + G - 1) / G, kWarps);  // experts at a time
+  const int wpe = kWarps / per_cta;                    // warps of an expert
+  const int v0 = warp % wpe * 32 + lane, step = wpe * 32, vecs = p.dim / 8;
+  uint4 gate_row[kGateVecs];
+  auto load_gate = [&](int e) {
+#pragma unroll
+    for (int i = 0; i < kGateVecs; ++i)
+      gate_row[i] = e < p.E && warp < per_cta * wpe && v0 + i * step < vecs
+                        ? __ldg(reinterpret_cast<const uint4*>(p.gate_w + static_cast<size_t>(e) * p.dim) + v0 + i * step)
+                        : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load_gate(c + warp / wpe * G);
+
   // This warp's phase-1 slots: first of the shared units, then of the routed
-  // ones, each a range of chunks of the CTA's units.
+  // ones, each a range of chunks of the CTA's units. A cursor walks a range.
+  struct Cursor {
+    int a, rb, ck, left;  // active expert, its 8-row block, chunk of K; chunks left
+  };
+  auto cursor = [&](int first, int u0, int q0, int q1) {
+    const int u = u0 + q0 / chunks;
+    return Cursor{first + u / upe, u % upe, q0 % chunks, q1 - q0};
+  };
+  auto advance = [&](Cursor& k, int n) {
+    k.left -= n;
+    k.ck += n;
+    if (k.ck == chunks) {
+      k.ck = 0;
+      if (++k.rb == upe) {
+        k.rb = 0;
+        ++k.a;
+      }
+    }
+  };
   const int us0 = even(p.ns * upe, c, G), us1 = even(p.ns * upe, c + 1, G);
   const int sq0 = even((us1 - us0) * chunks, warp, kWarps), sq1 = even((us1 - us0) * chunks, warp + 1, kWarps);
-  int ur0 = 0, ur1 = 0, rq0 = 0, rq1 = 0;  // routed: known after the gate
   const uint64_t policy = l2_policy_evict_first();  // weights are read once
-  auto issue1 = [&](int q) {  // slot q of this warp
-    const bool shared = q < sq1 - sq0;
-    const int at = shared ? sq0 + q : rq0 + q - (sq1 - sq0);
-    const int u = (shared ? us0 : ur0) + at / chunks;
-    const int e = shared ? p.E + u / upe : act[p.ns + u / upe];
+  int put = 0;                                      // the slot that the next copy goes to
+  Cursor ahead = cursor(0, us0, sq0, sq1);          // of the copies
+  auto issue1 = [&] {
     if (elect_one_sync()) {
-      const int y = e * p.inter + u % upe * 8, z = at % chunks * kChunk;
-      uint64_t* bar = &full[q % kSlots];
-      uint8_t* dst = ring + q % kSlots * kSlot1;
-      mbar_arrive_expect_tx(bar, kSlot1);
-      tma_load_3d_hint(dst, &map1, bar, 0, y, z, policy);
-      tma_load_3d_hint(dst + kSlot1 / 2, &map3, bar, 0, y, z, policy);
+      const int y = (ahead.a < p.ns ? p.E + ahead.a : act[ahead.a]) * p.inter + ahead.rb * 8, z = ahead.ck * kChunk;
+      uint8_t* dst = ring + put * kSlot1;
+      mbar_arrive_expect_tx(&full[put], kSlot1);
+      tma_load_3d_hint(dst, &map1, &full[put], 0, y, z, policy);
+      tma_load_3d_hint(dst + kSlot1 / 2, &map3, &full[put], 0, y, z, policy);
     }
     __syncwarp();
+    put = put + 1 == kSlots ? 0 : put + 1;
+    advance(ahead, 1);
   };
-  const int early = min(kSlots, sq1 - sq0);
 #pragma unroll 1
-  for (int q = 0; q < early; ++q) issue1(q);
+  for (int q = 0; q < kSlots && ahead.left > 0; ++q) issue1();
 
   // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
   auto grid_barrier = [&](int i) {
@@ -341,44 +373,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
   }
   {
-    const int per_cta = min((p.E + G - 1) / G, kWarps);  // experts at a time
-    const int wpe = kWarps / per_cta;                    // warps of an expert
-    float* sums = sel_w;                                 // [warp][columns]
+    float* sums = sel_w;  // [warp][columns]
 #pragma unroll 1
     for (int e0 = c; e0 < p.E; e0 += per_cta * G) {
-      const int e = e0 + warp / wpe * G;
       float acc[kCols];
 #pragma unroll
       for (int m = 0; m < kCols; ++m) acc[m] = 0.f;
-      if (warp < per_cta * wpe && e < p.E) {
-        const uint4* wv = reinterpret_cast<const uint4*>(p.gate_w + static_cast<size_t>(e) * p.dim);
-        const int n = p.dim / 8, step = wpe * 32;
-        // Two vectors of the gate row a pass, their loads and x's in flight together.
-#pragma unroll 1
-        for (int v = warp % wpe * 32 + lane; v < n; v += 2 * step) {
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          const uint4 a[2] = {__ldg(wv + v), v + step < n ? __ldg(wv + v + step) : zero};
-#pragma unroll
-          for (int m = 0; m < kCols; ++m) {
-            if (m < p.T) {
-              const uint4* xv = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim);
-              const uint4 b[2] = {__ldg(xv + v), v + step < n ? __ldg(xv + v + step) : zero};
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t aw[4] = {a[h].x, a[h].y, a[h].z, a[h].w}, bw[4] = {b[h].x, b[h].y, b[h].z, b[h].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
-                  acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
-                }
-              }
-            }
-          }
-        }
-      }
+      // (The row's K is at most kGateVecs passes, see kMaxDim.)
 #pragma unroll
       for (int m = 0; m < kCols; ++m) {
         if (m < p.T) {
+          const uint4* xv = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim) + v0;
+#pragma unroll
+          for (int i = 0; i < kGateVecs; ++i)
+            if (v0 + i * step < vecs) {
+              const uint4 b = __ldg(xv + i * step);
+              const uint32_t aw[4] = {gate_row[i].x, gate_row[i].y, gate_row[i].z, gate_row[i].w};
+              const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
+                acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
+              }
+            }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
           if (lane == 0) sums[warp * kCols + m] = acc[m];
@@ -392,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (e0 + k * G < p.E) p.logits[static_cast<size_t>(m) * p.E + e0 + k * G] = v;
       }
       __syncthreads();
+      if (e0 + per_cta * G < p.E) load_gate(e0 + per_cta * G + warp / wpe * G);
     }
   }
   grid_barrier(0);
@@ -456,117 +474,135 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int nact = scan[32], nrows = scan[33];
-  {
-    const int n = (nact - p.ns) * upe;
-    ur0 = routed_start(p.ns * upe, n, c, G);
-    ur1 = routed_start(p.ns * upe, n, c + 1, G);
-    rq0 = even((ur1 - ur0) * chunks, warp, kWarps);
-    rq1 = even((ur1 - ur0) * chunks, warp + 1, kWarps);
-  }
-  const int nq = (sq1 - sq0) + (rq1 - rq0);
+  const int routed_units = (nact - p.ns) * upe;
+  const int ur0 = routed_start(p.ns * upe, routed_units, c, G), ur1 = routed_start(p.ns * upe, routed_units, c + 1, G);
+  const int rq0 = even((ur1 - ur0) * chunks, warp, kWarps), rq1 = even((ur1 - ur0) * chunks, warp + 1, kWarps);
+  bool ahead_routed = false;
+  auto issue_next = [&] {  // the next copy, if any: the shared range's, then the routed one's
+    if (ahead.left == 0 && !ahead_routed) {
+      ahead = cursor(p.ns, ur0, rq0, rq1);
+      ahead_routed = true;
+    }
+    if (ahead.left > 0 && !*abort_flag) issue1();
+  };
 #pragma unroll 1
-  for (int q = early; q < min(kSlots, nq); ++q) issue1(q);
+  for (int q = min(kSlots, sq1 - sq0); q < kSlots; ++q) issue_next();
 
   // Phase 1: u = silu(w1 x) (w3 x).
-  auto count_of = [&](int a) { return __popc(mask[a]); };
-  auto store_u = [&](int a, int u, int col, int r, float h1, float h3) {
-    p.u[static_cast<size_t>(base[a] + col) * p.inter + u % upe * 8 + r] = silu_mul(h1, h3);
+  auto store_u = [&](int a, int rb, int cnt, int nt, const float (&v)[4]) {
+    // Lane (g, t4) has columns 2 t4, 2 t4 + 1 of row g: h1 and h3.
+    const int col = nt * 8 + 2 * t4;
+    float* dst = p.u + static_cast<size_t>(base[a] + col) * p.inter + rb * 8 + g;
+    if (col < cnt) dst[0] = silu_mul(v[0], v[2]);
+    if (col + 1 < cnt) dst[p.inter] = silu_mul(v[1], v[3]);
   };
-  float* my_part = p.part + (static_cast<size_t>(c) * kWarps + warp) * 4 * kTile;
-  {
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-    int first = 0;  // the slot of this unit's first chunk here
+  int take = 0;  // the slot that is multiplied next
 #pragma unroll 1
-    for (int q = 0; q < nq; ++q) {
-      const bool shared = q < sq1 - sq0;
-      const int at = shared ? sq0 + q : rq0 + q - (sq1 - sq0);
-      const int u = (shared ? us0 : ur0) + at / chunks, ck = at % chunks;
-      const int a = (shared ? 0 : p.ns) + u / upe;
-      const int cnt = count_of(a), r_base = base[a];
-      const size_t srow = static_cast<size_t>((static_cast<int64_t>(act[a]) * p.inter + u % upe * 8) / 128) * Kb1;
-      const int s = q % kSlots;
-      const uint8_t* w = ring + s * kSlot1;
-      // The first column tile's fragments are asked for before the wait.
-      auto frag = [&](int nt, int kb) {
-        Frag f;
-        const int col = nt * 8 + g, c2 = nt * 8 + 2 * t4;
-        f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
-        f.s0 = f.s1 = 0.f;
-        if (col < cnt) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.xq + static_cast<size_t>(row_t[r_base + col]) * p.dim +
-                                                            kb * 128 + t4 * 32);
-          f.b0 = __ldcg(src);
-          f.b1 = __ldcg(src + 1);
-        }
-        if (c2 < cnt) f.s0 = __ldcg(p.xs + row_t[r_base + c2] * Kb1 + kb);
-        if (c2 + 1 < cnt) f.s1 = __ldcg(p.xs + row_t[r_base + c2 + 1] * Kb1 + kb);
-        return f;
-      };
-      Frag f[kChunk];
-      float wlo[kChunk], whi[kChunk];
+  for (int range = 0; range < 2; ++range) {
+    Cursor at = range ? cursor(p.ns, ur0, rq0, rq1) : cursor(0, us0, sq0, sq1);
+#pragma unroll 1
+    while (at.left > 0) {
+      // One unit, or the part of it that falls to this warp.
+      const int n = min(at.left, chunks - at.ck);
+      const int cnt = __popc(mask[at.a]), rows0 = base[at.a];
+      const float* s1 = p.w1_s + static_cast<size_t>((act[at.a] * upe + at.rb) / 16) * Kb1;
+      const float* s3 = p.w3_s + (s1 - p.w1_s);
+      // Column tile 0's tokens: this lane's operand row and the two columns it scales.
+      const bool c0 = g < cnt, c1 = 2 * t4 < cnt, c2 = 2 * t4 + 1 < cnt;
+      const uint8_t* x0 = p.xq + static_cast<size_t>(c0 ? row_t[rows0 + g] : 0) * p.dim + t4 * 32;
+      const float* xs1 = p.xs + (c1 ? row_t[rows0 + 2 * t4] : 0) * Kb1;
+      const float* xs2 = p.xs + (c2 ? row_t[rows0 + 2 * t4 + 1] : 0) * Kb1;
+      float acc[NT][4];
 #pragma unroll
-      for (int h = 0; h < kChunk; ++h) {
-        const int kb = min(ck * kChunk + h, Kb1 - 1);  // past K: the weights are zeros
-        f[h] = frag(0, kb);
-        wlo[h] = __ldg(p.w1_s + srow + kb);
-        whi[h] = __ldg(p.w3_s + srow + kb);
-      }
-      wait(&full[s], (phase >> s) & 1, abort_flag, p.err);
-      phase ^= 1u << s;
-      __syncwarp();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt * 8 >= cnt) break;
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int kb0 = (at.ck + j) * kChunk;
+        Frag f[kChunk];
+        float wlo[kChunk], whi[kChunk];
 #pragma unroll
         for (int h = 0; h < kChunk; ++h) {
-          const Frag x = nt == 0 ? f[h] : frag(nt, min(ck * kChunk + h, Kb1 - 1));
-          block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, x, wlo[h], whi[h], g, t4, acc[nt]);
+          const int kb = min(kb0 + h, Kb1 - 1);  // past K: the weights are zeros
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          f[h].b0 = c0 ? __ldcg(reinterpret_cast<const uint4*>(x0 + kb * 128)) : zero;
+          f[h].b1 = c0 ? __ldcg(reinterpret_cast<const uint4*>(x0 + kb * 128) + 1) : zero;
+          f[h].s0 = c1 ? __ldcg(xs1 + kb) : 0.f;
+          f[h].s1 = c2 ? __ldcg(xs2 + kb) : 0.f;
+          wlo[h] = __ldg(s1 + kb);
+          whi[h] = __ldg(s3 + kb);
         }
-      }
-      __syncwarp();
-      if (q + kSlots < nq && !*abort_flag) issue1(q + kSlots);
-      const bool last = q + 1 == nq || q + 1 == sq1 - sq0;  // of the shared or of the routed range
-      if (ck + 1 == chunks || last) {
-        const int ck0 = ck - (q - first);
-        if (ck0 == 0 && ck + 1 == chunks) {
-          // The whole unit: lane (g, t4) has columns 2 t4, 2 t4 + 1 of row g, h1 and h3.
+        const uint8_t* w = ring + take * kSlot1;
+        wait(&full[take], (phase >> take) & 1, abort_flag, p.err);
+        phase ^= 1u << take;
+        take = take + 1 == kSlots ? 0 : take + 1;
+        __syncwarp();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + 2 * t4;
-            if (col < cnt) store_u(a, u, col, g, acc[nt][0], acc[nt][2]);
-            if (col + 1 < cnt) store_u(a, u, col + 1, g, acc[nt][1], acc[nt][3]);
+        for (int h = 0; h < kChunk; ++h)
+          block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, f[h], wlo[h], whi[h], g, t4, acc[0]);
+#pragma unroll
+        for (int nt = 1; nt < NT; ++nt) {
+          if (nt * 8 >= cnt) break;
+#pragma unroll
+          for (int h = 0; h < kChunk; ++h) {
+            const int kb = min(kb0 + h, Kb1 - 1), col = nt * 8 + g, cs = nt * 8 + 2 * t4;
+            Frag x;
+            x.b0 = x.b1 = make_uint4(0u, 0u, 0u, 0u);
+            if (col < cnt) {
+              const uint4* src = reinterpret_cast<const uint4*>(p.xq + static_cast<size_t>(row_t[rows0 + col]) * p.dim +
+                                                                kb * 128 + t4 * 32);
+              x.b0 = __ldcg(src);
+              x.b1 = __ldcg(src + 1);
+            }
+            x.s0 = cs < cnt ? __ldcg(p.xs + row_t[rows0 + cs] * Kb1 + kb) : 0.f;
+            x.s1 = cs + 1 < cnt ? __ldcg(p.xs + row_t[rows0 + cs + 1] * Kb1 + kb) : 0.f;
+            block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, x, wlo[h], whi[h], g, t4, acc[nt]);
           }
-        } else {
-          float* t = my_part + ((shared ? 0 : 2) + (ck0 == 0 ? 1 : 0)) * kTile;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (nt * 8 < cnt)
-              *reinterpret_cast<float4*>(t + (nt * 32 + lane) * 4) =
-                  make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        first = q + 1;
+        __syncwarp();
+        issue_next();
       }
+      if (n == chunks) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (nt * 8 < cnt) store_u(at.a, at.rb, cnt, nt, acc[nt]);
+      } else {  // sums of a cut unit: [range][it starts here]
+        float4* t = reinterpret_cast<float4*>(p.part + ((static_cast<size_t>(c) * kWarps + warp) * 4 + range * 2 +
+                                                        (at.ck == 0 ? 1 : 0)) * kTile) + lane;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (nt * 8 < cnt) t[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+      }
+      advance(at, n);
     }
   }
 
-  // The first w2 tiles: item i is K block i % Kb2 of active expert i / Kb2.
-  const int items = nact * Kb2;
-  auto issue2 = [&](int i) {
-    const int n = (i - warp) / kWarps, s = n % p.slots2;
+  // The first w2 tiles. Item i is K block i % Kb2 of active expert i / Kb2; this
+  // warp has items warp, warp + 16, ...
+  struct Item {
+    int a, kb;
+  };
+  auto next_item = [&](Item& k) {
+    k.kb += kWarps;
+    while (k.kb >= Kb2) {
+      k.kb -= Kb2;
+      ++k.a;
+    }
+  };
+  Item item_ahead{warp / Kb2, warp % Kb2};
+  put = 0;
+  auto issue2 = [&] {
+    if (item_ahead.a >= nact || *abort_flag) return;
     if (elect_one_sync()) {
-      uint64_t* bar = &full[s];
-      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.r2) * 128);
-      tma_load_3d_hint(ring + s * p.r2 * 128, &map2, bar, 0, act[i / Kb2] * p.dim + d0, i % Kb2, policy);
+      mbar_arrive_expect_tx(&full[put], static_cast<uint32_t>(p.r2) * 128);
+      tma_load_3d_hint(ring + put * p.r2 * 128, &map2, &full[put], 0, act[item_ahead.a] * p.dim + d0, item_ahead.kb,
+                       policy);
     }
     __syncwarp();
+    put = put + 1 == p.slots2 ? 0 : put + 1;
+    next_item(item_ahead);
   };
-  if (!*abort_flag)
 #pragma unroll 1
-    for (int n = 0; n < p.slots2 && warp + n * kWarps < items; ++n) issue2(warp + n * kWarps);
+  for (int q = 0; q < p.slots2; ++q) issue2();
 
   // Units cut between warps: warp w adds up units w, w + 16, ... of the CTA.
   __syncthreads();
@@ -579,28 +615,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int w0 = ((k * chunks + 1) * kWarps - 1) / total;
       const int w1 = ((k + 1) * chunks * kWarps - 1) / total;
       if (w0 == w1) continue;
-      const int u = u0 + k, a = (range ? p.ns : 0) + u / upe, cnt = count_of(a);
+      const int u = u0 + k, a = (range ? p.ns : 0) + u / upe, cnt = __popc(mask[a]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (nt * 8 >= cnt) break;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int w = w0; w <= w1; ++w) {
           const int from = even(total, w, kWarps);
           if (from == even(total, w + 1, kWarps)) continue;  // fewer chunks than warps: this one has none
-          const bool starts = from <= k * chunks;
           const float4 x = __ldcg(reinterpret_cast<const float4*>(
-                                      p.part + ((static_cast<size_t>(c) * kWarps + w) * 4 + range * 2 + (starts ? 1 : 0)) *
-                                                   kTile) +
+                                      p.part + ((static_cast<size_t>(c) * kWarps + w) * 4 + range * 2 +
+                                                (from <= k * chunks ? 1 : 0)) * kTile) +
                                   nt * 32 + lane);
-          v.x += x.x;
-          v.y += x.y;
-          v.z += x.z;
-          v.w += x.w;
+          v[0] += x.x;
+          v[1] += x.y;
+          v[2] += x.z;
+          v[3] += x.w;
         }
-        const int col = nt * 8 + 2 * t4;
-        if (col < cnt) store_u(a, u, col, g, v.x, v.z);
-        if (col + 1 < cnt) store_u(a, u, col + 1, g, v.y, v.w);
+        store_u(a, u % upe, cnt, nt, v);
       }
     }
   }
@@ -620,45 +653,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int q = 0; q < kMaxGroups; ++q)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
-  int n2 = 0;
+  // Weight-scale rows of the groups' low and high halves within an expert.
+  int slo[kMaxGroups], shi[kMaxGroups];
+#pragma unroll
+  for (int q = 0; q < kMaxGroups; ++q) {
+    slo[q] = (d0 + q * 16) / 128 * Kb2;
+    shi[q] = (d0 + q * 16 + 8) / 128 * Kb2;
+  }
+  const bool odd = ((d1 - d0) & 8) != 0;  // the last group has no high half
+  take = 0;
 #pragma unroll 1
-  for (int i = warp; i < items; i += kWarps, ++n2) {
-    const int a = i / Kb2, kb = i % Kb2, s = n2 % p.slots2;
+  for (Item it{warp / Kb2, warp % Kb2}; it.a < nact; next_item(it)) {
+    const int a = it.a, kb = it.kb;
     const uint32_t mk = mask[a];
     const int r_base = base[a];
+    const float* ws = p.w2_s + static_cast<size_t>(act[a]) * (p.dim / 128) * Kb2 + kb;
     auto frag = [&](int nt) {
       Frag f;
       f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
       f.s0 = f.s1 = 0.f;
-      auto row_of = [&](int m) { return r_base + __popc(mk & ((1u << m) - 1u)); };
       const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
+      const int r = r_base + __popc(mk & ((1u << m) - 1u)), r2 = r_base + __popc(mk & ((1u << m2) - 1u));
       if ((mk >> m) & 1u) {
-        const uint4* src =
-            reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(row_of(m)) * p.inter + kb * 128 + t4 * 32);
+        const uint4* src = reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(r) * p.inter + kb * 128 + t4 * 32);
         f.b0 = __ldcg(src);
         f.b1 = __ldcg(src + 1);
       }
-      if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + row_of(m2) * Kb2 + kb) * row_w[row_of(m2)];
-      if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + row_of(m2 + 1) * Kb2 + kb) * row_w[row_of(m2 + 1)];
+      const int r3 = r2 + ((mk >> m2) & 1u);
+      if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + r2 * Kb2 + kb) * row_w[r2];
+      if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + r3 * Kb2 + kb) * row_w[r3];
       return f;
     };
-    // Weight scales of the groups' low and high rows, and the lowest tile's fragment, before the wait.
     float wlo[kMaxGroups], whi[kMaxGroups];
 #pragma unroll
     for (int q = 0; q < kMaxGroups; ++q) {
-      wlo[q] = whi[q] = 0.f;
-      if (q < ngroups) {
-        const int64_t row = static_cast<int64_t>(act[a]) * p.dim + d0 + q * 16;
-        wlo[q] = __ldg(p.w2_s + row / 128 * Kb2 + kb);
-        if (d0 + q * 16 + 8 < d1) whi[q] = __ldg(p.w2_s + (row + 8) / 128 * Kb2 + kb);
-      }
+      wlo[q] = q < ngroups ? __ldg(ws + slo[q]) : 0.f;
+      whi[q] = q < ngroups && !(odd && q == ngroups - 1) ? __ldg(ws + shi[q]) : 0.f;
     }
     Frag f0;
     if (NT == 1) f0 = frag(0);
-    wait(&full[s], (phase >> s) & 1, abort_flag, p.err);
-    phase ^= 1u << s;
+    const uint8_t* w = ring + take * p.r2 * 128;
+    wait(&full[take], (phase >> take) & 1, abort_flag, p.err);
+    phase ^= 1u << take;
+    take = take + 1 == p.slots2 ? 0 : take + 1;
     __syncwarp();
-    const uint8_t* w = ring + s * p.r2 * 128;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
@@ -668,11 +706,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q < ngroups) {
           // A last group of 8 rows takes them twice; the second copy has scale 0.
           const uint8_t* lo = w + q * 2048;
-          block_product(lo, d0 + q * 16 + 8 < d1 ? lo + 1024 : lo, f, wlo[q], whi[q], g, t4, acc[q][nt]);
+          block_product(lo, odd && q == ngroups - 1 ? lo : lo + 1024, f, wlo[q], whi[q], g, t4, acc[q][nt]);
         }
     }
     __syncwarp();
-    if (i + p.slots2 * kWarps < items && !*abort_flag) issue2(i + p.slots2 * kWarps);
+    issue2();
   }
   __syncthreads();
   // Every warp's copies have landed and are used: the rings hold the warps'
@@ -826,6 +864,9 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   if (int st = current_device(&d)) return st;
   // Phase 2 keeps a CTA's rows of w2 in its accumulators.
   if ((dim / 8 + d->sm_count - 1) / d->sm_count > 2 * kMaxGroups || d->sm_count > kMaxCtas) return FP8BLK_ERR_SHAPE;
+  // The gate product keeps its share of an expert's row in registers.
+  const int64_t per_cta = (E + d->sm_count - 1) / d->sm_count;
+  if (per_cta > kWarps || dim / 8 > kWarps / per_cta * 32 * kGateVecs) return FP8BLK_ERR_SHAPE;
   LayerParams p{};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.x = static_cast<const __nv_bfloat16*>(x_bf16);
