@@ -27,10 +27,10 @@ __device__ __forceinline__ uint32_t gate_order(float z) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The index of the largest key over the warp, ties to the lower index.
-__device__ __forceinline__ uint32_t warp_argmax(uint32_t key, uint32_t index) {
+// The lowest lane that has the warp's largest key.
+__device__ __forceinline__ int warp_argmax_lane(uint32_t key) {
   const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key);
-  return __reduce_min_sync(0xFFFFFFFFu, key == best ? index : 0xFFFFFFFFu);
+  return __ffs(__ballot_sync(0xFFFFFFFFu, key == best)) - 1;
 }
 
 // The gate of one token, computed by one warp from its logits: lane l holds
@@ -97,41 +97,47 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
     const int g = lane / lpg;
     bool kept = false;
     for (int r = 0; r < TG; ++r) {
-      if (warp_argmax(kept ? 0u : gate_order(gscore), kept ? 0xFFFFFFFFu : static_cast<uint32_t>(g)) ==
-          static_cast<uint32_t>(g))
-        kept = true;
+      // A group's lanes agree, and lanes are in group order: ties go to the lower.
+      if (warp_argmax_lane(kept ? 0u : gate_order(gscore)) / lpg == g) kept = true;
     }
     eligible = kept;
   }
 
-  // Top-k experts among the eligible lanes' z: each lane offers its largest, the
-  // lane that wins looks for its next.
-  uint32_t taken = 0;
+  // Top-k experts among the eligible lanes' z: each lane offers its largest (a
+  // tree over its keys), the lane whose offer wins takes it out.
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = i < v && eligible ? gate_order(z[i]) : 0u;
   int my_idx = 0;
   float my_s = 0.0f, sum = 0.0f;
 #pragma unroll 1
   for (int j = 0; j < K; ++j) {
-    uint32_t key = 0, index = 0xFFFFFFFFu;
-    if (eligible) {
+    uint32_t k[V];
+    int at[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t k = gate_order(z[i]);
-        if (i < v && !((taken >> i) & 1u) && (index == 0xFFFFFFFFu || k > key)) {
-          key = k;
-          index = static_cast<uint32_t>(lane * v + i);
-        }
-      }
+    for (int i = 0; i < V; ++i) {
+      k[i] = key[i];
+      at[i] = i;
     }
-    const int e = static_cast<int>(warp_argmax(key, index));
-    const int owner = e / v;
+#pragma unroll
+    for (int w = 1; w < V; w *= 2)
+#pragma unroll
+      for (int i = 0; i + w < V; i += 2 * w)
+        if (k[i + w] > k[i]) {
+          k[i] = k[i + w];
+          at[i] = at[i + w];
+        }
+    // Lanes are in expert order: ties go to the lower expert.
+    const int owner = warp_argmax_lane(k[0]);
     float se = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane == owner && i < v && e - lane * v == i) {
+      if (lane == owner && at[0] == i) {
         se = s[i];
-        taken |= 1u << i;
+        key[i] = 0u;
       }
     se = __shfl_sync(0xFFFFFFFFu, se, owner);
+    const int e = __shfl_sync(0xFFFFFFFFu, lane * v + at[0], owner);
     sum = __fadd_rn(sum, se);
     if (lane == j) {
       my_idx = e;

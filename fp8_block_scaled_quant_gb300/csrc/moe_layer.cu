@@ -17,22 +17,26 @@
 // floor is those bytes at HBM rate. The kernel is built to keep that stream
 // from stopping:
 //   - One CTA per SM, one launch (cooperative: CTAs meet at three barriers).
-//     Each of the CTA's sixteen warps owns 12 KB of shared memory and streams
-//     and multiplies its own share of the weights: nothing but the phases'
-//     ends makes warps wait for one another, so one warp's latencies hide
-//     behind fifteen others. (A producer warp with stages that all sixteen
-//     warps multiplied together, then met to add up, ran at 3.9 TB/s.)
+//     Each of the CTA's sixteen warps owns 12.5 KB of shared memory and streams
+//     and multiplies its own share of the weights, 2 KB (16 rows of a K block)
+//     at a time, three such slots in flight (cp.async), the tokens' codes and all
+//     scales in the slot beside them: nothing but the phases' ends makes warps
+//     wait for one another, so one warp's latencies hide behind fifteen others.
+//     (Stages that all warps multiplied together ran at 3.9 TB/s; the same slots
+//     by TMA cost a warp 400 cycles a copy to issue; operands by plain loads wait
+//     behind the stream, 20 us of 100 for one token.)
 //   - The gate decides what the routed weights are, but not the shared ones:
-//     every warp asks for its share of the shared experts first, then x is
-//     quantised and the gate computed.
-//   - w2 does not depend on u, only its use does: a warp that is done with
-//     its part of phase 1 asks for its first w2 tiles before the barriers.
-//   - Phase 1 splits (expert, 8 rows of w1 and the same 8 of w3) evenly over
-//     the CTAs, and a CTA's units, K laid end to end, evenly over its warps; a
-//     unit cut between warps is added up in warp order. Phase 2 gives each CTA
-//     the same rows of every expert's w2, and its (expert, K block) pairs round
-//     robin to the warps: the sum over experts stays in registers. No atomics
-//     on values, one order of every sum.
+//     every warp asks for its share of the shared experts as soon as the gate's
+//     operands are here, and the gate is computed meanwhile.
+//   - w2 does not depend on u, only its use does: a warp's slots run on from
+//     its part of phase 1 into w2 before the barriers between them.
+//   - Phase 1 lays its units (expert, 8 rows of w1 and the same 8 of w3) end to
+//     end, K block by K block, and gives every warp of the GPU the same number
+//     of K blocks; the parts of a unit cut between warps are added in warp order
+//     where u is quantised. Phase 2 gives each CTA the same rows of every
+//     expert's w2, and its (expert, K block) pairs round robin to the warps: the
+//     sum over experts stays in registers. No atomics on values, one order of
+//     every sum.
 //
 // The products are warp-level FP8 MMAs (m16n8k32): tokens are the 8 columns,
 // so one MMA serves up to 8 tokens at the cost of one. In phase 1 rows 0-7 of
@@ -51,13 +55,10 @@
 //
 // Every wait is bounded (2 s): on expiry an error bit is set, waits return at
 // once from then on, and the control flow, whose loops are finite, runs out.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <mutex>
 
 #include "block_rule.cuh"
 #include "fp8blk.h"
@@ -81,15 +82,15 @@ constexpr int kMaxCtas = 192;                             // SMs a device may ha
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroups = 4;                             // 16-row groups of w2 per CTA
 constexpr int kMaxDim = 8192, kMaxInter = 16384;
-constexpr int kWarpRing = 12288;                          // a warp's weight tiles
-constexpr int kSlots = 3;                                 // at most
-constexpr int kChunk = 2;                                 // K blocks of a phase-1 slot
-constexpr int kSlot1 = kChunk * 2 * 1024;                 // 8 rows of w1 and of w3
+constexpr int kSlots = 4;                                 // slots of a warp
+constexpr int kOffTok = 2048;                             // after 16 weight rows x 128 bytes: 8 tokens' codes
+constexpr int kOffScl = 3072;                             // 8 token scales, 2 weight scales
+constexpr int kSlot = 3200;
+constexpr int kWarpRing = kSlots * kSlot;
 constexpr int kGateVecs = 4;                              // 16-byte vectors of a gate row per thread
 
-// Shared memory: rings, barriers, then the routing tables.
-constexpr int kOffBar = kWarps * kWarpRing;
-constexpr int kOffAct = kOffBar + kWarps * kSlots * 8 + 16;
+// Shared memory: the rings, then the routing tables.
+constexpr int kOffAct = kWarps * kWarpRing + 16;
 constexpr int kOffMask = kOffAct + kMaxActive * 4;
 constexpr int kOffBase = kOffMask + kMaxActive * 4;
 constexpr int kOffRowW = kOffBase + (kMaxActive + 1) * 4;
@@ -116,22 +117,33 @@ struct LayerParams {
   float* u;           // [rows][inter]
   uint8_t* uq;        // [rows][inter]
   float* us;          // [rows][inter / 128]
-  float* part;        // [CTA][warp][4][16 rows x columns] sums of units cut between warps
+  float* part;        // [warp of the grid][range][it starts the unit][16 rows x columns]: sums of cut units
   unsigned* err;
   int T, dim, inter, E, ns, k, groups, kept, sigmoid, normalize, ue8m0;
   float route_scale;
-  int r2, slots2;  // rows of w2 per CTA at most, ring slots of that size
+  const uint8_t* w1;  // weights
+  const uint8_t* w3;
+  const uint8_t* w2;
 };
 
 constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
 
-__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
+// 16 bytes from global to shared memory, past the L1 cache.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_plain(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but this thread's `N` latest groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // d += A (16 x 32, rows) * B (32 x 8, columns), e4m3 operands, fp32 accumulators.
@@ -141,29 +153,6 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The bounded wait, its slow part out of line (the loops that call it stay
-// small enough for the instruction cache).
-__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* err) {
-  const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((i & 63u) == 0) {
-      if (abort && *abort) return;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        if (abort) *abort = 1;
-        atomicOr(err, kDevErrTimeoutLayer);
-        return;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
-  const uint32_t a = smem_u32(bar);
-  if (!mbar_try_wait(a, parity)) wait_slow(a, parity, abort, err);
 }
 
 // Quantises one 128-element block, four elements per lane; lane 0 stores the scale.
@@ -184,11 +173,9 @@ __device__ __forceinline__ int even(int n, int c, int G) {
   return static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint32_t>(c) / static_cast<uint32_t>(G));
 }
 
-// First routed unit of CTA c, such that shared and routed units together are
-// split evenly (`us` shared units are split evenly by themselves).
-__device__ __forceinline__ int routed_start(int us, int ur, int c, int G) {
-  if (ur < 2 * G) return even(ur, c, G);
-  return even(us + ur, c, G) - even(us, c, G);
+// The same for large n (a K block count times a warp index).
+__device__ __forceinline__ int even_wide(int n, int c, int G) {
+  return static_cast<int>(static_cast<int64_t>(n) * c / G);
 }
 
 // The B fragment of one K block for 8 columns and the columns' scales.
@@ -245,13 +232,12 @@ __device__ __noinline__ void gate_of_token(const LayerParams& p, int m, int lane
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    moe_layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map3,
-                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ LayerParams p) {
+    moe_layer_kernel(const __grid_constant__ LayerParams p) {
   constexpr int kCols = 8 * NT;
   constexpr int kTile = 16 * kCols;  // sums of a 16-row tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffBar + kWarps * kSlots * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kWarps * kWarpRing);
   int* act = reinterpret_cast<int*>(smem + kOffAct);             // active experts, shared ones first
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kOffMask);  // tokens; by expert id until sorted
   int* base = reinterpret_cast<int*>(smem + kOffBase);           // first (token, expert) row; one past the last
@@ -265,24 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, t4 = lane & 3;
   const int G = gridDim.x, c = blockIdx.x;
   const int Kb1 = p.dim / 128, Kb2 = p.inter / 128;
-  const int chunks = (Kb1 + kChunk - 1) / kChunk;  // phase-1 slots of a unit
   const int upe = p.inter / 8;                     // units of an expert
   const int d0 = even(p.dim / 8, c, G) * 8, d1 = even(p.dim / 8, c + 1, G) * 8;  // this CTA's rows of w2
   const int ngroups = (d1 - d0 + 15) / 16;
   const uint32_t all_tokens = p.T == 32 ? 0xFFFFFFFFu : (1u << p.T) - 1u;
   uint8_t* ring = smem + warp * kWarpRing;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar) + warp * kSlots;
-  uint32_t phase = 0;  // bit s: phase of slot s
-
-  if (lane == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], 1);
-    fence_barrier_init();
-  }
   if (tid == 0) *abort_flag = 0;
-  __syncwarp();
 
-  // The gate rows of this CTA's experts, asked for before the weight stream
-  // fills the memory's queues. The experts share the warps, each with a slice of
+  // The gate rows of this CTA's experts. The experts share the warps, each with a slice of
   // K: warp's vectors v0, v0 + step, ... of its expert's row.
   const int per_cta = min((p.E + G - 1) / G, kWarps);  // experts at a time
   const int wpe = kWarps / per_cta;                    // warps of an expert
@@ -297,45 +273,101 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   load_gate(c + warp / wpe * G);
 
-  // This warp's phase-1 slots: first of the shared units, then of the routed
-  // ones, each a range of chunks of the CTA's units. A cursor walks a range.
+  // This warp's slots: K blocks of the shared units, then of the routed ones
+  // (each range of units, K laid end to end, split evenly over the grid's
+  // warps), then its w2 items, 16 rows at a time. A cursor walks a range.
   struct Cursor {
-    int a, rb, ck, left;  // active expert, its 8-row block, chunk of K; chunks left
+    int a, rb, kb, left;  // active expert, its 8-row block, K block; K blocks left
   };
-  auto cursor = [&](int first, int u0, int q0, int q1) {
-    const int u = u0 + q0 / chunks;
-    return Cursor{first + u / upe, u % upe, q0 % chunks, q1 - q0};
+  const int gw = c * kWarps + warp, W = G * kWarps;
+  auto cursor = [&](int first, int blocks) {
+    const int q0 = even_wide(blocks, gw, W), q1 = even_wide(blocks, gw + 1, W), u = q0 / Kb1;
+    return Cursor{first + u / upe, u % upe, q0 % Kb1, q1 - q0};
   };
-  auto advance = [&](Cursor& k, int n) {
-    k.left -= n;
-    k.ck += n;
-    if (k.ck == chunks) {
-      k.ck = 0;
+  auto advance = [&](Cursor& k) {
+    --k.left;
+    if (++k.kb == Kb1) {
+      k.kb = 0;
       if (++k.rb == upe) {
         k.rb = 0;
         ++k.a;
       }
     }
   };
-  const int us0 = even(p.ns * upe, c, G), us1 = even(p.ns * upe, c + 1, G);
-  const int sq0 = even((us1 - us0) * chunks, warp, kWarps), sq1 = even((us1 - us0) * chunks, warp + 1, kWarps);
-  const uint64_t policy = l2_policy_evict_first();  // weights are read once
-  int put = 0;                                      // the slot that the next copy goes to
-  Cursor ahead = cursor(0, us0, sq0, sq1);          // of the copies
-  auto issue1 = [&] {
-    if (elect_one_sync()) {
-      const int y = (ahead.a < p.ns ? p.E + ahead.a : act[ahead.a]) * p.inter + ahead.rb * 8, z = ahead.ck * kChunk;
-      uint8_t* dst = ring + put * kSlot1;
-      mbar_arrive_expect_tx(&full[put], kSlot1);
-      tma_load_3d_hint(dst, &map1, &full[put], 0, y, z, policy);
-      tma_load_3d_hint(dst + kSlot1 / 2, &map3, &full[put], 0, y, z, policy);
-    }
-    __syncwarp();
-    put = put + 1 == kSlots ? 0 : put + 1;
-    advance(ahead, 1);
+  const int shared_blocks = p.ns * upe * Kb1;
+  // Item i of phase 2 is K block i % Kb2 of active expert i / Kb2; this warp has
+  // items warp, warp + 16, ...
+  struct Item {
+    int a, kb;
   };
-#pragma unroll 1
-  for (int q = 0; q < kSlots && ahead.left > 0; ++q) issue1();
+  auto next_item = [&](Item& k) {
+    k.kb += kWarps;
+    while (k.kb >= Kb2) {
+      k.kb -= Kb2;
+      ++k.a;
+    }
+  };
+  // Copies: lane l has 16 bytes l % 8 of rows l / 8 and l / 8 + 4 of a slot's low
+  // and high eight weight rows and of its eight tokens; chunk j of row r goes to
+  // chunk j ^ r. Lanes 0-9 also have a scale each.
+  const uint64_t policy = l2_policy_evict_first();  // weights are read once
+  const int lane_row = lane >> 3, lane_byte = (lane & 7) * 16;
+  const uint32_t ring_addr = smem_u32(ring);
+  const uint32_t lane_dst = lane_row * 128 + (((lane & 7) ^ lane_row) << 4);
+  int put = 0;  // the slot that the next copy goes to
+  auto copy_weights = [&](const uint8_t* lo, const uint8_t* hi, int64_t pitch, bool has_hi) {
+    const uint32_t dst = ring_addr + put * kSlot + lane_dst, dst4 = ring_addr + put * kSlot + (lane_dst ^ 64) + 512;
+    copy16(dst, lo, policy);
+    copy16(dst4, lo + 4 * pitch, policy);
+    if (has_hi) {
+      copy16(dst + 1024, hi, policy);
+      copy16(dst4 + 1024, hi + 4 * pitch, policy);
+    }
+  };
+  // What the tokens bring to a slot: codes of two of them, one scale.
+  const uint8_t *tok0 = nullptr, *tok1 = nullptr;
+  const float* scl = nullptr;
+  auto copy_operands = [&](int slot) {
+    const uint32_t at = ring_addr + slot * kSlot;
+    if (tok0) copy16_plain(at + kOffTok + lane_dst, tok0);
+    if (tok1) copy16_plain(at + kOffTok + (lane_dst ^ 64) + 512, tok1);
+    if (scl) copy4(at + kOffScl + lane * 4, scl);
+  };
+  auto open_operands = [&](const Cursor& k) {
+    const int cnt = __popc(mask[k.a]), rows0 = base[k.a];
+    tok0 = lane_row < cnt ? p.xq + row_t[rows0 + lane_row] * p.dim + k.kb * 128 + lane_byte : nullptr;
+    tok1 = lane_row + 4 < cnt ? p.xq + row_t[rows0 + lane_row + 4] * p.dim + k.kb * 128 + lane_byte : nullptr;
+    const int srow = (act[k.a] * upe + k.rb) / 16 * Kb1 + k.kb;
+    scl = lane < min(cnt, 8) ? p.xs + row_t[rows0 + lane] * Kb1 + k.kb
+          : lane == 8        ? p.w1_s + srow
+          : lane == 9        ? p.w3_s + srow
+                             : nullptr;
+  };
+  Cursor ahead = cursor(0, shared_blocks);  // of the copies
+  const uint8_t *src1 = nullptr, *src3 = nullptr;
+  bool fresh = true;  // the sources are not the cursor's unit's yet
+  auto copy_unit = [&](bool operands) {  // the slot at `ahead`
+    if (fresh || ahead.kb == 0) {
+      const int64_t row =
+          static_cast<int64_t>(ahead.a < p.ns ? p.E + ahead.a : act[ahead.a]) * p.inter + ahead.rb * 8 + lane_row;
+      const int64_t off = row * p.dim + ahead.kb * 128 + lane_byte;
+      src1 = p.w1 + off;
+      src3 = p.w3 + off;
+      if (operands) open_operands(ahead);
+      fresh = false;
+    }
+    copy_weights(src1, src3, p.dim, true);
+    src1 += 128;
+    src3 += 128;
+    if (operands) {
+      copy_operands(put);
+      if (tok0) tok0 += 128;
+      if (tok1) tok1 += 128;
+      if (scl) ++scl;
+    }
+    put = put + 1 == kSlots ? 0 : put + 1;
+    advance(ahead);
+  };
 
   // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
   auto grid_barrier = [&](int i) {
@@ -366,12 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Phase 0: x quantised and the logits formed, both spread over the grid. A
   // CTA's experts share its warps, each with a slice of K.
 #pragma unroll 1
-  for (int i = c * kWarps + warp; i < p.T * Kb1; i += G * kWarps) {
+  for (int i = warp * G + c; i < p.T * Kb1; i += G * kWarps) {
     const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x) + static_cast<size_t>(i) * 32 + lane);
     const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
                         __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
     quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
   }
+  // The shared experts' stream starts when the gate's operands are here (its
+  // copies, asked for earlier, made the logits wait 4 us behind them).
+  const int early = min(kSlots - 1, ahead.left);
+  auto first_copies = [&] {
+#pragma unroll 1
+    for (int q = 0; q < early; ++q) {
+      copy_unit(false);
+      copy_commit();
+    }
+  };
+  if (c >= p.E) first_copies();
   {
     float* sums = sel_w;  // [warp][columns]
 #pragma unroll 1
@@ -408,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < wpe; ++w) v += sums[(k * wpe + w) * kCols + m];
         if (e0 + k * G < p.E) p.logits[static_cast<size_t>(m) * p.E + e0 + k * G] = v;
       }
+      if (e0 == c) first_copies();
       __syncthreads();
       if (e0 + per_cta * G < p.E) load_gate(e0 + per_cta * G + warp / wpe * G);
     }
@@ -474,19 +518,90 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int nact = scan[32], nrows = scan[33];
-  const int routed_units = (nact - p.ns) * upe;
-  const int ur0 = routed_start(p.ns * upe, routed_units, c, G), ur1 = routed_start(p.ns * upe, routed_units, c + 1, G);
-  const int rq0 = even((ur1 - ur0) * chunks, warp, kWarps), rq1 = even((ur1 - ur0) * chunks, warp + 1, kWarps);
-  bool ahead_routed = false;
-  auto issue_next = [&] {  // the next copy, if any: the shared range's, then the routed one's
-    if (ahead.left == 0 && !ahead_routed) {
-      ahead = cursor(p.ns, ur0, rq0, rq1);
-      ahead_routed = true;
-    }
-    if (ahead.left > 0 && !*abort_flag) issue1();
+  const int routed_blocks = (nact - p.ns) * upe * Kb1;
+  // The next slot's copies, one group: the shared units', the routed units',
+  // w2's. Operands of w2 come with them once u is quantised.
+  int stage = 0, group_ahead = 0, early2 = 0;
+  const int nact2 = ngroups > 0 ? nact : 0;  // a CTA without rows of w2 has no items
+  bool have_u = false;
+  Item item_ahead{warp / Kb2, warp % Kb2};
+  const uint8_t* src2 = nullptr;
+  const int sblk = d0 / 128 * Kb2, sblk2 = (d1 - 1) / 128 * Kb2;  // the CTA's rows lie in one or two 128-row blocks
+  auto open_item = [&](const Item& k) {
+    const uint32_t mk = mask[k.a];
+    const int m0 = NT == 1 ? 0 : (__ffs(mk) - 1) & ~7;  // its lowest column tile
+    auto row_of = [&](int m) { return base[k.a] + __popc(mk & ((1u << m) - 1u)); };
+    const int ma = m0 + lane_row, mb = ma + 4, ms = m0 + (lane & 7);
+    tok0 = (mk >> ma) & 1u ? p.uq + static_cast<size_t>(row_of(ma)) * p.inter + k.kb * 128 + lane_byte : nullptr;
+    tok1 = (mk >> mb) & 1u ? p.uq + static_cast<size_t>(row_of(mb)) * p.inter + k.kb * 128 + lane_byte : nullptr;
+    const int srow = act[k.a] * (p.dim / 128) * Kb2 + k.kb;
+    scl = lane < 8 ? ((mk >> ms) & 1u ? p.us + row_of(ms) * Kb2 + k.kb : nullptr)
+          : lane == 8 ? p.w2_s + srow + sblk
+          : lane == 9 ? p.w2_s + srow + sblk2
+                      : nullptr;
   };
+  auto copy_next = [&] {
+    if (ahead.left == 0 && stage == 0) {
+      stage = 1;
+      ahead = cursor(p.ns, routed_blocks);
+      fresh = true;
+    }
+    if (ahead.left > 0) {
+      copy_unit(true);
+    } else if (item_ahead.a < nact2) {
+      if (group_ahead == 0) {
+        src2 = p.w2 + (static_cast<int64_t>(act[item_ahead.a]) * p.dim + d0 + lane_row) * p.inter +
+               item_ahead.kb * 128 + lane_byte;
+        if (have_u) {
+          open_item(item_ahead);
+          copy_operands(put);
+        }
+      }
+      copy_weights(src2, src2 + 8 * static_cast<int64_t>(p.inter), p.inter, d0 + group_ahead * 16 + 8 < d1);
+      put = put + 1 == kSlots ? 0 : put + 1;
+      early2 += have_u ? 0 : 1;
+      src2 += 16 * static_cast<int64_t>(p.inter);
+      if (++group_ahead == ngroups) {
+        group_ahead = 0;
+        next_item(item_ahead);
+      }
+    }
+    copy_commit();
+  };
+  // Operands of the slots that were asked for before x was quantised.
+  {
+    Cursor k = cursor(0, shared_blocks);
 #pragma unroll 1
-  for (int q = min(kSlots, sq1 - sq0); q < kSlots; ++q) issue_next();
+    for (int q = 0; q < early; ++q) {
+      open_operands(k);
+      copy_operands(q);
+      advance(k);
+    }
+    copy_commit();
+    fresh = true;
+  }
+#pragma unroll 1
+  for (int q = early; q < kSlots - 1; ++q) copy_next();
+  copy_wait<0>();
+  int take = 0;  // the slot that is multiplied next
+  auto slot_ready = [&] {
+    copy_wait<kSlots - 2>();
+    __syncwarp();
+    const uint8_t* w = ring + take * kSlot;
+    take = take + 1 == kSlots ? 0 : take + 1;
+    return w;
+  };
+  // Column 8-tile's fragment and scales of a slot.
+  auto slot_frag = [&](const uint8_t* w) {
+    Frag f;
+    const uint8_t* x = w + kOffTok + g * 128;
+    f.b0 = *reinterpret_cast<const uint4*>(x + (((2 * t4) ^ g) << 4));
+    f.b1 = *reinterpret_cast<const uint4*>(x + (((2 * t4 + 1) ^ g) << 4));
+    const float2 sc = *reinterpret_cast<const float2*>(w + kOffScl + t4 * 8);
+    f.s0 = sc.x;
+    f.s1 = sc.y;
+    return f;
+  };
 
   // Phase 1: u = silu(w1 x) (w3 x).
   auto store_u = [&](int a, int rb, int cnt, int nt, const float (&v)[4]) {
@@ -496,152 +611,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (col < cnt) dst[0] = silu_mul(v[0], v[2]);
     if (col + 1 < cnt) dst[p.inter] = silu_mul(v[1], v[3]);
   };
-  int take = 0;  // the slot that is multiplied next
 #pragma unroll 1
   for (int range = 0; range < 2; ++range) {
-    Cursor at = range ? cursor(p.ns, ur0, rq0, rq1) : cursor(0, us0, sq0, sq1);
+    Cursor at = range ? cursor(p.ns, routed_blocks) : cursor(0, shared_blocks);
+    if (at.left == 0) continue;
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    int from = at.kb, cnt = __popc(mask[at.a]);  // the unit's first K block here, its tokens
 #pragma unroll 1
-    while (at.left > 0) {
-      // One unit, or the part of it that falls to this warp.
-      const int n = min(at.left, chunks - at.ck);
-      const int cnt = __popc(mask[at.a]), rows0 = base[at.a];
-      const float* s1 = p.w1_s + static_cast<size_t>((act[at.a] * upe + at.rb) / 16) * Kb1;
-      const float* s3 = p.w3_s + (s1 - p.w1_s);
-      // Column tile 0's tokens: this lane's operand row and the two columns it scales.
-      const bool c0 = g < cnt, c1 = 2 * t4 < cnt, c2 = 2 * t4 + 1 < cnt;
-      const uint8_t* x0 = p.xq + static_cast<size_t>(c0 ? row_t[rows0 + g] : 0) * p.dim + t4 * 32;
-      const float* xs1 = p.xs + (c1 ? row_t[rows0 + 2 * t4] : 0) * Kb1;
-      const float* xs2 = p.xs + (c2 ? row_t[rows0 + 2 * t4 + 1] : 0) * Kb1;
-      float acc[NT][4];
+    while (true) {
+      const uint8_t* w = slot_ready();
+      const float2 ws = *reinterpret_cast<const float2*>(w + kOffScl + 32);
+      block_product(w, w + 1024, slot_frag(w), ws.x, ws.y, g, t4, acc[0]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int kb0 = (at.ck + j) * kChunk;
-        Frag f[kChunk];
-        float wlo[kChunk], whi[kChunk];
-#pragma unroll
-        for (int h = 0; h < kChunk; ++h) {
-          const int kb = min(kb0 + h, Kb1 - 1);  // past K: the weights are zeros
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          f[h].b0 = c0 ? __ldcg(reinterpret_cast<const uint4*>(x0 + kb * 128)) : zero;
-          f[h].b1 = c0 ? __ldcg(reinterpret_cast<const uint4*>(x0 + kb * 128) + 1) : zero;
-          f[h].s0 = c1 ? __ldcg(xs1 + kb) : 0.f;
-          f[h].s1 = c2 ? __ldcg(xs2 + kb) : 0.f;
-          wlo[h] = __ldg(s1 + kb);
-          whi[h] = __ldg(s3 + kb);
-        }
-        const uint8_t* w = ring + take * kSlot1;
-        wait(&full[take], (phase >> take) & 1, abort_flag, p.err);
-        phase ^= 1u << take;
-        take = take + 1 == kSlots ? 0 : take + 1;
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < kChunk; ++h)
-          block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, f[h], wlo[h], whi[h], g, t4, acc[0]);
-#pragma unroll
-        for (int nt = 1; nt < NT; ++nt) {
-          if (nt * 8 >= cnt) break;
-#pragma unroll
-          for (int h = 0; h < kChunk; ++h) {
-            const int kb = min(kb0 + h, Kb1 - 1), col = nt * 8 + g, cs = nt * 8 + 2 * t4;
-            Frag x;
-            x.b0 = x.b1 = make_uint4(0u, 0u, 0u, 0u);
-            if (col < cnt) {
-              const uint4* src = reinterpret_cast<const uint4*>(p.xq + static_cast<size_t>(row_t[rows0 + col]) * p.dim +
-                                                                kb * 128 + t4 * 32);
-              x.b0 = __ldcg(src);
-              x.b1 = __ldcg(src + 1);
-            }
-            x.s0 = cs < cnt ? __ldcg(p.xs + row_t[rows0 + cs] * Kb1 + kb) : 0.f;
-            x.s1 = cs + 1 < cnt ? __ldcg(p.xs + row_t[rows0 + cs + 1] * Kb1 + kb) : 0.f;
-            block_product(w + h * 1024, w + kSlot1 / 2 + h * 1024, x, wlo[h], whi[h], g, t4, acc[nt]);
-          }
-        }
-        __syncwarp();
-        issue_next();
-      }
-      if (n == chunks) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (nt * 8 < cnt) store_u(at.a, at.rb, cnt, nt, acc[nt]);
-      } else {  // sums of a cut unit: [range][it starts here]
-        float4* t = reinterpret_cast<float4*>(p.part + ((static_cast<size_t>(c) * kWarps + warp) * 4 + range * 2 +
-                                                        (at.ck == 0 ? 1 : 0)) * kTile) + lane;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (nt * 8 < cnt) t[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-      }
-      advance(at, n);
-    }
-  }
-
-  // The first w2 tiles. Item i is K block i % Kb2 of active expert i / Kb2; this
-  // warp has items warp, warp + 16, ...
-  struct Item {
-    int a, kb;
-  };
-  auto next_item = [&](Item& k) {
-    k.kb += kWarps;
-    while (k.kb >= Kb2) {
-      k.kb -= Kb2;
-      ++k.a;
-    }
-  };
-  Item item_ahead{warp / Kb2, warp % Kb2};
-  put = 0;
-  auto issue2 = [&] {
-    if (item_ahead.a >= nact || *abort_flag) return;
-    if (elect_one_sync()) {
-      mbar_arrive_expect_tx(&full[put], static_cast<uint32_t>(p.r2) * 128);
-      tma_load_3d_hint(ring + put * p.r2 * 128, &map2, &full[put], 0, act[item_ahead.a] * p.dim + d0, item_ahead.kb,
-                       policy);
-    }
-    __syncwarp();
-    put = put + 1 == p.slots2 ? 0 : put + 1;
-    next_item(item_ahead);
-  };
-#pragma unroll 1
-  for (int q = 0; q < p.slots2; ++q) issue2();
-
-  // Units cut between warps: warp w adds up units w, w + 16, ... of the CTA.
-  __syncthreads();
-#pragma unroll 1
-  for (int range = 0; range < 2; ++range) {
-    const int u0 = range ? ur0 : us0, n = (range ? ur1 : us1) - u0, total = n * chunks;
-#pragma unroll 1
-    for (int k = warp; k < n; k += kWarps) {
-      // The warp of chunk x is the largest w with even(total, w) <= x.
-      const int w0 = ((k * chunks + 1) * kWarps - 1) / total;
-      const int w1 = ((k + 1) * chunks * kWarps - 1) / total;
-      if (w0 == w1) continue;
-      const int u = u0 + k, a = (range ? p.ns : 0) + u / upe, cnt = __popc(mask[a]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 1; nt < NT; ++nt) {
         if (nt * 8 >= cnt) break;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int w = w0; w <= w1; ++w) {
-          const int from = even(total, w, kWarps);
-          if (from == even(total, w + 1, kWarps)) continue;  // fewer chunks than warps: this one has none
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(
-                                      p.part + ((static_cast<size_t>(c) * kWarps + w) * 4 + range * 2 +
-                                                (from <= k * chunks ? 1 : 0)) * kTile) +
-                                  nt * 32 + lane);
-          v[0] += x.x;
-          v[1] += x.y;
-          v[2] += x.z;
-          v[3] += x.w;
+        const int rows0 = base[at.a], col = nt * 8 + g, cs = nt * 8 + 2 * t4;
+        Frag x;
+        x.b0 = x.b1 = make_uint4(0u, 0u, 0u, 0u);
+        if (col < cnt) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.xq + row_t[rows0 + col] * p.dim + at.kb * 128 + t4 * 32);
+          x.b0 = __ldcg(src);
+          x.b1 = __ldcg(src + 1);
         }
-        store_u(a, u % upe, cnt, nt, v);
+        x.s0 = cs < cnt ? __ldcg(p.xs + row_t[rows0 + cs] * Kb1 + at.kb) : 0.f;
+        x.s1 = cs + 1 < cnt ? __ldcg(p.xs + row_t[rows0 + cs + 1] * Kb1 + at.kb) : 0.f;
+        block_product(w, w + 1024, x, ws.x, ws.y, g, t4, acc[nt]);
+      }
+      copy_next();
+      const Cursor now = at;
+      advance(at);
+      if (at.kb == 0 || at.left == 0) {
+        if (from == 0 && at.kb == 0) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (nt * 8 < cnt) store_u(now.a, now.rb, cnt, nt, acc[nt]);
+        } else {
+          float4* t = reinterpret_cast<float4*>(p.part + (static_cast<size_t>(gw) * 4 + range * 2 + (from == 0 ? 1 : 0)) *
+                                                             kTile) + lane;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            if (nt * 8 < cnt) t[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+        }
+        if (at.left == 0) break;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        from = 0;
+        cnt = __popc(mask[at.a]);
       }
     }
   }
   grid_barrier(1);
+  // u by 128-column blocks of a row, four elements per lane: stored by the warp
+  // that had all of a unit's K, else added up from its parts; then quantised.
 #pragma unroll 1
-  for (int i = c * kWarps + warp; i < nrows * Kb2; i += G * kWarps) {
-    const float4 raw = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
-    const float v[4] = {raw.x, raw.y, raw.z, raw.w};
+  for (int i = warp * G + c; i < nrows * Kb2; i += W) {
+    const int row = i / Kb2, kb = i % Kb2;
+    int lo = 0, hi = nact - 1;  // the active expert of the row: the last whose base is not past it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (base[mid] <= row) lo = mid;
+      else hi = mid - 1;
+    }
+    const int col = row - base[lo], range = lo < p.ns ? 0 : 1, blocks = range ? routed_blocks : shared_blocks;
+    const int unit = (lo - (range ? p.ns : 0)) * upe + kb * 16 + lane / 2;
+    // The warp of K block x of a range is the largest w with even(blocks, w) <= x.
+    const int w0 = static_cast<int>((static_cast<int64_t>(unit * Kb1 + 1) * W - 1) / blocks);
+    const int w1 = static_cast<int>((static_cast<int64_t>((unit + 1) * Kb1) * W - 1) / blocks);
+    float v[4];
+    if (w0 == w1) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
+      v[0] = u.x;
+      v[1] = u.y;
+      v[2] = u.z;
+      v[3] = u.w;
+    } else {
+      float h1[4] = {0.f, 0.f, 0.f, 0.f}, h3[4] = {0.f, 0.f, 0.f, 0.f};
+      const int in_tile = ((col >> 3) * 32 + (lane & 1) * 16 + ((col & 7) >> 1)) * 4 + (col & 1);
+#pragma unroll 1
+      for (int w = w0; w <= w1; w += 4) {
+        float a[4][4], b[4][4];  // four parts' loads in flight together
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float* t = p.part + (static_cast<size_t>(w + k) * 4 + range * 2 + (w + k == w0 ? 1 : 0)) * kTile + in_tile;
+          // (With fewer K blocks than warps some warps have none.)
+          const bool there = w + k <= w1 && (blocks >= W || even_wide(blocks, w + k, W) < even_wide(blocks, w + k + 1, W));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            a[k][r] = there ? __ldcg(t + r * 16) : 0.f;
+            b[k][r] = there ? __ldcg(t + r * 16 + 2) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            h1[r] += a[k][r];
+            h3[r] += b[k][r];
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = silu_mul(h1[r], h3[r]);
+    }
     quant_block(v, p.ue8m0 != 0, lane, p.uq + static_cast<size_t>(i) * 128, p.us + i);
   }
   grid_barrier(2);
@@ -653,73 +725,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int q = 0; q < kMaxGroups; ++q)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
-  // Weight-scale rows of the groups' low and high halves within an expert.
-  int slo[kMaxGroups], shi[kMaxGroups];
-#pragma unroll
-  for (int q = 0; q < kMaxGroups; ++q) {
-    slo[q] = (d0 + q * 16) / 128 * Kb2;
-    shi[q] = (d0 + q * 16 + 8) / 128 * Kb2;
-  }
-  const bool odd = ((d1 - d0) & 8) != 0;  // the last group has no high half
-  take = 0;
+  const int rows_in_first = (d0 / 128 + 1) * 128 - d0;  // rows of the CTA's first 128-row block
+  const bool odd = ((d1 - d0) & 8) != 0;                // the last group has no high half
+  // Operands of the slots that were asked for before u was quantised.
+  have_u = true;
+  Item it{warp / Kb2, warp % Kb2};
+  {
+    Item k = it;
+    int slot = take;
 #pragma unroll 1
-  for (Item it{warp / Kb2, warp % Kb2}; it.a < nact; next_item(it)) {
-    const int a = it.a, kb = it.kb;
-    const uint32_t mk = mask[a];
-    const int r_base = base[a];
-    const float* ws = p.w2_s + static_cast<size_t>(act[a]) * (p.dim / 128) * Kb2 + kb;
-    auto frag = [&](int nt) {
-      Frag f;
-      f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
-      f.s0 = f.s1 = 0.f;
-      const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
-      const int r = r_base + __popc(mk & ((1u << m) - 1u)), r2 = r_base + __popc(mk & ((1u << m2) - 1u));
-      if ((mk >> m) & 1u) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(r) * p.inter + kb * 128 + t4 * 32);
-        f.b0 = __ldcg(src);
-        f.b1 = __ldcg(src + 1);
-      }
-      const int r3 = r2 + ((mk >> m2) & 1u);
-      if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + r2 * Kb2 + kb) * row_w[r2];
-      if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + r3 * Kb2 + kb) * row_w[r3];
-      return f;
-    };
-    float wlo[kMaxGroups], whi[kMaxGroups];
-#pragma unroll
-    for (int q = 0; q < kMaxGroups; ++q) {
-      wlo[q] = q < ngroups ? __ldg(ws + slo[q]) : 0.f;
-      whi[q] = q < ngroups && !(odd && q == ngroups - 1) ? __ldg(ws + shi[q]) : 0.f;
+    for (int q = 0; q < early2; q += ngroups) {
+      open_item(k);
+      copy_operands(slot);
+      slot = (slot + ngroups) % kSlots;
+      next_item(k);
     }
-    Frag f0;
-    if (NT == 1) f0 = frag(0);
-    const uint8_t* w = ring + take * p.r2 * 128;
-    wait(&full[take], (phase >> take) & 1, abort_flag, p.err);
-    phase ^= 1u << take;
-    take = take + 1 == p.slots2 ? 0 : take + 1;
-    __syncwarp();
+    copy_commit();
+    copy_wait<0>();
+  }
+#pragma unroll 1
+  while (it.a < nact2) {
+    const uint32_t mk = mask[it.a];
+    const int r_base = base[it.a], lowest = NT == 1 ? 0 : (__ffs(mk) - 1) >> 3;
+    Frag f0, more[NT > 1 ? NT - 1 : 1];  // column tiles' fragments, for all groups
+    float wa = 0.f, wb = 0.f;
+    if constexpr (NT > 1) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
-      const Frag f = NT == 1 ? f0 : frag(nt);
-#pragma unroll
-      for (int q = 0; q < kMaxGroups; ++q)
-        if (q < ngroups) {
-          // A last group of 8 rows takes them twice; the second copy has scale 0.
-          const uint8_t* lo = w + q * 2048;
-          block_product(lo, odd && q == ngroups - 1 ? lo : lo + 1024, f, wlo[q], whi[q], g, t4, acc[q][nt]);
+      for (int nt = 1; nt < NT; ++nt) {
+        if (nt == lowest || !((mk >> (nt * 8)) & 0xFFu)) continue;
+        Frag& f = more[nt - 1];
+        f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
+        f.s0 = f.s1 = 0.f;
+        const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
+        const int r = r_base + __popc(mk & ((1u << m) - 1u)), r2 = r_base + __popc(mk & ((1u << m2) - 1u));
+        if ((mk >> m) & 1u) {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(r) * p.inter + it.kb * 128 + t4 * 32);
+          f.b0 = __ldcg(src);
+          f.b1 = __ldcg(src + 1);
         }
+        const int r3 = r2 + ((mk >> m2) & 1u);
+        if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + r2 * Kb2 + it.kb) * row_w[r2];
+        if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + r3 * Kb2 + it.kb) * row_w[r3];
+      }
     }
-    __syncwarp();
-    issue2();
+#pragma unroll
+    for (int q = 0; q < kMaxGroups; ++q)
+      if (q < ngroups) {
+        const uint8_t* w = slot_ready();
+        if (q == 0) {
+          // The item's first slot carries the lowest tile's operands. Columns
+          // without a token have zero codes: their sums go on for other experts.
+          f0 = slot_frag(w);
+          const int m = lowest * 8 + g, m2 = lowest * 8 + 2 * t4;
+          const int r2 = r_base + __popc(mk & ((1u << m2) - 1u));
+          if (!((mk >> m) & 1u)) f0.b0 = f0.b1 = make_uint4(0u, 0u, 0u, 0u);
+          f0.s0 = (mk >> m2) & 1u ? f0.s0 * row_w[r2] : 0.f;
+          f0.s1 = (mk >> (m2 + 1)) & 1u ? f0.s1 * row_w[r2 + ((mk >> m2) & 1u)] : 0.f;
+          const float2 ws = *reinterpret_cast<const float2*>(w + kOffScl + 32);
+          wa = ws.x;
+          wb = ws.y;
+        }
+        const float wlo = q * 16 < rows_in_first ? wa : wb, whi = q * 16 + 8 < rows_in_first ? wa : wb;
+        // A last group of 8 rows takes them twice; the second copy is not stored.
+        const uint8_t* hi = odd && q == ngroups - 1 ? w : w + 1024;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
+          const Frag& f = nt == 0 || nt == lowest ? f0 : more[nt > 0 ? nt - 1 : 0];
+          block_product(w, hi, f, wlo, whi, g, t4, acc[q][nt]);
+        }
+        copy_next();
+      }
+    next_item(it);
   }
+  copy_wait<0>();
   __syncthreads();
-  // Every warp's copies have landed and are used: the rings hold the warps'
-  // sums [warp][row][columns] now (a copy still in flight after a wait that
-  // gave up is waited for first).
-  if (*abort_flag) {
-    for (int i = 0; i < kSlots; ++i) wait(&full[i], (phase >> i) & 1, nullptr, p.err);
-    __syncthreads();
-  }
+  // The rings hold the warps' sums [warp][row][columns] now.
   float* sums = reinterpret_cast<float*>(smem);
   const int rows2 = ngroups * 16;
 #pragma unroll
@@ -746,37 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn layer_map_encoder() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* q = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &st) == cudaSuccess &&
-        st == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(q);
-  });
-  return fn;
-}
-
-// An e4m3 weight [N, K] as (128 bytes of a K block, row, K block), read in
-// boxes of `rows` x kb blocks, 128-byte swizzled; blocks past K read as zeros.
-bool make_weight_map(CUtensorMap* map, const void* w, uint64_t N, uint64_t K, uint32_t rows, uint32_t kb) {
-  EncodeTiledFn enc = layer_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {128, N, K / 128};
-  const cuuint64_t strides[2] = {K, 128};
-  const cuuint32_t box[3] = {128, rows, kb};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 
 struct LayerSizes {
@@ -794,7 +845,7 @@ LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t
   z.us = z.uq + align256(rows * inter);
   z.part = z.us + align256(rows * (inter / 128) * 4);
   const size_t cols = T <= 8 ? 8 : T <= 16 ? 16 : 32;
-  z.total = z.part + static_cast<size_t>(kMaxCtas) * kWarps * 4 * 16 * cols * 4;
+  z.total = z.part + static_cast<size_t>(kMaxCtas) * kWarps * 4 * 16 * cols * 4;  // a tile is 16 rows x cols floats
   return z;
 }
 
@@ -805,8 +856,7 @@ bool layer_shape_ok(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t to
 }
 
 template <int NT>
-int layer_launch(const DevInfo* d, const CUtensorMap& m1, const CUtensorMap& m3, const CUtensorMap& m2,
-                 const LayerParams& p, cudaStream_t stream) {
+int layer_launch(const DevInfo* d, const LayerParams& p, cudaStream_t stream) {
   static bool attr_done[64] = {};
   auto kern = moe_layer_kernel<NT>;
   if (d->device >= 64 || !attr_done[d->device]) {
@@ -824,7 +874,7 @@ int layer_launch(const DevInfo* d, const CUtensorMap& m1, const CUtensorMap& m3,
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, m1, m3, m2, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 }  // namespace
@@ -899,17 +949,11 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.normalize = normalize != 0;
   p.ue8m0 = scale_fmt_ue8m0(scale_fmt);
   p.route_scale = route_scale;
-  p.r2 = static_cast<int>((dim / 8 + d->sm_count - 1) / d->sm_count) * 8;
-  p.slots2 = kWarpRing / (p.r2 * 128);
-  if (p.slots2 > kSlots) p.slots2 = kSlots;
-  const uint64_t K = static_cast<uint64_t>(E + n_shared);
-  CUtensorMap m1, m3, m2;
-  if (!make_weight_map(&m1, w1_e4m3, K * inter, dim, 8, kChunk) ||
-      !make_weight_map(&m3, w3_e4m3, K * inter, dim, 8, kChunk) ||
-      !make_weight_map(&m2, w2_e4m3, K * dim, inter, static_cast<uint32_t>(p.r2), 1))
-    return FP8BLK_ERR_CUDA;
+  p.w1 = static_cast<const uint8_t*>(w1_e4m3);
+  p.w3 = static_cast<const uint8_t*>(w3_e4m3);
+  p.w2 = static_cast<const uint8_t*>(w2_e4m3);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return T <= 8    ? layer_launch<1>(d, m1, m3, m2, p, cs)
-         : T <= 16 ? layer_launch<2>(d, m1, m3, m2, p, cs)
-                   : layer_launch<4>(d, m1, m3, m2, p, cs);
+  return T <= 8    ? layer_launch<1>(d, p, cs)
+         : T <= 16 ? layer_launch<2>(d, p, cs)
+                   : layer_launch<4>(d, p, cs);
 }
