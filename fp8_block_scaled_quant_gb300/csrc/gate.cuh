@@ -35,7 +35,8 @@ __device__ __forceinline__ int warp_argmax_lane(uint32_t key) {
 
 // The gate of one token, computed by one warp from its logits: lane l holds
 // x[i] = logit of expert l v + i for i < v <= V (E = 32 v experts; v = V where
-// the caller knows it at compile time), and the experts' biases likewise. Lane
+// the caller knows it at compile time; x[i] past v is any finite number), and the
+// experts' biases likewise. Lane
 // j < K ends with the expert of slot j in *out_idx and its weight (normalised,
 // times route_scale) in *out_w.
 template <int V>
@@ -45,8 +46,7 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
   float s[V], z[V];
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < v) s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-x[i])));
+    for (int i = 0; i < V; ++i) s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-x[i])));
   } else {
     float m = -INFINITY;
 #pragma unroll
@@ -68,23 +68,18 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
       if (i < v) s[i] = __fdiv_rn(x[i], sum);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < v) z[i] = has_bias ? __fadd_rn(s[i], bias[i]) : s[i];
+  for (int i = 0; i < V; ++i) z[i] = has_bias ? __fadd_rn(s[i], bias[i]) : s[i];
 
   // Group selection: a lane is eligible while its group is kept.
   bool eligible = true;
   if (G > 1) {
-    const int lpg = 32 / G;  // lanes per group
+    const int lpg = 32 / G;  // lanes per group (G divides 32)
     float a = -INFINITY, b = -INFINITY;  // this lane's two largest z
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (i >= v) continue;
-      if (z[i] > a) {
-        b = a;
-        a = z[i];
-      } else if (z[i] > b) {
-        b = z[i];
-      }
+      const float zi = i < v ? z[i] : -INFINITY;
+      b = fmaxf(b, fminf(a, zi));
+      a = fmaxf(a, zi);
     }
     for (int o = lpg >> 1; o > 0; o >>= 1) {  // merge the pairs of the group's lanes
       const float a2 = __shfl_xor_sync(0xFFFFFFFFu, a, o);
@@ -94,11 +89,11 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
       a = hi;
     }
     const float gscore = has_bias ? __fadd_rn(a, b) : a;
-    const int g = lane / lpg;
+    const int shift = __ffs(lpg) - 1, g = lane >> shift;  // lpg is a power of two
     bool kept = false;
     for (int r = 0; r < TG; ++r) {
       // A group's lanes agree, and lanes are in group order: ties go to the lower.
-      if (warp_argmax_lane(kept ? 0u : gate_order(gscore)) / lpg == g) kept = true;
+      if (warp_argmax_lane(kept ? 0u : gate_order(gscore)) >> shift == g) kept = true;
     }
     eligible = kept;
   }

@@ -16,49 +16,38 @@
 // (44 MB of codes for 7168 x 2048), whatever the number of its tokens, so the
 // floor is those bytes at HBM rate. The kernel is built to keep that stream
 // from stopping:
-//   - One CTA per SM, one launch (cooperative: CTAs meet at three barriers).
-//     Each of the CTA's sixteen warps owns 12.5 KB of shared memory and streams
-//     and multiplies its own share of the weights, 2 KB (16 rows of a K block)
-//     at a time, three such slots in flight (cp.async), the tokens' codes and all
-//     scales in the slot beside them: nothing but the phases' ends makes warps
-//     wait for one another, so one warp's latencies hide behind fifteen others.
-//     (Stages that all warps multiplied together ran at 3.9 TB/s; the same slots
-//     by TMA cost a warp 400 cycles a copy to issue; operands by plain loads wait
-//     behind the stream, 20 us of 100 for one token.)
-//   - The gate decides what the routed weights are, but not the shared ones:
-//     every warp asks for its share of the shared experts as soon as the gate's
-//     operands are here, and the gate is computed meanwhile.
-//   - w2 does not depend on u, only its use does: a warp's slots run on from
-//     its part of phase 1 into w2 before the barriers between them.
-//   - Phase 1 lays its units (expert, 8 rows of w1 and the same 8 of w3) end to
-//     end, K block by K block, and gives every warp of the GPU the same number
-//     of K blocks; the parts of a unit cut between warps are added in warp order
-//     where u is quantised. Phase 2 gives each CTA the same rows of every
-//     expert's w2, and its (expert, K block) pairs round robin to the warps: the
-//     sum over experts stays in registers. No atomics on values, one order of
-//     every sum.
+//   - One CTA per SM, one launch (cooperative: CTAs meet at three barriers). Per
+//     CTA a producer warp keeps 160 KB of weight tiles in flight by TMA (128 rows x
+//     one K block, 16 KB), a warp issues the MMAs, four promote and finish.
+//   - The gate decides what the routed weights are, but not the shared ones: the
+//     ring fills with the CTA's share of the shared experts while x is quantised
+//     and the gate computed.
+//   - w2 does not depend on u, only its use does: the ring runs on from phase 1
+//     into w2 before the barriers between them.
+//   - Phase 1 lays its units (expert, 128 rows of w1 and the same of w3) end to
+//     end, K block by K block, and phase 2 its row tiles of w2, over all experts
+//     and K blocks; each CTA has the same number of K blocks of either. A unit
+//     that one CTA has whole is quantised there (its 128 rows are one block of
+//     u); parts of cut units are added in CTA order behind the barrier, parts of
+//     a row tile by the CTA that finishes the tile last. One order of every sum.
 //
-// The products are warp-level FP8 MMAs (m16n8k32): tokens are the 8 columns,
-// so one MMA serves up to 8 tokens at the cost of one. In phase 1 rows 0-7 of
-// an MMA tile are w1's and rows 8-15 w3's, so one lane ends with h1 and h3 of
-// the same element. Each K block's product is promoted as acc += D * (a_s w_s).
-// A tcgen05.mma with so few columns takes about 130 cycles for 4 KB of weights,
-// 31 bytes a cycle, hardly the HBM rate of one SM (23); the warp MMAs take 64.
-// Operand fragments as in the decode GEMM: lane (g, t) reads bytes [32 t, 32 t +
-// 32) of a K block for row g, MMA j of the block takes bytes [8 j, 8 j + 8) of
-// those, the same for both operands.
-//
-// Columns. In phase 1 they are an expert's tokens, closely packed (one tile of 8
-// columns serves nearly every routed expert). In phase 2, whose accumulators
-// run over the experts, they are the tokens 0-7, 8-15, ... themselves, and a
-// tile without any token of the expert is skipped.
+// The products are tcgen05 MMAs with 128 weight rows as M and the tokens as N = 16
+// or 32 (all tokens for every expert: idle columns cost nothing): 156 or 160
+// cycles for a 16 KB tile (measured, 105 bytes a cycle and SM; HBM brings 23).
+// Each K block has its own accumulators in tensor memory (eight sets), promoted
+// as acc += D * (a_s w_s) by the thread that owns the row. Warp-level FP8 MMAs on
+// the same stream, which are carried out as conversions and half-precision MMAs,
+// ran the SM's issue slots full: 89 us for one token of 7168 x 2048 x 256.
 //
 // Every wait is bounded (2 s): on expiry an error bit is set, waits return at
 // once from then on, and the control flow, whose loops are finite, runs out.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "block_rule.cuh"
 #include "fp8blk.h"
@@ -76,29 +65,32 @@ namespace {
 constexpr int kMaxTokens = 32;
 constexpr int kMaxShared = 8;
 constexpr int kMaxActive = 256 + kMaxShared;
-constexpr int kMaxRows = kMaxTokens * (32 + kMaxShared);  // (token, expert) pairs
 constexpr int kWarps = 16;
-constexpr int kMaxCtas = 192;                             // SMs a device may have
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxGroups = 4;                             // 16-row groups of w2 per CTA
+constexpr int kMaxCtas = 192;             // SMs a device may have
 constexpr int kMaxDim = 8192, kMaxInter = 16384;
-constexpr int kSlots = 4;                                 // slots of a warp
-constexpr int kOffTok = 2048;                             // after 16 weight rows x 128 bytes: 8 tokens' codes
-constexpr int kOffScl = 3072;                             // 8 token scales, 2 weight scales
-constexpr int kSlot = 3200;
-constexpr int kWarpRing = kSlots * kSlot;
-constexpr int kGateVecs = 4;                              // 16-byte vectors of a gate row per thread
+constexpr int kGateVecs = 4;              // 16-byte vectors of a gate row per thread
+constexpr int kStages = 10;               // weight tiles in flight
+constexpr int kTileBytes = 128 * 128;
+constexpr int kSets = 8;                  // accumulator sets in tensor memory
+// Streaming roles; the other warps wait for the phase to end.
+constexpr int kProducer = 0, kIssuer = 1, kFinisher = 4;  // finishers: warps 4-7
+constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
 
-// Shared memory: the rings, then the routing tables.
-constexpr int kOffAct = kWarps * kWarpRing + 16;
-constexpr int kOffMask = kOffAct + kMaxActive * 4;
-constexpr int kOffBase = kOffMask + kMaxActive * 4;
-constexpr int kOffRowW = kOffBase + (kMaxActive + 1) * 4;
-constexpr int kOffRowT = kOffRowW + kMaxRows * 4;
-constexpr int kOffSel = kOffRowT + kMaxRows;              // ids, weights of the pairs; scratch before
-constexpr int kOffScan = kOffSel + 2 * kMaxTokens * 32 * 4;
-constexpr int kLayerSmem = 1024 + kOffScan + 48 * 4;
-static_assert(kLayerSmem <= 232448, "shared memory per CTA");
+// Shared memory: weight tiles, token tiles, token scales, barriers, tables.
+__host__ __device__ constexpr int off_tok() { return kStages * kTileBytes; }
+__host__ __device__ constexpr int off_scl(int n) { return off_tok() + kStages * n * 128; }
+__host__ __device__ constexpr int off_bar(int n) { return off_scl(n) + kStages * n * 4; }
+constexpr int kNumBars = 3 * kStages + 2 * kSets + 1;
+__host__ __device__ constexpr int off_act(int n) { return (off_bar(n) + kNumBars * 8 + 8 + 15) / 16 * 16; }
+__host__ __device__ constexpr int off_mask(int n) { return off_act(n) + kMaxActive * 4; }
+__host__ __device__ constexpr int off_sel(int n) { return off_mask(n) + kMaxActive * 4; }  // ids, weights; scratch before
+__host__ __device__ constexpr int off_scan(int n) { return off_sel(n) + 2 * kMaxTokens * 32 * 4; }
+__host__ __device__ constexpr int off_red(int n) { return off_scan(n) + 64 * 4; }          // [2][n][4] row maxima
+__host__ __device__ constexpr int off_bias(int n) { return off_red(n) + 2 * n * 4 * 4; }
+__host__ __device__ constexpr int layer_smem(int n) { return 1024 + off_bias(n) + 256 * 4; }
+static_assert(layer_smem(32) <= 232448, "shared memory per CTA");
+static_assert(off_red(16) % 16 == 0 && off_red(32) % 16 == 0 && off_scl(16) % 16 == 0, "16-byte reads");
 
 struct LayerParams {
   const __nv_bfloat16* x;
@@ -108,55 +100,61 @@ struct LayerParams {
   const float* w3_s;
   const float* w2_s;
   __nv_bfloat16* y;
-  int32_t* topk_idx;  // may be null
-  float* topk_w;      // may be null
-  unsigned* counters;  // [0..2] barrier arrivals, [3] CTAs done; zero between calls
-  float* logits;      // [T][E]
-  uint8_t* xq;        // [T][dim]
-  float* xs;          // [T][dim / 128]
-  float* u;           // [rows][inter]
-  uint8_t* uq;        // [rows][inter]
-  float* us;          // [rows][inter / 128]
-  float* part;        // [warp of the grid][range][it starts the unit][16 rows x columns]: sums of cut units
+  int32_t* topk_idx;    // may be null
+  float* topk_w;        // may be null
+  unsigned* counters;   // [0..2] barrier arrivals, [3] CTAs done, [16..31] row tiles, a byte each; zero between calls
+  float* logits;        // [T][E]
+  uint8_t* xq;          // [T][dim]
+  float* xs;            // [dim / 128][N]
+  uint8_t* uq;          // [active expert][T][inter], rows of routed tokens
+  float* us;            // [active expert][inter / 128][N]: scale * gate weight
+  float* part;          // [CTA][range][it starts the unit][h1, h3][T][128]
+  float* part2;         // [CTA][it starts the tile][T][128]
   unsigned* err;
   int T, dim, inter, E, ns, k, groups, kept, sigmoid, normalize, ue8m0;
   float route_scale;
-  const uint8_t* w1;  // weights
-  const uint8_t* w3;
-  const uint8_t* w2;
 };
 
-constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
+// The bounded wait, its slow part out of line (the loops that call it stay
+// small in the instruction cache). Returns at once after an abort.
+__device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((i & 63u) == 0) {
+      if (abort && *abort) return;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (abort) *abort = 1;
+        atomicOr(err, kDevErrTimeoutLayer);
+        return;
+      }
+    }
+  }
+}
 
-// 16 bytes from global to shared memory, past the L1 cache.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint32_t a = smem_u32(bar);
+  if (!mbar_try_wait(a, parity)) wait_slow(a, parity, abort, err);
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_plain(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but this thread's `N` latest groups of copies have landed.
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
-// d += A (16 x 32, rows) * B (32 x 8, columns), e4m3 operands, fp32 accumulators.
-__device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// Orders this thread's generic accesses, to any memory, before async-proxy ones.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// Quantises one 128-element block, four elements per lane; lane 0 stores the scale.
-__device__ __forceinline__ void quant_block(const float (&v)[4], bool ue8m0, int lane, uint8_t* q, float* s) {
+// N consecutive tensor-memory columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
+
+// Quantises one 128-element block, four elements per lane; returns its scale.
+__device__ __forceinline__ float quant_block(const float (&v)[4], bool ue8m0, int lane, uint8_t* q) {
   float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -164,58 +162,30 @@ __device__ __forceinline__ void quant_block(const float (&v)[4], bool ue8m0, int
   const uint32_t lo = e4m3x2(__fdiv_rn(v[0], sc), __fdiv_rn(v[1], sc));
   const uint32_t hi = e4m3x2(__fdiv_rn(v[2], sc), __fdiv_rn(v[3], sc));
   reinterpret_cast<uint32_t*>(q)[lane] = lo | (hi << 16);
-  if (lane == 0) *s = sc;
+  return sc;
 }
 
-// First unit of part c of G when n units are split evenly (n * c stays below
-// 2^31: at most 264 experts x 2048 units x 192 CTAs).
+// First block of part c of G when n blocks are split evenly, and the part of
+// block x. (n * G stays below 2^32: at most 264 experts x 128 x 64 K blocks and
+// 192 CTAs.)
 __device__ __forceinline__ int even(int n, int c, int G) {
   return static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint32_t>(c) / static_cast<uint32_t>(G));
 }
-
-// The same for large n (a K block count times a warp index).
-__device__ __forceinline__ int even_wide(int n, int c, int G) {
-  return static_cast<int>(static_cast<int64_t>(n) * c / G);
-}
-
-// The B fragment of one K block for 8 columns and the columns' scales.
-struct Frag {
-  uint4 b0, b1;
-  float s0, s1;
-};
-
-// One K block of a 16-row tile: rows g of `lo` and of `hi` (128-byte swizzled
-// rows of 128 bytes), promoted into acc with the rows' weight scales.
-__device__ __forceinline__ void block_product(const uint8_t* lo, const uint8_t* hi, const Frag& f, float wlo, float whi,
-                                              int g, int t4, float (&acc)[4]) {
-  uint4 al[2], ah[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int at = g * 128 + (((2 * t4 + h) ^ g) << 4);
-    al[h] = *reinterpret_cast<const uint4*>(lo + at);
-    ah[h] = *reinterpret_cast<const uint4*>(hi + at);
-  }
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-  mma_16x8x32(d, al[0].x, ah[0].x, al[0].y, ah[0].y, f.b0.x, f.b0.y);
-  mma_16x8x32(d, al[0].z, ah[0].z, al[0].w, ah[0].w, f.b0.z, f.b0.w);
-  mma_16x8x32(d, al[1].x, ah[1].x, al[1].y, ah[1].y, f.b1.x, f.b1.y);
-  mma_16x8x32(d, al[1].z, ah[1].z, al[1].w, ah[1].w, f.b1.z, f.b1.w);
-  acc[0] = fmaf(d[0], f.s0 * wlo, acc[0]);
-  acc[1] = fmaf(d[1], f.s1 * wlo, acc[1]);
-  acc[2] = fmaf(d[2], f.s0 * whi, acc[2]);
-  acc[3] = fmaf(d[3], f.s1 * whi, acc[3]);
+__device__ __forceinline__ int part_of(int n, int x, int G) {
+  return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(G) - 1u) / static_cast<uint32_t>(n));
 }
 
 __device__ __forceinline__ float silu_mul(float h1, float h3) { return h1 / (1.0f + expf(-h1)) * h3; }
 
 // Ids and weights of token m by one warp, into the pair tables.
-__device__ __noinline__ void gate_of_token(const LayerParams& p, int m, int lane, bool store, int* sel_e, float* sel_w) {
+__device__ __noinline__ void gate_of_token(const LayerParams& p, const float* bias, int m, int lane, bool store,
+                                           int* sel_e, float* sel_w) {
   const int v = p.E / 32;
   float xl[8], bl[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     xl[i] = i < v ? __ldcg(p.logits + static_cast<size_t>(m) * p.E + lane * v + i) : 0.f;
-    bl[i] = i < v && p.gate_bias ? __ldg(p.gate_bias + lane * v + i) : 0.f;
+    bl[i] = i < v ? bias[lane * v + i] : 0.f;
   }
   int e;
   float w;
@@ -230,33 +200,59 @@ __device__ __noinline__ void gate_of_token(const LayerParams& p, int m, int lane
   }
 }
 
-template <int NT>
+template <int N>  // token columns
 __global__ void __launch_bounds__(kThreads, 1)
-    moe_layer_kernel(const __grid_constant__ LayerParams p) {
-  constexpr int kCols = 8 * NT;
-  constexpr int kTile = 16 * kCols;  // sums of a 16-row tile
+    moe_layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map3,
+                     const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map_x,
+                     const __grid_constant__ CUtensorMap map_u, const __grid_constant__ LayerParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kWarps * kWarpRing);
-  int* act = reinterpret_cast<int*>(smem + kOffAct);             // active experts, shared ones first
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kOffMask);  // tokens; by expert id until sorted
-  int* base = reinterpret_cast<int*>(smem + kOffBase);           // first (token, expert) row; one past the last
-  float* row_w = reinterpret_cast<float*>(smem + kOffRowW);      // gate weight of each row
-  uint8_t* row_t = smem + kOffRowT;                              // token of each row
-  int* sel_e = reinterpret_cast<int*>(smem + kOffSel);
+  float* scl = reinterpret_cast<float*>(smem + off_scl(N));  // [stage][N] token scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + off_bar(N));
+  uint64_t* tok_full = full + kStages;
+  uint64_t* empty = tok_full + kStages;
+  uint64_t* set_full = empty + kStages;
+  uint64_t* set_empty = set_full + kSets;
+  uint64_t* drain = set_empty + kSets;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* act = reinterpret_cast<int*>(smem + off_act(N));              // active experts, shared ones first
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + off_mask(N));  // their tokens
+  int* sel_e = reinterpret_cast<int*>(smem + off_sel(N));
   float* sel_w = reinterpret_cast<float*>(sel_e + kMaxTokens * 32);
-  int* scan = reinterpret_cast<int*>(smem + kOffScan);  // [16] active, [16] rows, active experts, rows
+  int* scan = reinterpret_cast<int*>(smem + off_scan(N));            // [16] active; [32] all active
+  float* red = reinterpret_cast<float*>(smem + off_red(N));
+  float* bias = reinterpret_cast<float*>(smem + off_bias(N));
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t4 = lane & 3;
   const int G = gridDim.x, c = blockIdx.x;
-  const int Kb1 = p.dim / 128, Kb2 = p.inter / 128;
-  const int upe = p.inter / 8;                     // units of an expert
-  const int d0 = even(p.dim / 8, c, G) * 8, d1 = even(p.dim / 8, c + 1, G) * 8;  // this CTA's rows of w2
-  const int ngroups = (d1 - d0 + 15) / 16;
+  const int Kb1 = p.dim / 128, Kb2 = p.inter / 128;  // K blocks; Kb2 is also the units of an expert
   const uint32_t all_tokens = p.T == 32 ? 0xFFFFFFFFu : (1u << p.T) - 1u;
-  uint8_t* ring = smem + warp * kWarpRing;
-  if (tid == 0) *abort_flag = 0;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&tok_full[i], 1);
+      mbar_init(&empty[i], 5);  // the MMAs and the four finishers
+    }
+    for (int i = 0; i < kSets; ++i) {
+      mbar_init(&set_full[i], 1);
+      mbar_init(&set_empty[i], 4);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&map1);
+    tma_prefetch_desc(&map3);
+    tma_prefetch_desc(&map2);
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_u);
+  }
+  if (tid < p.E) bias[tid] = p.gate_bias ? __ldg(p.gate_bias + tid) : 0.f;
+  if (warp == kIssuer) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
 
   // The gate rows of this CTA's experts. The experts share the warps, each with a slice of
   // K: warp's vectors v0, v0 + step, ... of its expert's row.
@@ -273,100 +269,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   load_gate(c + warp / wpe * G);
 
-  // This warp's slots: K blocks of the shared units, then of the routed ones
-  // (each range of units, K laid end to end, split evenly over the grid's
-  // warps), then its w2 items, 16 rows at a time. A cursor walks a range.
+  // A cursor walks this CTA's K blocks of a range of units (the shared ones,
+  // the routed ones), K laid end to end.
   struct Cursor {
-    int a, rb, kb, left;  // active expert, its 8-row block, K block; K blocks left
+    int a, blk, kb, left;  // active expert, its 128-row block, K block; K blocks left
   };
-  const int gw = c * kWarps + warp, W = G * kWarps;
   auto cursor = [&](int first, int blocks) {
-    const int q0 = even_wide(blocks, gw, W), q1 = even_wide(blocks, gw + 1, W), u = q0 / Kb1;
-    return Cursor{first + u / upe, u % upe, q0 % Kb1, q1 - q0};
+    const int q0 = even(blocks, c, G), q1 = even(blocks, c + 1, G), u = q0 / Kb1;
+    return Cursor{first + u / Kb2, u % Kb2, q0 % Kb1, q1 - q0};
   };
   auto advance = [&](Cursor& k) {
     --k.left;
     if (++k.kb == Kb1) {
       k.kb = 0;
-      if (++k.rb == upe) {
-        k.rb = 0;
+      if (++k.blk == Kb2) {
+        k.blk = 0;
         ++k.a;
       }
     }
   };
-  const int shared_blocks = p.ns * upe * Kb1;
-  // Item i of phase 2 is K block i % Kb2 of active expert i / Kb2; this warp has
-  // items warp, warp + 16, ...
-  struct Item {
-    int a, kb;
-  };
-  auto next_item = [&](Item& k) {
-    k.kb += kWarps;
-    while (k.kb >= Kb2) {
-      k.kb -= Kb2;
-      ++k.a;
-    }
-  };
-  // Copies: lane l has 16 bytes l % 8 of rows l / 8 and l / 8 + 4 of a slot's low
-  // and high eight weight rows and of its eight tokens; chunk j of row r goes to
-  // chunk j ^ r. Lanes 0-9 also have a scale each.
+  const int shared_blocks = p.ns * Kb2 * Kb1;
+  // ---- producer (one lane): weight tiles, then the tokens' codes and scales that
+  // go with them, when those exist.
+  const bool producer = warp == kProducer && lane == 0;
   const uint64_t policy = l2_policy_evict_first();  // weights are read once
-  const int lane_row = lane >> 3, lane_byte = (lane & 7) * 16;
-  const uint32_t ring_addr = smem_u32(ring);
-  const uint32_t lane_dst = lane_row * 128 + (((lane & 7) ^ lane_row) << 4);
-  int put = 0;  // the slot that the next copy goes to
-  auto copy_weights = [&](const uint8_t* lo, const uint8_t* hi, int64_t pitch, bool has_hi) {
-    const uint32_t dst = ring_addr + put * kSlot + lane_dst, dst4 = ring_addr + put * kSlot + (lane_dst ^ 64) + 512;
-    copy16(dst, lo, policy);
-    copy16(dst4, lo + 4 * pitch, policy);
-    if (has_hi) {
-      copy16(dst + 1024, hi, policy);
-      copy16(dst4 + 1024, hi + 4 * pitch, policy);
-    }
+  int issued = 0;                                   // tiles
+  auto load_tile = [&](const CUtensorMap* map, int x, int y) {
+    const int s = issued % kStages;
+    if (issued >= kStages) wait(&empty[s], (issued / kStages - 1) & 1, abort_flag, p.err);
+    if (*abort_flag) return;
+    mbar_arrive_expect_tx(&full[s], kTileBytes);
+    tma_load_2d_hint(smem + s * kTileBytes, map, &full[s], x, y, policy);
+    ++issued;
   };
-  // What the tokens bring to a slot: codes of two of them, one scale.
-  const uint8_t *tok0 = nullptr, *tok1 = nullptr;
-  const float* scl = nullptr;
-  auto copy_operands = [&](int slot) {
-    const uint32_t at = ring_addr + slot * kSlot;
-    if (tok0) copy16_plain(at + kOffTok + lane_dst, tok0);
-    if (tok1) copy16_plain(at + kOffTok + (lane_dst ^ 64) + 512, tok1);
-    if (scl) copy4(at + kOffScl + lane * 4, scl);
+  auto load_tokens = [&](int s, const CUtensorMap* map, int x, int y, const float* scales) {
+    if (*abort_flag) return;
+    mbar_arrive_expect_tx(&tok_full[s], N * 128 + N * 4);
+    tma_load_2d(smem + off_tok() + s * N * 128, map, &tok_full[s], x, y);
+    bulk_load(scl + s * N, scales, N * 4, &tok_full[s]);
   };
-  auto open_operands = [&](const Cursor& k) {
-    const int cnt = __popc(mask[k.a]), rows0 = base[k.a];
-    tok0 = lane_row < cnt ? p.xq + row_t[rows0 + lane_row] * p.dim + k.kb * 128 + lane_byte : nullptr;
-    tok1 = lane_row + 4 < cnt ? p.xq + row_t[rows0 + lane_row + 4] * p.dim + k.kb * 128 + lane_byte : nullptr;
-    const int srow = (act[k.a] * upe + k.rb) / 16 * Kb1 + k.kb;
-    scl = lane < min(cnt, 8) ? p.xs + row_t[rows0 + lane] * Kb1 + k.kb
-          : lane == 8        ? p.w1_s + srow
-          : lane == 9        ? p.w3_s + srow
-                             : nullptr;
+  auto load_unit = [&](const Cursor& k) {  // one K block: w1's tile, w3's tile
+    const int y = ((k.a < p.ns ? p.E + k.a : act[k.a]) * Kb2 + k.blk) * 128;
+    load_tile(&map1, k.kb * 128, y);
+    load_tile(&map3, k.kb * 128, y);
   };
-  Cursor ahead = cursor(0, shared_blocks);  // of the copies
-  const uint8_t *src1 = nullptr, *src3 = nullptr;
-  bool fresh = true;  // the sources are not the cursor's unit's yet
-  auto copy_unit = [&](bool operands) {  // the slot at `ahead`
-    if (fresh || ahead.kb == 0) {
-      const int64_t row =
-          static_cast<int64_t>(ahead.a < p.ns ? p.E + ahead.a : act[ahead.a]) * p.inter + ahead.rb * 8 + lane_row;
-      const int64_t off = row * p.dim + ahead.kb * 128 + lane_byte;
-      src1 = p.w1 + off;
-      src3 = p.w3 + off;
-      if (operands) open_operands(ahead);
-      fresh = false;
-    }
-    copy_weights(src1, src3, p.dim, true);
-    src1 += 128;
-    src3 += 128;
-    if (operands) {
-      copy_operands(put);
-      if (tok0) tok0 += 128;
-      if (tok1) tok1 += 128;
-      if (scl) ++scl;
-    }
-    put = put + 1 == kSlots ? 0 : put + 1;
-    advance(ahead);
+  Cursor ahead = cursor(0, shared_blocks);
+  const int early = min(kStages / 2, ahead.left);  // K blocks asked for before the gate
+  auto first_tiles = [&] {
+    if (producer)
+#pragma unroll 1
+      for (int q = 0; q < early; ++q) {
+        load_unit(ahead);
+        advance(ahead);
+      }
+    __syncwarp();
   };
 
   // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
@@ -402,29 +358,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x) + static_cast<size_t>(i) * 32 + lane);
     const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
                         __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
-    quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128, p.xs + i);
+    const float s = quant_block(v, p.ue8m0 != 0, lane, p.xq + static_cast<size_t>(i) * 128);
+    if (lane == 0) p.xs[i % Kb1 * N + i / Kb1] = s;
   }
+  fence_proxy_async_all();  // TMA reads these
   // The shared experts' stream starts when the gate's operands are here (its
   // copies, asked for earlier, made the logits wait 4 us behind them).
-  const int early = min(kSlots - 1, ahead.left);
-  auto first_copies = [&] {
-#pragma unroll 1
-    for (int q = 0; q < early; ++q) {
-      copy_unit(false);
-      copy_commit();
-    }
-  };
-  if (c >= p.E) first_copies();
+  if (c >= p.E) first_tiles();
   {
     float* sums = sel_w;  // [warp][columns]
 #pragma unroll 1
     for (int e0 = c; e0 < p.E; e0 += per_cta * G) {
-      float acc[kCols];
+      float acc[N];
 #pragma unroll
-      for (int m = 0; m < kCols; ++m) acc[m] = 0.f;
+      for (int m = 0; m < N; ++m) acc[m] = 0.f;
       // (The row's K is at most kGateVecs passes, see kMaxDim.)
 #pragma unroll
-      for (int m = 0; m < kCols; ++m) {
+      for (int m = 0; m < N; ++m) {
         if (m < p.T) {
           const uint4* xv = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim) + v0;
 #pragma unroll
@@ -441,411 +391,440 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
-          if (lane == 0) sums[warp * kCols + m] = acc[m];
+          if (lane == 0) sums[warp * N + m] = acc[m];
         }
       }
       __syncthreads();
       for (int i = tid; i < per_cta * p.T; i += kThreads) {
         const int k = i / p.T, m = i % p.T;
         float v = 0.f;
-        for (int w = 0; w < wpe; ++w) v += sums[(k * wpe + w) * kCols + m];
+        for (int w = 0; w < wpe; ++w) v += sums[(k * wpe + w) * N + m];
         if (e0 + k * G < p.E) p.logits[static_cast<size_t>(m) * p.E + e0 + k * G] = v;
       }
-      if (e0 == c) first_copies();
+      if (e0 == c) first_tiles();
       __syncthreads();
       if (e0 + per_cta * G < p.E) load_gate(e0 + per_cta * G + warp / wpe * G);
     }
   }
   grid_barrier(0);
 
-  // The gate, by every CTA for itself, then the tables: tokens of each expert,
-  // active experts in order (shared ones first), their rows.
+  // The gate, by every CTA for itself, then the tables: active experts in order
+  // (shared ones first) and their tokens.
 #pragma unroll 1
-  for (int m = warp; m < p.T; m += kWarps) gate_of_token(p, m, lane, c == 0, sel_e, sel_w);
-  uint32_t* tokens_of = reinterpret_cast<uint32_t*>(base);  // by expert id, until the scan
+  for (int m = warp; m < p.T; m += kWarps) gate_of_token(p, bias, m, lane, c == 0, sel_e, sel_w);
+  uint32_t* tokens_of = reinterpret_cast<uint32_t*>(bias);  // by expert id; the bias has been used
+  __syncthreads();
   for (int e = tid; e < p.E; e += kThreads) tokens_of[e] = 0;
   __syncthreads();
-  const int pairs = p.T * p.k;
-  for (int i = tid; i < pairs; i += kThreads) atomicOr(&tokens_of[sel_e[i]], 1u << (i / p.k));
+  for (int i = tid; i < p.T * p.k; i += kThreads) atomicOr(&tokens_of[sel_e[i]], 1u << (i / p.k));
   __syncthreads();
   const uint32_t my_tokens = tid < p.E ? tokens_of[tid] : 0;
   const unsigned have = __ballot_sync(0xFFFFFFFFu, my_tokens != 0);
-  int upto = __popc(my_tokens);
+  if (lane == 0) scan[warp] = __popc(have);
+  __syncthreads();
+  int a0 = p.ns;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) {
-    scan[warp] = __popc(have);
-    scan[16 + warp] = upto;
-  }
-  __syncthreads();  // every thread has its tokens: base may be written
-  int a0 = p.ns, r0 = p.ns * p.T;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    a0 += w < warp ? scan[w] : 0;
-    r0 += w < warp ? scan[16 + w] : 0;
-  }
+  for (int w = 0; w < kWarps; ++w) a0 += w < warp ? scan[w] : 0;
   if (tid < p.ns) {
     act[tid] = p.E + tid;
     mask[tid] = all_tokens;
-    base[tid] = tid * p.T;
-  }
-  for (int i = tid; i < p.ns * p.T; i += kThreads) {
-    row_w[i] = 1.0f;
-    row_t[i] = static_cast<uint8_t>(i % p.T);
   }
   if (my_tokens) {
     const int a = a0 + __popc(have & ((1u << lane) - 1u));
-    const int r = r0 + upto - __popc(my_tokens);
     act[a] = tid;
     mask[a] = my_tokens;
-    base[a] = r;
-    int k = r;
-    for (uint32_t left = my_tokens; left; left &= left - 1, ++k) {
-      const int m = __ffs(left) - 1;
-      row_t[k] = static_cast<uint8_t>(m);
-      float w = 0.f;
-      for (int j = 0; j < p.k; ++j)
-        if (sel_e[m * p.k + j] == tid) w = sel_w[m * p.k + j];
-      row_w[k] = w;
-    }
   }
-  if (tid == kThreads - 1) {
-    scan[32] = a0 + __popc(have);
-    scan[33] = r0 + upto;
-  }
+  if (tid == kThreads - 1) scan[32] = a0 + __popc(have);
+  tc_fence_before_sync();
   __syncthreads();
-  const int nact = scan[32], nrows = scan[33];
-  const int routed_blocks = (nact - p.ns) * upe * Kb1;
-  // The next slot's copies, one group: the shared units', the routed units',
-  // w2's. Operands of w2 come with them once u is quantised.
-  int stage = 0, group_ahead = 0, early2 = 0;
-  const int nact2 = ngroups > 0 ? nact : 0;  // a CTA without rows of w2 has no items
-  bool have_u = false;
-  Item item_ahead{warp / Kb2, warp % Kb2};
-  const uint8_t* src2 = nullptr;
-  const int sblk = d0 / 128 * Kb2, sblk2 = (d1 - 1) / 128 * Kb2;  // the CTA's rows lie in one or two 128-row blocks
-  auto open_item = [&](const Item& k) {
-    const uint32_t mk = mask[k.a];
-    const int m0 = NT == 1 ? 0 : (__ffs(mk) - 1) & ~7;  // its lowest column tile
-    auto row_of = [&](int m) { return base[k.a] + __popc(mk & ((1u << m) - 1u)); };
-    const int ma = m0 + lane_row, mb = ma + 4, ms = m0 + (lane & 7);
-    tok0 = (mk >> ma) & 1u ? p.uq + static_cast<size_t>(row_of(ma)) * p.inter + k.kb * 128 + lane_byte : nullptr;
-    tok1 = (mk >> mb) & 1u ? p.uq + static_cast<size_t>(row_of(mb)) * p.inter + k.kb * 128 + lane_byte : nullptr;
-    const int srow = act[k.a] * (p.dim / 128) * Kb2 + k.kb;
-    scl = lane < 8 ? ((mk >> ms) & 1u ? p.us + row_of(ms) * Kb2 + k.kb : nullptr)
-          : lane == 8 ? p.w2_s + srow + sblk
-          : lane == 9 ? p.w2_s + srow + sblk2
-                      : nullptr;
+  tc_fence_after_sync();
+  const int nact = scan[32];
+  const uint32_t tmem = *tmem_slot;
+  const int routed_blocks = (nact - p.ns) * Kb2 * Kb1;
+  auto gate_weight = [&](int a, int m) {
+    if (a < p.ns) return 1.0f;
+    float w = 0.f;
+    for (int j = 0; j < p.k; ++j)
+      if (sel_e[m * p.k + j] == act[a]) w = sel_w[m * p.k + j];
+    return w;
   };
-  auto copy_next = [&] {
-    if (ahead.left == 0 && stage == 0) {
-      stage = 1;
-      ahead = cursor(p.ns, routed_blocks);
-      fresh = true;
-    }
-    if (ahead.left > 0) {
-      copy_unit(true);
-    } else if (item_ahead.a < nact2) {
-      if (group_ahead == 0) {
-        src2 = p.w2 + (static_cast<int64_t>(act[item_ahead.a]) * p.dim + d0 + lane_row) * p.inter +
-               item_ahead.kb * 128 + lane_byte;
-        if (have_u) {
-          open_item(item_ahead);
-          copy_operands(put);
+  constexpr uint32_t kIdesc = idesc_e4m3_f32(128, N);
+  // Streaming positions, alike in every role: tiles and K blocks so far.
+  int tile = 0, kblock = 0;
+  uint32_t tok_phase = 0;  // bit s: phase of tok_full[s]
+  auto tok_parity = [&](int s) {
+    const uint32_t ph = (tok_phase >> s) & 1;
+    tok_phase ^= 1u << s;
+    return ph;
+  };
+  // One K block's MMAs: `tiles` weight tiles against its tokens, into set
+  // kblock % kSets. The whole warp calls it.
+  auto multiply = [&](int tiles) {
+    const int set = kblock % kSets, s0 = tile % kStages;
+    if (kblock >= kSets) wait(&set_empty[set], (kblock / kSets - 1) & 1, abort_flag, p.err);
+    wait(&tok_full[s0], tok_parity(s0), abort_flag, p.err);
+    const uint64_t bd = sdesc_kmajor_sw128(smem_u32(smem + off_tok() + s0 * N * 128));
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+      const int s = (tile + t) % kStages;
+      wait(&full[s], ((tile + t) / kStages) & 1, abort_flag, p.err);
+      __syncwarp();
+      tc_fence_after_sync();
+      if (!__any_sync(0xFFFFFFFFu, *abort_flag != 0) && elect_one_sync()) {
+        const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + s * kTileBytes));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_e4m3(tmem + (set * 2 + t) * N, ad + 2 * k, bd + 2 * k, kIdesc, k > 0);
+        if (t == tiles - 1) {
+          for (int q = 0; q < tiles; ++q) mma_commit(&empty[(tile + q) % kStages]);
+          mma_commit(&set_full[set]);
         }
       }
-      copy_weights(src2, src2 + 8 * static_cast<int64_t>(p.inter), p.inter, d0 + group_ahead * 16 + 8 < d1);
-      put = put + 1 == kSlots ? 0 : put + 1;
-      early2 += have_u ? 0 : 1;
-      src2 += 16 * static_cast<int64_t>(p.inter);
-      if (++group_ahead == ngroups) {
-        group_ahead = 0;
-        next_item(item_ahead);
+      __syncwarp();
+    }
+    tile += tiles;
+    ++kblock;
+  };
+  // The finishers' side: the tokens' scales of the K block and its `tiles` products.
+  const int row = (warp - kFinisher) * 32 + lane;  // of the 128 weight rows
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  auto products_ready = [&] {
+    const int s0 = tile % kStages;
+    wait(&tok_full[s0], tok_parity(s0), abort_flag, p.err);
+    wait(&set_full[kblock % kSets], (kblock / kSets) & 1, abort_flag, p.err);
+    __syncwarp();
+    tc_fence_after_sync();
+  };
+  // acc += (product t of the K block) * (token scale * ws), for tokens in mk.
+  auto promote = [&](float (&acc)[N], int t, float ws, uint32_t mk) {
+    uint32_t d[N];
+    tmem_ld_cols(t_lane + (kblock % kSets * 2 + t) * N, d);
+    const float4* sc = reinterpret_cast<const float4*>(scl + tile % kStages * N);
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 v = sc[j / 4];
+      if ((mk >> j) & 1u) acc[j] = fmaf(__uint_as_float(d[j]), v.x * ws, acc[j]);
+      if ((mk >> (j + 1)) & 1u) acc[j + 1] = fmaf(__uint_as_float(d[j + 1]), v.y * ws, acc[j + 1]);
+      if ((mk >> (j + 2)) & 1u) acc[j + 2] = fmaf(__uint_as_float(d[j + 2]), v.z * ws, acc[j + 2]);
+      if ((mk >> (j + 3)) & 1u) acc[j + 3] = fmaf(__uint_as_float(d[j + 3]), v.w * ws, acc[j + 3]);
+    }
+  };
+  auto products_done = [&](int tiles) {
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&set_empty[kblock % kSets]);
+      for (int q = 0; q < tiles; ++q) mbar_arrive(&empty[(tile + q) % kStages]);
+    }
+    tile += tiles;
+    ++kblock;
+  };
+
+  // ---- phase 1 -------------------------------------------------------------------
+  // Items of phase 2: K blocks of row tiles of w2, expert by expert.
+  const int tile_blocks = nact * Kb2, blocks2 = p.dim / 128 * tile_blocks;
+  const int q2 = even(blocks2, c, G), n2 = even(blocks2, c + 1, G) - q2;
+  struct Item {
+    int tile, a, kb;
+  };
+  auto next_item = [&](Item& k) {
+    if (++k.kb == Kb2) {
+      k.kb = 0;
+      if (++k.a == nact) {
+        k.a = 0;
+        ++k.tile;
       }
     }
-    copy_commit();
   };
-  // Operands of the slots that were asked for before x was quantised.
-  {
+  const Item first_item{q2 / tile_blocks, q2 / Kb2 % nact, q2 % Kb2};
+  Item item_ahead = first_item;
+  auto load_item = [&](const Item& k) { load_tile(&map2, k.kb * 128, act[k.a] * p.dim + k.tile * 128); };
+  const int early2 = min(kStages, n2);  // w2 tiles asked for before u is quantised
+  const int phase1_tiles =
+      2 * (even(shared_blocks, c + 1, G) - even(shared_blocks, c, G) + even(routed_blocks, c + 1, G) - even(routed_blocks, c, G));
+  if (producer) {
+    fence_proxy_async_all();
     Cursor k = cursor(0, shared_blocks);
 #pragma unroll 1
     for (int q = 0; q < early; ++q) {
-      open_operands(k);
-      copy_operands(q);
+      load_tokens(2 * q, &map_x, k.kb * 128, 0, p.xs + k.kb * N);
       advance(k);
     }
-    copy_commit();
-    fresh = true;
-  }
 #pragma unroll 1
-  for (int q = early; q < kSlots - 1; ++q) copy_next();
-  copy_wait<0>();
-  int take = 0;  // the slot that is multiplied next
-  auto slot_ready = [&] {
-    copy_wait<kSlots - 2>();
-    __syncwarp();
-    const uint8_t* w = ring + take * kSlot;
-    take = take + 1 == kSlots ? 0 : take + 1;
-    return w;
-  };
-  // Column 8-tile's fragment and scales of a slot.
-  auto slot_frag = [&](const uint8_t* w) {
-    Frag f;
-    const uint8_t* x = w + kOffTok + g * 128;
-    f.b0 = *reinterpret_cast<const uint4*>(x + (((2 * t4) ^ g) << 4));
-    f.b1 = *reinterpret_cast<const uint4*>(x + (((2 * t4 + 1) ^ g) << 4));
-    const float2 sc = *reinterpret_cast<const float2*>(w + kOffScl + t4 * 8);
-    f.s0 = sc.x;
-    f.s1 = sc.y;
-    return f;
-  };
-
-  // Phase 1: u = silu(w1 x) (w3 x).
-  auto store_u = [&](int a, int rb, int cnt, int nt, const float (&v)[4]) {
-    // Lane (g, t4) has columns 2 t4, 2 t4 + 1 of row g: h1 and h3.
-    const int col = nt * 8 + 2 * t4;
-    float* dst = p.u + static_cast<size_t>(base[a] + col) * p.inter + rb * 8 + g;
-    if (col < cnt) dst[0] = silu_mul(v[0], v[2]);
-    if (col + 1 < cnt) dst[p.inter] = silu_mul(v[1], v[3]);
-  };
+    for (int range = 0; range < 2; ++range) {
+      if (range) ahead = cursor(p.ns, routed_blocks);
+#pragma unroll 1
+      for (; ahead.left > 0; advance(ahead)) {
+        const int s = issued % kStages;
+        load_unit(ahead);
+        load_tokens(s, &map_x, ahead.kb * 128, 0, p.xs + ahead.kb * N);
+      }
+    }
+#pragma unroll 1
+    for (int q = 0; q < early2; ++q) {
+      load_item(item_ahead);
+      next_item(item_ahead);
+    }
+  } else if (warp == kIssuer) {
+#pragma unroll 1
+    for (int q = phase1_tiles / 2; q > 0; --q) multiply(2);
+  } else if (warp >= kFinisher && warp < kFinisher + 4) {
+    int flips = 0;  // which half of `red`
+#pragma unroll 1
+    for (int range = 0; range < 2; ++range) {
+      Cursor at = range ? cursor(p.ns, routed_blocks) : cursor(0, shared_blocks);
+#pragma unroll 1
+      while (at.left > 0) {
+        // One unit, or this CTA's part of it.
+        const int a = at.a, blk = at.blk, from = at.kb, n = min(at.left, Kb1 - from);
+        const uint32_t mk = mask[a];
+        const float* s1 = p.w1_s + (act[a] * Kb2 + blk) * Kb1 + from;
+        const float* s3 = p.w3_s + (s1 - p.w1_s);
+        float acc1[N], acc3[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc1[j] = acc3[j] = 0.f;
+        float w1s = __ldg(s1), w3s = __ldg(s3);
+#pragma unroll 1
+        for (int q = 0; q < n; ++q) {
+          const float w1n = q + 1 < n ? __ldg(s1 + q + 1) : 0.f, w3n = q + 1 < n ? __ldg(s3 + q + 1) : 0.f;
+          products_ready();
+          promote(acc1, 0, w1s, 0xFFFFFFFFu);
+          promote(acc3, 1, w3s, 0xFFFFFFFFu);
+          products_done(2);
+          w1s = w1n;
+          w3s = w3n;
+          advance(at);
+        }
+        if (n == Kb1) {
+          // The whole unit: its 128 rows are one block of u for every token.
+          float* top = red + (flips & 1) * N * 4;
+          ++flips;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            if ((mk >> j) & 1u) {
+              acc1[j] = silu_mul(acc1[j], acc3[j]);
+              float m = fabsf(acc1[j]);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+              if (lane == 0) top[j * 4 + warp - kFinisher] = m;
+            }
+          }
+          named_barrier_sync(2, 128);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            if ((mk >> j) & 1u) {
+              const float4 m = *reinterpret_cast<const float4*>(top + j * 4);
+              const float s = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)), p.ue8m0 != 0);
+              p.uq[(static_cast<size_t>(a) * p.T + j) * p.inter + blk * 128 + row] =
+                  static_cast<uint8_t>(e4m3x2(__fdiv_rn(acc1[j], s), 0.f));
+              if (row == j) p.us[(a * Kb2 + blk) * N + j] = s * gate_weight(a, j);
+            }
+          }
+        } else {
+          float* t = p.part + static_cast<size_t>((c * 2 + range) * 2 + (from == 0 ? 1 : 0)) * 2 * p.T * 128 + row;
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if ((mk >> j) & 1u) {
+              t[j * 128] = acc1[j];
+              t[(p.T + j) * 128] = acc3[j];
+            }
+        }
+      }
+    }
+    fence_proxy_async_all();  // TMA reads uq and us
+  }
+  __syncwarp();
+  grid_barrier(1);
+  // Units cut between CTAs, a warp per (unit, token): the parts added in CTA
+  // order, then quantised.
 #pragma unroll 1
   for (int range = 0; range < 2; ++range) {
-    Cursor at = range ? cursor(p.ns, routed_blocks) : cursor(0, shared_blocks);
-    if (at.left == 0) continue;
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-    int from = at.kb, cnt = __popc(mask[at.a]);  // the unit's first K block here, its tokens
+    const int blocks = range ? routed_blocks : shared_blocks, first = range ? p.ns : 0;
 #pragma unroll 1
-    while (true) {
-      const uint8_t* w = slot_ready();
-      const float2 ws = *reinterpret_cast<const float2*>(w + kOffScl + 32);
-      block_product(w, w + 1024, slot_frag(w), ws.x, ws.y, g, t4, acc[0]);
-#pragma unroll
-      for (int nt = 1; nt < NT; ++nt) {
-        if (nt * 8 >= cnt) break;
-        const int rows0 = base[at.a], col = nt * 8 + g, cs = nt * 8 + 2 * t4;
-        Frag x;
-        x.b0 = x.b1 = make_uint4(0u, 0u, 0u, 0u);
-        if (col < cnt) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.xq + row_t[rows0 + col] * p.dim + at.kb * 128 + t4 * 32);
-          x.b0 = __ldcg(src);
-          x.b1 = __ldcg(src + 1);
-        }
-        x.s0 = cs < cnt ? __ldcg(p.xs + row_t[rows0 + cs] * Kb1 + at.kb) : 0.f;
-        x.s1 = cs + 1 < cnt ? __ldcg(p.xs + row_t[rows0 + cs + 1] * Kb1 + at.kb) : 0.f;
-        block_product(w, w + 1024, x, ws.x, ws.y, g, t4, acc[nt]);
+    for (int i = warp * G + c; i < blocks / Kb1 * p.T; i += G * kWarps) {
+      const int u = i / p.T, m = i - u * p.T, a = first + u / Kb2;
+      if (!((mask[a] >> m) & 1u)) continue;
+      const int c0 = part_of(blocks, u * Kb1, G), c1 = part_of(blocks, u * Kb1 + Kb1 - 1, G);
+      if (c0 == c1) continue;
+      float4 h1 = make_float4(0.f, 0.f, 0.f, 0.f), h3 = h1;
+#pragma unroll 4
+      for (int q = c0; q <= c1; ++q) {
+        // (With fewer K blocks than CTAs some CTAs have none.)
+        if (blocks < G && even(blocks, q, G) == even(blocks, q + 1, G)) continue;
+        const float* t = p.part + static_cast<size_t>((q * 2 + range) * 2 + (q == c0 ? 1 : 0)) * 2 * p.T * 128 + m * 128;
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(t) + lane);
+        const float4 z = __ldcg(reinterpret_cast<const float4*>(t + p.T * 128) + lane);
+        h1 = make_float4(h1.x + x.x, h1.y + x.y, h1.z + x.z, h1.w + x.w);
+        h3 = make_float4(h3.x + z.x, h3.y + z.y, h3.z + z.z, h3.w + z.w);
       }
-      copy_next();
-      const Cursor now = at;
-      advance(at);
-      if (at.kb == 0 || at.left == 0) {
-        if (from == 0 && at.kb == 0) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (nt * 8 < cnt) store_u(now.a, now.rb, cnt, nt, acc[nt]);
-        } else {
-          float4* t = reinterpret_cast<float4*>(p.part + (static_cast<size_t>(gw) * 4 + range * 2 + (from == 0 ? 1 : 0)) *
-                                                             kTile) + lane;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (nt * 8 < cnt) t[nt * 32] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
-        }
-        if (at.left == 0) break;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        from = 0;
-        cnt = __popc(mask[at.a]);
-      }
+      const float v[4] = {silu_mul(h1.x, h3.x), silu_mul(h1.y, h3.y), silu_mul(h1.z, h3.z), silu_mul(h1.w, h3.w)};
+      const int blk = u % Kb2;
+      const float s = quant_block(v, p.ue8m0 != 0, lane, p.uq + (static_cast<size_t>(a) * p.T + m) * p.inter + blk * 128);
+      if (lane == 0) p.us[(a * Kb2 + blk) * N + m] = s * gate_weight(a, m);
     }
   }
-  grid_barrier(1);
-  // u by 128-column blocks of a row, four elements per lane: stored by the warp
-  // that had all of a unit's K, else added up from its parts; then quantised.
-#pragma unroll 1
-  for (int i = warp * G + c; i < nrows * Kb2; i += W) {
-    const int row = i / Kb2, kb = i % Kb2;
-    int lo = 0, hi = nact - 1;  // the active expert of the row: the last whose base is not past it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (base[mid] <= row) lo = mid;
-      else hi = mid - 1;
-    }
-    const int col = row - base[lo], range = lo < p.ns ? 0 : 1, blocks = range ? routed_blocks : shared_blocks;
-    const int unit = (lo - (range ? p.ns : 0)) * upe + kb * 16 + lane / 2;
-    // The warp of K block x of a range is the largest w with even(blocks, w) <= x.
-    const int w0 = static_cast<int>((static_cast<int64_t>(unit * Kb1 + 1) * W - 1) / blocks);
-    const int w1 = static_cast<int>((static_cast<int64_t>((unit + 1) * Kb1) * W - 1) / blocks);
-    float v[4];
-    if (w0 == w1) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(p.u) + static_cast<size_t>(i) * 32 + lane);
-      v[0] = u.x;
-      v[1] = u.y;
-      v[2] = u.z;
-      v[3] = u.w;
-    } else {
-      float h1[4] = {0.f, 0.f, 0.f, 0.f}, h3[4] = {0.f, 0.f, 0.f, 0.f};
-      const int in_tile = ((col >> 3) * 32 + (lane & 1) * 16 + ((col & 7) >> 1)) * 4 + (col & 1);
-#pragma unroll 1
-      for (int w = w0; w <= w1; w += 4) {
-        float a[4][4], b[4][4];  // four parts' loads in flight together
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float* t = p.part + (static_cast<size_t>(w + k) * 4 + range * 2 + (w + k == w0 ? 1 : 0)) * kTile + in_tile;
-          // (With fewer K blocks than warps some warps have none.)
-          const bool there = w + k <= w1 && (blocks >= W || even_wide(blocks, w + k, W) < even_wide(blocks, w + k + 1, W));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            a[k][r] = there ? __ldcg(t + r * 16) : 0.f;
-            b[k][r] = there ? __ldcg(t + r * 16 + 2) : 0.f;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            h1[r] += a[k][r];
-            h3[r] += b[k][r];
-          }
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = silu_mul(h1[r], h3[r]);
-    }
-    quant_block(v, p.ue8m0 != 0, lane, p.uq + static_cast<size_t>(i) * 128, p.us + i);
-  }
+  fence_proxy_async_all();
   grid_barrier(2);
 
-  // Phase 2: this CTA's rows of every active expert's w2, weighted and summed
-  // over the experts in the accumulators.
-  float acc[kMaxGroups][NT][4];
-#pragma unroll
-  for (int q = 0; q < kMaxGroups; ++q)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.f;
-  const int rows_in_first = (d0 / 128 + 1) * 128 - d0;  // rows of the CTA's first 128-row block
-  const bool odd = ((d1 - d0) & 8) != 0;                // the last group has no high half
-  // Operands of the slots that were asked for before u was quantised.
-  have_u = true;
-  Item it{warp / Kb2, warp % Kb2};
-  {
-    Item k = it;
-    int slot = take;
+  // ---- phase 2 -------------------------------------------------------------------
+  if (producer) {
+    fence_proxy_async_all();
+    Item k = first_item;
 #pragma unroll 1
-    for (int q = 0; q < early2; q += ngroups) {
-      open_item(k);
-      copy_operands(slot);
-      slot = (slot + ngroups) % kSlots;
+    for (int q = 0; q < early2; ++q) {
+      load_tokens((phase1_tiles + q) % kStages, &map_u, k.kb * 128, k.a * p.T, p.us + (k.a * Kb2 + k.kb) * N);
       next_item(k);
     }
-    copy_commit();
-    copy_wait<0>();
-  }
 #pragma unroll 1
-  while (it.a < nact2) {
-    const uint32_t mk = mask[it.a];
-    const int r_base = base[it.a], lowest = NT == 1 ? 0 : (__ffs(mk) - 1) >> 3;
-    Frag f0, more[NT > 1 ? NT - 1 : 1];  // column tiles' fragments, for all groups
-    float wa = 0.f, wb = 0.f;
-    if constexpr (NT > 1) {
+    for (int q = early2; q < n2; ++q) {
+      const int s = issued % kStages;
+      load_item(item_ahead);
+      load_tokens(s, &map_u, item_ahead.kb * 128, item_ahead.a * p.T, p.us + (item_ahead.a * Kb2 + item_ahead.kb) * N);
+      next_item(item_ahead);
+    }
+  } else if (warp == kIssuer) {
+#pragma unroll 1
+    for (int q = 0; q < n2; ++q) multiply(1);
+  } else if (warp >= kFinisher && warp < kFinisher + 4) {
+    Item at = first_item;
+    int left = n2;
+#pragma unroll 1
+    while (left > 0) {
+      // One row tile, or this CTA's part of it.
+      const int from = at.a * Kb2 + at.kb, n = min(left, tile_blocks - from), tl = at.tile;
+      left -= n;
+      float acc[N];
 #pragma unroll
-      for (int nt = 1; nt < NT; ++nt) {
-        if (nt == lowest || !((mk >> (nt * 8)) & 0xFFu)) continue;
-        Frag& f = more[nt - 1];
-        f.b0 = f.b1 = make_uint4(0u, 0u, 0u, 0u);
-        f.s0 = f.s1 = 0.f;
-        const int m = nt * 8 + g, m2 = nt * 8 + 2 * t4;
-        const int r = r_base + __popc(mk & ((1u << m) - 1u)), r2 = r_base + __popc(mk & ((1u << m2) - 1u));
-        if ((mk >> m) & 1u) {
-          const uint4* src =
-              reinterpret_cast<const uint4*>(p.uq + static_cast<size_t>(r) * p.inter + it.kb * 128 + t4 * 32);
-          f.b0 = __ldcg(src);
-          f.b1 = __ldcg(src + 1);
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+      auto scale_of = [&](const Item& k) { return __ldg(p.w2_s + (act[k.a] * (p.dim / 128) + k.tile) * Kb2 + k.kb); };
+      float ws = scale_of(at);
+#pragma unroll 1
+      for (int q = 0; q < n; ++q) {
+        const uint32_t mk = mask[at.a];
+        next_item(at);
+        const float wn = q + 1 < n ? scale_of(at) : 0.f;
+        products_ready();
+        promote(acc, 0, ws, mk);  // columns of other tokens hold nothing of theirs
+        products_done(1);
+        ws = wn;
+      }
+      __nv_bfloat16* y = p.y + tl * 128 + row;
+      if (n == tile_blocks) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (j < p.T) y[static_cast<size_t>(j) * p.dim] = __float2bfloat16_rn(acc[j]);
+      } else {
+        float* t = p.part2 + static_cast<size_t>(c * 2 + (from == 0 ? 1 : 0)) * p.T * 128 + row;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (j < p.T) t[j * 128] = acc[j];
+        // The last of the tile's CTAs adds up the parts, in CTA order.
+        const int c0 = part_of(blocks2, tl * tile_blocks, G), c1 = part_of(blocks2, (tl + 1) * tile_blocks - 1, G);
+        const unsigned parts = blocks2 >= G ? c1 - c0 + 1 : tile_blocks;
+        __threadfence();
+        named_barrier_sync(2, 128);
+        if (warp == kFinisher && lane == 0) {
+          unsigned* count = p.counters + 16 + tl / 4;  // at most 192 parts: a byte per tile
+          const int sh = tl % 4 * 8;
+          const bool last = ((atomicAdd(count, 1u << sh) >> sh) & 0xFFu) == parts - 1;
+          if (last) atomicSub(count, parts << sh);
+          scan[48] = last;
+          __threadfence();
         }
-        const int r3 = r2 + ((mk >> m2) & 1u);
-        if ((mk >> m2) & 1u) f.s0 = __ldcg(p.us + r2 * Kb2 + it.kb) * row_w[r2];
-        if ((mk >> (m2 + 1)) & 1u) f.s1 = __ldcg(p.us + r3 * Kb2 + it.kb) * row_w[r3];
+        named_barrier_sync(2, 128);
+        if (scan[48]) {
+#pragma unroll 1
+          for (int j = 0; j < p.T; ++j) {
+            float v = 0.f;
+#pragma unroll 4
+            for (int q = c0; q <= c1; ++q) {
+              if (blocks2 < G && even(blocks2, q, G) == even(blocks2, q + 1, G)) continue;
+              v += __ldcg(p.part2 + (static_cast<size_t>(q * 2 + (q == c0 ? 1 : 0)) * p.T + j) * 128 + row);
+            }
+            y[static_cast<size_t>(j) * p.dim] = __float2bfloat16_rn(v);
+          }
+        }
+        named_barrier_sync(2, 128);  // before scan[48] is written again
       }
     }
-#pragma unroll
-    for (int q = 0; q < kMaxGroups; ++q)
-      if (q < ngroups) {
-        const uint8_t* w = slot_ready();
-        if (q == 0) {
-          // The item's first slot carries the lowest tile's operands. Columns
-          // without a token have zero codes: their sums go on for other experts.
-          f0 = slot_frag(w);
-          const int m = lowest * 8 + g, m2 = lowest * 8 + 2 * t4;
-          const int r2 = r_base + __popc(mk & ((1u << m2) - 1u));
-          if (!((mk >> m) & 1u)) f0.b0 = f0.b1 = make_uint4(0u, 0u, 0u, 0u);
-          f0.s0 = (mk >> m2) & 1u ? f0.s0 * row_w[r2] : 0.f;
-          f0.s1 = (mk >> (m2 + 1)) & 1u ? f0.s1 * row_w[r2 + ((mk >> m2) & 1u)] : 0.f;
-          const float2 ws = *reinterpret_cast<const float2*>(w + kOffScl + 32);
-          wa = ws.x;
-          wb = ws.y;
-        }
-        const float wlo = q * 16 < rows_in_first ? wa : wb, whi = q * 16 + 8 < rows_in_first ? wa : wb;
-        // A last group of 8 rows takes them twice; the second copy is not stored.
-        const uint8_t* hi = odd && q == ngroups - 1 ? w : w + 1024;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (NT > 1 && !((mk >> (nt * 8)) & 0xFFu)) continue;
-          const Frag& f = nt == 0 || nt == lowest ? f0 : more[nt > 0 ? nt - 1 : 0];
-          block_product(w, hi, f, wlo, whi, g, t4, acc[q][nt]);
-        }
-        copy_next();
-      }
-    next_item(it);
   }
-  copy_wait<0>();
+  __syncwarp();
+  if (*abort_flag) {
+    // Copies and MMAs in flight are waited for (bounded) before the CTA ends.
+    if (producer)
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        wait(&full[i % kStages], (i / kStages) & 1, nullptr, p.err);
+    if (warp == kIssuer) {
+      if (elect_one_sync()) mma_commit(drain);
+      __syncwarp();
+      wait(drain, 0, nullptr, p.err);
+    }
+  }
+  tc_fence_before_sync();
   __syncthreads();
-  // The rings hold the warps' sums [warp][row][columns] now.
-  float* sums = reinterpret_cast<float*>(smem);
-  const int rows2 = ngroups * 16;
-#pragma unroll
-  for (int q = 0; q < kMaxGroups; ++q)
-    if (q < ngroups)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float* t = sums + (warp * rows2 + q * 16 + g) * kCols + nt * 8 + 2 * t4;
-        *reinterpret_cast<float2*>(t) = make_float2(acc[q][nt][0], acc[q][nt][1]);
-        *reinterpret_cast<float2*>(t + 8 * kCols) = make_float2(acc[q][nt][2], acc[q][nt][3]);
-      }
-  __syncthreads();
-  for (int i = tid; i < (d1 - d0) * p.T; i += kThreads) {
-    const int m = i / (d1 - d0), r = i % (d1 - d0);
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sums[(w * rows2 + r) * kCols + m];
-    p.y[static_cast<size_t>(m) * p.dim + d0 + r] = __float2bfloat16_rn(v);
+  if (warp == kIssuer) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
   }
   // The last CTA to leave zeroes the counters for the next call.
   if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u) {
     p.counters[0] = p.counters[1] = p.counters[2] = 0;
     p.counters[3] = 0;
+    if (*abort_flag)
+      for (int i = 16; i < 32; ++i) p.counters[i] = 0;
   }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn layer_map_encoder() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* q = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &st) == cudaSuccess &&
+        st == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(q);
+  });
+  return fn;
+}
+
+// e4m3 rows x cols, boxes of 128 columns x box_rows, 128-byte swizzled; rows past
+// the end read as zeros.
+bool make_code_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  EncodeTiledFn enc = layer_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 
 struct LayerSizes {
-  size_t logits, xq, xs, u, uq, us, part, total;
+  int64_t active;  // experts at most
+  int cols;        // token columns
+  size_t logits, xq, xs, uq, us, part, part2, total;
 };
 
 LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t topk, int64_t ns) {
   LayerSizes z{};
-  const size_t rows = static_cast<size_t>(T) * (topk + ns);
+  z.active = (T * topk < E ? T * topk : E) + ns;
+  z.cols = T <= 16 ? 16 : 32;
   z.logits = 256;
   z.xq = z.logits + align256(static_cast<size_t>(T) * E * 4);
   z.xs = z.xq + align256(static_cast<size_t>(T) * dim);
-  z.u = z.xs + align256(static_cast<size_t>(T) * (dim / 128) * 4);
-  z.uq = z.u + align256(rows * inter * 4);
-  z.us = z.uq + align256(rows * inter);
-  z.part = z.us + align256(rows * (inter / 128) * 4);
-  const size_t cols = T <= 8 ? 8 : T <= 16 ? 16 : 32;
-  z.total = z.part + static_cast<size_t>(kMaxCtas) * kWarps * 4 * 16 * cols * 4;  // a tile is 16 rows x cols floats
+  z.uq = z.xs + align256(static_cast<size_t>(dim / 128) * z.cols * 4);
+  z.us = z.uq + align256(static_cast<size_t>(z.active) * T * inter);
+  z.part = z.us + align256(static_cast<size_t>(z.active) * (inter / 128) * z.cols * 4);
+  z.part2 = z.part + static_cast<size_t>(kMaxCtas) * 4 * 2 * T * 128 * 4;
+  z.total = z.part2 + static_cast<size_t>(kMaxCtas) * 2 * T * 128 * 4;
   return z;
 }
 
@@ -855,26 +834,27 @@ bool layer_shape_ok(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t to
          ns >= 0 && ns <= kMaxShared;
 }
 
-template <int NT>
-int layer_launch(const DevInfo* d, const LayerParams& p, cudaStream_t stream) {
+template <int N>
+int layer_launch(const DevInfo* d, const CUtensorMap& m1, const CUtensorMap& m3, const CUtensorMap& m2,
+                 const CUtensorMap& mx, const CUtensorMap& mu, const LayerParams& p, cudaStream_t stream) {
   static bool attr_done[64] = {};
-  auto kern = moe_layer_kernel<NT>;
+  auto kern = moe_layer_kernel<N>;
   if (d->device >= 64 || !attr_done[d->device]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLayerSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, layer_smem(N)) != cudaSuccess)
       return FP8BLK_ERR_CUDA;
     if (d->device < 64) attr_done[d->device] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(d->sm_count));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kLayerSmem;
+  cfg.dynamicSmemBytes = layer_smem(N);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, m1, m3, m2, mx, mu, p));
 }
 
 }  // namespace
@@ -912,8 +892,7 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   if (workspace_bytes < z.total) return FP8BLK_ERR_WORKSPACE;
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
-  // Phase 2 keeps a CTA's rows of w2 in its accumulators.
-  if ((dim / 8 + d->sm_count - 1) / d->sm_count > 2 * kMaxGroups || d->sm_count > kMaxCtas) return FP8BLK_ERR_SHAPE;
+  if (d->sm_count > kMaxCtas) return FP8BLK_ERR_SHAPE;
   // The gate product keeps its share of an expert's row in registers.
   const int64_t per_cta = (E + d->sm_count - 1) / d->sm_count;
   if (per_cta > kWarps || dim / 8 > kWarps / per_cta * 32 * kGateVecs) return FP8BLK_ERR_SHAPE;
@@ -932,10 +911,10 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.logits = reinterpret_cast<float*>(ws + z.logits);
   p.xq = ws + z.xq;
   p.xs = reinterpret_cast<float*>(ws + z.xs);
-  p.u = reinterpret_cast<float*>(ws + z.u);
   p.uq = ws + z.uq;
   p.us = reinterpret_cast<float*>(ws + z.us);
   p.part = reinterpret_cast<float*>(ws + z.part);
+  p.part2 = reinterpret_cast<float*>(ws + z.part2);
   p.err = d->err_word;
   p.T = static_cast<int>(T);
   p.dim = static_cast<int>(dim);
@@ -949,11 +928,12 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.normalize = normalize != 0;
   p.ue8m0 = scale_fmt_ue8m0(scale_fmt);
   p.route_scale = route_scale;
-  p.w1 = static_cast<const uint8_t*>(w1_e4m3);
-  p.w3 = static_cast<const uint8_t*>(w3_e4m3);
-  p.w2 = static_cast<const uint8_t*>(w2_e4m3);
+  const uint64_t K = static_cast<uint64_t>(E + n_shared);
+  CUtensorMap m1, m3, m2, mx, mu;
+  if (!make_code_map(&m1, w1_e4m3, K * inter, dim, 128) || !make_code_map(&m3, w3_e4m3, K * inter, dim, 128) ||
+      !make_code_map(&m2, w2_e4m3, K * dim, inter, 128) || !make_code_map(&mx, p.xq, T, dim, z.cols) ||
+      !make_code_map(&mu, p.uq, static_cast<uint64_t>(z.active) * T, inter, z.cols))
+    return FP8BLK_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return T <= 8    ? layer_launch<1>(d, p, cs)
-         : T <= 16 ? layer_launch<2>(d, p, cs)
-                   : layer_launch<4>(d, p, cs);
+  return z.cols == 16 ? layer_launch<16>(d, m1, m3, m2, mx, mu, p, cs) : layer_launch<32>(d, m1, m3, m2, mx, mu, p, cs);
 }
