@@ -16,20 +16,21 @@
 // (44 MB of codes for 7168 x 2048), whatever the number of its tokens, so the
 // floor is those bytes at HBM rate. The kernel is built to keep that stream
 // from stopping:
-//   - One CTA per SM, one launch (cooperative: CTAs meet at three barriers). Per
+//   - One CTA per SM, one launch (cooperative: CTAs meet at two barriers). Per
 //     CTA a producer warp keeps 160 KB of weight tiles in flight by TMA (128 rows x
 //     one K block, 16 KB), a warp issues the MMAs, four promote and finish.
 //   - The gate decides what the routed weights are, but not the shared ones: the
 //     ring fills with the CTA's share of the shared experts while x is quantised
 //     and the gate computed.
 //   - w2 does not depend on u, only its use does: the ring runs on from phase 1
-//     into w2 before the barriers between them.
+//     into w2 before the barrier between them.
 //   - Phase 1 lays its units (expert, 128 rows of w1 and the same of w3) end to
 //     end, K block by K block, and phase 2 its row tiles of w2, over all experts
-//     and K blocks; each CTA has the same number of K blocks of either. A unit
-//     that one CTA has whole is quantised there (its 128 rows are one block of
-//     u); parts of cut units are added in CTA order behind the barrier, parts of
-//     a row tile by the CTA that finishes the tile last. One order of every sum.
+//     and K blocks; each CTA has the same number of K blocks of either. Where a
+//     unit or a row tile is cut between CTAs, the one that finishes last adds the
+//     parts in CTA order (in warps of their own, while the stream goes on): one
+//     order of every sum. A unit's 128 rows are one block
+//     of u, quantised where the unit is finished.
 //
 // The products are tcgen05 MMAs with 128 weight rows as M and the tokens as N = 16
 // or 32 (all tokens for every expert: idle columns cost nothing): 156 or 160
@@ -74,20 +75,21 @@ constexpr int kStages = 10;               // weight tiles in flight
 constexpr int kTileBytes = 128 * 128;
 constexpr int kSets = 8;                  // accumulator sets in tensor memory
 // Streaming roles; the other warps wait for the phase to end.
-constexpr int kProducer = 0, kIssuer = 1, kFinisher = 4;  // finishers: warps 4-7
+constexpr int kProducer = 2, kIssuer = 1, kFinisher = 4, kCloser = 8;  // finishers: warps 4-7, closers: 8-11
 constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
 
 // Shared memory: weight tiles, token tiles, token scales, barriers, tables.
 __host__ __device__ constexpr int off_tok() { return kStages * kTileBytes; }
 __host__ __device__ constexpr int off_scl(int n) { return off_tok() + kStages * n * 128; }
 __host__ __device__ constexpr int off_bar(int n) { return off_scl(n) + kStages * n * 4; }
-constexpr int kNumBars = 3 * kStages + 2 * kSets + 1;
+constexpr int kCuts = 6;                  // cut units and tiles of a CTA: two per range
+constexpr int kNumBars = 3 * kStages + 2 * kSets + kCuts + 1;
 __host__ __device__ constexpr int off_act(int n) { return (off_bar(n) + kNumBars * 8 + 8 + 15) / 16 * 16; }
 __host__ __device__ constexpr int off_mask(int n) { return off_act(n) + kMaxActive * 4; }
 __host__ __device__ constexpr int off_sel(int n) { return off_mask(n) + kMaxActive * 4; }  // ids, weights; scratch before
 __host__ __device__ constexpr int off_scan(int n) { return off_sel(n) + 2 * kMaxTokens * 32 * 4; }
-__host__ __device__ constexpr int off_red(int n) { return off_scan(n) + 64 * 4; }          // [2][n][4] row maxima
-__host__ __device__ constexpr int off_bias(int n) { return off_red(n) + 2 * n * 4 * 4; }
+__host__ __device__ constexpr int off_red(int n) { return off_scan(n) + 64 * 4; }          // [4][n][4] row maxima
+__host__ __device__ constexpr int off_bias(int n) { return off_red(n) + 4 * n * 4 * 4; }
 __host__ __device__ constexpr int layer_smem(int n) { return 1024 + off_bias(n) + 256 * 4; }
 static_assert(layer_smem(32) <= 232448, "shared memory per CTA");
 static_assert(off_red(16) % 16 == 0 && off_red(32) % 16 == 0 && off_scl(16) % 16 == 0, "16-byte reads");
@@ -102,7 +104,8 @@ struct LayerParams {
   __nv_bfloat16* y;
   int32_t* topk_idx;    // may be null
   float* topk_w;        // may be null
-  unsigned* counters;   // [0..2] barrier arrivals, [3] CTAs done, [16..31] row tiles, a byte each; zero between calls
+  unsigned* counters;   // [0..1] barrier arrivals, [3] CTAs done, [16..31] row tiles, a byte each; zero between calls
+  unsigned* unit_parts;  // [unit] parts so far; zeroed before the first barrier
   float* logits;        // [T][E]
   uint8_t* xq;          // [T][dim]
   float* xs;            // [dim / 128][N]
@@ -111,7 +114,7 @@ struct LayerParams {
   float* part;          // [CTA][range][it starts the unit][h1, h3][T][128]
   float* part2;         // [CTA][it starts the tile][T][128]
   unsigned* err;
-  int T, dim, inter, E, ns, k, groups, kept, sigmoid, normalize, ue8m0;
+  int T, dim, inter, E, ns, k, groups, kept, sigmoid, normalize, ue8m0, max_units;
   float route_scale;
 };
 
@@ -213,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = tok_full + kStages;
   uint64_t* set_full = empty + kStages;
   uint64_t* set_empty = set_full + kSets;
-  uint64_t* drain = set_empty + kSets;
+  uint64_t* cut_stored = set_empty + kSets;  // this CTA's part of its i-th cut unit or tile is in memory
+  uint64_t* drain = cut_stored + kCuts;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* act = reinterpret_cast<int*>(smem + off_act(N));              // active experts, shared ones first
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&set_full[i], 1);
       mbar_init(&set_empty[i], 4);
     }
+    for (int i = 0; i < kCuts; ++i) mbar_init(&cut_stored[i], 4);
     mbar_init(drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&map1);
@@ -322,13 +327,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_unit(ahead);
         advance(ahead);
       }
-    __syncwarp();
   };
 
   // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
-  auto grid_barrier = [&](int i) {
+  // (`meanwhile` runs between a CTA's arrival and the wait.)
+  auto grid_barrier = [&](int i, auto meanwhile) {
     __threadfence();
     __syncthreads();
+    meanwhile();
     if (tid == 0) {
       atomicAdd(p.counters + i, 1u);
       const uint64_t t0 = global_timer_ns();
@@ -362,9 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) p.xs[i % Kb1 * N + i / Kb1] = s;
   }
   fence_proxy_async_all();  // TMA reads these
+  for (int i = c * kThreads + tid; i < p.max_units; i += G * kThreads) p.unit_parts[i] = 0;
   // The shared experts' stream starts when the gate's operands are here (its
   // copies, asked for earlier, made the logits wait 4 us behind them).
-  if (c >= p.E) first_tiles();
   {
     float* sums = sel_w;  // [warp][columns]
 #pragma unroll 1
@@ -401,12 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < wpe; ++w) v += sums[(k * wpe + w) * N + m];
         if (e0 + k * G < p.E) p.logits[static_cast<size_t>(m) * p.E + e0 + k * G] = v;
       }
-      if (e0 == c) first_tiles();
       __syncthreads();
       if (e0 + per_cta * G < p.E) load_gate(e0 + per_cta * G + warp / wpe * G);
     }
   }
-  grid_barrier(0);
+  grid_barrier(0, first_tiles);
 
   // The gate, by every CTA for itself, then the tables: active experts in order
   // (shared ones first) and their tokens.
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++kblock;
   };
   // The finishers' side: the tokens' scales of the K block and its `tiles` products.
-  const int row = (warp - kFinisher) * 32 + lane;  // of the 128 weight rows
+  const int row = (warp & 3) * 32 + lane;  // of the 128 weight rows: finishers and closers
   const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   auto products_ready = [&] {
     const int s0 = tile % kStages;
@@ -493,6 +498,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait(&set_full[kblock % kSets], (kblock / kSets) & 1, abort_flag, p.err);
     __syncwarp();
     tc_fence_after_sync();
+  };
+  // The parts of cut units and tiles. The finishers store this CTA's and go on;
+  // the closers count it in, and where it was the last of its unit add them up.
+  int cuts = 0;
+  auto part_stored = [&] {
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&cut_stored[cuts]);
+    ++cuts;
+  };
+  // (`count` holds a counter of `parts` in `field` << shift.)
+  auto last_part = [&](unsigned* count, unsigned field, int shift, unsigned parts) {
+    wait(&cut_stored[cuts], 0, abort_flag, p.err);
+    ++cuts;
+    __threadfence();
+    named_barrier_sync(3, 128);
+    if (warp == kCloser && lane == 0) {
+      const bool last = ((atomicAdd(count, 1u << shift) >> shift) & field) == parts - 1;
+      if (last) atomicSub(count, parts << shift);
+      scan[48] = last;
+      __threadfence();
+    }
+    named_barrier_sync(3, 128);
+    const bool last = scan[48] != 0;
+    named_barrier_sync(3, 128);  // before scan[48] is written again
+    return last;
+  };
+  // u of a finished unit for its tokens, by 128 threads (one per row): the rows
+  // are one block of u. `group` 0: finishers, 1: closers; they alternate between
+  // two halves of their maxima.
+  int flips = 0;
+  auto quantise_unit = [&](float (&h1)[N], const float (&h3)[N], int a, int blk, uint32_t mk, int group, int r) {
+    float* top = red + (group * 2 + (flips & 1)) * N * 4;
+    ++flips;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if ((mk >> j) & 1u) {
+        h1[j] = silu_mul(h1[j], h3[j]);
+        float m = fabsf(h1[j]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane == 0) top[j * 4 + (warp & 3)] = m;
+      }
+    }
+    named_barrier_sync(2 + group, 128);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if ((mk >> j) & 1u) {
+        const float4 m = *reinterpret_cast<const float4*>(top + j * 4);
+        const float sc = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)), p.ue8m0 != 0);
+        p.uq[(static_cast<size_t>(a) * p.T + j) * p.inter + blk * 128 + r] =
+            static_cast<uint8_t>(e4m3x2(__fdiv_rn(h1[j], sc), 0.f));
+        if (r == j) p.us[(a * Kb2 + blk) * N + j] = sc * gate_weight(a, j);
+      }
+    }
   };
   // acc += (product t of the K block) * (token scale * ws), for tokens in mk.
   auto promote = [&](float (&acc)[N], int t, float ws, uint32_t mk) {
@@ -568,7 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int q = phase1_tiles / 2; q > 0; --q) multiply(2);
   } else if (warp >= kFinisher && warp < kFinisher + 4) {
-    int flips = 0;  // which half of `red`
 #pragma unroll 1
     for (int range = 0; range < 2; ++range) {
       Cursor at = range ? cursor(p.ns, routed_blocks) : cursor(0, shared_blocks);
@@ -595,30 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance(at);
         }
         if (n == Kb1) {
-          // The whole unit: its 128 rows are one block of u for every token.
-          float* top = red + (flips & 1) * N * 4;
-          ++flips;
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            if ((mk >> j) & 1u) {
-              acc1[j] = silu_mul(acc1[j], acc3[j]);
-              float m = fabsf(acc1[j]);
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-              if (lane == 0) top[j * 4 + warp - kFinisher] = m;
-            }
-          }
-          named_barrier_sync(2, 128);
-#pragma unroll
-          for (int j = 0; j < N; ++j) {
-            if ((mk >> j) & 1u) {
-              const float4 m = *reinterpret_cast<const float4*>(top + j * 4);
-              const float s = block_scale(fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)), p.ue8m0 != 0);
-              p.uq[(static_cast<size_t>(a) * p.T + j) * p.inter + blk * 128 + row] =
-                  static_cast<uint8_t>(e4m3x2(__fdiv_rn(acc1[j], s), 0.f));
-              if (row == j) p.us[(a * Kb2 + blk) * N + j] = s * gate_weight(a, j);
-            }
-          }
+          quantise_unit(acc1, acc3, a, blk, mk, 0, row);
         } else {
           float* t = p.part + static_cast<size_t>((c * 2 + range) * 2 + (from == 0 ? 1 : 0)) * 2 * p.T * 128 + row;
 #pragma unroll
@@ -627,43 +663,48 @@ __global__ void __launch_bounds__(kThreads, 1)
               t[j * 128] = acc1[j];
               t[(p.T + j) * 128] = acc3[j];
             }
+          part_stored();
         }
       }
     }
     fence_proxy_async_all();  // TMA reads uq and us
+  } else if (warp >= kCloser && warp < kCloser + 4) {
+#pragma unroll 1
+    for (int range = 0; range < 2; ++range) {
+      const int blocks = range ? routed_blocks : shared_blocks, first = range ? p.ns : 0;
+      const int q0 = even(blocks, c, G), q1 = even(blocks, c + 1, G);
+#pragma unroll 1
+      for (int q = q0; q < q1;) {
+        const int u = q / Kb1, end = (u + 1) * Kb1;
+        const bool whole = q == u * Kb1 && end <= q1;
+        q = end;
+        if (whole) continue;
+        const int a = first + u / Kb2, blk = u % Kb2;
+        const uint32_t mk = mask[a];
+        const int c0 = part_of(blocks, u * Kb1, G), c1 = part_of(blocks, end - 1, G);
+        if (!last_part(p.unit_parts + a * Kb2 + blk, 0xFFFFFFFFu, 0, blocks >= G ? c1 - c0 + 1 : Kb1)) continue;
+        float h1[N], h3[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) h1[j] = h3[j] = 0.f;
+#pragma unroll 1
+        for (int k = c0; k <= c1; ++k) {
+          // (With fewer K blocks than CTAs some CTAs have none.)
+          if (blocks < G && even(blocks, k, G) == even(blocks, k + 1, G)) continue;
+          const float* v = p.part + static_cast<size_t>((k * 2 + range) * 2 + (k == c0 ? 1 : 0)) * 2 * p.T * 128 + row;
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if ((mk >> j) & 1u) {
+              h1[j] += __ldcg(v + j * 128);
+              h3[j] += __ldcg(v + (p.T + j) * 128);
+            }
+        }
+        quantise_unit(h1, h3, a, blk, mk, 1, row);
+      }
+    }
+    fence_proxy_async_all();
   }
   __syncwarp();
-  grid_barrier(1);
-  // Units cut between CTAs, a warp per (unit, token): the parts added in CTA
-  // order, then quantised.
-#pragma unroll 1
-  for (int range = 0; range < 2; ++range) {
-    const int blocks = range ? routed_blocks : shared_blocks, first = range ? p.ns : 0;
-#pragma unroll 1
-    for (int i = warp * G + c; i < blocks / Kb1 * p.T; i += G * kWarps) {
-      const int u = i / p.T, m = i - u * p.T, a = first + u / Kb2;
-      if (!((mask[a] >> m) & 1u)) continue;
-      const int c0 = part_of(blocks, u * Kb1, G), c1 = part_of(blocks, u * Kb1 + Kb1 - 1, G);
-      if (c0 == c1) continue;
-      float4 h1 = make_float4(0.f, 0.f, 0.f, 0.f), h3 = h1;
-#pragma unroll 4
-      for (int q = c0; q <= c1; ++q) {
-        // (With fewer K blocks than CTAs some CTAs have none.)
-        if (blocks < G && even(blocks, q, G) == even(blocks, q + 1, G)) continue;
-        const float* t = p.part + static_cast<size_t>((q * 2 + range) * 2 + (q == c0 ? 1 : 0)) * 2 * p.T * 128 + m * 128;
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(t) + lane);
-        const float4 z = __ldcg(reinterpret_cast<const float4*>(t + p.T * 128) + lane);
-        h1 = make_float4(h1.x + x.x, h1.y + x.y, h1.z + x.z, h1.w + x.w);
-        h3 = make_float4(h3.x + z.x, h3.y + z.y, h3.z + z.z, h3.w + z.w);
-      }
-      const float v[4] = {silu_mul(h1.x, h3.x), silu_mul(h1.y, h3.y), silu_mul(h1.z, h3.z), silu_mul(h1.w, h3.w)};
-      const int blk = u % Kb2;
-      const float s = quant_block(v, p.ue8m0 != 0, lane, p.uq + (static_cast<size_t>(a) * p.T + m) * p.inter + blk * 128);
-      if (lane == 0) p.us[(a * Kb2 + blk) * N + m] = s * gate_weight(a, m);
-    }
-  }
-  fence_proxy_async_all();
-  grid_barrier(2);
+  grid_barrier(1, [] {});
 
   // ---- phase 2 -------------------------------------------------------------------
   if (producer) {
@@ -717,34 +758,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < N; ++j)
           if (j < p.T) t[j * 128] = acc[j];
-        // The last of the tile's CTAs adds up the parts, in CTA order.
-        const int c0 = part_of(blocks2, tl * tile_blocks, G), c1 = part_of(blocks2, (tl + 1) * tile_blocks - 1, G);
-        const unsigned parts = blocks2 >= G ? c1 - c0 + 1 : tile_blocks;
-        __threadfence();
-        named_barrier_sync(2, 128);
-        if (warp == kFinisher && lane == 0) {
-          unsigned* count = p.counters + 16 + tl / 4;  // at most 192 parts: a byte per tile
-          const int sh = tl % 4 * 8;
-          const bool last = ((atomicAdd(count, 1u << sh) >> sh) & 0xFFu) == parts - 1;
-          if (last) atomicSub(count, parts << sh);
-          scan[48] = last;
-          __threadfence();
-        }
-        named_barrier_sync(2, 128);
-        if (scan[48]) {
-#pragma unroll 1
-          for (int j = 0; j < p.T; ++j) {
-            float v = 0.f;
-#pragma unroll 4
-            for (int q = c0; q <= c1; ++q) {
-              if (blocks2 < G && even(blocks2, q, G) == even(blocks2, q + 1, G)) continue;
-              v += __ldcg(p.part2 + (static_cast<size_t>(q * 2 + (q == c0 ? 1 : 0)) * p.T + j) * 128 + row);
-            }
-            y[static_cast<size_t>(j) * p.dim] = __float2bfloat16_rn(v);
-          }
-        }
-        named_barrier_sync(2, 128);  // before scan[48] is written again
+        part_stored();
       }
+    }
+  } else if (warp >= kCloser && warp < kCloser + 4) {
+#pragma unroll 1
+    for (int q = q2; q < q2 + n2;) {
+      const int tl = q / tile_blocks, end = (tl + 1) * tile_blocks;
+      const bool whole = q == tl * tile_blocks && end <= q2 + n2;
+      q = end;
+      if (whole) continue;
+      const int c0 = part_of(blocks2, tl * tile_blocks, G), c1 = part_of(blocks2, end - 1, G);
+      // (At most 192 parts: a byte per tile.)
+      if (!last_part(p.counters + 16 + tl / 4, 0xFFu, tl % 4 * 8, blocks2 >= G ? c1 - c0 + 1 : tile_blocks)) continue;
+      float acc[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] = 0.f;
+#pragma unroll 2
+      for (int k = c0; k <= c1; ++k) {
+        if (blocks2 < G && even(blocks2, k, G) == even(blocks2, k + 1, G)) continue;
+        const float* v = p.part2 + static_cast<size_t>(k * 2 + (k == c0 ? 1 : 0)) * p.T * 128 + row;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (j < p.T) acc[j] += __ldcg(v + j * 128);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (j < p.T) p.y[static_cast<size_t>(j) * p.dim + tl * 128 + row] = __float2bfloat16_rn(acc[j]);
     }
   }
   __syncwarp();
@@ -767,8 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // The last CTA to leave zeroes the counters for the next call.
   if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u) {
-    p.counters[0] = p.counters[1] = p.counters[2] = 0;
-    p.counters[3] = 0;
+    p.counters[0] = p.counters[1] = p.counters[3] = 0;
     if (*abort_flag)
       for (int i = 16; i < 32; ++i) p.counters[i] = 0;
   }
@@ -810,7 +849,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 struct LayerSizes {
   int64_t active;  // experts at most
   int cols;        // token columns
-  size_t logits, xq, xs, uq, us, part, part2, total;
+  size_t logits, xq, xs, uq, us, units, part, part2, total;
 };
 
 LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t topk, int64_t ns) {
@@ -822,7 +861,8 @@ LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t
   z.xs = z.xq + align256(static_cast<size_t>(T) * dim);
   z.uq = z.xs + align256(static_cast<size_t>(dim / 128) * z.cols * 4);
   z.us = z.uq + align256(static_cast<size_t>(z.active) * T * inter);
-  z.part = z.us + align256(static_cast<size_t>(z.active) * (inter / 128) * z.cols * 4);
+  z.units = z.us + align256(static_cast<size_t>(z.active) * (inter / 128) * z.cols * 4);
+  z.part = z.units + align256(static_cast<size_t>(z.active) * (inter / 128) * 4);
   z.part2 = z.part + static_cast<size_t>(kMaxCtas) * 4 * 2 * T * 128 * 4;
   z.total = z.part2 + static_cast<size_t>(kMaxCtas) * 2 * T * 128 * 4;
   return z;
@@ -913,6 +953,8 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.xs = reinterpret_cast<float*>(ws + z.xs);
   p.uq = ws + z.uq;
   p.us = reinterpret_cast<float*>(ws + z.us);
+  p.unit_parts = reinterpret_cast<unsigned*>(ws + z.units);
+  p.max_units = static_cast<int>(z.active * (inter / 128));
   p.part = reinterpret_cast<float*>(ws + z.part);
   p.part2 = reinterpret_cast<float*>(ws + z.part2);
   p.err = d->err_word;
