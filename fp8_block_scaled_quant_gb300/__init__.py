@@ -107,6 +107,8 @@ def _stream(device: torch.device):
 
 
 def _need(t: torch.Tensor, dtype, name: str, ndim: int = 2):
+    if t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+        return
     if not t.is_cuda:
         raise Fp8BlkError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -134,6 +136,48 @@ def workspace(nbytes: int, device: torch.device, key: str = "gemm") -> torch.Ten
         _ws_cache[k] = buf
     off = (-buf.data_ptr()) % 256
     return buf[off:off + max(nbytes, 1)]
+
+
+# The calls of a decode step are issued in less time than their kernels run
+# only if the host side is short: these find the stream once per call, bind a
+# function's types once, and pass addresses as plain integers.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_bound: dict = {}
+
+
+def _stream_on(t: torch.Tensor) -> int:
+    """The handle of the current stream of t's device."""
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _function(name: str, argtypes: str, restype=ctypes.c_int):
+    """The library's function, its argument types bound at the first call: p pointer, i int64, e int, f float,
+    z size_t."""
+    f = _bound.get(name)
+    if f is None:
+        kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int64, "e": ctypes.c_int, "f": ctypes.c_float,
+                 "z": ctypes.c_size_t}
+        f = _bound[name] = _set_types(name, [kinds[k] for k in argtypes], restype)
+    return f
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(ws: torch.Tensor | None, nbytes: int, t: torch.Tensor, stream: int, key: str):
+    """(address, bytes) of the caller's workspace, or of the one kept for the device and stream."""
+    if ws is not None:
+        return ws.data_ptr(), ws.numel()
+    buf = _ws_cache.get((t.get_device(), stream, key))
+    if buf is None or buf.numel() < nbytes + 256:
+        buf = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=t.device)
+        _ws_cache[(t.get_device(), stream, key)] = buf
+    at = buf.data_ptr()
+    return at + (-at) % 256, nbytes
 
 
 # ---- operations --------------------------------------------------------------
@@ -380,7 +424,7 @@ def mla_append(kv: torch.Tensor, norm_w: torch.Tensor, rope: torch.Tensor, posit
     _need(positions, torch.int64, "positions", ndim=1)
     _need(slots, torch.int64, "slots", ndim=1)
     _need(cache, torch.bfloat16, "cache", ndim=3)
-    if norm_w.shape[0] != MLA_LATENT or tuple(rope.shape[1:]) != (MLA_ROPE // 2, 2) or cache.shape[2] != kv.shape[1]:
+    if norm_w.shape[0] != MLA_LATENT or rope.shape[1:] != (MLA_ROPE // 2, 2) or cache.shape[2] != kv.shape[1]:
         raise Fp8BlkError("norm_w must be [512], rope [max_pos, 32, 2], cache [pages, page_size, 576]")
     if positions.shape[0] != T or slots.shape[0] != T:
         raise Fp8BlkError("positions and slots must be [T]")
@@ -395,25 +439,25 @@ def mla_append(kv: torch.Tensor, norm_w: torch.Tensor, rope: torch.Tensor, posit
         q_stride = q.stride(0) if T > 1 else H * (MLA_NOPE + MLA_ROPE)
         if q_nope is None:
             q_nope = torch.empty((T, H, MLA_NOPE), dtype=torch.bfloat16, device=q.device)
+        else:
+            _need(q_nope, torch.bfloat16, "q_nope", ndim=3)
         if q_pe is None:
             q_pe = torch.empty((T, H, MLA_ROPE), dtype=torch.bfloat16, device=q.device)
-        _need(q_nope, torch.bfloat16, "q_nope", ndim=3)
-        _need(q_pe, torch.bfloat16, "q_pe", ndim=3)
-        if tuple(q_nope.shape) != (T, H, MLA_NOPE) or tuple(q_pe.shape) != (T, H, MLA_ROPE):
+        else:
+            _need(q_pe, torch.bfloat16, "q_pe", ndim=3)
+        if q_nope.shape != (T, H, MLA_NOPE) or q_pe.shape != (T, H, MLA_ROPE):
             raise Fp8BlkError("q_nope must be [T, H, 128] and q_pe [T, H, 64]")
-    vp, i64 = ctypes.c_void_p, ctypes.c_int64
-    f = _set_types("fp8blk_mla_append", [vp, i64, vp, ctypes.c_float, vp, i64, i64, vp, i64, vp, vp, i64, vp, i64,
-                                         vp, vp, vp])
-    _check(f(_ptr(kv), kv.stride(0) if T > 1 else kv.shape[1], _ptr(norm_w), float(eps), _ptr(q), q_stride, H,
-             _ptr(rope), rope.shape[0], _ptr(positions), _ptr(slots), T, _ptr(cache), cache.shape[0] * cache.shape[1],
-             _ptr(q_nope if q is not None else None), _ptr(q_pe if q is not None else None), _stream(kv.device)),
-           "mla_append")
+    else:
+        q_nope = q_pe = None
+    f = _function("fp8blk_mla_append", "pipfpiipippipippp")
+    _check(f(kv.data_ptr(), kv.stride(0) if T > 1 else MLA_LATENT + MLA_ROPE, norm_w.data_ptr(), float(eps), _addr(q),
+             q_stride, H, rope.data_ptr(), rope.shape[0], positions.data_ptr(), slots.data_ptr(), T, cache.data_ptr(),
+             cache.shape[0] * cache.shape[1], _addr(q_nope), _addr(q_pe), _stream_on(kv)), "mla_append")
     return None if q is None else (q_nope, q_pe)
 
 
 def mla_attention_workspace_bytes(B: int, H: int, prefix_len: int = 0) -> int:
-    i64 = ctypes.c_int64
-    return int(_set_types("fp8blk_mla_attention_workspace_bytes", [i64] * 3, ctypes.c_size_t)(B, H, prefix_len))
+    return int(_function("fp8blk_mla_attention_workspace_bytes", "iii", ctypes.c_size_t)(B, H, prefix_len))
 
 
 def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -430,7 +474,7 @@ def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, bloc
     _need(block_table, torch.int32, "block_table")
     _need(lens, torch.int32, "lens", ndim=1)
     B, H = q.shape[0], q.shape[1]
-    if q.shape[2] != MLA_LATENT or tuple(q_pe.shape) != (B, H, MLA_ROPE) or \
+    if q.shape[2] != MLA_LATENT or q_pe.shape != (B, H, MLA_ROPE) or \
             cache.shape[2] != MLA_LATENT + MLA_ROPE:
         raise Fp8BlkError("q must be [B, H, 512], q_pe [B, H, 64], cache [pages, page_size, 576]")
     if block_table.shape[0] != B or lens.shape[0] != B:
@@ -444,21 +488,21 @@ def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, bloc
             raise Fp8BlkError("prefix_pages has fewer than prefix_len keys")
     if out is None:
         out = torch.empty((B, H, MLA_LATENT), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, "out", ndim=3)
-    if tuple(out.shape) != (B, H, MLA_LATENT):
-        raise Fp8BlkError("out must be [B, H, 512]")
+    else:
+        _need(out, torch.bfloat16, "out", ndim=3)
+        if out.shape != (B, H, MLA_LATENT):
+            raise Fp8BlkError("out must be [B, H, 512]")
     if lse is not None:
         _need(lse, torch.float32, "lse")
         if tuple(lse.shape) != (B, H):
             raise Fp8BlkError("lse must be [B, H]")
-    if ws is None:
-        ws = workspace(mla_attention_workspace_bytes(B, H, prefix_len), q.device, "mla_attention")
-    vp, i64 = ctypes.c_void_p, ctypes.c_int64
-    f = _set_types("fp8blk_mla_attention", [vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp,
-                                            vp, vp, ctypes.c_size_t, vp])
-    _check(f(_ptr(q), _ptr(q_pe), B, H, _ptr(cache), pages, page_size, _ptr(prefix_pages if prefix_len else None),
-             prefix_len, _ptr(block_table), block_table.shape[1], _ptr(lens), float(scale), _ptr(out), _ptr(lse),
-             _ptr(ws), ws.numel(), _stream(q.device)), "mla_attention")
+    stream = _stream_on(q)
+    at, room = _scratch(ws, 0 if ws is not None else mla_attention_workspace_bytes(B, H, prefix_len), q, stream,
+                        "mla_attention")
+    f = _function("fp8blk_mla_attention", "ppiipiipipipfpppzp")
+    _check(f(q.data_ptr(), q_pe.data_ptr(), B, H, cache.data_ptr(), pages, page_size,
+             prefix_pages.data_ptr() if prefix_len else None, prefix_len, block_table.data_ptr(), block_table.shape[1],
+             lens.data_ptr(), float(scale), out.data_ptr(), _addr(lse), at, room, stream), "mla_attention")
     return out
 
 
@@ -550,9 +594,8 @@ MOE_LAYER_MAX_TOKENS = 32
 
 
 def moe_layer_workspace_bytes(T: int, topk: int, E: int, dim: int, inter: int, n_shared: int = 0) -> int:
-    i64 = ctypes.c_int64
-    return int(_set_types("fp8blk_moe_layer_workspace_bytes", [i64] * 6, ctypes.c_size_t)(T, topk, E, dim, inter,
-                                                                                          n_shared))
+    return int(_function("fp8blk_moe_layer_workspace_bytes", "iiiiii", ctypes.c_size_t)(T, topk, E, dim, inter,
+                                                                                        n_shared))
 
 
 def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_s, topk: int,
@@ -571,12 +614,12 @@ def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_
     T, dim = x.shape
     E, inter = gate_w.shape[0], w2.shape[1]
     K = E + n_shared
-    if gate_w.shape[1] != dim or tuple(w1.shape) != (K * inter, dim) or tuple(w3.shape) != (K * inter, dim) or \
+    if gate_w.shape[1] != dim or w1.shape != (K * inter, dim) or w3.shape != (K * inter, dim) or \
             w2.shape[0] != K * dim:
         raise Fp8BlkError("gate_w must be [E, dim], w1 and w3 [(E + n_shared) * inter, dim], "
                           "w2 [(E + n_shared) * dim, inter]")
     s13, s2 = (K * inter // BLOCK, dim // BLOCK), (K * dim // BLOCK, inter // BLOCK)
-    if tuple(w1_s.shape) != s13 or tuple(w3_s.shape) != s13 or tuple(w2_s.shape) != s2:
+    if w1_s.shape != s13 or w3_s.shape != s13 or w2_s.shape != s2:
         raise Fp8BlkError("block scales must have one entry per 128x128 block")
     if gate_bias is not None:
         _need(gate_bias, torch.float32, "gate_bias", ndim=1)
@@ -584,20 +627,21 @@ def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_
             raise Fp8BlkError("gate_bias must be [E]")
     if out is None:
         out = torch.empty((T, dim), dtype=torch.bfloat16, device=x.device)
-    _need(out, torch.bfloat16, "out")
-    if tuple(out.shape) != (T, dim):
-        raise Fp8BlkError("out must be [T, dim]")
+    else:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != (T, dim):
+            raise Fp8BlkError("out must be [T, dim]")
     for t, n, dt in ((idx, "idx", torch.int32), (w, "w", torch.float32)):
         if t is not None:
             _need(t, dt, n)
             if tuple(t.shape) != (T, topk):
                 raise Fp8BlkError(f"{n} must be [T, topk]")
-    if ws is None:
-        ws = workspace(moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared), x.device, "moe_layer")
-    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
-    f = _set_types("fp8blk_moe_layer", [vp] * 10 + [i64] * 8 + [i32, f32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp])
-    _check(f(_ptr(x), _ptr(gate_w), _ptr(gate_bias), _ptr(w1), _ptr(w1_s), _ptr(w3), _ptr(w3_s), _ptr(w2), _ptr(w2_s),
-             _ptr(out), T, topk, E, dim, inter, n_shared, n_groups, topk_groups, score_func, float(route_scale),
-             int(bool(normalize)), scale_fmt, _ptr(idx), _ptr(w), _ptr(ws), ws.numel(), _stream(x.device)),
-           "moe_layer")
+    stream = _stream_on(x)
+    at, room = _scratch(ws, 0 if ws is not None else moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared), x,
+                        stream, "moe_layer")
+    f = _function("fp8blk_moe_layer", "p" * 10 + "i" * 8 + "efeepppzp")
+    _check(f(x.data_ptr(), gate_w.data_ptr(), _addr(gate_bias), w1.data_ptr(), w1_s.data_ptr(), w3.data_ptr(),
+             w3_s.data_ptr(), w2.data_ptr(), w2_s.data_ptr(), out.data_ptr(), T, topk, E, dim, inter, n_shared, n_groups,
+             topk_groups, score_func, float(route_scale), 1 if normalize else 0, scale_fmt, _addr(idx), _addr(w), at, room,
+             stream), "moe_layer")
     return out
