@@ -80,8 +80,8 @@ constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 1;
 constexpr int kAttnSmem = 1024 + kOffBar + kNumBars * 8 + 32;
 static_assert(kAttnSmem <= 232448, "shared memory per CTA");
 
-// Warps: 0-3 softmax (warp w: tensor-memory lanes 32 w ..), 4 queries and
-// keys, 5 values, 6 MMA.
+// Warps: 0-3 softmax (warp w: tensor-memory lanes 32 w ..), 4 keys, 5
+// queries and values, 6 MMA.
 constexpr int kAttnThreads = 224;
 constexpr int kMaxPairs = 96;
 constexpr uint32_t kTmemS = 256;            // columns 0-255: output; 256-383: two score buffers
@@ -119,7 +119,7 @@ __device__ __forceinline__ int own_len(const AttnParams& p, int b) {
   return min(max(__ldg(p.lens + b), 0), p.max_own);
 }
 
-__device__ __noinline__ Item get_item(const AttnParams& p, int i) {
+__device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
   Item it;
   if (p.merged) {
     it.row0 = i * kTileRows;
@@ -161,7 +161,22 @@ __host__ __device__ __forceinline__ int64_t part_row(int merged, int prefix_item
   return base + static_cast<int64_t>(q) * kTileRows;
 }
 
-__device__ __forceinline__ int64_t unit_of_pair(int64_t units, int pairs, int q) { return units * q / pairs; }
+// First unit of pair q, units q / pairs rounded down, without a 64-bit product
+// (whose division costs as much as the loads it would wait beside).
+__device__ __forceinline__ int unit_of_pair(int units, int pairs, int q) {
+  const int each = units / pairs;
+  return each * q + (units - each * pairs) * q / pairs;
+}
+
+// The pair whose range holds unit u: the largest q with units q / pairs <= u,
+// that is units q < (u + 1) pairs. An estimate, then put right.
+__device__ __forceinline__ int pair_of_unit(int units, int pairs, int u) {
+  const int64_t x = static_cast<int64_t>(u + 1) * pairs;
+  int q = static_cast<int>(__fdividef(static_cast<float>(u + 1) * static_cast<float>(pairs), static_cast<float>(units)));
+  while (static_cast<int64_t>(units) * (q + 1) < x) ++q;
+  while (static_cast<int64_t>(units) * q >= x) --q;
+  return q;
+}
 
 // ---- instructions of the CTA pair ----------------------------------------------
 
@@ -387,19 +402,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       units += v;
     }
     const int pairs = max(1, min(npairs_max, units));
-    const int64_t u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
-    const int64_t u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
+    const int u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
+    const int u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       const int n = hi - lo == 1 ? own : item_tiles(p, i);
       if (u0 < u1 && u0 >= at && u0 < at + n) {
         start[0] = i;
-        start[1] = static_cast<int>(u0 - at);
+        start[1] = u0 - at;
       }
       if (blockIdx.x == 0) p.plan[2 + i] = at;
       at += n;
     }
-    if (tid == 0) start[2] = static_cast<int>(u1 - u0);
+    if (tid == 0) start[2] = u1 - u0;
     if (blockIdx.x == 0 && tid == 0) {
       p.plan[0] = units;
       p.plan[1] = pairs;
@@ -416,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   const int item0 = nunits ? start[0] : 0, tile0 = nunits ? start[1] : 0;
 
   if (warp == 4 || warp == 5) {
-    // ---- loads: queries and keys (warp 4), values (warp 5) -------------------
+    // ---- loads: keys (warp 4), queries and values (warp 5) -------------------
     const bool is_k = warp == 4;
     uint32_t n = 0, seg = 0;
     int left = nunits, i = item0, t0 = tile0;
@@ -448,7 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         return looks && t < t1 && key < (t < it.pt ? p.P : it.len) ? entry_row(p, entry, key) : p.total_rows;
       };
       int entry1 = page_entry(t0), entry2 = page_entry(t0 + 1);
-      if (is_k && t1 > t0) {
+      // (The first by the value warp, beside the first keys; later ones, whose
+      // wait would hold the values up, by the key warp.)
+      if (t1 > t0 && is_k == (seg > 0)) {
         if (seg > 0) ok = wait_warp(q_empty, (seg - 1) & 1, abort_flag, p.err);
         if (!ok) break;
         if (elect_one_sync()) {
@@ -461,8 +478,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                              s < kC / 64 ? s * 64 : 0, y);
         }
         __syncwarp();
-        ++seg;
       }
+      if (t1 > t0) ++seg;
       int y_next = row_of(t0, entry1);
       entry1 = entry2;
 #pragma unroll 1
@@ -473,19 +490,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         const int y16 = y_next;
         y_next = row_of(t + 1, entry1);
         entry1 = page_entry(t + 2);
-        if (is_k && (t + 1 >= it.pt || p.lone_prefix)) {
-          // Keys that no other pair reads come from HBM: ask for the next
-          // tile's while this one is loaded.
-#pragma unroll 1
-          for (int q = 0; q < 64 / p.kbox; ++q) {
-            const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
-            if (y < p.total_rows && elect_one_sync()) {
-#pragma unroll 1
-              for (int x = 0; x < kRow; x += 64) tma_prefetch_l2_2d(&map_k, x, y);
-            }
-            __syncwarp();
-          }
-        }
         if (is_k) {
           // This CTA's 64 keys, in boxes of kbox keys x 64 columns.
           const int nbox = 64 / p.kbox;
@@ -502,6 +506,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
                   tma_load_2d_pair(dst + s * kSlab, &map_k, bars + g * 8, (3 * g + s) * 64, y);
+              }
+              __syncwarp();
+            }
+          }
+          if (t + 1 >= it.pt || p.lone_prefix) {
+            // Keys that no other pair reads come from HBM: ask for the next
+            // tile's while this one is loaded.
+#pragma unroll 1
+            for (int q = 0; q < 64 / p.kbox; ++q) {
+              const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
+              if (y < p.total_rows && elect_one_sync()) {
+#pragma unroll 1
+                for (int x = 0; x < kRow; x += 64) tma_prefetch_l2_2d(&map_k, x, y);
               }
               __syncwarp();
             }
@@ -559,8 +576,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     if (*abort_flag && rank == 0) {
       // Copies of both CTAs complete on this CTA's barriers: wait for the last
       // phase each was armed for.
+      if (seg > 0) wait_slow(smem_u32(q_full), (seg - 1) & 1, nullptr, p.err);
       if (is_k) {
-        if (seg > 0) wait_slow(smem_u32(q_full), (seg - 1) & 1, nullptr, p.err);
 #pragma unroll 1
         for (int g = 0; g < kKGroups; ++g)
           if (n > 0) wait_slow(smem_u32(&k_full[g]), (n - 1) & 1, nullptr, p.err);
@@ -873,11 +890,11 @@ __global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const At
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.H;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int rows = p.B * p.H;
+  const int r = static_cast<int>(blockIdx.x) * 32 + lane;
   const int quad = (S > 1 ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y) * 4 + warp) * Q;
   const int slot = S > 1 ? warp : 0;
-  const int b = static_cast<int>(min(r, rows - 1) / p.H), h = static_cast<int>(min(r, rows - 1) % p.H);
+  const int rc = min(r, rows - 1), b = rc / p.H, h = rc - b * p.H;
   const int units = p.plan[0], pairs = p.plan[1];
   // Up to two items hold the row's keys: the prefix's (or both together) and
   // its own. Per item: parts, first part's row and quad-0 address, quad pitch.
@@ -887,17 +904,15 @@ __global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const At
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     int item = -1;
-    if (k == 0 && (p.merged || p.prefix_tiles > 0)) item = static_cast<int>(min(r, rows - 1) / kTileRows);
+    if (k == 0 && (p.merged || p.prefix_tiles > 0)) item = rc / kTileRows;
     if (k == 1 && !p.merged) item = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
-    local[k] = k == 0 ? static_cast<int>(r % kTileRows) : h % kTileRows;
+    local[k] = k == 0 ? r % kTileRows : h % kTileRows;
     pitch[k] = k == 0 ? kTileRows : p.own_rows;
     if (item < 0) continue;
-    const int64_t a = p.plan[2 + item], e = p.plan[3 + item];
+    const int a = p.plan[2 + item], e = p.plan[3 + item];
     if (e <= a) continue;
-    // Pair q has the units [units q / pairs, units (q + 1) / pairs): that of unit
-    // u is the largest q with units q / pairs <= u.
-    const int q0 = static_cast<int>(((a + 1) * pairs - 1) / units);
-    n[k] = static_cast<int>((e * pairs - 1) / units) - q0 + 1;
+    const int q0 = pair_of_unit(units, pairs, a);
+    n[k] = pair_of_unit(units, pairs, e - 1) - q0 + 1;
     at[k] = part_row(p.merged, p.prefix_items, p.own_rows, item, q0);
   }
   const int parts = r < rows ? n[0] + n[1] : 0;
@@ -992,7 +1007,7 @@ __global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const At
                          y = __floats2bfloat162_rn(acc[c].z * inv, acc[c].w * inv);
     o[c] = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  uint2* dst = reinterpret_cast<uint2*>(p.out + r * kC) + quad;
+  uint2* dst = reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(r) * kC) + quad;
   if constexpr (Q % 2 == 0) {
 #pragma unroll
     for (int c = 0; c < Q; c += 2)
