@@ -77,6 +77,7 @@ constexpr int kOffV = kOffK + kQSlabs * kSlab;
 constexpr int kOffRed = kOffV + kVChunks * kVChunk;  // [2][2][64] row maxima, then sums
 constexpr int kOffBar = kOffRed + 2 * 2 * 64 * 4;
 constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 1;
+static_assert(kNumBars <= 32, "a lane of a warp initialises each");
 constexpr int kAttnSmem = 1024 + kOffBar + kNumBars * 8 + 32;
 static_assert(kAttnSmem <= 232448, "shared memory per CTA");
 
@@ -89,6 +90,23 @@ constexpr float kRaise = 8.0f;              // log2 by which a tile's maximum mu
 constexpr unsigned kDevErrTimeoutMla = 1u << 6;
 constexpr unsigned kDevErrBadSlot = 1u << 8;
 
+// Division of 0 <= n < 2^30 by a constant d of the launch, 1 <= d <= 2^20: with
+// 2^(L-1) < d <= 2^L and mul = floor(2^(30+L) / d) + 1, mul d exceeds 2^(30+L) by
+// at most 2^L, so n mul / 2^(30+L) passes n / d by less than 1 / d.
+struct Divisor {
+  uint32_t mul, shift;
+};
+
+__host__ Divisor divisor(int64_t d) {
+  uint32_t l = 0;
+  while ((int64_t{1} << l) < d) ++l;
+  return {static_cast<uint32_t>((uint64_t{1} << (30 + l)) / static_cast<uint64_t>(d) + 1), 30 + l};
+}
+
+__device__ __forceinline__ int div_by(int n, const Divisor& d) {
+  return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul >> d.shift);
+}
+
 struct AttnParams {
   const int* prefix_pages;
   const int* table;        // [B][table_stride]
@@ -99,7 +117,8 @@ struct AttnParams {
   float4* part_ml;         // [part rows] (maximum in log2 units, sum of the rounded weights, of the fp32 weights)
   int* plan;               // [0] units, [1] pairs in use, [2 + i] first unit of item i (items + 1 entries)
   unsigned* err;
-  int B, H, P, page, page_shift, num_pages, table_stride, max_own;
+  Divisor by_page, by_per, by_pairs;  // page size, row tiles per request, pairs of the launch
+  int B, H, P, page, per, num_pages, table_stride, max_own;
   int total_rows;          // cache rows: the out-of-range row coordinate
   int prefix_tiles, prefix_items, items, own_rows;
   int merged;              // H % 128 == 0: prefix and own keys in one item
@@ -124,7 +143,7 @@ __device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
   if (p.merged) {
     it.row0 = i * kTileRows;
     it.nrows = kTileRows;
-    it.b = it.row0 / p.H;
+    it.b = div_by(i, p.by_per);
     it.pt = p.prefix_tiles;
   } else if (i < p.prefix_items) {
     it.row0 = i * kTileRows;
@@ -132,10 +151,9 @@ __device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
     it.b = -1;
     it.pt = p.prefix_tiles;
   } else {
-    const int per = (p.H + kTileRows - 1) / kTileRows;
     const int k = i - p.prefix_items;
-    it.b = k / per;
-    it.row0 = it.b * p.H + (k % per) * kTileRows;
+    it.b = div_by(k, p.by_per);
+    it.row0 = it.b * p.H + (k - it.b * p.per) * kTileRows;
     it.nrows = min(kTileRows, (it.b + 1) * p.H - it.row0);
     it.pt = 0;
   }
@@ -146,8 +164,7 @@ __device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
 
 __device__ __forceinline__ int item_tiles(const AttnParams& p, int i) {
   if (!p.merged && i < p.prefix_items) return p.prefix_tiles;
-  const int per = (p.H + kTileRows - 1) / kTileRows;
-  const int len = own_len(p, (i - p.prefix_items) / per);
+  const int len = own_len(p, div_by(i - p.prefix_items, p.by_per));
   return (p.merged ? p.prefix_tiles : 0) + (len + kTileKeys - 1) / kTileKeys;
 }
 
@@ -161,11 +178,12 @@ __host__ __device__ __forceinline__ int64_t part_row(int merged, int prefix_item
   return base + static_cast<int64_t>(q) * kTileRows;
 }
 
-// First unit of pair q, units q / pairs rounded down, without a 64-bit product
-// (whose division costs as much as the loads it would wait beside).
-__device__ __forceinline__ int unit_of_pair(int units, int pairs, int q) {
-  const int each = units / pairs;
-  return each * q + (units - each * pairs) * q / pairs;
+// First unit of pair q: units q / pairs rounded down, without 64-bit products.
+// Fewer units than the launch has pairs go to a pair each.
+__device__ __forceinline__ int unit_of_pair(const AttnParams& p, int units, int pairs, int launched, int q) {
+  if (pairs < launched) return q;
+  const int each = div_by(units, p.by_pairs);
+  return each * q + div_by((units - each * pairs) * q, p.by_pairs);
 }
 
 // The pair whose range holds unit u: the largest q with units q / pairs <= u,
@@ -298,7 +316,7 @@ __device__ __forceinline__ int entry_row(const AttnParams& p, int pg, int key) {
     atomicOr(p.err, kDevErrBadSlot);
     return p.total_rows;
   }
-  return pg * p.page + (p.page_shift >= 0 ? key & (p.page - 1) : key % p.page);
+  return pg * p.page + key - div_by(key, p.by_page) * p.page;
 }
 
 // Value chunks of a tile that hold keys.
@@ -339,27 +357,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   const int pair = static_cast<int>(blockIdx.x) >> 1;
   const int npairs_max = static_cast<int>(gridDim.x) >> 1;
 
-  if (tid == 0) {
-    *abort_flag = 0;
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int i = 0; i < kKGroups; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < kVChunks; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 8);  // four softmax warps of each CTA
-    }
-    mbar_init(p_full, 8);
-    mbar_init(pv_done, 1);
-    mbar_init(o_empty, 8);
-    mbar_init(red_bar, 4);
-    mbar_init(drain, 1);
+  if (warp == 0) {
+    // A lane per barrier. Arrivals: the softmax warps of both CTAs, of one, or one.
+    uint64_t* bar = q_full + lane;
+    const bool both = bar == s_empty || bar == s_empty + 1 || bar == p_full || bar == o_empty;
+    if (lane < kNumBars) mbar_init(bar, both ? 8 : bar == red_bar ? 4 : 1);
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 6) {
@@ -379,10 +382,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   griddep_wait();
 
   // The plan: every CTA sums the items' tiles (thread-contiguous ranges, then
-  // a scan over the threads) and finds the item its range starts in.
-  {
+  // a scan over the threads) and finds the item its range starts in. Warp 6 is
+  // not waited for: it allocates tensor memory.
+  if (warp < 6) {
+    constexpr int kPlanners = 192;
     int* sums = reinterpret_cast<int*>(red);
-    const int lo = split(p.items, tid, kAttnThreads), hi = split(p.items, tid + 1, kAttnThreads);
+    const int lo = split(p.items, tid, kPlanners), hi = split(p.items, tid + 1, kPlanners);
     int own = 0;
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) own += item_tiles(p, i);
@@ -393,17 +398,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (lane >= o) upto += v;
     }
     if (lane == 31) sums[warp] = upto;
-    __syncthreads();
+    named_barrier_sync(1, kPlanners);
     int at = upto - own, units = 0;
 #pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
+    for (int w = 0; w < kPlanners / 32; ++w) {
       const int v = sums[w];
       at += w < warp ? v : 0;
       units += v;
     }
     const int pairs = max(1, min(npairs_max, units));
-    const int u0 = pair < pairs ? unit_of_pair(units, pairs, pair) : units;
-    const int u1 = pair < pairs ? unit_of_pair(units, pairs, pair + 1) : units;
+    const int u0 = pair < pairs ? unit_of_pair(p, units, pairs, npairs_max, pair) : units;
+    const int u1 = pair < pairs ? unit_of_pair(p, units, pairs, npairs_max, pair + 1) : units;
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       const int n = hi - lo == 1 ? own : item_tiles(p, i);
@@ -456,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         const int limit = pre ? p.P : it.len;
         if (t >= t1 || !looks || key >= limit) return -1;
         const int* pages = pre ? p.prefix_pages : p.table + static_cast<int64_t>(it.b) * p.table_stride;
-        return __ldg(pages + (p.page_shift >= 0 ? key >> p.page_shift : key / p.page));
+        return __ldg(pages + div_by(key, p.by_page));
       };
       auto row_of = [&](int t, int entry) {
         const int key = first_key(t) + mine + lane * rows;
@@ -886,7 +891,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 // item was not cut were stored by the attention kernel; rows without any key
 // become zeros.
 template <int Q, int S, int U>
-__global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(S > 1 ? S * 32 : 128) mla_join_kernel(const AttnParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -905,7 +910,7 @@ __global__ void __launch_bounds__(S > 4 ? S * 32 : 128) mla_join_kernel(const At
   for (int k = 0; k < 2; ++k) {
     int item = -1;
     if (k == 0 && (p.merged || p.prefix_tiles > 0)) item = rc / kTileRows;
-    if (k == 1 && !p.merged) item = p.prefix_items + b * ((p.H + kTileRows - 1) / kTileRows) + h / kTileRows;
+    if (k == 1 && !p.merged) item = p.prefix_items + b * p.per + h / kTileRows;
     local[k] = k == 0 ? r % kTileRows : h % kTileRows;
     pitch[k] = k == 0 ? kTileRows : p.own_rows;
     if (item < 0) continue;
@@ -1132,10 +1137,10 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   if (!is_aligned(workspace, 256)) return FP8BLK_ERR_ALIGN;
   const AttnSizes z = attention_sizes(B, H, prefix_len);
   if (workspace_bytes < z.plan_bytes + z.ml_bytes + z.o_bytes) return FP8BLK_ERR_WORKSPACE;
-  // The tile counts are summed in 32 bits.
+  // The tile counts stay below 2^30.
   const int64_t most = (prefix_len + kTileKeys - 1) / kTileKeys * (z.merged ? z.items : z.prefix_items) +
                        (table_stride * page_size / kTileKeys + 1) * (z.items - z.prefix_items);
-  if (most > (int64_t{1} << 31) - 1) return FP8BLK_ERR_SHAPE;
+  if (most >= int64_t{1} << 30) return FP8BLK_ERR_SHAPE;
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
   static bool attr_done[64] = {};
@@ -1160,9 +1165,10 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   p.H = static_cast<int>(H);
   p.P = static_cast<int>(prefix_len);
   p.page = static_cast<int>(page_size);
-  p.page_shift = -1;
-  for (int s = 0; s < 21; ++s)
-    if ((int64_t{1} << s) == page_size) p.page_shift = s;
+  p.per = static_cast<int>((H + kTileRows - 1) / kTileRows);
+  p.by_page = divisor(page_size);
+  p.by_per = divisor(p.per);
+  p.by_pairs = divisor(resident_pairs(d));
   p.num_pages = static_cast<int>(num_pages);
   p.table_stride = static_cast<int>(table_stride);
   p.max_own = static_cast<int>(table_stride * page_size);
@@ -1204,12 +1210,12 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   const int64_t rows = B * H;
   const int variant = rows <= 256 ? 0 : rows <= 2048 ? 1 : 2;
   cudaLaunchConfig_t join = {};
-  join.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32), variant == 0 ? kC / 4 : variant == 1 ? kC / 8 : kC / 64);
-  join.blockDim = dim3(variant == 0 ? 256 : 128);
+  join.gridDim = dim3(static_cast<unsigned>((rows + 31) / 32), variant == 0 ? kC / 4 : variant == 1 ? kC / 16 : kC / 128);
+  join.blockDim = dim3(variant == 0 ? 256 : variant == 1 ? 64 : 128);
   join.stream = cfg.stream;
   join.attrs = attr;
   join.numAttrs = 1;
-  return cuda_status(variant == 0   ? cudaLaunchKernelEx(&join, mla_join_kernel<1, 8, 5>, p)
-                     : variant == 1 ? cudaLaunchKernelEx(&join, mla_join_kernel<2, 4, 2>, p)
-                                    : cudaLaunchKernelEx(&join, mla_join_kernel<4, 1, 2>, p));
+  return cuda_status(variant == 0   ? cudaLaunchKernelEx(&join, mla_join_kernel<1, 8, 6>, p)
+                     : variant == 1 ? cudaLaunchKernelEx(&join, mla_join_kernel<4, 2, 4>, p)
+                                    : cudaLaunchKernelEx(&join, mla_join_kernel<8, 1, 3>, p));
 }
