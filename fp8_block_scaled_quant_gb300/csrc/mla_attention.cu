@@ -39,9 +39,9 @@
 // output is rescaled in tensor memory on few tiles). P is rounded to bf16, the
 // type the tensor cores take next to bf16 keys; the weight sum adds the
 // rounded weights, so equal keys give exactly their mean. Keys past the end
-// are masked by position, not by value, and their rows enter the output
-// product as zeros (out-of-range TMA rows), so whatever an unused cache row
-// holds, NaN included, stays out. The logarithm of the sum, where asked for,
+// are masked by position, not by value, and their rows are overwritten with
+// zeros before the output product, so whatever an unused cache row holds, NaN
+// included, stays out. The logarithm of the sum, where asked for,
 // comes from a second sum of the weights before their rounding.
 //
 // Every wait is bounded (2 s): on expiry roles leave their loops, in-flight
@@ -76,7 +76,7 @@ constexpr int kOffK = kOffP + 2 * kSlab;
 constexpr int kOffV = kOffK + kQSlabs * kSlab;
 constexpr int kOffRed = kOffV + kVChunks * kVChunk;  // [2][2][64] row maxima, then sums
 constexpr int kOffBar = kOffRed + 2 * 2 * 64 * 4;
-constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 1;
+constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 2;
 static_assert(kNumBars <= 32, "a lane of a warp initialises each");
 constexpr int kAttnSmem = 1024 + kOffBar + kNumBars * 8 + 32;
 static_assert(kAttnSmem <= 232448, "shared memory per CTA");
@@ -123,6 +123,7 @@ struct AttnParams {
   int prefix_tiles, prefix_items, items, own_rows;
   int merged;              // H % 128 == 0: prefix and own keys in one item
   int kbox, vbox;          // rows of a TMA box of keys / values
+  int kslabs, vslabs;      // and its 64-column slabs (several where a box has a slab's rows)
   int lone_prefix;         // few row tiles: the prefix's keys come from HBM too
   int direct;              // no item can be cut or share a row: no join
   float scale_log2;
@@ -238,6 +239,11 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
   return ok;
 }
 
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait(a, parity) || wait_slow(a, parity, abort, err);
+}
+
 // The same for a whole warp: true in all lanes or in none.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
   const uint32_t a = smem_u32(bar);
@@ -246,14 +252,22 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return ok;
 }
 
-// 2-D tiled load into this CTA's shared memory; the bytes complete on the
-// mbarrier at shared::cluster address `bar`, in this CTA or its pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+// Tiled load (column in a slab, row, slab) into this CTA's shared memory; the
+// bytes complete on the mbarrier at shared::cluster address `bar`, in this CTA
+// or its pair.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int slab) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(slab)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int y, int slab) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(0), "r"(y), "r"(slab)
+               : "memory");
 }
 
 // D (+)= A B^T over the pair for one K = 16 slice; issued by one thread of CTA 0.
@@ -330,7 +344,6 @@ __device__ __forceinline__ int split(int items, int tid, int n) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     mla_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qpe,
                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                         const __grid_constant__ CUtensorMap map_four, const __grid_constant__ CUtensorMap map_row,
                          const AttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
@@ -347,7 +360,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   uint64_t* pv_done = p_full + 1;
   uint64_t* o_empty = pv_done + 1;
   uint64_t* red_bar = o_empty + 1;
-  uint64_t* drain = red_bar + 1;
+  uint64_t* v_end = red_bar + 1;  // this CTA's part of the chunk that holds the end of the keys
+  uint64_t* drain = v_end + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* start = reinterpret_cast<int*>(tmem_slot + 2);  // first item, its first tile, unit count
@@ -361,7 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     // A lane per barrier. Arrivals: the softmax warps of both CTAs, of one, or one.
     uint64_t* bar = q_full + lane;
     const bool both = bar == s_empty || bar == s_empty + 1 || bar == p_full || bar == o_empty;
-    if (lane < kNumBars) mbar_init(bar, both ? 8 : bar == red_bar ? 4 : 1);
+    const bool values = bar >= v_full && bar < v_full + kVChunks;  // a value warp of each CTA
+    if (lane < kNumBars) mbar_init(bar, both ? 8 : bar == red_bar ? 4 : values ? 2 : 1);
     if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
@@ -444,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const uint32_t bars = map_to_cta(smem_u32(is_k ? k_full : v_full), 0);
     const uint32_t dst0 = smem_u32(smem + (is_k ? kOffK : kOffV));
     const int rows = is_k ? p.kbox : 16;   // keys per looked-up page entry
-    uint32_t vphase = 0;                   // bit c: phase of value chunk c
+    uint32_t vphase = 0, ends = 0;         // bit c: phase of value chunk c; uses of v_end
     const int mine = is_k ? static_cast<int>(rank) * 64 : 0;
     const bool looks = lane * rows < (is_k ? 64 : kTileKeys);
 #pragma unroll 1
@@ -477,10 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(q_full, 2 * kQSlabs * kSlab);
           const uint32_t bar = map_to_cta(smem_u32(q_full), 0);
           const int y = it.row0 + static_cast<int>(rank) * 64;
-#pragma unroll 1
-          for (int s = 0; s < kQSlabs; ++s)
-            tma_load_2d_pair(smem_u32(smem + kOffQ + s * kSlab), s < kC / 64 ? &map_q : &map_qpe, bar,
-                             s < kC / 64 ? s * 64 : 0, y);
+          tma_load_pair(smem_u32(smem + kOffQ), &map_q, bar, y, 0);
+          tma_load_pair(smem_u32(smem + kOffQ + kC / 64 * kSlab), &map_qpe, bar, y, 0);
         }
         __syncwarp();
       }
@@ -508,9 +521,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               const int y = __shfl_sync(0xFFFFFFFFu, y16, q);
               const uint32_t dst = dst0 + g * kGroupBytes + q * p.kbox * 128;
               if (elect_one_sync()) {
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-                  tma_load_2d_pair(dst + s * kSlab, &map_k, bars + g * 8, (3 * g + s) * 64, y);
+                tma_load_pair(dst, &map_k, bars + g * 8, y, 3 * g);
+                if (p.kslabs == 1) {
+                  tma_load_pair(dst + kSlab, &map_k, bars + g * 8, y, 3 * g + 1);
+                  tma_load_pair(dst + 2 * kSlab, &map_k, bars + g * 8, y, 3 * g + 2);
+                }
               }
               __syncwarp();
             }
@@ -523,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
               if (y < p.total_rows && elect_one_sync()) {
 #pragma unroll 1
-                for (int x = 0; x < kRow; x += 64) tma_prefetch_l2_2d(&map_k, x, y);
+                for (int x = 0; x < kQSlabs; x += p.kslabs) tma_prefetch_l2(&map_k, y, x);
               }
               __syncwarp();
             }
@@ -531,47 +546,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         } else {
           // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
           // the half 128 rank .. + 128, as slabs 2 j and 2 j + 1 of each chunk.
-          // The rows past the end in the chunk that holds it are zeros; chunks past
-          // it are neither loaded nor multiplied.
-          const int x0 = static_cast<int>(rank) * 128;
+          // The chunk that holds the end completes on a barrier of this CTA; its
+          // rows past the end are zeroed here before the MMA thread hears of it.
+          // (Out-of-range rows of the copy itself took up to 44 copies, 3.5 us.)
+          // Chunks past the end are neither loaded nor multiplied.
 #pragma unroll 1
           for (int c = 0; c < chunks_of(key0, limit); ++c) {
-            const int kc = key0 + c * 32;
+            const int keys = limit - (key0 + c * 32);
             const uint32_t dst = dst0 + c * kVChunk;
+            const uint32_t full = bars + c * 8;
+            const uint32_t bar = keys < 32 ? map_to_cta(smem_u32(v_end), rank) : full;
             ok = wait_warp(&v_empty[c], ((vphase >> c) & 1) ^ 1, abort_flag, p.err);
             if (!ok) break;
-            vphase ^= 1u << c;
-            if (rank == 0 && elect_one_sync()) mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
-            if (kc + 32 <= limit) {
-#pragma unroll 1
-              for (int q = 0; q < 32; q += p.vbox) {
-                const int y = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (q >> 4));
-                if (elect_one_sync()) {
-#pragma unroll
-                  for (int s = 0; s < 4; ++s)
-                    tma_load_2d_pair(dst + s * kVSlab + q * 128, &map_v, bars + c * 8,
-                                     (s >> 1) * 256 + x0 + (s & 1) * 64, y);
-                }
-                __syncwarp();
-              }
-            } else {
-              // Four rows at a time, the four with the end one by one.
-#pragma unroll 1
-              for (int r = 0; r < 32;) {
-                const int y0 = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (r >> 4));
-                const int left = limit - kc - r;
-                const bool four = left <= 0 || left >= 4 ? (r & 3) == 0 : false;
-                const int y = left > 0 && y0 < p.total_rows ? y0 + (r & 15) : p.total_rows;
-                if (elect_one_sync()) {
-#pragma unroll
-                  for (int s = 0; s < 4; ++s)
-                    tma_load_2d_pair(dst + s * kVSlab + r * 128, four ? &map_four : &map_row, bars + c * 8,
-                                     (s >> 1) * 256 + x0 + (s & 1) * 64, y);
-                }
-                __syncwarp();
-                r += four ? 4 : 1;
-              }
+            if (elect_one_sync()) {
+              if (keys < 32)
+                mbar_arrive_expect_tx(v_end, kVChunk);
+              else if (rank == 0)
+                mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
+              else
+                mbar_arrive_cluster(full);
             }
+            __syncwarp();
+#pragma unroll 1
+            for (int q = 0; q < 32; q += p.vbox) {
+              const int y = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (q >> 4));
+              if (elect_one_sync()) {
+                const uint32_t to = dst + q * 128;
+                const int slab = static_cast<int>(rank) * 2;
+                tma_load_pair(to, &map_v, bar, y, slab);
+                tma_load_pair(to + 2 * kVSlab, &map_v, bar, y, slab + 4);
+                if (p.vslabs == 1) {
+                  tma_load_pair(to + kVSlab, &map_v, bar, y, slab + 1);
+                  tma_load_pair(to + 3 * kVSlab, &map_v, bar, y, slab + 5);
+                }
+              }
+              __syncwarp();
+            }
+            if (keys < 32) {
+              ok = wait_warp(v_end, ends & 1, abort_flag, p.err);
+              if (!ok) {
+                wait_slow(smem_u32(v_end), ends & 1, nullptr, p.err);  // the copies in flight
+                break;
+              }
+              ++ends;
+#pragma unroll 1
+              for (int e = keys * 8 + lane; e < 32 * 8; e += 32)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  *reinterpret_cast<uint4*>(smem + kOffV + c * kVChunk + s * kVSlab + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(full);
+            }
+            vphase ^= 1u << c;
           }
         }
       }
@@ -594,7 +621,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     }
   } else if (warp == 6) {
     // ---- MMA (CTA 0 issues for the pair) -------------------------------------
-    if (rank == 0) {
+    // One thread runs the whole role: a warp's votes and elections around each of
+    // a tile's nine waits left the tensor cores idle between products.
+    if (rank == 0 && elect_one_sync()) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 256, true);
       const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + kOffQ)), kd = sdesc_kmajor_sw128(smem_u32(smem + kOffK));
       const uint64_t pd = sdesc_kmajor_sw128(smem_u32(smem + kOffP));
@@ -610,14 +639,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       uint32_t vphase = 0;
       auto output = [&](uint32_t k, bool first, uint32_t sg, int chunks) {
         if (first && sg > 0)
-          ok = ok && wait_warp(o_empty, (sg - 1) & 1, abort_flag, p.err);
-        ok = ok && wait_warp(p_full, k & 1, abort_flag, p.err);
+          ok = ok && wait_one(o_empty, (sg - 1) & 1, abort_flag, p.err);
+        ok = ok && wait_one(p_full, k & 1, abort_flag, p.err);
 #pragma unroll 1
         for (int c = 0; ok && c < chunks; ++c) {
-          ok = wait_warp(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
+          ok = wait_one(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after_sync();
-          if (elect_one_sync()) {
+          {
             const uint64_t ad = pd + static_cast<uint32_t>(c >> 1) * (kSlab >> 4) + 4 * (c & 1);
             const uint64_t bd = vd + static_cast<uint32_t>(c) * (kVChunk >> 4);
 #pragma unroll
@@ -629,7 +658,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             mma_commit_pair(&v_empty[c]);
             if (c == chunks - 1) mma_commit_pair(pv_done);
           }
-          __syncwarp();
           vphase ^= 1u << c;
         }
       };
@@ -641,15 +669,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
         for (int t = t0; ok && t < t1; ++t) {
           const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
-          if (t == t0) ok = wait_warp(q_full, seg & 1, abort_flag, p.err);
+          if (t == t0) {
+            // The next queries are asked for when the last scores are done: their
+            // way here is spent on the last output product.
+            if (n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
+            ok = ok && wait_one(q_full, seg & 1, abort_flag, p.err);
+          }
           if (n > 1)
-            ok = ok && wait_warp(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
+            ok = ok && wait_one(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
 #pragma unroll 1
           for (int g = 0; ok && g < kKGroups; ++g) {
-            ok = wait_warp(&k_full[g], n & 1, abort_flag, p.err);
+            ok = wait_one(&k_full[g], n & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after_sync();
-            if (elect_one_sync()) {
+            {
               const uint64_t ad = qd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
               const uint64_t bd = kd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
 #pragma unroll
@@ -662,9 +695,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                 if (t == t1 - 1) mma_commit_pair(q_empty);
               }
             }
-            __syncwarp();
           }
-          if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
+          if (ok && t > t0) output(n - 1, prev_first, prev_seg, prev_chunks);
           prev_first = t == t0;
           prev_seg = seg;
           const bool pre = t < it.pt;
@@ -677,11 +709,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       }
       if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
       if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
-        if (elect_one_sync()) mma_commit_pair(drain);
-        __syncwarp();
+        mma_commit_pair(drain);
         wait_slow(smem_u32(drain), 0, nullptr, p.err);
       }
     }
+    __syncwarp();
   } else {
     // ---- softmax and stores ---------------------------------------------------
     if (p.direct && rank == 0) {
@@ -943,7 +975,7 @@ __global__ void __launch_bounds__(S > 1 ? S * 32 : 128) mla_join_kernel(const At
         const float4* src = p.part_o + at[g] * (kC / 4) + static_cast<int64_t>(kk) * kStride +
                             static_cast<int64_t>(quad) * pitch[g] + local[g];
 #pragma unroll
-        for (int c = 0; c < Q; ++c) v[u][c] = __ldcs(src + c * pitch[g]);
+        for (int c = 0; c < Q; ++c) v[u][c] = __ldcg(src + c * pitch[g]);
       }
     }
     float mn = m;
@@ -1044,15 +1076,16 @@ EncodeTiledFn attention_map_encoder() {
   return fn;
 }
 
-// bf16 rows x cols, boxes of 64 columns x box_rows, 128-byte swizzled.
-bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+// bf16 rows x cols as (64 columns, row, slab): boxes of 64 columns x box_rows
+// x box_slabs, 128-byte swizzled, a slab's rows together.
+bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, int box_rows, int box_slabs) {
   EncodeTiledFn enc = attention_map_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint64_t dims[3] = {64, rows, cols / 64};
+  const cuuint64_t strides[2] = {cols * 2, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_slabs)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1180,6 +1213,8 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   p.merged = z.merged ? 1 : 0;
   p.kbox = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   p.vbox = page_size % 32 == 0 ? 32 : 16;
+  p.kslabs = p.kbox == 64 ? 3 : 1;
+  p.vslabs = p.vbox == 32 ? 2 : 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.lone_prefix = B * H <= 2 * kTileRows;
   p.direct = (z.merged || p.prefix_tiles == 0) && p.prefix_tiles + (p.max_own + kTileKeys - 1) / kTileKeys <= 1;
@@ -1187,12 +1222,11 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   const void* cbase = num_pages > 0 ? cache_bf16 : q_bf16;
   const uint64_t crows = num_pages > 0 ? static_cast<uint64_t>(num_pages * page_size) : 1;
   const uint64_t ccols = num_pages > 0 ? kRow : kC;
-  CUtensorMap mq, mqp, mk, mv, m4, mr;
-  if (!make_bf16_map(&mq, q_bf16, static_cast<uint64_t>(B * H), kC, 64) ||
-      !make_bf16_map(&mqp, q_pe_bf16, static_cast<uint64_t>(B * H), kR, 64) ||
-      !make_bf16_map(&mk, cbase, crows, ccols, static_cast<uint32_t>(p.kbox)) ||
-      !make_bf16_map(&mv, cbase, crows, ccols, static_cast<uint32_t>(p.vbox)) ||
-      !make_bf16_map(&m4, cbase, crows, ccols, 4) || !make_bf16_map(&mr, cbase, crows, ccols, 1))
+  CUtensorMap mq, mqp, mk, mv;
+  if (!make_bf16_map(&mq, q_bf16, static_cast<uint64_t>(B * H), kC, 64, kC / 64) ||
+      !make_bf16_map(&mqp, q_pe_bf16, static_cast<uint64_t>(B * H), kR, 64, 1) ||
+      !make_bf16_map(&mk, cbase, crows, ccols, p.kbox, p.kslabs) ||
+      !make_bf16_map(&mv, cbase, crows, ccols, p.vbox, p.vslabs))
     return FP8BLK_ERR_CUDA;
   if (num_pages == 0) p.total_rows = 1;
   cudaLaunchConfig_t cfg = {};
@@ -1205,7 +1239,7 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, m4, mr, p))) return st;
+  if (int st = cuda_status(cudaLaunchKernelEx(&cfg, mla_attention_kernel, mq, mqp, mk, mv, p))) return st;
   if (p.direct) return FP8BLK_OK;
   const int64_t rows = B * H;
   const int variant = rows <= 256 ? 0 : rows <= 2048 ? 1 : 2;
