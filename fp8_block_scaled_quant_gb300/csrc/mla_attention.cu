@@ -641,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (first && sg > 0)
           ok = ok && wait_one(o_empty, (sg - 1) & 1, abort_flag, p.err);
         ok = ok && wait_one(p_full, k & 1, abort_flag, p.err);
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; ok && c < chunks; ++c) {
           ok = wait_one(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
           if (!ok) break;
