@@ -20,8 +20,8 @@
 //     CTA a producer warp keeps 160 KB of weight tiles in flight by TMA (128 rows x
 //     one K block, 16 KB), a warp issues the MMAs, four promote and finish.
 //   - The gate decides what the routed weights are, but not the shared ones: the
-//     ring fills with the CTA's share of the shared experts while x is quantised
-//     and the gate computed.
+//     CTA's share of the shared experts streams through while the gate is computed
+//     by the warps that do not stream.
 //   - w2 does not depend on u, only its use does: the ring runs on from phase 1
 //     into w2 before the barrier between them.
 //   - Phase 1 lays its units (expert, 128 rows of w1 and the same of w3) end to
@@ -74,8 +74,11 @@ constexpr int kGateVecs = 4;              // 16-byte vectors of a gate row per t
 constexpr int kStages = 10;               // weight tiles in flight
 constexpr int kTileBytes = 128 * 128;
 constexpr int kSets = 8;                  // accumulator sets in tensor memory
-// Streaming roles; the other warps wait for the phase to end.
-constexpr int kProducer = 2, kIssuer = 1, kFinisher = 4, kCloser = 8;  // finishers: warps 4-7, closers: 8-11
+// Streaming roles: finishers are warps 4-7, closers 8-11. All but producer,
+// issuer and finishers compute the gate first (0, 3, 8-15).
+constexpr int kProducer = 2, kIssuer = 1, kFinisher = 4, kCloser = 8;
+constexpr int kGaters = 10;
+constexpr int kFewTokens = 4;             // up to here the closers load eight parts at a time
 constexpr unsigned kDevErrTimeoutLayer = 1u << 9;
 
 // Shared memory: weight tiles, token tiles, token scales, barriers, tables.
@@ -83,7 +86,7 @@ __host__ __device__ constexpr int off_tok() { return kStages * kTileBytes; }
 __host__ __device__ constexpr int off_scl(int n) { return off_tok() + kStages * n * 128; }
 __host__ __device__ constexpr int off_bar(int n) { return off_scl(n) + kStages * n * 4; }
 constexpr int kCuts = 6;                  // cut units and tiles of a CTA: two per range
-constexpr int kNumBars = 3 * kStages + 2 * kSets + kCuts + 1;
+constexpr int kNumBars = 3 * kStages + 2 * kSets + kCuts + 2;
 __host__ __device__ constexpr int off_act(int n) { return (off_bar(n) + kNumBars * 8 + 8 + 15) / 16 * 16; }
 __host__ __device__ constexpr int off_mask(int n) { return off_act(n) + kMaxActive * 4; }
 __host__ __device__ constexpr int off_sel(int n) { return off_mask(n) + kMaxActive * 4; }  // ids, weights; scratch before
@@ -178,6 +181,33 @@ __device__ __forceinline__ int part_of(int n, int x, int G) {
   return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(G) - 1u) / static_cast<uint32_t>(n));
 }
 
+// h1 (and, of kTwo, h3) += the parts 0, 1, ..., of which each has [h1, h3][T][128]
+// of this thread's row: U parts are loaded together, tokens mk < 2^J of them.
+template <int U, int J, bool kTwo, int N, class F>
+__device__ __forceinline__ void add_parts(float (&h1)[N], float (&h3)[N], int parts, int T, uint32_t mk, F part) {
+#pragma unroll 1
+  for (int i = 0; i < parts; i += U) {
+    float a[U][J], b[U][kTwo ? J : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* v = part(min(i + u, parts - 1));
+      const uint32_t want = i + u < parts ? mk : 0u;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        a[u][j] = (want >> j) & 1u ? __ldcg(v + j * 128) : 0.f;
+        if (kTwo) b[u][kTwo ? j : 0] = (want >> j) & 1u ? __ldcg(v + (T + j) * 128) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        h1[j] += a[u][j];
+        if (kTwo) h3[j] += b[u][kTwo ? j : 0];
+      }
+  }
+}
+
 __device__ __forceinline__ float silu_mul(float h1, float h3) { return h1 / (1.0f + expf(-h1)) * h3; }
 
 // Ids and weights of token m by one warp, into the pair tables.
@@ -217,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* set_full = empty + kStages;
   uint64_t* set_empty = set_full + kSets;
   uint64_t* cut_stored = set_empty + kSets;  // this CTA's part of its i-th cut unit or tile is in memory
-  uint64_t* drain = cut_stored + kCuts;
+  uint64_t* tables = cut_stored + kCuts;     // the gate's tables are there
+  uint64_t* drain = tables + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* act = reinterpret_cast<int*>(smem + off_act(N));              // active experts, shared ones first
@@ -245,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&set_empty[i], 4);
     }
     for (int i = 0; i < kCuts; ++i) mbar_init(&cut_stored[i], 4);
+    mbar_init(tables, 1);
     mbar_init(drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&map1);
@@ -252,6 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map2);
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_u);
+  }
+  if (tid < p.ns) {
+    act[tid] = p.E + tid;
+    mask[tid] = all_tokens;
   }
   if (tid < p.E) bias[tid] = p.gate_bias ? __ldg(p.gate_bias + tid) : 0.f;
   if (warp == kIssuer) {
@@ -411,41 +447,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e0 + per_cta * G < p.E) load_gate(e0 + per_cta * G + warp / wpe * G);
     }
   }
+  tc_fence_before_sync();
   grid_barrier(0, first_tiles);
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
 
   // The gate, by every CTA for itself, then the tables: active experts in order
   // (shared ones first) and their tokens.
+  if (warp == 0 || warp == 3 || warp >= kCloser) {
+    const int gw = warp == 0 ? 0 : warp == 3 ? 1 : warp - kCloser + 2, gt = gw * 32 + lane;
+    auto meet = [&] { named_barrier_sync(4, kGaters * 32); };
 #pragma unroll 1
-  for (int m = warp; m < p.T; m += kWarps) gate_of_token(p, bias, m, lane, c == 0, sel_e, sel_w);
-  uint32_t* tokens_of = reinterpret_cast<uint32_t*>(bias);  // by expert id; the bias has been used
-  __syncthreads();
-  for (int e = tid; e < p.E; e += kThreads) tokens_of[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < p.T * p.k; i += kThreads) atomicOr(&tokens_of[sel_e[i]], 1u << (i / p.k));
-  __syncthreads();
-  const uint32_t my_tokens = tid < p.E ? tokens_of[tid] : 0;
-  const unsigned have = __ballot_sync(0xFFFFFFFFu, my_tokens != 0);
-  if (lane == 0) scan[warp] = __popc(have);
-  __syncthreads();
-  int a0 = p.ns;
+    for (int m = gw; m < p.T; m += kGaters) gate_of_token(p, bias, m, lane, c == 0, sel_e, sel_w);
+    uint32_t* tokens_of = reinterpret_cast<uint32_t*>(bias);  // by expert id; the bias has been used
+    meet();
+    if (gt < p.E) tokens_of[gt] = 0;
+    meet();
+    for (int i = gt; i < p.T * p.k; i += kGaters * 32) atomicOr(&tokens_of[sel_e[i]], 1u << (i / p.k));
+    meet();
+    const uint32_t my_tokens = gt < p.E ? tokens_of[gt] : 0;
+    const unsigned have = __ballot_sync(0xFFFFFFFFu, my_tokens != 0);
+    if (lane == 0) scan[gw] = __popc(have);
+    meet();
+    int a0 = p.ns;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) a0 += w < warp ? scan[w] : 0;
-  if (tid < p.ns) {
-    act[tid] = p.E + tid;
-    mask[tid] = all_tokens;
+    for (int w = 0; w < kGaters; ++w) a0 += w < gw ? scan[w] : 0;
+    if (my_tokens) {
+      const int a = a0 + __popc(have & ((1u << lane) - 1u));
+      act[a] = gt;
+      mask[a] = my_tokens;
+    }
+    if (gt == kGaters * 32 - 1) scan[32] = a0 + __popc(have);
+    meet();
+    if (gt == 0) mbar_arrive(tables);
   }
-  if (my_tokens) {
-    const int a = a0 + __popc(have & ((1u << lane) - 1u));
-    act[a] = tid;
-    mask[a] = my_tokens;
-  }
-  if (tid == kThreads - 1) scan[32] = a0 + __popc(have);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const int nact = scan[32];
-  const uint32_t tmem = *tmem_slot;
-  const int routed_blocks = (nact - p.ns) * Kb2 * Kb1;
+  // What follows from the tables, learnt by each role when it needs it. Items of
+  // phase 2: K blocks of row tiles of w2, expert by expert.
+  struct Item {
+    int tile, a, kb;
+  };
+  int nact = 0, routed_blocks = 0, tile_blocks = 0, blocks2 = 0, q2 = 0, n2 = 0;
+  Item first_item{0, 0, 0};
+  auto learn = [&] {
+    wait(tables, 0, abort_flag, p.err);
+    nact = *abort_flag ? p.ns : scan[32];
+    routed_blocks = (nact - p.ns) * Kb2 * Kb1;
+    tile_blocks = nact * Kb2;
+    blocks2 = p.dim / 128 * tile_blocks;
+    q2 = even(blocks2, c, G);
+    n2 = even(blocks2, c + 1, G) - q2;
+    if (n2 > 0) first_item = Item{q2 / tile_blocks, q2 / Kb2 % nact, q2 % Kb2};
+  };
   auto gate_weight = [&](int a, int m) {
     if (a < p.ns) return 1.0f;
     float w = 0.f;
@@ -580,12 +632,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   // ---- phase 1 -------------------------------------------------------------------
-  // Items of phase 2: K blocks of row tiles of w2, expert by expert.
-  const int tile_blocks = nact * Kb2, blocks2 = p.dim / 128 * tile_blocks;
-  const int q2 = even(blocks2, c, G), n2 = even(blocks2, c + 1, G) - q2;
-  struct Item {
-    int tile, a, kb;
-  };
   auto next_item = [&](Item& k) {
     if (++k.kb == Kb2) {
       k.kb = 0;
@@ -595,12 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   };
-  const Item first_item{q2 / tile_blocks, q2 / Kb2 % nact, q2 % Kb2};
-  Item item_ahead = first_item;
   auto load_item = [&](const Item& k) { load_tile(&map2, k.kb * 128, act[k.a] * p.dim + k.tile * 128); };
-  const int early2 = min(kStages, n2);  // w2 tiles asked for before u is quantised
-  const int phase1_tiles =
-      2 * (even(shared_blocks, c + 1, G) - even(shared_blocks, c, G) + even(routed_blocks, c + 1, G) - even(routed_blocks, c, G));
+  Item item_ahead = first_item;
+  int early2 = 0, phase1_tiles = 0;
   if (producer) {
     fence_proxy_async_all();
     Cursor k = cursor(0, shared_blocks);
@@ -611,7 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll 1
     for (int range = 0; range < 2; ++range) {
-      if (range) ahead = cursor(p.ns, routed_blocks);
+      if (range) {
+        learn();
+        ahead = cursor(p.ns, routed_blocks);
+      }
 #pragma unroll 1
       for (; ahead.left > 0; advance(ahead)) {
         const int s = issued % kStages;
@@ -619,6 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tokens(s, &map_x, ahead.kb * 128, 0, p.xs + ahead.kb * N);
       }
     }
+    phase1_tiles = issued;
+    early2 = min(kStages, n2);  // w2 tiles asked for before u is quantised
+    item_ahead = first_item;
 #pragma unroll 1
     for (int q = 0; q < early2; ++q) {
       load_item(item_ahead);
@@ -626,10 +675,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kIssuer) {
 #pragma unroll 1
-    for (int q = phase1_tiles / 2; q > 0; --q) multiply(2);
+    for (int range = 0; range < 2; ++range) {
+      if (range) learn();
+      const int blocks = range ? routed_blocks : shared_blocks;
+#pragma unroll 1
+      for (int q = even(blocks, c + 1, G) - even(blocks, c, G); q > 0; --q) multiply(2);
+    }
   } else if (warp >= kFinisher && warp < kFinisher + 4) {
 #pragma unroll 1
     for (int range = 0; range < 2; ++range) {
+      if (range) learn();
       Cursor at = range ? cursor(p.ns, routed_blocks) : cursor(0, shared_blocks);
 #pragma unroll 1
       while (at.left > 0) {
@@ -671,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kCloser && warp < kCloser + 4) {
 #pragma unroll 1
     for (int range = 0; range < 2; ++range) {
+      if (range) learn();
       const int blocks = range ? routed_blocks : shared_blocks, first = range ? p.ns : 0;
       const int q0 = even(blocks, c, G), q1 = even(blocks, c + 1, G);
 #pragma unroll 1
@@ -681,23 +737,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole) continue;
         const int a = first + u / Kb2, blk = u % Kb2;
         const uint32_t mk = mask[a];
+        // (With fewer K blocks than CTAs some CTAs have none, the others one.)
         const int c0 = part_of(blocks, u * Kb1, G), c1 = part_of(blocks, end - 1, G);
-        if (!last_part(p.unit_parts + a * Kb2 + blk, 0xFFFFFFFFu, 0, blocks >= G ? c1 - c0 + 1 : Kb1)) continue;
+        const int parts = blocks >= G ? c1 - c0 + 1 : Kb1;
+        if (!last_part(p.unit_parts + a * Kb2 + blk, 0xFFFFFFFFu, 0, parts)) continue;
+        auto part = [&](int i) {
+          const int k = blocks >= G ? c0 + i : part_of(blocks, u * Kb1 + i, G);
+          return p.part + static_cast<size_t>((k * 2 + range) * 2 + (i == 0 ? 1 : 0)) * 2 * p.T * 128 + row;
+        };
         float h1[N], h3[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) h1[j] = h3[j] = 0.f;
-#pragma unroll 1
-        for (int k = c0; k <= c1; ++k) {
-          // (With fewer K blocks than CTAs some CTAs have none.)
-          if (blocks < G && even(blocks, k, G) == even(blocks, k + 1, G)) continue;
-          const float* v = p.part + static_cast<size_t>((k * 2 + range) * 2 + (k == c0 ? 1 : 0)) * 2 * p.T * 128 + row;
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if ((mk >> j) & 1u) {
-              h1[j] += __ldcg(v + j * 128);
-              h3[j] += __ldcg(v + (p.T + j) * 128);
-            }
-        }
+        if (N == 16 && p.T <= kFewTokens)
+          add_parts<8, kFewTokens, true>(h1, h3, parts, p.T, mk, part);
+        else
+          add_parts<N == 16 ? 2 : 1, N, true>(h1, h3, parts, p.T, mk, part);
         quantise_unit(h1, h3, a, blk, mk, 1, row);
       }
     }
@@ -769,19 +823,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       q = end;
       if (whole) continue;
       const int c0 = part_of(blocks2, tl * tile_blocks, G), c1 = part_of(blocks2, end - 1, G);
+      const int parts = blocks2 >= G ? c1 - c0 + 1 : tile_blocks;
       // (At most 192 parts: a byte per tile.)
-      if (!last_part(p.counters + 16 + tl / 4, 0xFFu, tl % 4 * 8, blocks2 >= G ? c1 - c0 + 1 : tile_blocks)) continue;
+      if (!last_part(p.counters + 16 + tl / 4, 0xFFu, tl % 4 * 8, parts)) continue;
+      auto part = [&](int i) {
+        const int k = blocks2 >= G ? c0 + i : part_of(blocks2, tl * tile_blocks + i, G);
+        return p.part2 + static_cast<size_t>(k * 2 + (i == 0 ? 1 : 0)) * p.T * 128 + row;
+      };
       float acc[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] = 0.f;
-#pragma unroll 2
-      for (int k = c0; k <= c1; ++k) {
-        if (blocks2 < G && even(blocks2, k, G) == even(blocks2, k + 1, G)) continue;
-        const float* v = p.part2 + static_cast<size_t>(k * 2 + (k == c0 ? 1 : 0)) * p.T * 128 + row;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (j < p.T) acc[j] += __ldcg(v + j * 128);
-      }
+      if (N == 16 && p.T <= kFewTokens)
+        add_parts<8, kFewTokens, false>(acc, acc, parts, p.T, all_tokens, part);
+      else
+        add_parts<N == 16 ? 4 : 2, N, false>(acc, acc, parts, p.T, all_tokens, part);
 #pragma unroll
       for (int j = 0; j < N; ++j)
         if (j < p.T) p.y[static_cast<size_t>(j) * p.dim + tl * 128 + row] = __float2bfloat16_rn(acc[j]);
