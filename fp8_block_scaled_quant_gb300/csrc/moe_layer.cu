@@ -107,9 +107,11 @@ struct LayerParams {
   __nv_bfloat16* y;
   int32_t* topk_idx;    // may be null
   float* topk_w;        // may be null
-  unsigned* counters;   // [0..1] barrier arrivals, [3] CTAs done, [16..31] row tiles, a byte each; zero between calls
+  unsigned* counters;   // [0..1] barrier arrivals, [2] tokens gated, [3] CTAs done, [16..31] row tiles, a byte each; zero between calls
   unsigned* unit_parts;  // [unit] parts so far; zeroed before the first barrier
   float* logits;        // [T][E]
+  int* ids;             // [T][k], where the grid shares the gate
+  float* weights;
   uint8_t* xq;          // [T][dim]
   float* xs;            // [dim / 128][N]
   uint8_t* uq;          // [active expert][T][inter], rows of routed tokens
@@ -365,6 +367,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   };
 
+  // Waits until counter i has `goal` arrivals.
+  auto arrived = [&](int i, unsigned goal) {
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t spin = 0;; ++spin) {
+      unsigned v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters + i) : "memory");
+      if (v >= goal) break;
+      if ((spin & 63u) == 63u) {
+        if (*abort_flag) break;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicOr(p.err, kDevErrTimeoutLayer);
+          break;
+        }
+      }
+    }
+    __threadfence();
+  };
   // Grid barrier i: every CTA's threads have arrived, their global writes are visible.
   // (`meanwhile` runs between a CTA's arrival and the wait.)
   auto grid_barrier = [&](int i, auto meanwhile) {
@@ -373,22 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     meanwhile();
     if (tid == 0) {
       atomicAdd(p.counters + i, 1u);
-      const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-      for (uint32_t spin = 0;; ++spin) {
-        unsigned v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.counters + i) : "memory");
-        if (v >= static_cast<unsigned>(G)) break;
-        if ((spin & 63u) == 63u) {
-          if (*abort_flag) break;
-          if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            atomicOr(p.err, kDevErrTimeoutLayer);
-            break;
-          }
-        }
-      }
-      __threadfence();
+      arrived(i, static_cast<unsigned>(G));
     }
     __syncthreads();
   };
@@ -411,30 +417,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sums = sel_w;  // [warp][columns]
 #pragma unroll 1
     for (int e0 = c; e0 < p.E; e0 += per_cta * G) {
-      float acc[N];
+      // (The row's K is at most kGateVecs passes, see kMaxDim.) Four tokens' vectors
+      // are loaded together: a token at a time was 1700 cycles each, a load's way
+      // and a reduction's.
+#pragma unroll 1
+      for (int m0 = 0; m0 < p.T; m0 += 4) {
+        uint4 xv[4][kGateVecs];
 #pragma unroll
-      for (int m = 0; m < N; ++m) acc[m] = 0.f;
-      // (The row's K is at most kGateVecs passes, see kMaxDim.)
-#pragma unroll
-      for (int m = 0; m < N; ++m) {
-        if (m < p.T) {
-          const uint4* xv = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m) * p.dim) + v0;
+        for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int i = 0; i < kGateVecs; ++i)
-            if (v0 + i * step < vecs) {
-              const uint4 b = __ldg(xv + i * step);
-              const uint32_t aw[4] = {gate_row[i].x, gate_row[i].y, gate_row[i].z, gate_row[i].w};
-              const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+            xv[m][i] = m0 + m < p.T && v0 + i * step < vecs
+                           ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(m0 + m) * p.dim) + v0 + i * step)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
-                acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
-              }
+        for (int i = 0; i < kGateVecs; ++i) {
+          const uint32_t aw[4] = {gate_row[i].x, gate_row[i].y, gate_row[i].z, gate_row[i].w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t bw[4] = {xv[m][i].x, xv[m][i].y, xv[m][i].z, xv[m][i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              acc[m] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), acc[m]);
+              acc[m] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), acc[m]);
             }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
-          if (lane == 0) sums[warp * N + m] = acc[m];
+          }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[m] += __shfl_xor_sync(0xFFFFFFFFu, acc[m], o);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (lane == m && m0 + m < p.T) sums[warp * N + m0 + m] = acc[m];
       }
       __syncthreads();
       for (int i = tid; i < per_cta * p.T; i += kThreads) {
@@ -452,13 +468,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  // The gate, by every CTA for itself, then the tables: active experts in order
-  // (shared ones first) and their tokens.
+  // The gate, then the tables: active experts in order (shared ones first) and
+  // their tokens. Every CTA gates up to kGaters tokens for itself, a warp each.
+  // Of more, a CTA gates one and all read the results: 32 tokens took four
+  // rounds, 34 K cycles, where one round and the exchange take 18 K.
   if (warp == 0 || warp == 3 || warp >= kCloser) {
     const int gw = warp == 0 ? 0 : warp == 3 ? 1 : warp - kCloser + 2, gt = gw * 32 + lane;
     auto meet = [&] { named_barrier_sync(4, kGaters * 32); };
+    if (p.T <= kGaters) {
+      if (gw < p.T) gate_of_token(p, bias, gw, lane, c == 0, sel_e, sel_w);
+    } else {
+      if (gw == 0) {
 #pragma unroll 1
-    for (int m = gw; m < p.T; m += kGaters) gate_of_token(p, bias, m, lane, c == 0, sel_e, sel_w);
+        for (int m = c; m < p.T; m += G) {
+          gate_of_token(p, bias, m, lane, true, p.ids, p.weights);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) atomicAdd(p.counters + 2, 1u);
+        }
+        if (lane == 0) arrived(2, static_cast<unsigned>(p.T));
+      }
+      meet();
+      for (int i = gt; i < p.T * p.k; i += kGaters * 32) {
+        sel_e[i] = min(max(__ldcg(p.ids + i), 0), p.E - 1);
+        sel_w[i] = __ldcg(p.weights + i);
+      }
+    }
     uint32_t* tokens_of = reinterpret_cast<uint32_t*>(bias);  // by expert id; the bias has been used
     meet();
     if (gt < p.E) tokens_of[gt] = 0;
@@ -862,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // The last CTA to leave zeroes the counters for the next call.
   if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u) {
-    p.counters[0] = p.counters[1] = p.counters[3] = 0;
+    p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = 0;
     if (*abort_flag)
       for (int i = 16; i < 32; ++i) p.counters[i] = 0;
   }
@@ -904,7 +939,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 struct LayerSizes {
   int64_t active;  // experts at most
   int cols;        // token columns
-  size_t logits, xq, xs, uq, us, units, part, part2, total;
+  size_t logits, ids, weights, xq, xs, uq, us, units, part, part2, total;
 };
 
 LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t topk, int64_t ns) {
@@ -912,7 +947,9 @@ LayerSizes layer_sizes(int64_t T, int64_t dim, int64_t inter, int64_t E, int64_t
   z.active = (T * topk < E ? T * topk : E) + ns;
   z.cols = T <= 16 ? 16 : 32;
   z.logits = 256;
-  z.xq = z.logits + align256(static_cast<size_t>(T) * E * 4);
+  z.ids = z.logits + align256(static_cast<size_t>(T) * E * 4);
+  z.weights = z.ids + align256(static_cast<size_t>(T) * topk * 4);
+  z.xq = z.weights + align256(static_cast<size_t>(T) * topk * 4);
   z.xs = z.xq + align256(static_cast<size_t>(T) * dim);
   z.uq = z.xs + align256(static_cast<size_t>(dim / 128) * z.cols * 4);
   z.us = z.uq + align256(static_cast<size_t>(z.active) * T * inter);
@@ -1004,6 +1041,8 @@ extern "C" int fp8blk_moe_layer(const void* x_bf16, const void* gate_w_bf16, con
   p.topk_w = topk_w;
   p.counters = reinterpret_cast<unsigned*>(ws);
   p.logits = reinterpret_cast<float*>(ws + z.logits);
+  p.ids = reinterpret_cast<int*>(ws + z.ids);
+  p.weights = reinterpret_cast<float*>(ws + z.weights);
   p.xq = ws + z.xq;
   p.xs = reinterpret_cast<float*>(ws + z.xs);
   p.uq = ws + z.uq;
