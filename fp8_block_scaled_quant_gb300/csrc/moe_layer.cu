@@ -357,7 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_tile(&map3, k.kb * 128, y);
   };
   Cursor ahead = cursor(0, shared_blocks);
-  const int early = min(kStages / 2, ahead.left);  // K blocks asked for before the gate
+  // K blocks asked for before the gate: their 64 KB a CTA are on their way while
+  // the CTAs meet; more (half the ring's stages, 160 KB) hold the meeting's atomics
+  // up: 86.0 us for one token of 7168 x 2048 x 256 where two blocks take 84.5.
+  const int early = min(2, ahead.left);
   auto first_tiles = [&] {
     if (producer)
 #pragma unroll 1
