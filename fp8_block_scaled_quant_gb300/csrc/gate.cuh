@@ -98,47 +98,56 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
     eligible = kept;
   }
 
-  // Top-k experts among the eligible lanes' z: each lane offers its largest (a
-  // tree over its keys), the lane whose offer wins takes it out.
+  // Top-k experts among the eligible lanes' z. Each lane puts its keys in
+  // descending order (equal ones in expert order) and offers the first; the lane
+  // whose offer wins takes it out. A round is then an argmax and a move: scores
+  // are fetched for all slots at once afterwards.
   uint32_t key[V];
+  int at[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = i < v && eligible ? gate_order(z[i]) : 0u;
+  for (int i = 0; i < V; ++i) {
+    key[i] = i < v && eligible ? gate_order(z[i]) : 0u;
+    at[i] = i;
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < V; i += 2) {
+      const bool swap = key[i + 1] > key[i];
+      const uint32_t k = key[i];
+      const int a = at[i];
+      key[i] = swap ? key[i + 1] : k;
+      key[i + 1] = swap ? k : key[i + 1];
+      at[i] = swap ? at[i + 1] : a;
+      at[i + 1] = swap ? a : at[i + 1];
+    }
   int my_idx = 0;
-  float my_s = 0.0f, sum = 0.0f;
 #pragma unroll 1
   for (int j = 0; j < K; ++j) {
-    uint32_t k[V];
-    int at[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      k[i] = key[i];
-      at[i] = i;
-    }
-#pragma unroll
-    for (int w = 1; w < V; w *= 2)
-#pragma unroll
-      for (int i = 0; i + w < V; i += 2 * w)
-        if (k[i + w] > k[i]) {
-          k[i] = k[i + w];
-          at[i] = at[i + w];
-        }
     // Lanes are in expert order: ties go to the lower expert.
-    const int owner = warp_argmax_lane(k[0]);
-    float se = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane == owner && at[0] == i) {
-        se = s[i];
-        key[i] = 0u;
-      }
-    se = __shfl_sync(0xFFFFFFFFu, se, owner);
+    const int owner = warp_argmax_lane(key[0]);
     const int e = __shfl_sync(0xFFFFFFFFu, lane * v + at[0], owner);
-    sum = __fadd_rn(sum, se);
-    if (lane == j) {
-      my_idx = e;
-      my_s = se;
+    if (lane == j) my_idx = e;
+    if (lane == owner) {
+#pragma unroll
+      for (int i = 0; i + 1 < V; ++i) {
+        key[i] = key[i + 1];
+        at[i] = at[i + 1];
+      }
+      key[V - 1] = 0u;
     }
   }
+  const int from = my_idx / v, which = my_idx - from * v;
+  float my_s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float si = __shfl_sync(0xFFFFFFFFu, s[i], from);
+    if (which == i) my_s = si;
+  }
+  float sum = 0.0f;
+  if (normalize)
+#pragma unroll 4
+    for (int j = 0; j < K; ++j) sum = __fadd_rn(sum, __shfl_sync(0xFFFFFFFFu, my_s, j));
   *out_idx = my_idx;
   *out_w = __fmul_rn(normalize ? __fdiv_rn(my_s, sum) : my_s, route_scale);
 }
