@@ -124,7 +124,6 @@ struct AttnParams {
   int merged;              // H % 128 == 0: prefix and own keys in one item
   int kbox, vbox;          // rows of a TMA box of keys / values
   int kslabs, vslabs;      // and its 64-column slabs (several where a box has a slab's rows)
-  int lone_prefix;         // few row tiles: the prefix's keys come from HBM too
   int direct;              // no item can be cut or share a row: no join
   float scale_log2;
 };
@@ -163,10 +162,29 @@ __device__ __forceinline__ Item get_item(const AttnParams& p, int i) {
   return it;
 }
 
+// What an item costs beside its tiles (queries loaded, rows stored), in tiles:
+// the split's units are its tiles after that many units without one.
+constexpr int kItemCost = 1;
+
+struct Span {
+  int t0, t1, units;  // tiles, and the units they took from the pair's range
+};
+
+// The tiles of an item of `tiles` in its units [v0, v0 + left).
+__device__ __forceinline__ Span span_of(int tiles, int v0, int left) {
+  const int v1 = min(tiles > 0 ? tiles + kItemCost : 0, v0 + left);
+  return {max(v0 - kItemCost, 0), max(v1 - kItemCost, 0), v1 - v0};
+}
+
 __device__ __forceinline__ int item_tiles(const AttnParams& p, int i) {
   if (!p.merged && i < p.prefix_items) return p.prefix_tiles;
   const int len = own_len(p, div_by(i - p.prefix_items, p.by_per));
   return (p.merged ? p.prefix_tiles : 0) + (len + kTileKeys - 1) / kTileKeys;
+}
+
+__device__ __forceinline__ int item_units(const AttnParams& p, int i) {
+  const int n = item_tiles(p, i);
+  return n > 0 ? n + kItemCost : 0;
 }
 
 // First row of the parts of item i written by pair q: item-major, 128 rows
@@ -364,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   uint64_t* drain = v_end + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* start = reinterpret_cast<int*>(tmem_slot + 2);  // first item, its first tile, unit count
+  int* start = reinterpret_cast<int*>(tmem_slot + 2);  // first item, first unit in it, unit count
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
@@ -405,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int lo = split(p.items, tid, kPlanners), hi = split(p.items, tid + 1, kPlanners);
     int own = 0;
 #pragma unroll 1
-    for (int i = lo; i < hi; ++i) own += item_tiles(p, i);
+    for (int i = lo; i < hi; ++i) own += item_units(p, i);
     int upto = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -426,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const int u1 = pair < pairs ? unit_of_pair(p, units, pairs, npairs_max, pair + 1) : units;
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
-      const int n = hi - lo == 1 ? own : item_tiles(p, i);
+      const int n = hi - lo == 1 ? own : item_units(p, i);
       if (u0 < u1 && u0 >= at && u0 < at + n) {
         start[0] = i;
         start[1] = u0 - at;
@@ -448,13 +466,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int nunits = start[2];
-  const int item0 = nunits ? start[0] : 0, tile0 = nunits ? start[1] : 0;
+  const int item0 = nunits ? start[0] : 0, unit0 = nunits ? start[1] : 0;
 
   if (warp == 4 || warp == 5) {
     // ---- loads: keys (warp 4), queries and values (warp 5) -------------------
     const bool is_k = warp == 4;
     uint32_t n = 0, seg = 0;
-    int left = nunits, i = item0, t0 = tile0;
+    int left = nunits, i = item0, v0 = unit0;
     bool ok = true;
     const uint32_t bars = map_to_cta(smem_u32(is_k ? k_full : v_full), 0);
     const uint32_t dst0 = smem_u32(smem + (is_k ? kOffK : kOffV));
@@ -465,8 +483,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
     while (ok && left > 0 && i < p.items) {
       const Item it = get_item(p, i);
-      const int t1 = min(it.tiles, t0 + left);
-      left -= t1 - t0;
+      const Span in = span_of(it.tiles, v0, left);
+      const int t0 = in.t0, t1 = in.t1;
+      left -= in.units;
       // Lane l's page entry of tile t: that of its l-th `rows` keys. Entries are
       // loaded two tiles ahead and become cache rows when they are needed.
       auto first_key = [&](int t) { return (t < it.pt ? t : t - it.pt) * kTileKeys; };
@@ -530,9 +549,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               __syncwarp();
             }
           }
-          if (t + 1 >= it.pt || p.lone_prefix) {
-            // Keys that no other pair reads come from HBM: ask for the next
-            // tile's while this one is loaded.
+          if (t + 1 >= it.pt) {
+            // Keys that no other pair reads come from HBM: ask for the next tile's
+            // while this one is loaded (32 requests x 128 heads, own keys: 53.4 us
+            // without, 51.4 with; asked for by every pair, a shared prefix's keys
+            // cost more than they give: 61 x 16 rows 22.7 us against 21.4).
 #pragma unroll 1
             for (int q = 0; q < 64 / p.kbox; ++q) {
               const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
@@ -603,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         }
       }
       ++i;
-      t0 = 0;
+      v0 = 0;
     }
     if (*abort_flag && rank == 0) {
       // Copies of both CTAs complete on this CTA's barriers: wait for the last
@@ -629,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       const uint64_t pd = sdesc_kmajor_sw128(smem_u32(smem + kOffP));
       const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + kOffV), kVSlab);
       uint32_t n = 0, seg = 0;
-      int left = nunits, i = item0, t0 = tile0;
+      int left = nunits, i = item0, v0 = unit0;
       bool ok = true;
       bool prev_first = false;
       uint32_t prev_seg = 0;
@@ -664,8 +685,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
       while (ok && left > 0 && i < p.items) {
         const Item it = get_item(p, i);
-        const int t1 = min(it.tiles, t0 + left);
-        left -= t1 - t0;
+        const Span in = span_of(it.tiles, v0, left);
+        const int t0 = in.t0, t1 = in.t1;
+        left -= in.units;
 #pragma unroll 1
         for (int t = t0; ok && t < t1; ++t) {
           const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
@@ -705,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         }
         if (t1 > t0) ++seg;
         ++i;
-        t0 = 0;
+        v0 = 0;
       }
       if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
       if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
@@ -735,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     const uint32_t leader_p = map_to_cta(smem_u32(p_full), 0), leader_o = map_to_cta(smem_u32(o_empty), 0);
     uint8_t* prow = smem + kOffP + kh * kSlab + row * 128;
     uint32_t n = 0, nred = 0;
-    int left = nunits, i = item0, t0 = tile0;
+    int left = nunits, i = item0, v0 = unit0;
     bool ok = true;
     // Both threads of a row give a value; returns the partner's (bounded wait:
     // the four warps meet on an mbarrier).
@@ -751,8 +773,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
     while (ok && left > 0 && i < p.items) {
       const Item it = get_item(p, i);
-      const int t1 = min(it.tiles, t0 + left);
-      left -= t1 - t0;
+      const Span in = span_of(it.tiles, v0, left);
+      const int t0 = in.t0, t1 = in.t1;
+      left -= in.units;
       const int rt = static_cast<int>(rank) * 64 + row;  // row of the tile
       const bool have = rt < it.nrows;
       float m = -INFINITY, l = 0.f, lx = 0.f;  // running maximum, sums of rounded and of fp32 weights
@@ -899,7 +922,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
         if (lane == 0) mbar_arrive_cluster(leader_o);
       }
       ++i;
-      t0 = 0;
+      v0 = 0;
     }
   }
 
@@ -948,7 +971,7 @@ __global__ void __launch_bounds__(S > 1 ? S * 32 : 128) mla_join_kernel(const At
     if (item < 0) continue;
     const int a = p.plan[2 + item], e = p.plan[3 + item];
     if (e <= a) continue;
-    const int q0 = pair_of_unit(units, pairs, a);
+    const int q0 = pair_of_unit(units, pairs, a + kItemCost);  // the first tile's
     n[k] = pair_of_unit(units, pairs, e - 1) - q0 + 1;
     at[k] = part_row(p.merged, p.prefix_items, p.own_rows, item, q0);
   }
@@ -1172,7 +1195,7 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   if (workspace_bytes < z.plan_bytes + z.ml_bytes + z.o_bytes) return FP8BLK_ERR_WORKSPACE;
   // The tile counts stay below 2^30.
   const int64_t most = (prefix_len + kTileKeys - 1) / kTileKeys * (z.merged ? z.items : z.prefix_items) +
-                       (table_stride * page_size / kTileKeys + 1) * (z.items - z.prefix_items);
+                       (table_stride * page_size / kTileKeys + 1) * (z.items - z.prefix_items) + kItemCost * z.items;
   if (most >= int64_t{1} << 30) return FP8BLK_ERR_SHAPE;
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
@@ -1216,7 +1239,6 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   p.kslabs = p.kbox == 64 ? 3 : 1;
   p.vslabs = p.vbox == 32 ? 2 : 1;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.lone_prefix = B * H <= 2 * kTileRows;
   p.direct = (z.merged || p.prefix_tiles == 0) && p.prefix_tiles + (p.max_own + kTileKeys - 1) / kTileKeys <= 1;
   // A cache without pages is never read: its maps describe one row of q.
   const void* cbase = num_pages > 0 ? cache_bf16 : q_bf16;
