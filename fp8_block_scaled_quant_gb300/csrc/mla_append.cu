@@ -12,7 +12,8 @@
 //
 // in fp32 with one rounding to bf16. One launch, one pass: every input byte
 // is read once and every output byte written once, so HBM bounds long
-// prompts and launch latency single tokens.
+// prompts and launch latency single tokens (measured: 6151 tokens of 128 heads,
+// 621 MB, 104.6 us, 5.9 TB/s; one token 2.1 us, 129 tokens of 16 heads 2.4 us).
 //
 // Layout: a head's 192 columns are 24 vectors of 16 bytes, so 192 threads take
 // eight heads of one token: thread i always has vector i % 24 of a head, and
