@@ -121,6 +121,7 @@ __device__ __forceinline__ int div_by(int n, const Divisor& d) {
 }
 
 struct AttnParams {
+  const __nv_bfloat16* cache;
   const int* prefix_pages;
   const int* table;        // [B][table_stride]
   const int* lens;         // [B]
@@ -296,11 +297,9 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* map, int y, int slab) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(0), "r"(y), "r"(slab)
-               : "memory");
+// Asks for `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // D (+)= A B^T over the pair for one K = 16 slice; issued by one thread of CTA 0.
@@ -569,15 +568,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             // while this one is loaded (32 requests x 128 heads, own keys: 53.4 us
             // without, 51.4 with; asked for by every pair, a shared prefix's keys
             // cost more than they give: 61 x 16 rows 22.7 us against 21.4).
-#pragma unroll 1
-            for (int q = 0; q < 64 / p.kbox; ++q) {
-              const int y = __shfl_sync(0xFFFFFFFFu, y_next, q);
-              if (y < p.total_rows && elect_one_sync()) {
-#pragma unroll 1
-                for (int x = 0; x < kQSlabs; x += p.kslabs) tma_prefetch_l2(&map_k, y, x);
-              }
-              __syncwarp();
-            }
+            // A box's rows are one piece of memory.
+            if (lane < 64 / p.kbox && y_next < p.total_rows)
+              bulk_prefetch_l2(p.cache + static_cast<int64_t>(y_next) * kRow, static_cast<uint32_t>(p.kbox * kRow * 2));
+            __syncwarp();
           }
         } else {
           // All 128 keys, this CTA's columns: of output columns [256 j, 256 j + 256)
@@ -1225,6 +1219,7 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
     if (d->device < 64) attr_done[d->device] = true;
   }
   AttnParams p{};
+  p.cache = static_cast<const __nv_bfloat16*>(cache_bf16);
   p.prefix_pages = prefix_pages;
   p.table = block_table;
   p.lens = lens;
