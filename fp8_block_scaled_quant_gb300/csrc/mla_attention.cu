@@ -80,8 +80,9 @@ constexpr int kSlab = 64 * 128;             // 64 rows x 64 bf16, 128-byte swizz
 constexpr int kQSlabs = kRow / 64;          // 9 slabs of 64 columns
 constexpr int kKGroups = 3;                 // key slabs signalled three at a time
 constexpr int kGroupBytes = 3 * kSlab;
-constexpr int kVChunks = 4;                 // 32 keys x 256 columns each
-constexpr int kVSlab = 32 * 128;            // 32 keys x 64 columns
+constexpr int kVRows = 64;                  // keys of a value chunk, 256 columns each
+constexpr int kVChunks = kTileKeys / kVRows;
+constexpr int kVSlab = kVRows * 128;        // kVRows keys x 64 columns
 constexpr int kVChunk = 4 * kVSlab;
 constexpr int kOffQ = 0;
 constexpr int kOffP = kOffQ + kQSlabs * kSlab;
@@ -366,7 +367,7 @@ __device__ __forceinline__ int entry_row(const AttnParams& p, int pg, int key) {
 }
 
 // Value chunks of a tile that hold keys.
-__device__ __forceinline__ int chunks_of(int key0, int limit) { return min(kVChunks, (limit - key0 + 31) / 32); }
+__device__ __forceinline__ int chunks_of(int key0, int limit) { return min(kVChunks, (limit - key0 + kVRows - 1) / kVRows); }
 
 // Items [lo, hi) of thread `tid` of `n`.
 __device__ __forceinline__ int split(int items, int tid, int n) {
@@ -548,20 +549,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           for (int g = 0; g < kKGroups; ++g) {
             if (n > 0) ok = wait_warp(&k_empty[g], (n - 1) & 1, abort_flag, p.err);
             if (!ok) break;
-            if (rank == 0 && elect_one_sync()) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
-#pragma unroll 1
-            for (int q = 0; q < nbox; ++q) {
-              const int y = __shfl_sync(0xFFFFFFFFu, y16, q);
-              const uint32_t dst = dst0 + g * kGroupBytes + q * p.kbox * 128;
-              if (elect_one_sync()) {
-                tma_load_pair(dst, &map_k, bars + g * 8, y, 3 * g);
-                if (p.kslabs == 1) {
-                  tma_load_pair(dst + kSlab, &map_k, bars + g * 8, y, 3 * g + 1);
-                  tma_load_pair(dst + 2 * kSlab, &map_k, bars + g * 8, y, 3 * g + 2);
-                }
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&k_full[g], 2 * kGroupBytes);
+            __syncwarp();
+            if (lane < nbox) {  // box `lane`: its rows are this lane's
+              const uint32_t dst = dst0 + g * kGroupBytes + lane * p.kbox * 128;
+              tma_load_pair(dst, &map_k, bars + g * 8, y16, 3 * g);
+              if (p.kslabs == 1) {
+                tma_load_pair(dst + kSlab, &map_k, bars + g * 8, y16, 3 * g + 1);
+                tma_load_pair(dst + 2 * kSlab, &map_k, bars + g * 8, y16, 3 * g + 2);
               }
-              __syncwarp();
             }
+            __syncwarp();
           }
           if (t + 1 >= it.pt) {
             // Keys that no other pair reads come from HBM: ask for the next tile's
@@ -582,14 +580,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           // Chunks past the end are neither loaded nor multiplied.
 #pragma unroll 1
           for (int c = 0; c < chunks_of(key0, limit); ++c) {
-            const int keys = limit - (key0 + c * 32);
+            const int keys = limit - (key0 + c * kVRows);
             const uint32_t dst = dst0 + c * kVChunk;
             const uint32_t full = bars + c * 8;
-            const uint32_t bar = keys < 32 ? map_to_cta(smem_u32(v_end), rank) : full;
+            const uint32_t bar = keys < kVRows ? map_to_cta(smem_u32(v_end), rank) : full;
             ok = wait_warp(&v_empty[c], ((vphase >> c) & 1) ^ 1, abort_flag, p.err);
             if (!ok) break;
             if (elect_one_sync()) {
-              if (keys < 32)
+              if (keys < kVRows)
                 mbar_arrive_expect_tx(v_end, kVChunk);
               else if (rank == 0)
                 mbar_arrive_expect_tx(&v_full[c], 2 * kVChunk);
@@ -598,8 +596,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
             }
             __syncwarp();
 #pragma unroll 1
-            for (int q = 0; q < 32; q += p.vbox) {
-              const int y = __shfl_sync(0xFFFFFFFFu, y16, 2 * c + (q >> 4));
+            for (int q = 0; q < kVRows; q += p.vbox) {
+              const int y = __shfl_sync(0xFFFFFFFFu, y16, kVRows / 16 * c + (q >> 4));
               if (elect_one_sync()) {
                 const uint32_t to = dst + q * 128;
                 const int slab = static_cast<int>(rank) * 2;
@@ -612,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               }
               __syncwarp();
             }
-            if (keys < 32) {
+            if (keys < kVRows) {
               ok = wait_warp(v_end, ends & 1, abort_flag, p.err);
               if (!ok) {
                 wait_slow(smem_u32(v_end), ends & 1, nullptr, p.err);  // the copies in flight
@@ -620,7 +618,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               }
               ++ends;
 #pragma unroll 1
-              for (int e = keys * 8 + lane; e < 32 * 8; e += 32)
+              for (int e = keys * 8 + lane; e < kVRows * 8; e += 32)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                   *reinterpret_cast<uint4*>(smem + kOffV + c * kVChunk + s * kVSlab + e * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -678,10 +676,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
           {
-            const uint64_t ad = pd + static_cast<uint32_t>(c >> 1) * (kSlab >> 4) + 4 * (c & 1);
+            const uint64_t ad = pd + static_cast<uint32_t>(c) * (kSlab >> 4);
             const uint64_t bd = vd + static_cast<uint32_t>(c) * (kVChunk >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)  // 16 keys
+            for (int h = 0; h < kVRows / 16; ++h)  // 16 keys
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 mma_bf16_pair(tmem + j * 128, ad + 2 * h, bd + j * (2 * kVSlab >> 4) + h * (2048 >> 4), kIdO,
@@ -1248,9 +1246,9 @@ extern "C" int fp8blk_mla_attention(const void* q_bf16, const void* q_pe_bf16, i
   p.own_rows = static_cast<int>(z.own_rows);
   p.merged = z.merged ? 1 : 0;
   p.kbox = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
-  p.vbox = page_size % 32 == 0 ? 32 : 16;
+  p.vbox = page_size % kVRows == 0 ? kVRows : page_size % 32 == 0 ? 32 : 16;
   p.kslabs = p.kbox == 64 ? 3 : 1;
-  p.vslabs = p.vbox == 32 ? 2 : 1;
+  p.vslabs = p.vbox == kVRows ? 2 : 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.direct = (z.merged || p.prefix_tiles == 0) && p.prefix_tiles + (p.max_own + kTileKeys - 1) / kTileKeys <= 1;
   // A cache without pages is never read: its maps describe one row of q.
