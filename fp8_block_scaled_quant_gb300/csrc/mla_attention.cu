@@ -45,15 +45,15 @@
 // comes from a second sum of the weights before their rounding.
 //
 // What bounds it, measured (GPU time): 64 requests of 128 heads behind 32768
-// shared keys take 345-370 us, 1.6-1.7 PFLOP/s of the 1.94 that a library GEMM
-// reaches: the tensor cores, 74 % of the cycles active. 32 requests of 128 heads
-// with up to 8191 own keys take 47.9 us, of which HBM needs 25.5 and the products
+// shared keys take 327 us, 1.8 PFLOP/s of the 1.94 that a library GEMM reaches:
+// the tensor cores (power holds long runs of it at 380). 32 requests of 128 heads
+// with up to 8191 own keys take 47.8 us, of which HBM needs 25.5 and the products
 // 20, side by side but for the first loads (6 us) and the join (7 us). Where a
-// call is short the chain of latencies is all there is: 24.5 us for one request
-// of 128 heads and 32768 keys, 21.3 us for 61 of 16 heads behind 2011, are 5 us
+// call is short the chain of latencies is all there is: 23.8 us for one request
+// of 128 heads and 32768 keys, 20.9 us for 61 of 16 heads behind 2011, are 5 us
 // of launch, plan and first loads, 6 us of tiles, 2 us for 20 MB of parts to L2,
 // 1.7 us between the kernels and 5 us to read the parts back; one short
-// request is 7.2 us. (One kernel whose CTAs meet at a barrier and join with their
+// request is 7.3 us. (One kernel whose CTAs meet at a barrier and join with their
 // own seven warps took 29.6 us for that one request: the join wants more loads in
 // flight than those warps have.)
 //
@@ -80,7 +80,9 @@ constexpr int kSlab = 64 * 128;             // 64 rows x 64 bf16, 128-byte swizz
 constexpr int kQSlabs = kRow / 64;          // 9 slabs of 64 columns
 constexpr int kKGroups = 3;                 // key slabs signalled three at a time
 constexpr int kGroupBytes = 3 * kSlab;
-constexpr int kVRows = 64;                  // keys of a value chunk, 256 columns each
+// Keys of a value chunk, 256 columns each: with 32 the twice as many waits and
+// commits cost the large case 342 us against 322; pages of 16 rows lose 0.4 us of 21.
+constexpr int kVRows = 64;
 constexpr int kVChunks = kTileKeys / kVRows;
 constexpr int kVSlab = kVRows * 128;        // kVRows keys x 64 columns
 constexpr int kVChunk = 4 * kVSlab;
@@ -90,14 +92,14 @@ constexpr int kOffK = kOffP + 2 * kSlab;
 constexpr int kOffV = kOffK + kQSlabs * kSlab;
 constexpr int kOffRed = kOffV + kVChunks * kVChunk;  // [2][2][64] row maxima, then sums
 constexpr int kOffBar = kOffRed + 2 * 2 * 64 * 4;
-constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 2;
+constexpr int kNumBars = 2 + 2 * kKGroups + 2 * kVChunks + 4 + 4 + 3;
 static_assert(kNumBars <= 32, "a lane of a warp initialises each");
 constexpr int kAttnSmem = 1024 + kOffBar + kNumBars * 8 + 32;
 static_assert(kAttnSmem <= 232448, "shared memory per CTA");
 
 // Warps: 0-3 softmax (warp w: tensor-memory lanes 32 w ..), 4 keys, 5
-// queries and values, 6 MMA.
-constexpr int kAttnThreads = 224;
+// queries and values, 6 the scores' MMAs, 7 the output's.
+constexpr int kAttnThreads = 256;
 constexpr int kMaxPairs = 96;
 constexpr uint32_t kTmemS = 256;            // columns 0-255: output; 256-383: two score buffers
 constexpr float kRaise = 8.0f;              // log2 by which a tile's maximum must pass the running one
@@ -394,8 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   uint64_t* o_empty = pv_done + 1;
   uint64_t* red_bar = o_empty + 1;
   uint64_t* v_end = red_bar + 1;  // this CTA's part of the chunk that holds the end of the keys
-  uint64_t* drain = v_end + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = v_end + 1;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* start = reinterpret_cast<int*>(tmem_slot + 2);  // first item, first unit in it, unit count
 
@@ -647,72 +649,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           if (n > 0) wait_slow(smem_u32(&v_full[c]), ((vphase >> c) & 1) ^ 1, nullptr, p.err);
       }
     }
-  } else if (warp == 6) {
-    // ---- MMA (CTA 0 issues for the pair) -------------------------------------
-    // One thread runs the whole role: a warp's votes and elections around each of
-    // a tile's nine waits left the tensor cores idle between products (64 x 128
-    // rows, 32768 shared keys: 407 us against 358).
+  } else if (warp >= 6) {
+    // ---- MMA (CTA 0 issues for the pair): scores (warp 6), output (warp 7) ----
+    // One thread of each warp runs its whole role: votes and elections around each
+    // of a tile's waits leave the tensor cores idle between products (64 x 128
+    // rows, 32768 shared keys: 407 us against 358). Two roles, so that an item's
+    // last output product is not queued behind the next item's first scores (61 x
+    // 16 rows: 21.4 us with one thread for both, 20.9).
+    const bool scores = warp == 6;
     if (rank == 0 && elect_one_sync()) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 256, true);
-      const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + kOffQ)), kd = sdesc_kmajor_sw128(smem_u32(smem + kOffK));
-      const uint64_t pd = sdesc_kmajor_sw128(smem_u32(smem + kOffP));
-      const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + kOffV), kVSlab);
       uint32_t n = 0, seg = 0;
       int left = nunits, i = item0, v0 = unit0;
       bool ok = true;
-      bool prev_first = false;
-      uint32_t prev_seg = 0;
-      int prev_chunks = 0;
-      // The output product of tile k (whose weights the softmax warps publish
-      // while the scores of tile k + 1 are formed).
-      uint32_t vphase = 0;
-      auto output = [&](uint32_t k, bool first, uint32_t sg, int chunks) {
-        if (first && sg > 0)
-          ok = ok && wait_one(o_empty, (sg - 1) & 1, abort_flag, p.err);
-        ok = ok && wait_one(p_full, k & 1, abort_flag, p.err);
-#pragma unroll 2
-        for (int c = 0; ok && c < chunks; ++c) {
-          ok = wait_one(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
-          if (!ok) break;
-          tc_fence_after_sync();
-          {
-            const uint64_t ad = pd + static_cast<uint32_t>(c) * (kSlab >> 4);
-            const uint64_t bd = vd + static_cast<uint32_t>(c) * (kVChunk >> 4);
-#pragma unroll
-            for (int h = 0; h < kVRows / 16; ++h)  // 16 keys
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma_bf16_pair(tmem + j * 128, ad + 2 * h, bd + j * (2 * kVSlab >> 4) + h * (2048 >> 4), kIdO,
-                              first && c == 0 && h == 0 ? 0u : 1u);
-            mma_commit_pair(&v_empty[c]);
-            if (c == chunks - 1) mma_commit_pair(pv_done);
-          }
-          vphase ^= 1u << c;
-        }
-      };
+      if (scores) {
+        const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + kOffQ)), kd = sdesc_kmajor_sw128(smem_u32(smem + kOffK));
 #pragma unroll 1
-      while (ok && left > 0 && i < p.items) {
-        const Item it = get_item(p, i);
-        const Span in = span_of(it.tiles, v0, left);
-        const int t0 = in.t0, t1 = in.t1;
-        left -= in.units;
+        while (ok && left > 0 && i < p.items) {
+          const Item it = get_item(p, i);
+          const Span in = span_of(it.tiles, v0, left);
+          left -= in.units;
+          if (in.t1 > in.t0) ok = wait_one(q_full, seg++ & 1, abort_flag, p.err);
 #pragma unroll 1
-        for (int t = t0; ok && t < t1; ++t) {
-          const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
-          if (t == t0) {
-            // The next queries are asked for when the last scores are done: their
-            // way here is spent on the last output product.
-            if (n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
-            ok = ok && wait_one(q_full, seg & 1, abort_flag, p.err);
-          }
-          if (n > 1)
-            ok = ok && wait_one(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
+          for (int t = in.t0; ok && t < in.t1; ++t, ++n) {
+            const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
+            if (n > 1) ok = wait_one(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
 #pragma unroll 1
-          for (int g = 0; ok && g < kKGroups; ++g) {
-            ok = wait_one(&k_full[g], n & 1, abort_flag, p.err);
-            if (!ok) break;
-            tc_fence_after_sync();
-            {
+            for (int g = 0; ok && g < kKGroups; ++g) {
+              ok = wait_one(&k_full[g], n & 1, abort_flag, p.err);
+              if (!ok) break;
+              tc_fence_after_sync();
               const uint64_t ad = qd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
               const uint64_t bd = kd + static_cast<uint32_t>(g) * (kGroupBytes >> 4);
 #pragma unroll
@@ -722,25 +688,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
               mma_commit_pair(&k_empty[g]);
               if (g == kKGroups - 1) {
                 mma_commit_pair(&s_full[buf]);
-                if (t == t1 - 1) mma_commit_pair(q_empty);
+                if (t == in.t1 - 1) mma_commit_pair(q_empty);
               }
             }
           }
-          if (ok && t > t0) output(n - 1, prev_first, prev_seg, prev_chunks);
-          prev_first = t == t0;
-          prev_seg = seg;
-          const bool pre = t < it.pt;
-          prev_chunks = chunks_of((pre ? t : t - it.pt) * kTileKeys, pre ? p.P : it.len);
-          ++n;
+          ++i;
+          v0 = 0;
         }
-        if (t1 > t0) ++seg;
-        ++i;
-        v0 = 0;
+      } else {
+        const uint64_t pd = sdesc_kmajor_sw128(smem_u32(smem + kOffP));
+        const uint64_t vd = sdesc_mn_sw128(smem_u32(smem + kOffV), kVSlab);
+        uint32_t vphase = 0;
+#pragma unroll 1
+        while (ok && left > 0 && i < p.items) {
+          const Item it = get_item(p, i);
+          const Span in = span_of(it.tiles, v0, left);
+          left -= in.units;
+          if (in.t1 > in.t0 && seg++ > 0) ok = wait_one(o_empty, (seg - 2) & 1, abort_flag, p.err);
+#pragma unroll 1
+          for (int t = in.t0; ok && t < in.t1; ++t, ++n) {
+            const bool pre = t < it.pt;
+            const int chunks = chunks_of((pre ? t : t - it.pt) * kTileKeys, pre ? p.P : it.len);
+            ok = wait_one(p_full, n & 1, abort_flag, p.err);
+#pragma unroll 2
+            for (int c = 0; ok && c < chunks; ++c) {
+              ok = wait_one(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
+              if (!ok) break;
+              tc_fence_after_sync();
+              const uint64_t ad = pd + static_cast<uint32_t>(c) * (kSlab >> 4);
+              const uint64_t bd = vd + static_cast<uint32_t>(c) * (kVChunk >> 4);
+#pragma unroll
+              for (int h = 0; h < kVRows / 16; ++h)  // 16 keys
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  mma_bf16_pair(tmem + j * 128, ad + 2 * h, bd + j * (2 * kVSlab >> 4) + h * (2048 >> 4), kIdO,
+                                t == in.t0 && c == 0 && h == 0 ? 0u : 1u);
+              mma_commit_pair(&v_empty[c]);
+              if (c == chunks - 1) mma_commit_pair(pv_done);
+              vphase ^= 1u << c;
+            }
+          }
+          ++i;
+          v0 = 0;
+        }
       }
-      if (ok && n > 0) output(n - 1, prev_first, prev_seg, prev_chunks);
       if (!ok) {  // let the MMAs in flight finish before tensor memory is freed
-        mma_commit_pair(drain);
-        wait_slow(smem_u32(drain), 0, nullptr, p.err);
+        mma_commit_pair(drain + (scores ? 0 : 1));
+        wait_slow(smem_u32(drain + (scores ? 0 : 1)), 0, nullptr, p.err);
       }
     }
     __syncwarp();
