@@ -46,7 +46,7 @@
 //
 // What bounds it, measured (GPU time): 64 requests of 128 heads behind 32768
 // shared keys take 327 us, 1.8 PFLOP/s of the 1.94 that a library GEMM reaches:
-// the tensor cores (power holds long runs of it at 380). 32 requests of 128 heads
+// the tensor cores (364 us a call in long runs). 32 requests of 128 heads
 // with up to 8191 own keys take 47.8 us, of which HBM needs 25.5 and the products
 // 20, side by side but for the first loads (6 us) and the join (7 us). Where a
 // call is short the chain of latencies is all there is: 23.8 us for one request
