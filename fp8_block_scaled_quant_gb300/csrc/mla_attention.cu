@@ -119,7 +119,7 @@ __host__ Divisor divisor(int64_t d) {
   return {static_cast<uint32_t>((uint64_t{1} << (30 + l)) / static_cast<uint64_t>(d) + 1), 30 + l};
 }
 
-__device__ __forceinline__ int div_by(int n, const Divisor& d) {
+__host__ __device__ __forceinline__ int div_by(int n, const Divisor& d) {
   return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul >> d.shift);
 }
 
@@ -216,12 +216,14 @@ __host__ __device__ __forceinline__ int64_t part_row(int merged, int prefix_item
   return base + static_cast<int64_t>(q) * kTileRows;
 }
 
-// First unit of pair q: units q / pairs rounded down, without 64-bit products.
-// Fewer units than the launch has pairs go to a pair each.
-__device__ __forceinline__ int unit_of_pair(const AttnParams& p, int units, int pairs, int launched, int q) {
-  if (pairs < launched) return q;
-  const int each = div_by(units, p.by_pairs);
-  return each * q + div_by((units - each * pairs) * q, p.by_pairs);
+// First unit of pair q of `launched` (by_pairs divides by that many): units q /
+// launched rounded down, without 64-bit products. Fewer units than pairs go to a
+// pair each, and the pairs past the last unit start at the end: their ranges, and
+// every range of a batch without any key, are empty.
+__host__ __device__ __forceinline__ int unit_of_pair(const Divisor& by_pairs, int units, int launched, int q) {
+  if (units < launched) return q < units ? q : units;
+  const int each = div_by(units, by_pairs);
+  return each * q + div_by((units - each * launched) * q, by_pairs);
 }
 
 // The pair whose range holds unit u: the largest q with units q / pairs <= u,
@@ -448,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       if (lane >= o) upto += v;
     }
     if (lane == 31) sums[warp] = upto;
+    if (tid == 0) start[0] = start[1] = 0;  // where the range is empty
     named_barrier_sync(1, kPlanners);
     int at = upto - own, units = 0;
 #pragma unroll
@@ -456,9 +459,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
       at += w < warp ? v : 0;
       units += v;
     }
-    const int pairs = max(1, min(npairs_max, units));
-    const int u0 = pair < pairs ? unit_of_pair(p, units, pairs, npairs_max, pair) : units;
-    const int u1 = pair < pairs ? unit_of_pair(p, units, pairs, npairs_max, pair + 1) : units;
+    const int u0 = unit_of_pair(p.by_pairs, units, npairs_max, pair);
+    const int u1 = unit_of_pair(p.by_pairs, units, npairs_max, pair + 1);
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
       const int n = hi - lo == 1 ? own : item_units(p, i);
@@ -472,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
     if (tid == 0) start[2] = u1 - u0;
     if (blockIdx.x == 0 && tid == 0) {
       p.plan[0] = units;
-      p.plan[1] = pairs;
+      p.plan[1] = min(npairs_max, units);
       p.plan[2 + p.items] = units;
     }
   }
@@ -483,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int nunits = start[2];
-  const int item0 = nunits ? start[0] : 0, unit0 = nunits ? start[1] : 0;
+  const int item0 = start[0], unit0 = start[1];
 
   if (warp == 4 || warp == 5) {
     // ---- loads: keys (warp 4), queries and values (warp 5) -------------------

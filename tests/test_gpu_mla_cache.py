@@ -444,3 +444,18 @@ def test_attention_refusals():
         call_attention(a, lse=torch.empty((2, 15), device="cuda"))
     assert fb.mla_attention_workspace_bytes(-1, 16, 0) == 0 and fb.mla_attention_workspace_bytes(1, 0, 0) == 0
     assert fb.last_device_error() == 0
+
+
+@pytest.mark.parametrize("H", [7, 16, 128, 130])
+@pytest.mark.parametrize("stride", [1, 9])
+def test_attention_without_any_key(H, stride):
+    """No prefix and every length zero: zeros and -inf, whether or not rows can have several parts (stride pages of
+    64 keys). The lengths are on the device, so the host launches as for any batch. Shared memory was used by a call
+    with keys before."""
+    a = make_attention(5, H, 0, [64 * stride] * 5, 64, 23)
+    for _ in range(3):
+        call_attention(a)
+        lse = torch.full((5, H), 5.0, device="cuda")
+        out = call_attention(dict(a, lens=torch.zeros_like(a["lens"])), lse)
+        assert (out == 0).all() and (lse == -math.inf).all()
+    assert fb.last_device_error() == 0
