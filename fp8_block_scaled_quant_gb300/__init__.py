@@ -120,8 +120,38 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: int = 2):
 
 
 # ---- workspaces: zero-filled device buffers cached per (device, stream) ------
+#
+# A captured graph keeps the addresses of its calls' workspaces, so a buffer that
+# a capture was given is never freed, also where a later call needs a larger one.
+# A buffer made during a capture belongs to that graph alone: its fill is one
+# of the graph's nodes, so no other call may rely on it. Replays of graphs captured
+# on one stream share that stream's workspaces with its other calls: they must
+# not run at the same time.
 
 _ws_cache: dict = {}
+_ws_captured: dict = {}   # by address: buffers that a graph may hold
+
+
+def _capturing(device: torch.device) -> bool:
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
+def _buffer(nbytes: int, device: torch.device, key: tuple, zeroed: int | None = None) -> torch.Tensor:
+    """A uint8 buffer with nbytes after its first 256-byte boundary, all zeros when it was made. `zeroed`: how many
+    of them a call needs as zeros (None: all), for a buffer made during a capture and filled in every replay."""
+    buf = _ws_cache.get(key)
+    fits = buf is not None and buf.numel() >= nbytes + 256
+    if _capturing(device):
+        if fits:
+            _ws_captured[buf.data_ptr()] = buf
+            return buf
+        buf = torch.empty(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
+        if zeroed != 0:
+            buf[:buf.numel() if zeroed is None else zeroed + 256].zero_()
+        return buf
+    if not fits:
+        buf = _ws_cache[key] = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
+    return buf
 
 
 def workspace(nbytes: int, device: torch.device, key: str = "gemm") -> torch.Tensor:
@@ -129,11 +159,7 @@ def workspace(nbytes: int, device: torch.device, key: str = "gemm") -> torch.Ten
     every call on the same device, stream and key. The GEMM leaves its
     counters at zero, so the buffer never needs clearing again."""
     stream = torch.cuda.current_stream(device).cuda_stream
-    k = (device.index, stream, key)
-    buf = _ws_cache.get(k)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
-        _ws_cache[k] = buf
+    buf = _buffer(nbytes, device, (device.index, stream, key))
     off = (-buf.data_ptr()) % 256
     return buf[off:off + max(nbytes, 1)]
 
@@ -168,16 +194,14 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(ws: torch.Tensor | None, nbytes: int, t: torch.Tensor, stream: int, key: str):
-    """(address, bytes) of the caller's workspace, or of the one kept for the device and stream."""
+def _scratch(ws: torch.Tensor | None, nbytes: int, t: torch.Tensor, stream: int, key: str, zeroed: int):
+    """(address, bytes, tensor to hold until the launch) of the caller's workspace, or of the one kept for the device
+    and stream; `zeroed`: its leading bytes that have to be zeros."""
     if ws is not None:
-        return ws.data_ptr(), ws.numel()
-    buf = _ws_cache.get((t.get_device(), stream, key))
-    if buf is None or buf.numel() < nbytes + 256:
-        buf = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=t.device)
-        _ws_cache[(t.get_device(), stream, key)] = buf
+        return ws.data_ptr(), ws.numel(), ws
+    buf = _buffer(nbytes, t.device, (t.get_device(), stream, key), zeroed)
     at = buf.data_ptr()
-    return at + (-at) % 256, nbytes
+    return at + (-at) % 256, nbytes, buf
 
 
 # ---- operations --------------------------------------------------------------
@@ -497,8 +521,8 @@ def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, bloc
         if tuple(lse.shape) != (B, H):
             raise Fp8BlkError("lse must be [B, H]")
     stream = _stream_on(q)
-    at, room = _scratch(ws, 0 if ws is not None else mla_attention_workspace_bytes(B, H, prefix_len), q, stream,
-                        "mla_attention")
+    at, room, held = _scratch(ws, 0 if ws is not None else mla_attention_workspace_bytes(B, H, prefix_len), q, stream,
+                              "mla_attention", 0)
     f = _function("fp8blk_mla_attention", "ppiipiipipipfpppzp")
     _check(f(q.data_ptr(), q_pe.data_ptr(), B, H, cache.data_ptr(), pages, page_size,
              prefix_pages.data_ptr() if prefix_len else None, prefix_len, block_table.data_ptr(), block_table.shape[1],
@@ -637,8 +661,8 @@ def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_
             if tuple(t.shape) != (T, topk):
                 raise Fp8BlkError(f"{n} must be [T, topk]")
     stream = _stream_on(x)
-    at, room = _scratch(ws, 0 if ws is not None else moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared), x,
-                        stream, "moe_layer")
+    at, room, held = _scratch(ws, 0 if ws is not None else moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared),
+                              x, stream, "moe_layer", 256)
     f = _function("fp8blk_moe_layer", "p" * 10 + "i" * 8 + "efeepppzp")
     _check(f(x.data_ptr(), gate_w.data_ptr(), _addr(gate_bias), w1.data_ptr(), w1_s.data_ptr(), w3.data_ptr(),
              w3_s.data_ptr(), w2.data_ptr(), w2_s.data_ptr(), out.data_ptr(), T, topk, E, dim, inter, n_shared, n_groups,

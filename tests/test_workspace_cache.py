@@ -1,0 +1,177 @@
+"""The binding's workspaces and captured graphs: a graph keeps the addresses it was captured with, so their buffers
+stay allocated whatever later calls need; a buffer made during a capture is filled by that graph and shared with no
+other call."""
+import types
+
+import pytest
+import torch
+
+import fp8_block_scaled_quant_gb300 as fb
+
+
+class Host:
+    """The cache on host tensors, with a capture switched on and off by the test."""
+
+    def __init__(self, monkeypatch):
+        self.capturing = False
+        monkeypatch.setattr(fb, "_ws_cache", {})
+        monkeypatch.setattr(fb, "_ws_captured", {})
+        monkeypatch.setattr(fb, "_capturing", lambda device: self.capturing)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=7))
+        self.t = torch.zeros(1)
+
+    def scratch(self, nbytes, capturing=False):
+        self.capturing = capturing
+        return fb._scratch(None, nbytes, self.t, 7, "op", 256)
+
+    def workspace(self, nbytes, capturing=False):
+        self.capturing = capturing
+        return fb.workspace(nbytes, torch.device("cpu"), "op")
+
+
+def alive(at):
+    return any(b.data_ptr() <= at < b.data_ptr() + b.numel() for b in fb._ws_captured.values())
+
+
+def test_a_captured_buffer_outlives_a_larger_one(monkeypatch):
+    h = Host(monkeypatch)
+    first, room, _ = h.scratch(1000)
+    assert h.scratch(1000, capturing=True)[0] == first and room == 1000     # warmed up: the same buffer
+    larger, _, _ = h.scratch(1 << 20)
+    assert larger != first and alive(first)
+    assert h.scratch(500)[0] == larger                                      # and the larger one serves from now on
+
+
+def test_a_captured_workspace_outlives_a_larger_one(monkeypatch):
+    h = Host(monkeypatch)
+    first = h.workspace(1000).data_ptr()
+    assert h.workspace(900, capturing=True).data_ptr() == first
+    assert h.workspace(1 << 20).data_ptr() != first and alive(first)
+
+
+def test_buffers_of_no_graph_are_given_back(monkeypatch):
+    h = Host(monkeypatch)
+    for n in (1000, 10000, 100000):
+        h.scratch(n)
+    assert len(fb._ws_cache) == 1 and not fb._ws_captured
+
+
+@pytest.mark.parametrize("take", ["scratch", "workspace"])
+def test_a_buffer_made_in_a_capture_serves_that_call_alone(monkeypatch, take):
+    """Its fill runs in that graph's replays only: neither another capture nor an eager call may be given it."""
+    h = Host(monkeypatch)
+    in_capture = getattr(h, take)(4096, capturing=True)
+    assert not fb._ws_cache and not fb._ws_captured
+    eager = getattr(h, take)(4096)
+    held = [b for b in fb._ws_cache.values()]
+    assert len(held) == 1 and not held[0].any()
+    if take == "scratch":
+        assert not in_capture[2][:512].any() and eager[2] is held[0]
+    else:
+        assert not in_capture.any()
+
+
+def moe(T, dim, inter, E, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    w = [(n(E * r, c) * 100).clamp(-448, 448).to(torch.float8_e4m3fn) for r, c in ((inter, dim), (inter, dim), (dim, inter))]
+    s = [torch.full((t.shape[0] // 128, t.shape[1] // 128), 2e-4, device="cuda") for t in w]
+    return dict(x=n(T, dim).bfloat16(), gate=(n(E, dim) * dim ** -0.5).bfloat16(), w=w, s=s)
+
+
+def run_moe(a, out=None):
+    (w1, w3, w2), (s1, s3, s2) = a["w"], a["s"]
+    return fb.moe_layer(a["x"], a["gate"], w1, s1, w3, s3, w2, s2, topk=4, out=out)
+
+
+def attention(B, H, n, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    pages = -(-n // 64)
+    return dict(q=r(B, H, 512), pe=r(B, H, 64), cache=r(B * pages, 64, 576),
+                table=torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages),
+                lens=torch.full((B,), n, dtype=torch.int32, device="cuda"))
+
+
+def run_attention(a, out=None):
+    return fb.mla_attention(a["q"], a["pe"], a["cache"], a["table"], a["lens"], 0.07, out=out)
+
+
+def linear(M, N, K, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return dict(x=torch.randn(M, K, generator=g, device="cuda").bfloat16(),
+                w=fb.weight_quant(torch.randn(N, K, generator=g, device="cuda")))
+
+
+def run_linear(a, out=None):
+    return fb.linear(a["x"], *a["w"], out=out)
+
+
+CASES = {
+    "moe_layer": (run_moe, lambda: moe(2, 512, 256, 32, 1), lambda: moe(32, 2048, 512, 64, 2)),
+    "mla_attention": (run_attention, lambda: attention(1, 16, 700, 3), lambda: attention(64, 128, 300, 4)),
+    "linear": (run_linear, lambda: linear(8, 1024, 2048, 5), lambda: linear(700, 7000, 7168, 6)),
+}
+
+
+def ready(stream):
+    stream.wait_stream(torch.cuda.current_stream())
+    return torch.cuda.stream(stream)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CASES)
+def test_a_graph_survives_a_larger_call_on_its_stream(name):
+    run, small, large = CASES[name]
+    a, b = small(), large()
+    ref, out = run(a), torch.empty_like(run(a))
+    stream = torch.cuda.Stream()
+    with ready(stream):
+        run(a)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            run(a, out)
+        want = run(b)
+        # What the allocator may now hand out again is someone else's.
+        others = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (1 << 10, 1 << 20, 1 << 21, 1 << 23)
+                  for _ in range(8)]
+        for _ in range(2):
+            out.zero_()
+            graph.replay()
+        again = run(b)
+    stream.synchronize()
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    assert torch.equal(want.view(torch.int16), again.view(torch.int16))
+    assert all(bool((t == 0x5A).all()) for t in others)
+    assert fb.last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CASES)
+def test_graphs_captured_without_a_call_before(name):
+    """Two graphs of a stream that no call ran on: each brings its own zeros, in whatever order they are replayed, and
+    so does a call on that stream."""
+    run, small, _ = CASES[name]
+    a = small()
+    ref = run(a)
+    outs = [torch.empty_like(ref) for _ in range(2)]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with ready(stream):
+        graphs = []
+        for o in outs:
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=stream):
+                run(a, o)
+        got = run(a)
+        for k in (1, 0, 1):
+            outs[k].zero_()
+            graphs[k].replay()
+    stream.synchronize()
+    for o in (*outs, got):
+        assert torch.equal(o.view(torch.int16), ref.view(torch.int16))
+    assert fb.last_device_error() == 0
