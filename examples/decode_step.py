@@ -142,14 +142,14 @@ def main(argv=None):
     x, graph, seen = first.clone(), None, []
     if a.graph:
         side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())  # weights, page table, lengths and prompt are written there
         with torch.cuda.stream(side):
             step(layer, cache, x)  # workspaces of this stream
-            side.synchronize()
-            cache.lens.zero_()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph, stream=side):
                 outs = step(layer, cache, x)
                 x.copy_(outs[0])
+        torch.cuda.current_stream().wait_stream(side)
         cache.lens.zero_()
         x.copy_(first)
     for i in range(a.steps):

@@ -1,6 +1,7 @@
 """The decode example: its steps run the cache, attention and MoE layer calls together."""
 import importlib.util
 import os
+import time
 
 import pytest
 
@@ -35,6 +36,33 @@ def test_a_captured_step_replays_as_the_calls():
     plain = example().main(args)
     torch.manual_seed(7)
     assert example().main(args + ["--graph"]) == plain
+
+
+@pytest.mark.gpu
+def test_the_side_stream_waits_for_what_it_reads():
+    """Weights, page table, lengths and prompt are written on the default stream: nothing runs on the capturing stream
+    before they are there. (The default stream is held up behind the prompt; the check comes before the step's work.)"""
+    m = example()
+    write_prompt, step, seen = m.write_prompt, m.step, []
+
+    def held_up(*args):
+        write_prompt(*args)
+        torch.cuda._sleep(1 << 30)
+
+    def checked(*args):
+        stream = torch.cuda.current_stream()
+        if stream != torch.cuda.default_stream() and not torch.cuda.is_current_stream_capturing():
+            reached = [torch.cuda.Event() for _ in range(2)]
+            reached[0].record(torch.cuda.default_stream())
+            reached[1].record(stream)
+            time.sleep(0.02)
+            seen.append([e.query() for e in reached])
+            assert seen[-1] == [False, False]
+        return step(*args)
+
+    m.write_prompt, m.step = held_up, checked
+    assert len(m.main(["--batch", "2", "--prefix", "70", "--steps", "2", "--graph"])) == 2
+    assert len(seen) == 1
 
 
 def test_batch_is_checked():
