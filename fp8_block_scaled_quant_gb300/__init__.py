@@ -198,7 +198,9 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, t: torch.Tensor, stream: int,
     """(address, bytes, tensor to hold until the launch) of the caller's workspace, or of the one kept for the device
     and stream; `zeroed`: its leading bytes that have to be zeros."""
     if ws is not None:
-        return ws.data_ptr(), ws.numel(), ws
+        if ws.get_device() != t.get_device() or not ws.is_contiguous():
+            raise Fp8BlkError("ws must be a contiguous tensor on the device of the inputs")
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
     buf = _buffer(nbytes, t.device, (t.get_device(), stream, key), zeroed)
     at = buf.data_ptr()
     return at + (-at) % 256, nbytes, buf

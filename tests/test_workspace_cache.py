@@ -71,6 +71,35 @@ def test_a_buffer_made_in_a_capture_serves_that_call_alone(monkeypatch, take):
         assert not in_capture.any()
 
 
+class OnGpu:
+    """Stands for a tensor of GPU 0, as far as a workspace's check looks."""
+
+    def get_device(self):
+        return 0
+
+
+def test_a_given_workspace_is_checked():
+    """A kernel would write to whatever address it is given: host memory and strided views are refused, and the size is
+    counted in bytes."""
+    for bad, t in ((torch.zeros(4096, dtype=torch.uint8), OnGpu()), (torch.zeros(8192, dtype=torch.uint8)[::2],
+                                                                     torch.zeros(1))):
+        with pytest.raises(fb.Fp8BlkError):
+            fb._scratch(bad, 1000, t, 7, "op", 256)
+    ws = torch.zeros(1024, dtype=torch.int32)
+    assert fb._scratch(ws, 1000, torch.zeros(1), 7, "op", 256)[:2] == (ws.data_ptr(), 4096)
+
+
+@pytest.mark.gpu
+def test_a_host_workspace_is_refused():
+    a, b = moe(2, 512, 256, 32, 7), attention(1, 16, 20, 8)
+    (w1, w3, w2), (s1, s3, s2) = a["w"], a["s"]
+    with pytest.raises(fb.Fp8BlkError):
+        fb.moe_layer(a["x"], a["gate"], w1, s1, w3, s3, w2, s2, topk=4, ws=torch.zeros(1 << 25, dtype=torch.uint8))
+    with pytest.raises(fb.Fp8BlkError):
+        fb.mla_attention(b["q"], b["pe"], b["cache"], b["table"], b["lens"], 0.07,
+                         ws=torch.zeros(1 << 25, dtype=torch.uint8))
+
+
 def moe(T, dim, inter, E, seed):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
