@@ -493,7 +493,8 @@ def mla_attention(q: torch.Tensor, q_pe: torch.Tensor, cache: torch.Tensor, bloc
     """Latent attention of one query token per request: q bf16 [B, H, 512] (mla_absorb "qk" output), q_pe bf16
     [B, H, 64], cache bf16 [pages, page_size, 576], block_table int32 [B, max_pages] and lens int32 [B] (a
     request's own keys), after prefix_len keys of prefix_pages (int32) that every request shares
-    -> bf16 [B, H, 512]; lse fp32 [B, H] is written where given."""
+    -> bf16 [B, H, 512]; lse fp32 [B, H] is written where given. ws: a workspace of mla_attention_workspace_bytes,
+    256-byte aligned, any contents."""
     _need(q, torch.bfloat16, "q", ndim=3)
     _need(q_pe, torch.bfloat16, "q_pe", ndim=3)
     _need(cache, torch.bfloat16, "cache", ndim=3)
@@ -631,7 +632,9 @@ def moe_layer(x: torch.Tensor, gate_w: torch.Tensor, w1, w1_s, w3, w3_s, w2, w2_
               w: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """A whole MoE layer for up to 32 tokens in one kernel: gate product and gate (x bf16 [T, dim], gate_w bf16
     [E, dim], gate_bias fp32 [E]), routed and shared experts (stacked e4m3 weights and block scales as for
-    moe_grouped_gemm) and their sum -> bf16 [T, dim]. idx int32 / w fp32 [T, topk] receive the routing where given."""
+    moe_grouped_gemm) and their sum -> bf16 [T, dim]. idx int32 / w fp32 [T, topk] receive the routing where given.
+    ws: a workspace of moe_layer_workspace_bytes, 256-byte aligned, whose first 256 bytes were ZERO-FILLED before its
+    first use (every call leaves them at zero), used by one stream at a time."""
     _need(x, torch.bfloat16, "x")
     _need(gate_w, torch.bfloat16, "gate_w")
     for t, n, dt in ((w1, "w1", torch.float8_e4m3fn), (w3, "w3", torch.float8_e4m3fn), (w2, "w2", torch.float8_e4m3fn),
