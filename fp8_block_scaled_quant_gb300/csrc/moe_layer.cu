@@ -246,6 +246,16 @@ __device__ __noinline__ void gate_of_token(const LayerParams& p, const float* bi
   }
 }
 
+// The phases that copies were given on kStages barriers: which barriers, and the
+// parity of the last one of each.
+struct Armed {
+  uint32_t used, parity;
+  __host__ __device__ __forceinline__ void arm(int s) {
+    parity ^= used & (1u << s);
+    used |= 1u << s;
+  }
+};
+
 template <int N>  // token columns
 __global__ void __launch_bounds__(kThreads, 1)
     moe_layer_kernel(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map3,
@@ -356,8 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_load_2d_hint(smem + s * kTileBytes, map, &full[s], x, y, policy);
     ++issued;
   };
+  Armed tokens_armed{0, 0};
   auto load_tokens = [&](int s, const CUtensorMap* map, int x, int y, const float* scales) {
     if (*abort_flag) return;
+    tokens_armed.arm(s);
     mbar_arrive_expect_tx(&tok_full[s], N * 128 + N * 4);
     tma_load_2d(smem + off_tok() + s * N * 128, map, &tok_full[s], x, y);
     bulk_load(scl + s * N, scales, N * 4, &tok_full[s]);
@@ -893,19 +905,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
   if (*abort_flag) {
-    // Copies and MMAs in flight are waited for (bounded) before the CTA ends.
-    if (producer)
+    // (No role sets it any more.) Copies and MMAs in flight are waited for
+    // (bounded) before the CTA ends.
+    if (producer) {
+#pragma unroll 1
       for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
         wait(&full[i % kStages], (i / kStages) & 1, nullptr, p.err);
+#pragma unroll 1
+      for (int s = 0; s < kStages; ++s)
+        if ((tokens_armed.used >> s) & 1u) wait(&tok_full[s], (tokens_armed.parity >> s) & 1, nullptr, p.err);
+    }
     if (warp == kIssuer) {
       if (elect_one_sync()) mma_commit(drain);
       __syncwarp();
       wait(drain, 0, nullptr, p.err);
+      __syncwarp();
     }
   }
-  tc_fence_before_sync();
-  __syncthreads();
   if (warp == kIssuer) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
