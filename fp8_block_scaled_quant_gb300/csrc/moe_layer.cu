@@ -929,12 +929,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
-  // The last CTA to leave zeroes the counters for the next call.
-  if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u) {
-    p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = 0;
-    if (*abort_flag)
-      for (int i = 16; i < 32; ++i) p.counters[i] = 0;
-  }
+  // The last CTA to leave zeroes the counters for the next call. (After a wait
+  // that gave up, in whichever CTA, the row tiles' may hold a part of a count.)
+  if (tid == 0 && atomicAdd(p.counters + 3, 1u) == static_cast<unsigned>(G) - 1u)
+    for (int i = 0; i < 32; ++i) p.counters[i] = 0;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

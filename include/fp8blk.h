@@ -498,9 +498,11 @@ FP8BLK_API int fp8blk_gemm_noalloc(const void *a_e4m3, const float *a_s, const v
  * 0x20: an expert id outside [0, E) (MoE); 0x40: an MLA kernel gave up
  * waiting; 0x80: a UE8M0-format scale that is not a positive normal power of
  * two; 0x100: a cache slot, page id or position out of range;
- * 0x200: the few-token MoE layer gave up waiting. After a wait gave up, that kernel returned early: its outputs are
- * undefined and the workspace's first 64 KB must be zero-filled again before
- * reuse. The function returns FP8BLK_ERR_TIMEOUT when any bit is set.
+ * 0x200: the few-token MoE layer gave up waiting. After a wait gave up, that
+ * kernel returned early: its outputs are undefined and the workspace's first
+ * 64 KB must be zero-filled again before reuse (not fp8blk_moe_layer's: it
+ * leaves its counters at zero then too). The function returns
+ * FP8BLK_ERR_TIMEOUT when any bit is set.
  */
 FP8BLK_API int fp8blk_last_device_error(fp8blk_stream_t stream, unsigned *device_error_bits);
 

@@ -213,6 +213,19 @@ def test_layer_workspace_is_left_ready_and_shared_by_shapes():
     assert fb.last_device_error() == 0
 
 
+def test_layer_leaves_every_counter_at_zero():
+    """Also those of row tiles that this shape does not have (512 rows: the first 4 of 64), where another shape's call
+    that gave up may have left a part of a count."""
+    a = make(3, 512, 256, 64, 1, 8)
+    ref = run_layer(a, 6, 1)
+    buf = torch.zeros(fb.moe_layer_workspace_bytes(3, 6, 64, 512, 256, 1) + 256, dtype=torch.uint8, device="cuda")
+    ws = buf[(-buf.data_ptr()) % 256:]
+    ws[64 + 4:64 + 64] = 0x11      # row tile k's count is byte 64 + k
+    y = run_layer(a, 6, 1, ws=ws)
+    assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+    assert (ws[:256] == 0).all() and fb.last_device_error() == 0
+
+
 def test_layer_in_a_graph_and_on_a_side_stream():
     a = make(4, 512, 256, 64, 1, 5)
     ref = run_layer(a, 6, 1)
