@@ -77,9 +77,10 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
     float a = -INFINITY, b = -INFINITY;  // this lane's two largest z
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      // (Comparisons, which a NaN fails: fminf of it and the largest is the largest.)
       const float zi = i < v ? z[i] : -INFINITY;
-      b = fmaxf(b, fminf(a, zi));
-      a = fmaxf(a, zi);
+      b = zi > a ? a : zi > b ? zi : b;
+      a = zi > a ? zi : a;
     }
     for (int o = lpg >> 1; o > 0; o >>= 1) {  // merge the pairs of the group's lanes
       const float a2 = __shfl_xor_sync(0xFFFFFFFFu, a, o);

@@ -145,3 +145,32 @@ def test_gate_argument_errors():
     assert f(None, None, 0, 256, 8, 4, 8, 1, 1.0, 1, None, None, None) == 0          # T == 0: nothing to do
     torch.cuda.synchronize()
     del L
+
+
+@pytest.mark.parametrize("E,G,TG", [(256, 8, 4), (64, 4, 1), (160, 8, 3), (32, 8, 2)])
+def test_nan_keys_do_not_count_in_a_group_score(E, G, TG):
+    """A group's score is the sum of its two largest keys that are numbers: a NaN next to the largest must not let that
+    one count twice. The chosen experts lie in the groups that are kept by that, and those of them that are numbers are
+    the best numbers there, in order, each with its own score as its weight. (Where a NaN key goes among the chosen is
+    left open.) Scores are 0.5 exactly, so the keys and their sums here are the kernel's own fp32 numbers."""
+    T, K, per = 40, 4, E // G
+    rng = np.random.default_rng(E)
+    z = np.stack([rng.permutation(E) for _ in range(T)]) / E + 1.0     # the bias carries the order; all scores are 0.5
+    l = np.zeros((T, E), dtype=np.float32)
+    bad = rng.random((T, E)) < 2.0 / per
+    l[bad] = np.nan
+    for t in range(T):
+        b = z[t].astype(np.float32)
+        idx, w = fb.moe_gate(torch.from_numpy(l[t:t + 1]).cuda(), torch.from_numpy(b).cuda(), G, TG, K,
+                             fb.SCORE_SIGMOID, 1.0, False)
+        idx, w = idx[0].cpu().numpy(), w[0].cpu().numpy()
+        zt = np.where(bad[t], np.float32(-np.inf), np.float32(0.5) + b)
+        top = np.sort(zt.reshape(G, per), axis=1)[:, -2:]
+        score = np.where(np.isinf(top[:, 0]), -np.inf, top.sum(axis=1))
+        kept = np.argsort(-score, kind="stable")[:TG]
+        assert len(set(idx.tolist())) == K and set(idx // per) <= set(kept), (t, idx, kept)
+        best = [e for e in np.argsort(-zt, kind="stable") if e // per in kept and not bad[t, e]]
+        numbers = [e for e in idx if not bad[t, e]]
+        assert numbers == best[:len(numbers)], (t, idx, best[:K])
+        assert np.array_equal(np.isnan(w), bad[t][idx]) and np.all(w[~bad[t][idx]] == 0.5)
+    assert fb.last_device_error() == 0
