@@ -439,7 +439,8 @@ def mla_append(kv: torch.Tensor, norm_w: torch.Tensor, rope: torch.Tensor, posit
     """Writes each token's cache row: kv bf16 [T, 576] -> RMS-normed latent (norm_w fp32 [512]) and rotated key
     (rope fp32 [max_pos, 32, 2], positions int64 [T]) at row slots[t] (int64 [T], negative: not written) of
     cache bf16 [pages, page_size, 576]. With q bf16 [T, H, 192] returns (q_nope [T, H, 128], rotated q_pe
-    [T, H, 64]), else None. kv and q may have strided rows (inner dimensions contiguous)."""
+    [T, H, 64]), else None. kv and q may have strided rows (inner dimensions contiguous). A slot past the cache is not
+    written; a position outside [0, max_pos) is taken as 0. Both set bit 0x100 of last_device_error()."""
     if not kv.is_cuda or kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != MLA_LATENT + MLA_ROPE:
         raise Fp8BlkError("kv must be a CUDA bfloat16 tensor [T, 576]")
     T = kv.shape[0]

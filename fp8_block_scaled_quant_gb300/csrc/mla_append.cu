@@ -10,7 +10,10 @@
 //   q_pe[t, h]   = bf16(rot(q[t, h, 128:192]))
 //   rot: (a, b) = (v[2i], v[2i+1]) -> (a c_i - b s_i, a s_i + b c_i)
 //
-// in fp32 with one rounding to bf16. One launch, one pass: every input byte
+// A negative slot is a padding token: no cache row. A slot past the cache writes
+// none either and sets an error bit; a position outside the table sets it too
+// and is taken as 0 (row and queries are written, turned by that angle).
+// fp32 with one rounding to bf16. One launch, one pass: every input byte
 // is read once and every output byte written once, so HBM bounds long
 // prompts and launch latency single tokens (measured: 6151 tokens of 128 heads,
 // 621 MB, 104.6 us, 5.9 TB/s; one token 2.1 us, 129 tokens of 16 heads 2.4 us).

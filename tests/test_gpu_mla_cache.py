@@ -459,3 +459,21 @@ def test_attention_without_any_key(H, stride):
         out = call_attention(dict(a, lens=torch.zeros_like(a["lens"])), lse)
         assert (out == 0).all() and (lse == -math.inf).all()
     assert fb.last_device_error() == 0
+
+
+def test_append_takes_a_position_out_of_range_as_zero():
+    """Row and queries are those of position 0, and the error word says so; a slot past the cache leaves no row."""
+    g = gen(31)
+    w, rope = 1.0 + normal(g, C, std=0.2, dtype=torch.float32), rope_table(4)
+    kv, q = normal(g, 3, C + R), normal(g, 3, 9, DN + R)
+    slots = torch.tensor([5, 17, 32], device="cuda")
+    got = []
+    for pos in ([0, 0, 3], [4, -1, 3]):
+        cache = torch.full((2, 16, C + R), 7.0, dtype=torch.bfloat16, device="cuda")
+        qn, qp = fb.mla_append(kv, w, rope, torch.tensor(pos, device="cuda"), slots, cache, q=q)
+        assert fb.last_device_error() == 0x100          # the third token's slot, then the positions too
+        got.append((cache, qn, qp))
+        rows = cache.view(-1, C + R)
+        assert sorted((rows != 7).any(-1).nonzero()[:, 0].tolist()) == [5, 17]
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
