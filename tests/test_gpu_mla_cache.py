@@ -477,3 +477,32 @@ def test_append_takes_a_position_out_of_range_as_zero():
         assert sorted((rows != 7).any(-1).nonzero()[:, 0].tolist()) == [5, 17]
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_attention_bad_values_reach_every_row_of_their_request():
+    """A NaN key makes all its request's outputs NaN. An infinite entry makes a score +-Inf (or NaN for a zero query
+    column), hence a weight NaN or 0: 0 * Inf in that column, at least. The other requests keep their bits."""
+    a = make_attention(4, 16, 200, [40, 50, 60, 70], 16, 10)
+    clean = call_attention(a)
+    rows = a["cache"].view(-1, C + R)
+    rows[a["keys_o"][1][7]] = math.nan
+    rows[a["keys_o"][2][9], 3] = math.inf
+    lse = torch.zeros((4, 16), device="cuda")
+    out = call_attention(a, lse)
+    assert out[1].isnan().all()
+    assert not out[2][:, 3].isfinite().any()
+    assert lse[1].isnan().all()
+    for b in (0, 3):
+        assert torch.equal(out[b].view(torch.int16), clean[b].view(torch.int16)) and lse[b].isfinite().all()
+
+
+def test_attention_bad_values_in_one_part_of_a_long_row():
+    """The same where the row's keys are cut into parts that are joined: one NaN key among 9000, heads of 128 and of 5."""
+    for H in (5, 128):
+        a = make_attention(2, H, 0, [9000, 3000], 64, 33)
+        a["cache"].view(-1, C + R)[a["keys_o"][0][8191]] = math.nan
+        lse = torch.zeros((2, H), device="cuda")
+        out = call_attention(a, lse)
+        assert out[0].isnan().all() and lse[0].isnan().all()
+        check_attention(a, out, lse, requests=[1])
+    assert fb.last_device_error() == 0
