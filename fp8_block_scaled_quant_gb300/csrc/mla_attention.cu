@@ -245,13 +245,22 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
 }
 
 // Arrives on an mbarrier of any CTA of the cluster (shared::cluster address).
-// What it orders for the MMA thread are tensor-memory accesses, by the
-// tcgen05 fences around it, and shared-memory writes that the tensor cores read
-// through the async proxy, by the proxy fence before it; the waiting thread
-// itself reads none of that memory, and a release of cluster scope would stall
-// the warp for more than 1000 cycles here.
+// What it orders are tensor-memory accesses, by the tcgen05 fences around it, or
+// nothing but a count: no release of memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// The same for shared memory written before it (made visible to the async proxy
+// by the writers' proxy fences): the thread that waits issues MMAs whose operands
+// are read in this CTA, so the release is of cluster scope, restricted to this
+// CTA's shared memory. (A release of cluster scope over all memory stalls the
+// warp for about 800 cycles here: 64 x 128 rows, 32768 shared keys 482 us; an
+// arrival of CTA scope, which orders nothing between the two, 325; this one,
+// with the acquires below, 329.)
+__device__ __forceinline__ void mbar_publish_cluster(uint32_t addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_cluster(addr);
 }
 
 // The bounded wait of every role, out of line: the roles' loops have to stay
@@ -281,6 +290,12 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
   const uint32_t a = smem_u32(bar);
   return mbar_try_wait(a, parity) || wait_slow(a, parity, abort, err);
+}
+
+// The same for a phase that threads of both CTAs arrive in.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait_cluster(a, parity) || (wait_slow(a, parity, abort, err) && mbar_try_wait_cluster(a, parity));
 }
 
 // The same for a whole warp: true in all lanes or in none.
@@ -628,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
                   *reinterpret_cast<uint4*>(smem + kOffV + c * kVChunk + s * kVSlab + e * 16) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(full);
+              if (lane == 0) mbar_publish_cluster(full);
             }
             vphase ^= 1u << c;
           }
@@ -675,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
 #pragma unroll 1
           for (int t = in.t0; ok && t < in.t1; ++t, ++n) {
             const uint32_t buf = n & 1, d = tmem + kTmemS + buf * 64;
-            if (n > 1) ok = wait_one(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
+            if (n > 1) ok = wait_cluster(&s_empty[buf], ((n >> 1) - 1) & 1, abort_flag, p.err);
 #pragma unroll 1
             for (int g = 0; ok && g < kKGroups; ++g) {
               ok = wait_one(&k_full[g], n & 1, abort_flag, p.err);
@@ -706,15 +721,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           const Item it = get_item(p, i);
           const Span in = span_of(it.tiles, v0, left);
           left -= in.units;
-          if (in.t1 > in.t0 && seg++ > 0) ok = wait_one(o_empty, (seg - 2) & 1, abort_flag, p.err);
+          if (in.t1 > in.t0 && seg++ > 0) ok = wait_cluster(o_empty, (seg - 2) & 1, abort_flag, p.err);
 #pragma unroll 1
           for (int t = in.t0; ok && t < in.t1; ++t, ++n) {
             const bool pre = t < it.pt;
-            const int chunks = chunks_of((pre ? t : t - it.pt) * kTileKeys, pre ? p.P : it.len);
-            ok = wait_one(p_full, n & 1, abort_flag, p.err);
+            const int keys = (pre ? p.P : it.len) - (pre ? t : t - it.pt) * kTileKeys;
+            const int chunks = chunks_of(0, keys);
+            ok = wait_cluster(p_full, n & 1, abort_flag, p.err);
 #pragma unroll 2
             for (int c = 0; ok && c < chunks; ++c) {
               ok = wait_one(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
+              // (The end of the keys: zeros stored by both CTAs.)
+              if (ok && keys < (c + 1) * kVRows) ok = wait_cluster(&v_full[c], (vphase >> c) & 1, abort_flag, p.err);
               if (!ok) break;
               tc_fence_after_sync();
               const uint64_t ad = pd + static_cast<uint32_t>(c) * (kSlab >> 4);
@@ -858,7 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttnThreads, 1)
           tc_fence_before_sync();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_p);
+        if (lane == 0) mbar_publish_cluster(leader_p);
       }
       if (ok && t1 > t0) {
         const float lt = l + exchange(l);
