@@ -132,8 +132,8 @@ _ws_cache: dict = {}
 _ws_captured: dict = {}   # by address: buffers that a graph may hold
 
 
-def _capturing(device: torch.device) -> bool:
-    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+def _capturing(on_gpu: bool) -> bool:
+    return on_gpu and torch.cuda.is_current_stream_capturing()
 
 
 def _buffer(nbytes: int, device: torch.device, key: tuple, zeroed: int | None = None) -> torch.Tensor:
@@ -141,7 +141,7 @@ def _buffer(nbytes: int, device: torch.device, key: tuple, zeroed: int | None = 
     of them a call needs as zeros (None: all), for a buffer made during a capture and filled in every replay."""
     buf = _ws_cache.get(key)
     fits = buf is not None and buf.numel() >= nbytes + 256
-    if _capturing(device):
+    if _capturing(device.type == "cuda"):
         if fits:
             _ws_captured[buf.data_ptr()] = buf
             return buf
@@ -201,7 +201,10 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, t: torch.Tensor, stream: int,
         if ws.get_device() != t.get_device() or not ws.is_contiguous():
             raise Fp8BlkError("ws must be a contiguous tensor on the device of the inputs")
         return ws.data_ptr(), ws.numel() * ws.element_size(), ws
-    buf = _buffer(nbytes, t.device, (t.get_device(), stream, key), zeroed)
+    key = (t.get_device(), stream, key)
+    buf = _ws_cache.get(key)
+    if buf is None or buf.numel() < nbytes + 256 or _capturing(t.is_cuda):
+        buf = _buffer(nbytes, t.device, key, zeroed)
     at = buf.data_ptr()
     return at + (-at) % 256, nbytes, buf
 
