@@ -123,41 +123,53 @@ def _need(t: torch.Tensor, dtype, name: str, ndim: int = 2):
 #
 # A captured graph keeps the addresses of its calls' workspaces, so a buffer that
 # a capture was given is never freed, also where a later call needs a larger one.
-# A buffer made during a capture belongs to that graph alone: its fill is one
-# of the graph's nodes, so no other call may rely on it. Replays of graphs captured
-# on one stream share that stream's workspaces with its other calls: they must
-# not run at the same time.
+# A buffer made during a capture serves that capture alone: its fill is one of the
+# graph's nodes, so no other graph and no eager call may rely on it. Replays of
+# graphs captured on one stream share that stream's workspaces with its other calls:
+# they must not run at the same time.
 
 _ws_cache: dict = {}
-_ws_captured: dict = {}   # by address: buffers that a graph may hold
+_ws_captured: dict = {}   # by address: buffers of _ws_cache that a graph may hold
+_ws_graph: dict = {}      # the last capture's own buffers: (its id, buffer)
+_COUNTERS = 64 * 1024     # what any call needs as zeros lies in the first 64 KB of its workspace
 
 
 def _capturing(on_gpu: bool) -> bool:
     return on_gpu and torch.cuda.is_current_stream_capturing()
 
 
-def _buffer(nbytes: int, device: torch.device, key: tuple, zeroed: int | None = None) -> torch.Tensor:
-    """A uint8 buffer with nbytes after its first 256-byte boundary, all zeros when it was made. `zeroed`: how many
-    of them a call needs as zeros (None: all), for a buffer made during a capture and filled in every replay."""
+def _capture_id(stream: int) -> int:
+    n = ctypes.c_ulonglong(0)
+    _check(_function("fp8blk_capture_id", "pp")(stream, ctypes.addressof(n)), "capture_id")
+    return n.value
+
+
+def _buffer(nbytes: int, device: torch.device, key: tuple, zeroed: int = _COUNTERS) -> torch.Tensor:
+    """A uint8 buffer of (device, stream, name) with nbytes after its first 256-byte boundary, all zeros when it was
+    made; `zeroed`: how many of them a call needs so, for a buffer that a graph fills in every replay."""
     buf = _ws_cache.get(key)
     fits = buf is not None and buf.numel() >= nbytes + 256
-    if _capturing(device.type == "cuda"):
-        if fits:
-            _ws_captured[buf.data_ptr()] = buf
-            return buf
-        buf = torch.empty(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
-        if zeroed != 0:
-            buf[:buf.numel() if zeroed is None else zeroed + 256].zero_()
-        return buf
-    if not fits:
-        buf = _ws_cache[key] = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
+    if not _capturing(device.type == "cuda"):
+        if not fits:
+            buf = _ws_cache[key] = torch.zeros(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
+    elif fits:
+        _ws_captured[buf.data_ptr()] = buf
+    else:
+        capture = _capture_id(key[1])
+        held, buf = _ws_graph.get(key, (None, None))
+        if held != capture or buf.numel() < nbytes + 256:
+            buf = torch.empty(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
+            if zeroed:
+                buf[:zeroed + 256].zero_()
+            _ws_graph[key] = capture, buf
     return buf
 
 
 def workspace(nbytes: int, device: torch.device, key: str = "gemm") -> torch.Tensor:
     """A zero-initialised uint8 device buffer of at least nbytes, reused by
     every call on the same device, stream and key. The GEMM leaves its
-    counters at zero, so the buffer never needs clearing again."""
+    counters at zero, so the buffer never needs clearing again. (First needed
+    during a capture: the graph zeroes its first 64 KB, where the counters are.)"""
     stream = torch.cuda.current_stream(device).cuda_stream
     buf = _buffer(nbytes, device, (device.index, stream, key))
     off = (-buf.data_ptr()) % 256

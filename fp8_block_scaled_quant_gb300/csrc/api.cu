@@ -115,6 +115,16 @@ extern "C" int fp8blk_last_device_error(fp8blk_stream_t stream, unsigned* bits) 
   return v ? FP8BLK_ERR_TIMEOUT : FP8BLK_OK;
 }
 
+extern "C" int fp8blk_capture_id(fp8blk_stream_t stream, unsigned long long* id) {
+  if (!id) return FP8BLK_ERR_NULL;
+  cudaStreamCaptureStatus status;
+  unsigned long long n = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &n) != cudaSuccess)
+    return FP8BLK_ERR_CUDA;
+  *id = status == cudaStreamCaptureStatusNone ? 0 : n;
+  return FP8BLK_OK;
+}
+
 // Workspace of the linear layer: [GEMM workspace][x_q e4m3 M*K][x_s fp32 M*K/128],
 // each part 256-byte aligned. The GEMM workspace comes first so that its tile
 // counters sit at the same offset whatever the shape: one workspace can serve

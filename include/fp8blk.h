@@ -506,6 +506,14 @@ FP8BLK_API int fp8blk_gemm_noalloc(const void *a_e4m3, const float *a_s, const v
  */
 FP8BLK_API int fp8blk_last_device_error(fp8blk_stream_t stream, unsigned *device_error_bits);
 
+/*
+ * The number of the capture that `stream` is part of (calls with the same
+ * number end up in one graph), 0 where the stream is not being captured. For
+ * callers that keep workspaces: one that was filled within a capture holds
+ * what it needs in that graph's replays alone.
+ */
+FP8BLK_API int fp8blk_capture_id(fp8blk_stream_t stream, unsigned long long *id);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,13 +10,15 @@ import fp8_block_scaled_quant_gb300 as fb
 
 
 class Host:
-    """The cache on host tensors, with a capture switched on and off by the test."""
+    """The cache on host tensors, with a capture switched on and off by the test (`capturing`: its number)."""
 
     def __init__(self, monkeypatch):
         self.capturing = False
+        monkeypatch.setattr(fb, "_ws_graph", {})
+        monkeypatch.setattr(fb, "_capture_id", lambda stream: self.capturing)
         monkeypatch.setattr(fb, "_ws_cache", {})
         monkeypatch.setattr(fb, "_ws_captured", {})
-        monkeypatch.setattr(fb, "_capturing", lambda device: self.capturing)
+        monkeypatch.setattr(fb, "_capturing", lambda on_gpu: bool(self.capturing))
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=7))
         self.t = torch.zeros(1)
 
@@ -57,18 +59,21 @@ def test_buffers_of_no_graph_are_given_back(monkeypatch):
 
 
 @pytest.mark.parametrize("take", ["scratch", "workspace"])
-def test_a_buffer_made_in_a_capture_serves_that_call_alone(monkeypatch, take):
-    """Its fill runs in that graph's replays only: neither another capture nor an eager call may be given it."""
+def test_a_buffer_made_in_a_capture_serves_that_capture_alone(monkeypatch, take):
+    """Its fill runs once in each of that graph's replays: the graph's other calls share it, another graph or an eager
+    call may not."""
     h = Host(monkeypatch)
-    in_capture = getattr(h, take)(4096, capturing=True)
-    assert not fb._ws_cache and not fb._ws_captured
+    tensor = lambda got: got[2] if take == "scratch" else got
+    at = lambda got: got[0] if take == "scratch" else got.data_ptr()
+    first = getattr(h, take)(4096, capturing=11)
+    assert not tensor(first)[:512].any() and not fb._ws_cache and not fb._ws_captured
+    assert at(getattr(h, take)(3000, capturing=11)) == at(first)
+    assert at(getattr(h, take)(1 << 20, capturing=11)) != at(first)
+    other = getattr(h, take)(4096, capturing=12)
     eager = getattr(h, take)(4096)
-    held = [b for b in fb._ws_cache.values()]
-    assert len(held) == 1 and not held[0].any()
-    if take == "scratch":
-        assert not in_capture[2][:512].any() and eager[2] is held[0]
-    else:
-        assert not in_capture.any()
+    assert len({at(first), at(other), at(eager)}) == 3
+    kept, = fb._ws_cache.values()
+    assert not kept.any() and at(getattr(h, take)(4096, capturing=13)) == at(eager)
 
 
 class OnGpu:
@@ -176,6 +181,45 @@ def test_a_graph_survives_a_larger_call_on_its_stream(name):
     assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
     assert torch.equal(want.view(torch.int16), again.view(torch.int16))
     assert all(bool((t == 0x5A).all()) for t in others)
+    assert fb.last_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_capture_id():
+    assert fb._capture_id(torch.cuda.current_stream().cuda_stream) == 0
+    seen, x = [], torch.zeros(1, device="cuda")
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(2):
+                x += 1
+                seen.append(fb._capture_id(torch.cuda.current_stream().cuda_stream))
+    assert seen[0] == seen[1] != seen[2] == seen[3] and 0 not in seen
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CASES)
+def test_calls_of_one_capture_share_their_buffer(name):
+    """Warmed up on the default stream, captured on the capture's own: one buffer, filled once in a replay."""
+    run, small, _ = CASES[name]
+    a = small()
+    ref = run(a)
+    outs = [torch.empty_like(ref) for _ in range(3)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    before = dict(fb._ws_graph)
+    with torch.cuda.graph(graph):
+        held = []
+        for o in outs:
+            run(a, o)
+            new = [v[1].data_ptr() for k, v in fb._ws_graph.items() if v is not before.get(k)]
+            held.append(new)
+    assert held[0] == held[1] == held[2] and len(held[0]) <= 1
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.view(torch.int16), ref.view(torch.int16))
     assert fb.last_device_error() == 0
 
 
