@@ -27,6 +27,13 @@ __device__ __forceinline__ uint32_t gate_order(float z) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The smaller number, or NaN where one of the two is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float c;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
 // The lowest lane that has the warp's largest key.
 __device__ __forceinline__ int warp_argmax_lane(uint32_t key) {
   const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, key);
@@ -77,10 +84,9 @@ __device__ __forceinline__ void gate_warp(float (&x)[V], const float (&bias)[V],
     float a = -INFINITY, b = -INFINITY;  // this lane's two largest z
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      // (Comparisons, which a NaN fails: fminf of it and the largest is the largest.)
       const float zi = i < v ? z[i] : -INFINITY;
-      b = zi > a ? a : zi > b ? zi : b;
-      a = zi > a ? zi : a;
+      b = fmaxf(b, min_nan(a, zi));  // (fminf of a NaN and the largest would be the largest)
+      a = fmaxf(a, zi);
     }
     for (int o = lpg >> 1; o > 0; o >>= 1) {  // merge the pairs of the group's lanes
       const float a2 = __shfl_xor_sync(0xFFFFFFFFu, a, o);
