@@ -45,17 +45,17 @@
 // comes from a second sum of the weights before their rounding.
 //
 // What bounds it, measured (GPU time): 64 requests of 128 heads behind 32768
-// shared keys take 327 us, 1.8 PFLOP/s of the 1.94 that a library GEMM reaches:
-// the tensor cores (364 us a call in long runs). 32 requests of 128 heads
-// with up to 8191 own keys take 47.8 us, of which HBM needs 25.5 and the products
-// 20, side by side but for the first loads (6 us) and the join (7 us). Where a
-// call is short the chain of latencies is all there is: 23.8 us for one request
-// of 128 heads and 32768 keys, 20.9 us for 61 of 16 heads behind 2011, are 5 us
-// of launch, plan and first loads, 6 us of tiles, 2 us for 20 MB of parts to L2,
-// 1.7 us between the kernels and 5 us to read the parts back; one short
-// request is 7.3 us. (One kernel whose CTAs meet at a barrier and join with their
-// own seven warps took 29.6 us for that one request: the join wants more loads in
-// flight than those warps have.)
+// shared keys take 328 us, 1.8 PFLOP/s of the 1.94 that a library GEMM reaches:
+// the tensor cores (369 us a call in long runs). 32 requests of 128 heads
+// with up to 8191 own keys take 48.2 us, of which HBM needs 25.5 and the products
+// 20, side by side; first loads (6 us) and join (7 us) leave 9 us unexplained.
+// Where a call is short the chain of latencies is all there is: 24.0 us for one
+// request of 128 heads and 32768 keys are 5 us of launch, plan and first loads, 6
+// us of tiles, 2 us for 20 MB of parts to L2, 1.7 us between the kernels and 5 us
+// to read the parts back; 61 requests of 16 heads behind 2011 keys take 21.2 us,
+// one short request 7.5. (One kernel whose CTAs meet at a barrier and join with
+// their own seven warps, loading the parts into registers, took 29.6 us for that
+// one long request where two kernels took 27.)
 //
 // Every wait is bounded (2 s): on expiry roles leave their loops, in-flight
 // copies are waited for (bounded), tensor memory is freed, an error bit set.
@@ -257,7 +257,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 // CTA's shared memory. (A release of cluster scope over all memory stalls the
 // warp for about 800 cycles here: 64 x 128 rows, 32768 shared keys 482 us; an
 // arrival of CTA scope, which orders nothing between the two, 325; this one,
-// with the acquires below, 329.)
+// with the acquires below, 328.)
 __device__ __forceinline__ void mbar_publish_cluster(uint32_t addr) {
   asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
   mbar_arrive_cluster(addr);

@@ -45,9 +45,12 @@
 // reached: 83-85 us for 400 MB, 4.8 TB/s over the call, 6.1 to 6.6 of a copy's 6.7 in the
 // two phases; 14 us go by before the routed weights can be asked for (x read,
 // logits, the CTAs' meeting, the gate), 6 between the phases, 3 after them. 16
-// tokens of it 480-540 us (which experts they reach varies), 32 tokens of
-// 5120 x 1536, 160 experts, 491 us, 5.5 TB/s; 5 tokens of 2048 x 1408, 64 experts,
-// 66.6 us, 3.5 TB/s.
+// tokens of it that reach 78 experts 542 us, 6.35 TB/s; 32 tokens of 5120 x 1536,
+// 160 experts (112 reached), 492 us, 5.4 TB/s; 5 tokens of 2048 x 1408, 64 experts,
+// 67.1 us, 3.6 TB/s. Two token-column widths share 128 registers a thread: the
+// wider one spills 604 bytes. For all of 1 to 32 tokens it is ahead of the chain of
+// gate product, gate, act_quant and grouped GEMMs (1.6 times for one token of 7168
+// x 2048, 1.13 for 32).
 //
 // Every wait is bounded (2 s): on expiry an error bit is set, waits return at
 // once from then on, and the control flow, whose loops are finite, runs out.

@@ -443,8 +443,9 @@ FP8BLK_API int fp8blk_moe_grouped_gemm(const void *x_e4m3, const float *x_s, con
  * ones); y: bf16 [T, dim]. topk_idx int32 / topk_w fp32 [T, topk] are written
  * where not NULL. T <= 32 (more tokens: fp8blk_moe_grouped_gemm), dim and
  * inter multiples of 128, dim <= 8192, inter <= 16384, n_shared <= 8, and the
- * rules of fp8blk_moe_gate for E, topk and the groups; else FP8BLK_ERR_SHAPE. bf16 and e4m3 inputs 16-byte aligned. An expert without a
- * token reads none of its weights. One cooperative launch of one CTA per SM;
+ * rules of fp8blk_moe_gate for E, topk and the groups; else FP8BLK_ERR_SHAPE.
+ * bf16 and e4m3 inputs 16-byte aligned. An expert without a token reads none
+ * of its weights. One cooperative launch of one CTA per SM;
  * the result does not vary from run to run.
  * Workspace: fp8blk_moe_layer_workspace_bytes(T, topk, E, dim, inter, n_shared),
  * 256-byte aligned; its first 256 bytes hold counters: ZERO-FILLED before the
