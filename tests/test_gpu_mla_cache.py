@@ -506,3 +506,14 @@ def test_attention_bad_values_in_one_part_of_a_long_row():
         assert out[0].isnan().all() and lse[0].isnan().all()
         check_attention(a, out, lse, requests=[1])
     assert fb.last_device_error() == 0
+
+
+@pytest.mark.parametrize("H,P,own", [(16, 0, 200001), (128, 140003, 60000), (5, 170000, 33)])
+def test_attention_of_long_contexts(H, P, own):
+    """Hundreds of thousands of keys for one row (several requests' worth of parts); the weights' rounding errors stay
+    independent, so the norm's bound is the short rows'."""
+    a = make_attention(2, H, P, [own, 7], 64, 41)
+    lse = torch.empty((2, H), device="cuda")
+    out = call_attention(a, lse)
+    check_attention(a, out, lse)
+    assert torch.equal(call_attention(a).view(torch.int16), out.view(torch.int16)) and fb.last_device_error() == 0
