@@ -463,6 +463,105 @@ FP8BLK_API int fp8blk_moe_layer(const void *x_bf16, const void *gate_w_bf16, con
                                 fp8blk_stream_t stream);
 
 /*
+ * Microscaled 4-bit floats. e2m1 holds 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives (code = sign * 8 + index); element 2i of a row is the low half of
+ * byte i. Two formats:
+ *   FP8BLK_FP4_E4M3   an e4m3 scale s for every 16 columns and an fp32 scale g
+ *                     for every row; a value is q * s * g;
+ *   FP8BLK_FP4_UE8M0  a power of two for every 32 columns (byte e: 2^(e - 127),
+ *                     255: NaN), no row scale; a value is q * s.
+ * The scale bytes are kept in tiles of 128 rows x 4 blocks (512 bytes), in the
+ * order in which the tensor cores read them: the byte of (row, block) is
+ *   s[row / 128][block / 4][row % 32][row % 128 / 32][block % 4]
+ * of ceil(rows / 128) x (blocks / 4) tiles, fp8blk_fp4_scale_bytes in all. The
+ * bytes of rows past the last one may hold anything.
+ * K is a multiple of 128 throughout (FP8BLK_ERR_SHAPE).
+ */
+#define FP8BLK_FP4_E4M3 0
+#define FP8BLK_FP4_UE8M0 1
+FP8BLK_API size_t fp8blk_fp4_scale_bytes(int64_t rows, int64_t K, int fmt);
+
+/*
+ * Quantisation of x [M, K], bf16 or fp32 (is_fp32), rows x_stride elements
+ * apart, to q [M, K / 2], scale tiles s and, for FP8BLK_FP4_E4M3, row scales
+ * g [M]. With amax the largest |x| of a row (a_r) or of a block (a_b), every
+ * step in fp32, rounded to nearest even:
+ *   E4M3:  a = max(a_r, 2^-100), g = a / 2688, s = e4m3(a_b * (448 / a)),
+ *          q = e2m1(x * (1 / (s * g))), zeros where s = 0. A row that holds a NaN
+ *          or an infinity gets g = NaN, zero codes and zero scales.
+ *   UE8M0: s = 2^e, the least power of two >= a_b / 6 with e >= -126,
+ *          q = e2m1(x / s). A block that holds a NaN or an infinity gets the NaN
+ *          scale and zero codes.
+ * e2m1() rounds to nearest (ties to the even code) and saturates at +-6.
+ * x, q, s 16-byte aligned, x_stride a multiple of 16 bytes and >= K. M or K zero
+ * launches nothing. One launch, no workspace.
+ */
+FP8BLK_API int fp8blk_fp4_quant(const void *x, int is_fp32, int64_t x_stride, int64_t M, int64_t K, int fmt, void *q,
+                                void *s, float *g, fp8blk_stream_t stream);
+
+/* out[m, k] = bf16(q * s * g) (E4M3; q * s is exact, one fp32 multiply) or
+ * bf16(q * s) (UE8M0). out: bf16 [M, K], 16-byte aligned. */
+FP8BLK_API int fp8blk_fp4_dequant(const void *q, const void *s, const float *g, int64_t M, int64_t K, int fmt,
+                                  void *out_bf16, fp8blk_stream_t stream);
+
+/*
+ * Product of two 4-bit matrices of one format:
+ *   C[m, n] = bf16( a_g[m] * w_g[n] * sum over blocks b of
+ *                   a_s[m, b] * w_s[n, b] * sum_{k in b} a[m, k] * w[n, k] )
+ * (UE8M0: without a_g and w_g, which may be NULL). The block-scaled MMA applies
+ * the block scales and sums in fp32. a [M, K/2], w [N, K/2] and scale tiles
+ * 16-byte aligned, c bf16 [M, N] of any alignment of its elements, row scales
+ * 4-byte aligned; any M and N up to 2^28. K == 0 writes zeros. The result does
+ * not vary from run to run. No workspace. Weights (w, w_s) may be read before
+ * the previous kernel on the stream has ended (the overlap rule above); w_g may
+ * not.
+ */
+FP8BLK_API int fp8blk_fp4_gemm(const void *a, const void *a_s, const float *a_g, const void *w, const void *w_s,
+                               const float *w_g, void *c_bf16, int64_t M, int64_t N, int64_t K, int fmt,
+                               fp8blk_stream_t stream);
+
+/*
+ * FP4 linear layer: y = fp8blk_fp4_gemm(fp8blk_fp4_quant(x), w), x bf16 [M, K]
+ * with rows x_stride elements apart, y bf16 [M, N]. The quantised activation
+ * lives in the workspace: fp8blk_fp4_linear_workspace_bytes, 256-byte aligned,
+ * any contents; one workspace serves layers of any shape, one stream at a time.
+ */
+FP8BLK_API size_t fp8blk_fp4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt);
+FP8BLK_API int fp8blk_fp4_linear(const void *x_bf16, int64_t x_stride, const void *w, const void *w_s, const float *w_g,
+                                 void *y_bf16, int64_t M, int64_t N, int64_t K, int fmt, void *workspace,
+                                 size_t workspace_bytes, fp8blk_stream_t stream);
+
+/*
+ * The norms around a block of a layer, with the block's gate and the residual's
+ * scale, and the next product's operand ("Administrator & Developer Guide", 1.2:
+ * RMSNorm before each block; 6.3: every Linear quantises its input). Per token,
+ * with the means over the D columns:
+ *   z = post_w ? y / sqrt(mean of y^2 + eps) * post_w : y     (the block's output)
+ *   r = residual_scale * x + gate * z                         (x NULL: gate * z)
+ *   h = r / sqrt(mean of r^2 + eps) * norm_w
+ * fp32 from the inputs to one rounding of each output: r as bf16 (r NULL: not
+ * written), and h by out_kind as
+ *   FP8BLK_NORM_BF16  bf16 [T, D];
+ *   FP8BLK_NORM_E4M3  act_quant of h (scale_fmt as there): e4m3 [T, D], h_s fp32 [T, D/128];
+ *   FP8BLK_NORM_E2M1  fp4_quant of h (scale_fmt FP8BLK_FP4_*): codes [T, D/2], scale
+ *                     tiles h_s, row scales h_g [T] (E4M3 format).
+ * y, x: bf16 [T, D], rows y_stride / x_stride elements apart. The gate is one of
+ * gate_col (fp32 [D]) and gate_tok (bf16 [T, D], rows gate_stride apart), or none.
+ * norm_w, post_w: fp32 [D]. r may be x or y itself (in place, rows D apart); no other
+ * output may overlap an input. 1 <= D <= 16384, a multiple of 8 (BF16) or 128; strides
+ * multiples of 8; every tensor 16-byte aligned, h_s of E4M3 and h_g 4-byte aligned.
+ * Both gates, or eps < 0: FP8BLK_ERR_ARG. T == 0 launches nothing. One launch, no workspace.
+ */
+#define FP8BLK_NORM_BF16 0
+#define FP8BLK_NORM_E4M3 1
+#define FP8BLK_NORM_E2M1 2
+FP8BLK_API int fp8blk_residual_norm(const void *y_bf16, int64_t y_stride, const void *x_bf16, int64_t x_stride,
+                                    const float *post_w, const float *gate_col, const void *gate_tok_bf16,
+                                    int64_t gate_stride, float residual_scale, const float *norm_w, float eps, int64_t T,
+                                    int64_t D, int out_kind, int scale_fmt, void *r_bf16, void *h, void *h_s, float *h_g,
+                                    fp8blk_stream_t stream);
+
+/*
  * fp8_gemm with no workspace argument and no device allocation: the same
  * computation, result and argument rules as fp8blk_gemm, but its scratch
  * (tile counters and stream-K partial sums) lives in a buffer of
