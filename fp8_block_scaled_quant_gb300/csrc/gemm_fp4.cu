@@ -248,11 +248,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     cluster_sync();
     if (warp >= 2) {
+      // Four columns at a time, so that 4 ks loads are under way together.
       const int c1 = cols * (rank + 1) / ks;
-      for (int c = cols * rank / ks; c < c1; ++c) {
-        float v = 0.0f;
-        for (int k = 0; k < ks; ++k) v += ld_shared_cluster_f32(part + c * 128 + q * 32 + lane, static_cast<uint32_t>(k));
-        if (finished) store(c, v);
+      for (int c = cols * rank / ks; c < c1; c += 4) {
+        float v[4][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i][k] = k < ks && c + i < c1
+                          ? ld_shared_cluster_f32(part + (c + i) * 128 + q * 32 + lane, static_cast<uint32_t>(k))
+                          : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float sum = v[i][0];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) sum += v[i][k];
+          if (finished && c + i < c1) store(c + i, sum);
+        }
       }
     }
     cluster_sync();  // no CTA ends while another reads its sums
