@@ -51,7 +51,7 @@ struct Fp4Params {
   int64_t M, N, ktiles;  // ktiles: scale tiles along K
   int ksteps;            // K / 64
   int stages_k;          // ceil(K / 256)
-  int tiles_n;           // weight tiles
+  int tiles_n, tiles_m;  // weight tiles; token tiles (pairs)
   int ksplit;            // CTAs of a tile's cluster
 };
 
@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after_sync();
   }
 
+  __syncwarp();
   // The accumulator: lane = weight row, column = token.
   const int q = warp & 3;  // lane quarter of an epilogue warp
   const int64_t row = static_cast<int64_t>(tile_n) * 128 + q * 32 + lane;
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc_fence_before_sync();
     }
+    __syncwarp();
     cluster_sync();
     if (warp >= 2) {
       // Four columns at a time, so that 4 ks loads are under way together.
@@ -268,12 +270,329 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
+    __syncwarp();
     cluster_sync();  // no CTA ends while another reads its sums
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---- CTA pairs -----------------------------------------------------------------------
+//
+// Many tokens: 256 tokens x 256 weight rows to a pair of CTAs (cta_group::2), tokens
+// as tensor-memory lanes. Each CTA has 128 tokens and half of the weight rows, so a
+// byte of either operand is fetched once per 256 products; both have the scales of
+// all 256 weight rows. One accumulator of 256 columns: the epilogue's eight warps
+// take it out in bf16 registers, hand it back, and store from there while the next
+// tile is summed.
+//
+//   warp 0       producer: this CTA's operands, completing on the leader's barriers
+//   warp 1       MMA issuer (leader CTA); both allocate tensor memory
+//   warps 4-11   epilogue: lane quarter warp % 4, columns 128 (warp >= 8) on
+
+constexpr int kPairThreads = 384;
+constexpr int kPairN = 256;
+
+template <int FMT_>
+struct PairCfg {
+  static constexpr int FMT = FMT_;
+  static constexpr int kTiles = FMT == kFp4E4M3 ? 4 : 2;
+  static constexpr int kSfBytes = kTiles * kScaleTile;           // 128 rows of a stage
+  static constexpr int kSfaAt = 2 * kLaneBytes, kSfbAt = kSfaAt + kSfBytes;
+  static constexpr int kTxBytes = kSfbAt + 2 * kSfBytes;         // of one CTA
+  static constexpr int kStageBytes = (kTxBytes + 1023) / 1024 * 1024;
+  static constexpr int kStages = 5;
+  static constexpr int kSfCols = kTiles * 12;                    // 4 for the tokens, 8 for the weights
+  static constexpr int kOutAt = kStages * kStageBytes;           // 8 warps x 4 KB
+  static constexpr int kFactorsAt = kOutAt + 8 * 4096;           // the tile's 256 weight row scales
+  static constexpr int kBarsAt = kFactorsAt + kPairN * 4;
+  static constexpr int kSmem = 1024 + kBarsAt + (2 * kStages + 3) * 8 + 8;
+  static_assert(kPairN + 2 * kSfCols <= 512, "tensor memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t pair_leader_addr(const void* local) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(cluster_ctarank() & ~1u));
+  return a;
+}
+
+// A box into this CTA's shared memory, completing on the leader's barrier.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+  if constexpr (FMT == kFp4E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// (Relaxed: what it hands over is tensor memory, ordered by the tcgen05 fences.)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// mbar_wait for a barrier that threads of both CTAs arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
+                                                  unsigned code) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait_cluster(a, parity) ||
+         (mbar_wait(bar, parity, abort, err, code) && mbar_try_wait_cluster(a, parity));
+}
+
+template <class C>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    fp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                         const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_ws,
+                         const __grid_constant__ CUtensorMap map_c, const Fp4Params p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+  const int tiles = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);  // the epilogue warps of both CTAs
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_as);
+    tma_prefetch_desc(&map_ws);
+    tma_prefetch_desc(&map_c);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int total = ((tiles - pair + pairs - 1) / pairs) * p.stages_k;  // stages of this pair's tiles
+      auto where = [&](int i, int& tile_m, int& tile_n, int& k) {
+        const int tile = pair + i / p.stages_k * pairs;
+        k = i % p.stages_k;
+        tile_m = tile % p.tiles_m;
+        tile_n = tile / p.tiles_m;
+      };
+      auto weights = [&](int i) {
+        int tm, tn, k;
+        where(i, tm, tn, k);
+        const int st = i % C::kStages;
+        const uint32_t at = smem_u32(smem + st * C::kStageBytes), bar = pair_leader_addr(&full[st]);
+        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kTxBytes);
+        tma_load_pair(at + kLaneBytes, &map_w, bar, k * 128, tn * kPairN + rank * 128);
+        for (int h = 0; h < 2; ++h)
+          tma_load_pair(at + C::kSfbAt + h * C::kSfBytes, &map_ws, bar, 0,
+                        (tn * 2 + h) * static_cast<int>(p.ktiles) + k * C::kTiles);
+      };
+      auto tokens = [&](int i) {
+        int tm, tn, k;
+        where(i, tm, tn, k);
+        const int st = i % C::kStages;
+        const uint32_t at = smem_u32(smem + st * C::kStageBytes), bar = pair_leader_addr(&full[st]);
+        tma_load_pair(at, &map_a, bar, k * 128, tm * 256 + rank * 128);
+        tma_load_pair(at + C::kSfaAt, &map_as, bar, 0, (tm * 2 + rank) * static_cast<int>(p.ktiles) + k * C::kTiles);
+      };
+      const int pre = total < C::kStages ? total : C::kStages;
+      for (int i = 0; i < pre; ++i) weights(i);
+      griddep_wait();
+      int i = 0;
+      for (; i < total; ++i) {
+        if (i >= pre) {
+          if (!mbar_wait(&empty[i % C::kStages], ((i / C::kStages) & 1) ^ 1, abort_flag, p.err, kDevErrTimeoutProducer))
+            break;
+          weights(i);
+        }
+        tokens(i);
+      }
+      // The MMAs have read the last stages (or, after a wait that gave up, the copies have landed).
+      for (int j = i > C::kStages ? i - C::kStages : 0; j < i; ++j) {
+        if (i == total) mbar_wait(&empty[j % C::kStages], (j / C::kStages) & 1, abort_flag, p.err, kDevErrTimeoutDrain);
+        else if (rank == 0) mbar_wait(&full[j % C::kStages], (j / C::kStages) & 1, nullptr, p.err, kDevErrTimeoutDrain);
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    const bool leader = elect_one_sync();
+    const uint32_t sf0 = tmem + kPairN;
+    bool ok = true;
+    int i = 0;
+    uint32_t turn = 0;
+    for (int tile = pair; ok && tile < tiles; tile += pairs, turn ^= 1) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty, turn ^ 1, abort_flag, p.err, kDevErrTimeoutMma))) break;
+      tc_fence_after_sync();
+      for (int k = 0; k < p.stages_k; ++k, ++i) {
+        const int st = i % C::kStages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::kStages) & 1, abort_flag, p.err, kDevErrTimeoutMma))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t at = smem_u32(smem + st * C::kStageBytes);
+        const uint64_t ad = sdesc_kmajor_sw128(at), bd = sdesc_kmajor_sw128(at + kLaneBytes);
+        const uint32_t sf = sf0 + static_cast<uint32_t>((i & 1) * C::kSfCols);
+        const int left = p.ksteps - k * 4;
+        if (leader) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= left) break;
+            const int t = C::FMT == kFp4E4M3 ? j : j / 2;
+            const uint32_t sfa = sf + static_cast<uint32_t>(12 * t), sfb = sfa + 4;
+            if (C::FMT == kFp4E4M3 || (j & 1) == 0) {
+              tmem_cp_scales_pair(sfa, sdesc_scale_tile(at + C::kSfaAt + t * kScaleTile));
+              tmem_cp_scales_pair(sfb, sdesc_scale_tile(at + C::kSfbAt + t * kScaleTile));
+              tmem_cp_scales_pair(sfb + 4, sdesc_scale_tile(at + C::kSfbAt + C::kSfBytes + t * kScaleTile));
+            }
+            mma_fp4_pair<C::FMT>(tmem, ad + 2 * j, bd + 2 * j,
+                                 idesc_fp4(256, kPairN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa, sfb,
+                                 k > 0 || j > 0 ? 1u : 0u);
+          }
+          mma_commit_pair(&empty[st]);
+          if (k + 1 == p.stages_k) mma_commit_pair(acc_full);
+        }
+        __syncwarp();
+      }
+    }
+    // Every MMA issued has ended before tensor memory is released.
+    if (leader) {
+      mma_commit_pair(drain);
+      mbar_wait(drain, 0, nullptr, p.err, kDevErrTimeoutDrain);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    griddep_wait();  // row scales of the tokens; the output may be the previous kernel's to read
+    const int w = warp - 4, q = warp & 3, half = w >> 2;
+    uint8_t* out = smem + C::kOutAt + w * 4096;
+    float* factors = reinterpret_cast<float*>(smem + C::kFactorsAt + half * 512);
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
+    const uint32_t hand_back = pair_leader_addr(acc_empty);
+    uint32_t turn = 0;
+    bool ok = true;
+    for (int tile = pair; tile < tiles; tile += pairs, turn ^= 1) {
+      const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+      const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32 + lane;
+      const int64_t col0 = static_cast<int64_t>(tn) * kPairN + half * 128;
+      float ag = 1.0f;
+      if (p.a_g) {
+        // The four warps of these columns bring 32 of their scales each.
+        const int64_t c = col0 + q * 32 + lane;
+        const float wg = c < p.N ? __ldg(p.w_g + c) : 0.0f;
+        if (row < p.M) ag = __ldg(p.a_g + row);
+        named_barrier_sync(1 + half, 128);  // the tile before has been multiplied
+        factors[q * 32 + lane] = wg;
+        named_barrier_sync(1 + half, 128);
+      }
+      // (After a wait that gave up the warps still meet at their barriers, and store nothing.)
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, turn, abort_flag, p.err, kDevErrTimeoutEpilogue));
+      if (!ok) continue;
+      tc_fence_after_sync();
+      uint32_t packed[64];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + c * 32, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+          if (p.a_g) {
+            const float4 g4 = *reinterpret_cast<const float4*>(factors + c * 32 + i * 4);
+            f[0] = ag * g4.x, f[1] = ag * g4.y, f[2] = ag * g4.z, f[3] = ag * g4.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[4 * i + 2 * j]) * f[2 * j],
+                                                           __uint_as_float(r[4 * i + 2 * j + 1]) * f[2 * j + 1]);
+            packed[c * 16 + i * 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(hand_back);
+      // 64 columns at a time through a swizzled box of 32 rows.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(out + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(packed[h * 32 + c * 4], packed[h * 32 + c * 4 + 1], packed[h * 32 + c * 4 + 2],
+                         packed[h * 32 + c * 4 + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < p.M && col0 + h * 64 < p.N) {  // (lane 0 has the box's first row)
+          tma_store_2d(&map_c, out, static_cast<int>(col0 + h * 64), static_cast<int>(row));
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+    tc_fence_before_sync();
+  }
+  __syncthreads();
+  cluster_sync();  // no CTA ends while its pair may still write into it
+  if (warp == 1) {
+    tc_fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
 
@@ -309,7 +628,72 @@ bool make_code_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles [tiles, 512 bytes] in boxes of box_tiles.
+bool make_scale_map(CUtensorMap* map, const void* base, uint64_t tiles, int box_tiles) {
+  EncodeTiledFn enc = fp4_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {kScaleTile / 4, tiles};
+  const cuuint64_t strides[1] = {kScaleTile};
+  const cuuint32_t box[2] = {kScaleTile / 4, static_cast<cuuint32_t>(box_tiles)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output [rows, cols] in boxes of 64 columns x 32 rows, 128-byte swizzled.
+bool make_out_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols) {
+  EncodeTiledFn enc = fp4_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
+
+template <int FMT>
+int launch_pair(const DevInfo* d, const void* a, const void* w, int64_t K, Fp4Params p, cudaStream_t stream) {
+  using C = PairCfg<FMT>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t set[kMaxDevices];
+  std::call_once(once[d->device], [&] {
+    set[d->device] = cudaFuncSetAttribute(fp4_gemm_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (set[d->device] != cudaSuccess) return FP8BLK_ERR_CUDA;
+  CUtensorMap ma, mw, mas, mws, mc;
+  const uint64_t at = static_cast<uint64_t>((p.M + 127) / 128 * p.ktiles), wt = static_cast<uint64_t>((p.N + 127) / 128 * p.ktiles);
+  if (!make_code_map(&ma, a, p.M, K / 2, 128) || !make_code_map(&mw, w, p.N, K / 2, 128) ||
+      !make_scale_map(&mas, p.a_s, at, C::kTiles) || !make_scale_map(&mws, p.w_s, wt, C::kTiles) ||
+      !make_out_map(&mc, p.c, p.M, p.N))
+    return FP8BLK_ERR_CUDA;
+  p.tiles_m = static_cast<int>((p.M + 255) / 256);
+  p.tiles_n = static_cast<int>((p.N + kPairN - 1) / kPairN);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n, pairs = d->sm_count / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, fp4_gemm_pair_kernel<C>, ma, mw, mas, mws, mc, p));
+}
+
+// Whether a product's sizes fit the pair kernel's 32-bit tile coordinates and its
+// output the vector stores.
+bool pair_fits(const Fp4Params& p) {
+  const int64_t tiles = (p.M + 255) / 256 * ((p.N + kPairN - 1) / kPairN);
+  return p.N % 8 == 0 && is_aligned(p.c, 16) && tiles * p.stages_k < int64_t{1} << 30 &&
+         (p.M + 255) / 128 * p.ktiles < int64_t{1} << 30 && (p.N + 255) / 128 * p.ktiles < int64_t{1} << 30;
+}
 
 template <class C>
 int launch_swapped(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, Fp4Params p, cudaStream_t stream) {
@@ -342,6 +726,10 @@ int launch_swapped(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& m
 
 template <int FMT>
 int run_fmt(const DevInfo* d, const void* a, const void* w, int64_t K, const Fp4Params& p, cudaStream_t stream) {
+#ifndef FP4_PAIR_MIN
+#define FP4_PAIR_MIN 256
+#endif
+  if (p.M >= FP4_PAIR_MIN && pair_fits(p)) return launch_pair<FMT>(d, a, w, K, p, stream);
   const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   CUtensorMap mw, ma;
   if (!make_code_map(&mw, w, p.N, K / 2, 128) || !make_code_map(&ma, a, p.M, K / 2, bn)) return FP8BLK_ERR_CUDA;
