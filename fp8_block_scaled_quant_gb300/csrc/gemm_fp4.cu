@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // take it out in bf16 registers, hand it back, and store from there while the next
 // tile is summed.
 //
-//   warp 0       producer: this CTA's operands, completing on the leader's barriers
+//   warps 0, 2   producers: this CTA's codes and scales, completing on the leader's barriers
 //   warp 1       MMA issuer (leader CTA); both allocate tensor memory
 //   warps 4-11   epilogue: lane quarter warp % 4, columns 128 (warp >= 8) on
 
@@ -424,45 +424,62 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
+    // Two producers: warp 0 the codes, warp 2 the scales (a thread that asks for
+    // all five boxes of a stage takes longer than the stage's MMAs).
+    const bool codes = warp == 0;
     if (lane == 0) {
-      const int total = ((tiles - pair + pairs - 1) / pairs) * p.stages_k;  // stages of this pair's tiles
-      auto where = [&](int i, int& tile_m, int& tile_n, int& k) {
-        const int tile = pair + i / p.stages_k * pairs;
-        k = i % p.stages_k;
-        tile_m = tile % p.tiles_m;
-        tile_n = tile / p.tiles_m;
+      // A cursor over this pair's stages; every CTA asks for the operands of its own half.
+      struct Cursor {
+        int tile, k, st, y_a, y_w;
+        uint32_t at, bar;
       };
-      auto weights = [&](int i) {
-        int tm, tn, k;
-        where(i, tm, tn, k);
-        const int st = i % C::kStages;
-        const uint32_t at = smem_u32(smem + st * C::kStageBytes), bar = pair_leader_addr(&full[st]);
-        if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kTxBytes);
-        tma_load_pair(at + kLaneBytes, &map_w, bar, k * 128, tn * kPairN + rank * 128);
-        for (int h = 0; h < 2; ++h)
-          tma_load_pair(at + C::kSfbAt + h * C::kSfBytes, &map_ws, bar, 0,
-                        (tn * 2 + h) * static_cast<int>(p.ktiles) + k * C::kTiles);
+      const uint32_t smem0 = smem_u32(smem), bar0 = pair_leader_addr(full);
+      const int ktiles = static_cast<int>(p.ktiles);
+      auto place = [&](Cursor& c) {  // at the head of a tile
+        const int tm = c.tile % p.tiles_m, tn = c.tile / p.tiles_m;
+        c.k = 0;
+        c.y_a = codes ? tm * 256 + rank * 128 : (tm * 2 + rank) * ktiles;
+        c.y_w = codes ? tn * kPairN + rank * 128 : tn * 2 * ktiles;
       };
-      auto tokens = [&](int i) {
-        int tm, tn, k;
-        where(i, tm, tn, k);
-        const int st = i % C::kStages;
-        const uint32_t at = smem_u32(smem + st * C::kStageBytes), bar = pair_leader_addr(&full[st]);
-        tma_load_pair(at, &map_a, bar, k * 128, tm * 256 + rank * 128);
-        tma_load_pair(at + C::kSfaAt, &map_as, bar, 0, (tm * 2 + rank) * static_cast<int>(p.ktiles) + k * C::kTiles);
-      };
-      const int pre = total < C::kStages ? total : C::kStages;
-      for (int i = 0; i < pre; ++i) weights(i);
-      griddep_wait();
-      int i = 0;
-      for (; i < total; ++i) {
-        if (i >= pre) {
-          if (!mbar_wait(&empty[i % C::kStages], ((i / C::kStages) & 1) ^ 1, abort_flag, p.err, kDevErrTimeoutProducer))
-            break;
-          weights(i);
+      auto advance = [&](Cursor& c) {
+        if (++c.st == C::kStages) c.st = 0, c.at = smem0, c.bar = bar0;
+        else c.at += C::kStageBytes, c.bar += 8;
+        if (++c.k == p.stages_k) {
+          c.tile += pairs;
+          place(c);
         }
-        tokens(i);
+      };
+      auto weights = [&](const Cursor& c) {
+        if (codes) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[c.st], 2 * C::kTxBytes);
+          tma_load_pair(c.at + kLaneBytes, &map_w, c.bar, c.k * 128, c.y_w);
+        } else {
+          tma_load_pair(c.at + C::kSfbAt, &map_ws, c.bar, 0, c.y_w + c.k * C::kTiles);
+          tma_load_pair(c.at + C::kSfbAt + C::kSfBytes, &map_ws, c.bar, 0, c.y_w + ktiles + c.k * C::kTiles);
+        }
+      };
+      auto tokens = [&](const Cursor& c) {
+        if (codes) tma_load_pair(c.at, &map_a, c.bar, c.k * 128, c.y_a);
+        else tma_load_pair(c.at + C::kSfaAt, &map_as, c.bar, 0, c.y_a + c.k * C::kTiles);
+      };
+      const int total = ((tiles - pair + pairs - 1) / pairs) * p.stages_k;
+      const int pre = total < C::kStages ? total : C::kStages;
+      Cursor c{pair, 0, 0, 0, 0, smem0, bar0};
+      place(c);
+      const Cursor head = c;
+      for (int i = 0; i < pre; ++i, advance(c)) weights(c);
+      griddep_wait();
+      c = head;
+      int i = 0;
+      uint32_t phase = 1;  // of the stages before they are filled again
+      for (; i < total; ++i, advance(c)) {
+        if (i >= pre) {
+          if (!mbar_wait(&empty[c.st], phase, abort_flag, p.err, kDevErrTimeoutProducer)) break;
+          weights(c);
+        }
+        tokens(c);
+        if (c.st == C::kStages - 1) phase ^= 1;
       }
       // The MMAs have read the last stages (or, after a wait that gave up, the copies have landed).
       for (int j = i > C::kStages ? i - C::kStages : 0; j < i; ++j) {
@@ -474,21 +491,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     const bool leader = elect_one_sync();
     const uint32_t sf0 = tmem + kPairN;
     bool ok = true;
-    int i = 0;
-    uint32_t turn = 0;
+    int st = 0;
+    uint32_t turn = 0, phase = 0, sf_turn = 0;
     for (int tile = pair; ok && tile < tiles; tile += pairs, turn ^= 1) {
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(acc_empty, turn ^ 1, abort_flag, p.err, kDevErrTimeoutMma))) break;
       tc_fence_after_sync();
-      for (int k = 0; k < p.stages_k; ++k, ++i) {
-        const int st = i % C::kStages;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::kStages) & 1, abort_flag, p.err, kDevErrTimeoutMma))) {
+      for (int k = 0; k < p.stages_k; ++k, sf_turn ^= 1) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], phase, abort_flag, p.err, kDevErrTimeoutMma))) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         const uint32_t at = smem_u32(smem + st * C::kStageBytes);
         const uint64_t ad = sdesc_kmajor_sw128(at), bd = sdesc_kmajor_sw128(at + kLaneBytes);
-        const uint32_t sf = sf0 + static_cast<uint32_t>((i & 1) * C::kSfCols);
+        const uint32_t sf = sf0 + sf_turn * C::kSfCols;
         const int left = p.ksteps - k * 4;
         if (leader) {
 #pragma unroll
@@ -509,6 +525,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           if (k + 1 == p.stages_k) mma_commit_pair(acc_full);
         }
         __syncwarp();
+        if (++st == C::kStages) st = 0, phase ^= 1;
       }
     }
     // Every MMA issued has ended before tensor memory is released.
