@@ -370,168 +370,56 @@ def fp4_scale_shape(rows: int, K: int, fmt: int = FP4_E4M3):
     return ((rows + 127) // 128, K // (64 if fmt == FP4_E4M3 else 128), 32, 4, 4)
 
 
-def _fault(name: str, t, dtype, shape=None, rows: bool = False):
-    """Raises for a tensor that is not what a call needs: its type, its shape, contiguity (rows: of its rows alone)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise Fp8BlkError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise Fp8BlkError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise Fp8BlkError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dim() != (2 if shape is None else len(shape)):
-        raise Fp8BlkError(f"{name} must be a matrix")
-    if rows and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise Fp8BlkError(f"{name}: the columns of a row must be contiguous")
-    if not rows and not t.is_contiguous():
-        raise Fp8BlkError(f"{name}: Input tensor must be contiguous")
-    raise Fp8BlkError("all tensors must be on one device")
+_bind = None
 
 
-# The checks below are one expression per tensor, and say what is wrong (_fault)
-# only where one fails: a small call is issued in little more than the launch takes.
-
-def _plain(t, dtype, shape, dev, name):
-    """t is contiguous, of this type and shape and on device dev."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        _fault(name, t, dtype, shape)
-
-
-def _rows(t, dtype, dev, name):
-    """(rows, columns, row stride) of a matrix on device dev whose rows are contiguous."""
-    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev or dev < 0:
-        _fault(name, t, dtype, rows=True)
-    rows, cols = t.shape
-    stride, one = t.stride()
-    if one != 1 and cols > 1:
-        _fault(name, t, dtype, rows=True)
-    return rows, cols, stride if rows > 1 else cols
-
-
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _raise_for(status: int, f, dev: int, what: str, args):
-    """A call that did not return 0, or was not made because its tensors are on another device than the current one."""
-    if status is None:
-        with torch.cuda.device(dev):
-            status = f(*args)
-    if status:
-        _check(status, what)
-
-
-def _call(f, dev: int, what: str, *args):
-    """The library's call, on the device of its tensors."""
-    status = f(*args) if _current_device() == dev else None
-    if status != 0:
-        _raise_for(status, f, dev, what, args)
-
-
-def _fp4_check(fmt):
-    if fmt != FP4_E4M3 and fmt != FP4_UE8M0:
-        raise Fp8BlkError("fmt must be FP4_E4M3 or FP4_UE8M0")
-
-
-def _fp4_operand(q, s, g, fmt, dev, name):
-    """(rows, K) of a 4-bit matrix."""
-    if q.dtype is not torch.uint8 or q.dim() != 2 or not q.is_contiguous() or q.get_device() != dev or dev < 0:
-        _fault(name, q, torch.uint8)
-    rows, half = q.shape
-    if half % 64:
-        raise Fp8BlkError(f"{name}: the columns must be a multiple of {BLOCK}")
-    if s.dtype is not torch.uint8 or s.numel() != (rows + 127) // 128 * (half // (32 if fmt == FP4_E4M3 else 64)) * 512 or \
-            not s.is_contiguous() or s.get_device() != dev:
-        _fault(name + "_s", s, torch.uint8, fp4_scale_shape(rows, 2 * half, fmt))
-    if fmt == FP4_E4M3:
-        if g is None:
-            raise Fp8BlkError(f"{name}_g: FP4_E4M3 needs row scales")
-        if g.dtype is not torch.float32 or g.dim() != 1 or g.shape[0] != rows or not g.is_contiguous() or \
-                g.get_device() != dev:
-            _fault(name + "_g", g, torch.float32, (rows,))
-    return rows, 2 * half
+def _native():
+    """The compiled part of this binding (csrc/bind.cpp): its calls check their tensors, allocate their outputs and call
+    the library in a few microseconds less than Python needs for that."""
+    global _bind
+    if _bind is None:
+        path = os.path.join(_PKG, "_bind.so")
+        if not os.path.exists(path):
+            raise Fp8BlkError(f"{path} is missing: build it with __graft_entry__.build() "
+                              "or python fp8_block_scaled_quant_gb300/_build.py")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__name__ + "._bind", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        names = ["fp8blk_status_string"] + [n for n in header_functions() if "fp4" in n or "residual_norm" in n]
+        m.setup({n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names}, Fp8BlkError, _ws_cache, _buffer)
+        _bind = m
+    return _bind
 
 
 def fp4_quant(x: torch.Tensor, fmt: int = FP4_E4M3):
     """x bf16 or float32 [M, K] (rows may be strided) -> (q uint8 [M, K/2], s uint8 scale tiles of fp4_scale_shape,
     g float32 [M]; g is None for FP4_UE8M0): e2m1 codes, low half first, with their block and row scales. The scale
     bytes of rows past M are not written."""
-    fp32 = x.dtype is torch.float32
-    at = x.get_device()
-    M, K, stride = _rows(x, torch.float32 if fp32 else torch.bfloat16, at, "x")
-    _fp4_check(fmt)
-    if K % BLOCK:
-        raise Fp8BlkError(f"Last dimension size must be divisible by block_size (block_size={BLOCK})")
-    dev = x.device
-    q = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-    s = torch.empty(fp4_scale_shape(M, K, fmt), dtype=torch.uint8, device=dev)
-    g = torch.empty(M, dtype=torch.float32, device=dev) if fmt == FP4_E4M3 else None
-    f = _bound.get("fp8blk_fp4_quant") or _function("fp8blk_fp4_quant", "peiiiepppp")
-    _call(f, at, "fp4_quant", x.data_ptr(), fp32, stride, M, K, fmt, q.data_ptr(), s.data_ptr(),
-          None if g is None else g.data_ptr(), _stream_on(x))
-    return q, s, g
+    return (_bind or _native()).fp4_quant(x, fmt)
 
 
 def fp4_dequant(q: torch.Tensor, s: torch.Tensor, g: torch.Tensor | None, fmt: int = FP4_E4M3,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """What fp4_quant gave -> bf16 [M, K]."""
-    at = q.get_device()
-    _fp4_check(fmt)
-    M, K = _fp4_operand(q, s, g, fmt, at, "q")
-    if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-    else:
-        _plain(out, torch.bfloat16, (M, K), at, "out")
-    f = _bound.get("fp8blk_fp4_dequant") or _function("fp8blk_fp4_dequant", "pppiiepp")
-    _call(f, at, "fp4_dequant", q.data_ptr(), s.data_ptr(), None if g is None else g.data_ptr(), M, K, fmt, out.data_ptr(),
-          _stream_on(q))
-    return out
+    return (_bind or _native()).fp4_dequant(q, s, g, fmt, out)
 
 
 def fp4_gemm(a: torch.Tensor, a_s: torch.Tensor, a_g: torch.Tensor | None, w: torch.Tensor, w_s: torch.Tensor,
              w_g: torch.Tensor | None, fmt: int = FP4_E4M3, out: torch.Tensor | None = None) -> torch.Tensor:
     """Two 4-bit matrices as fp4_quant gives them, a [M, K] and w [N, K] -> bf16 [M, N] = a w^T."""
-    at = a.get_device()
-    _fp4_check(fmt)
-    M, K = _fp4_operand(a, a_s, a_g, fmt, at, "a")
-    N, kw = _fp4_operand(w, w_s, w_g, fmt, at, "w")
-    if kw != K:
-        raise Fp8BlkError("a and w must share K")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
-    else:
-        _plain(out, torch.bfloat16, (M, N), at, "out")
-    f = _bound.get("fp8blk_fp4_gemm") or _function("fp8blk_fp4_gemm", "pppppppiiiep")
-    _call(f, at, "fp4_gemm", a.data_ptr(), a_s.data_ptr(), None if a_g is None else a_g.data_ptr(), w.data_ptr(),
-          w_s.data_ptr(), None if w_g is None else w_g.data_ptr(), out.data_ptr(), M, N, K, fmt, _stream_on(a))
-    return out
+    return (_bind or _native()).fp4_gemm(a, a_s, a_g, w, w_s, w_g, fmt, out)
 
 
 def fp4_linear_workspace_bytes(M: int, N: int, K: int, fmt: int = FP4_E4M3) -> int:
-    f = _bound.get("fp8blk_fp4_linear_workspace_bytes") or \
-        _function("fp8blk_fp4_linear_workspace_bytes", "iiie", ctypes.c_size_t)
-    return f(M, N, K, fmt)
+    return int(_function("fp8blk_fp4_linear_workspace_bytes", "iiie", ctypes.c_size_t)(M, N, K, fmt))
 
 
 def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, w_g: torch.Tensor | None, fmt: int = FP4_E4M3,
                out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """FP4 linear layer: fp4_gemm(fp4_quant(x), w). x bf16 [M, K] (rows may be strided) -> bf16 [M, N]. ws: a workspace
     of fp4_linear_workspace_bytes, 256-byte aligned, any contents, used by one stream at a time."""
-    at = x.get_device()
-    _fp4_check(fmt)
-    M, K, stride = _rows(x, torch.bfloat16, at, "x")
-    N, kw = _fp4_operand(w, w_s, w_g, fmt, at, "w")
-    if kw != K:
-        raise Fp8BlkError("x and w must share K")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        _plain(out, torch.bfloat16, (M, N), at, "out")
-    stream = _stream_on(x)
-    scratch, room, held = _scratch(ws, 0 if ws is not None else fp4_linear_workspace_bytes(M, N, K, fmt), x, stream,
-                                   "fp4_linear", 0)
-    f = _bound.get("fp8blk_fp4_linear") or _function("fp8blk_fp4_linear", "pippppiiiepzp")
-    _call(f, at, "fp4_linear", x.data_ptr(), stride, w.data_ptr(), w_s.data_ptr(), None if w_g is None else w_g.data_ptr(),
-          out.data_ptr(), M, N, K, fmt, scratch, room, stream)
-    return out
+    return (_bind or _native()).fp4_linear(x, w, w_s, w_g, fmt, out, ws)
 
 
 def residual_norm(y: torch.Tensor, x: torch.Tensor | None, norm_w: torch.Tensor, post_w: torch.Tensor | None = None,
@@ -542,59 +430,7 @@ def residual_norm(y: torch.Tensor, x: torch.Tensor | None, norm_w: torch.Tensor,
     [D], gate float32 [D] or bf16 [T, D]. Returns (r bf16 [T, D], h): h is bf16 [T, D], or with quant="fp8"
     act_quant's (q, s) of it (scale_fmt SCALE_*), or with quant="fp4" fp4_quant's (q, s, g) of it (scale_fmt FP4_*).
     r may be given; it may be x or y itself. fp32 until each output's one rounding."""
-    at = y.get_device()
-    T, D, y_stride = _rows(y, torch.bfloat16, at, "y")
-    _plain(norm_w, torch.float32, (D,), at, "norm_w")
-    x_at, x_stride, col_at, tok_at, tok_stride = None, D, None, None, D
-    if x is not None:
-        rows, cols, x_stride = _rows(x, torch.bfloat16, at, "x")
-        if cols != D or rows != T:
-            raise Fp8BlkError("x and y must have one shape")
-        x_at = x.data_ptr()
-    if post_w is not None:
-        _plain(post_w, torch.float32, (D,), at, "post_w")
-    if gate is not None:
-        if gate.dim() == 1:
-            _plain(gate, torch.float32, (D,), at, "gate")
-            col_at = gate.data_ptr()
-        else:
-            rows, cols, tok_stride = _rows(gate, torch.bfloat16, at, "gate")
-            if cols != D or rows != T:
-                raise Fp8BlkError("gate must be float32 [D] or bf16 [T, D]")
-            tok_at = gate.data_ptr()
-    dev = y.device
-    if r is None:
-        r = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    else:
-        _plain(r, torch.bfloat16, (T, D), at, "r")
-    s_at = g_at = None
-    if quant is None:
-        kind = 0
-        out = h = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    elif D % BLOCK:
-        raise Fp8BlkError(f"Last dimension size must be divisible by block_size (block_size={BLOCK})")
-    elif quant == "fp8":
-        kind = 1
-        h = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=dev)
-        s = torch.empty((T, D // BLOCK), dtype=torch.float32, device=dev)
-        out, s_at = (h, s), s.data_ptr()
-    elif quant == "fp4":
-        kind = 2
-        _fp4_check(scale_fmt)
-        h = torch.empty((T, D // 2), dtype=torch.uint8, device=dev)
-        s = torch.empty(fp4_scale_shape(T, D, scale_fmt), dtype=torch.uint8, device=dev)
-        g = None
-        if scale_fmt == FP4_E4M3:
-            g = torch.empty(T, dtype=torch.float32, device=dev)
-            g_at = g.data_ptr()
-        out, s_at = (h, s, g), s.data_ptr()
-    else:
-        raise Fp8BlkError('quant must be None, "fp8" or "fp4"')
-    f = _bound.get("fp8blk_residual_norm") or _function("fp8blk_residual_norm", "pipipppifpfiieeppppp")
-    _call(f, at, "residual_norm", y.data_ptr(), y_stride, x_at, x_stride, None if post_w is None else post_w.data_ptr(),
-          col_at, tok_at, tok_stride, residual_scale, norm_w.data_ptr(), eps, T, D, kind, scale_fmt, r.data_ptr(),
-          h.data_ptr(), s_at, g_at, _stream_on(y))
-    return r, out
+    return (_bind or _native()).residual_norm(y, x, norm_w, post_w, gate, residual_scale, eps, quant, scale_fmt, r)
 
 
 # ---- SwiGLU FFN and routed experts -------------------------------------------

@@ -18,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8blk.so")
+BIND = os.path.join(PKG, "_bind.so")
 BUILD = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,6 +50,20 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def bind_command(out: str) -> list[str]:
+    """Compiles the native part of the Python binding against the installed torch."""
+    import sysconfig
+
+    import torch
+    inc, lib = (os.path.join(os.path.dirname(torch.__file__), d) for d in ("include", "lib"))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", inc,
+            "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(cuda, "include"), os.path.join(CSRC, "bind.cpp"), "-o", out,
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -69,8 +84,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(r.stdout, r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    def compile_bind():
+        if force or _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "fp8blk.h")]):
+            tmp = BIND + f".tmp{os.getpid()}"
+            r = subprocess.run(bind_command(tmp), capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, BIND)
+
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        bind = ex.submit(compile_bind)
         list(ex.map(compile_one, zip(srcs, objs)))
+        bind.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]

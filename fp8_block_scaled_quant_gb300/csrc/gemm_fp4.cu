@@ -722,7 +722,11 @@ int launch_swapped(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& m
   if (set[d->device] != cudaSuccess) return FP8BLK_ERR_CUDA;
   const int64_t tiles = p.tiles_n * ((p.M + C::BN - 1) / C::BN);
   int ks = 1;
+#ifdef FP4_KS
+  while (ks < FP4_KS && ks < p.stages_k) ++ks;
+#else
   while (ks < 8 && ks < p.stages_k && tiles * (ks + 1) <= 2 * d->sm_count) ++ks;
+#endif
   if (tiles * ks >= int64_t{1} << 31) return FP8BLK_ERR_SHAPE;
   p.ksplit = ks;
   cudaLaunchConfig_t cfg = {};
