@@ -33,7 +33,7 @@ namespace fp8blk {
 
 bool fp4_fmt_valid(int fmt);
 int fp4_quant_launch(const void* x, bool fp32, int64_t x_stride, int64_t M, int64_t K, int fmt, void* q, void* s, float* g,
-                     cudaStream_t stream);
+                     int sm_count, cudaStream_t stream);
 
 namespace {
 
@@ -848,7 +848,7 @@ extern "C" int fp8blk_fp4_linear(const void* x_bf16, int64_t x_stride, const voi
   uint8_t* q = static_cast<uint8_t*>(workspace);
   uint8_t* qs = q + align256(static_cast<size_t>(M) * (K / 2));
   float* g = reinterpret_cast<float*>(qs + align256(static_cast<size_t>(fp4_scale_bytes(M, K, fmt))));
-  if (int st = fp4_quant_launch(x_bf16, false, x_stride, M, K, fmt, q, qs, g, s)) return st;
+  if (int st = fp4_quant_launch(x_bf16, false, x_stride, M, K, fmt, q, qs, g, d->sm_count, s)) return st;
   const bool rows = fmt == kFp4E4M3;
   return gemm_checked(d, q, qs, rows ? g : nullptr, w, w_s, rows ? w_g : nullptr, y_bf16, M, N, K, fmt, s);
 }

@@ -500,7 +500,7 @@ FP8BLK_API int fp8blk_fp4_quant(const void *x, int is_fp32, int64_t x_stride, in
                                 void *s, float *g, fp8blk_stream_t stream);
 
 /* out[m, k] = bf16(q * s * g) (E4M3; q * s is exact, one fp32 multiply) or
- * bf16(q * s) (UE8M0). out: bf16 [M, K], 16-byte aligned. */
+ * bf16(q * s) (UE8M0). out: bf16 [M, K], 32-byte aligned. */
 FP8BLK_API int fp8blk_fp4_dequant(const void *q, const void *s, const float *g, int64_t M, int64_t K, int fmt,
                                   void *out_bf16, fp8blk_stream_t stream);
 
