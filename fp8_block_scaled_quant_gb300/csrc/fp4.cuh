@@ -120,48 +120,35 @@ __device__ __forceinline__ uint8_t fp4_block_scale_ue8m0(uint32_t amax_bits, flo
   return static_cast<uint8_t>(e);
 }
 
-// v[0..7] times mul, as 8 codes. mul == 0 (a block of zeros or one that is not
-// finite) gives zero codes whatever v holds.
-__device__ __forceinline__ uint32_t e2m1x8_scaled(const float* v, float mul) {
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = mul == 0.0f ? 0.0f : __fmul_rn(v[i], mul);
-  return e2m1x8(y);
-}
-
-__device__ __forceinline__ uint32_t amax8(const float* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  return m;
-}
-
-// Quantises a row's columns 8 vec .. 8 vec + 7, of a warp whose lanes have
-// consecutive vecs (lane 0 a multiple of 32) and call it together: a block's amax
-// and a scale word are put together from 2 and 8 (e4m3) or 4 and 16 lanes.
-// Lanes with vec >= vecs store nothing; their v is zeros.
+// Quantises a row's columns 16 unit .. 16 unit + 15, of a warp whose lanes have
+// consecutive units (lane 0 a multiple of 32) and call it together: a scale word
+// is put together from the lanes of its four blocks. Lanes with unit >= units
+// store nothing. amax: the bits of the unit's largest |v|.
 template <int FMT>
-__device__ __forceinline__ void fp4_store8(const float* v, uint32_t amax, const RowScale& rs, int64_t row, int vec,
-                                           int vecs, uint32_t* q, uint8_t* s, int64_t ktiles) {
+__device__ __forceinline__ void fp4_store16(const float2* v, uint32_t amax, const RowScale& rs, int64_t row, int unit,
+                                            int units, uint2* q, uint8_t* s, int64_t ktiles) {
   const uint32_t lane = threadIdx.x & 31;
   float mul;
   uint32_t word;
-  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   if constexpr (FMT == kFp4E4M3) {
-    word = static_cast<uint32_t>(fp4_block_scale_e4m3(amax, rs, &mul)) << (8 * ((lane >> 1) & 3));
+    word = static_cast<uint32_t>(fp4_block_scale_e4m3(amax, rs, &mul)) << (8 * (lane & 3));
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+  } else {
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    word = static_cast<uint32_t>(fp4_block_scale_ue8m0(amax, &mul)) << (8 * ((lane >> 1) & 3));
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  } else {
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    word = static_cast<uint32_t>(fp4_block_scale_ue8m0(amax, &mul)) << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
   }
-  if (vec >= vecs) return;
-  q[row * vecs + vec] = e2m1x8_scaled(v, mul);
-  constexpr int kPer = FMT == kFp4E4M3 ? 8 : 16;  // lanes of a scale word
-  if ((vec & (kPer - 1)) == 0)
-    *reinterpret_cast<uint32_t*>(s + fp4_scale_at(row, vec / (kPer / 4), ktiles)) = word;
+  if (unit >= units) return;
+  float2 y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(v[i], make_float2(mul, mul));
+  // mul == 0: a block of zeros, or one that is not finite
+  q[row * units + unit] = mul == 0.0f ? make_uint2(0, 0) : make_uint2(e2m1x8(&y[0].x), e2m1x8(&y[4].x));
+  constexpr int kPer = FMT == kFp4E4M3 ? 4 : 8;  // lanes of a scale word
+  if ((unit & (kPer - 1)) == 0)
+    *reinterpret_cast<uint32_t*>(s + fp4_scale_at(row, unit / (kPer / 4), ktiles)) = word;
 }
 
 // ---- tensor cores -------------------------------------------------------------

@@ -82,33 +82,13 @@ struct Unit<float> {
   }
 };
 
-// The codes and the scale byte of a unit; a scale word is put together from the
-// lanes of four blocks, which call this together.
 template <int FMT, typename T>
 __device__ __forceinline__ void store_unit(const QuantParams& p, int64_t row, int unit, const Unit<T>& x, uint32_t amax,
                                            const RowScale& rs) {
-  const uint32_t lane = threadIdx.x & 31;
-  float mul;
-  uint32_t word;
-  if constexpr (FMT == kFp4E4M3) {
-    word = static_cast<uint32_t>(fp4_block_scale_e4m3(amax, rs, &mul)) << (8 * (lane & 3));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-  } else {
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    word = static_cast<uint32_t>(fp4_block_scale_ue8m0(amax, &mul)) << (8 * ((lane >> 1) & 3));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-  }
-  if (unit >= p.units) return;
-  float2 y[8];
+  float2 v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fmul2_rn(x.pair(i), make_float2(mul, mul));
-  // mul == 0: a block of zeros, or one that is not finite
-  p.q[row * p.units + unit] = mul == 0.0f ? make_uint2(0, 0) : make_uint2(e2m1x8(&y[0].x), e2m1x8(&y[4].x));
-  constexpr int kPer = FMT == kFp4E4M3 ? 4 : 8;
-  if ((unit & (kPer - 1)) == 0)
-    *reinterpret_cast<uint32_t*>(p.s + fp4_scale_at(row, unit / (kPer / 4), p.ktiles)) = word;
+  for (int i = 0; i < 8; ++i) v[i] = x.pair(i);
+  fp4_store16<FMT>(v, amax, rs, row, unit, p.units, p.q, p.s, p.ktiles);
 }
 
 // P passes of p.threads units stay in registers.
@@ -252,11 +232,11 @@ int fp4_quant_launch(const void* x, bool fp32, int64_t x_stride, int64_t M, int6
   p.wide = is_aligned(x, 32) && x_stride * (fp32 ? 4 : 2) % 32 == 0;
   // Up to 128 bytes of a row to a thread, which are under way together (4096 x 7168
   // bf16: 14.5 us; 64 bytes 15.8, 32 bytes 21; 18432 x 7168 fp32: 90, of 256 bytes
-  // 95), as long as that leaves 16 warps to an SM (1407 x 2048 bf16: 3.5 us, of 128
+  // 95), as long as that leaves 24 warps to an SM (1407 x 2048 bf16: 3.5 us, of 128
   // bytes to a thread 4.2); more where the row is longer than 512 threads have.
   const auto warps = [&](int P) { return M * ((p.units + 32 * P - 1) / (32 * P)); };
   int P = 1;
-  while (P < (fp32 ? 2 : 4) && warps(2 * P) >= 16 * sm_count) P *= 2;
+  while (P < (fp32 ? 2 : 4) && p.units > 32 * P && warps(2 * P) >= 24 * sm_count) P *= 2;
   while (P < 6 && (p.units + P - 1) / P > kMaxThreads) P = P == 4 ? 6 : 2 * P;
   p.threads = ((p.units + P - 1) / P + 31) / 32 * 32;
   if (p.threads > kMaxThreads) p.threads = kMaxThreads;

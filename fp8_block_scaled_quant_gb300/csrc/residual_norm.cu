@@ -7,19 +7,13 @@
 //   h = r * rsqrt(mean(r^2) + eps) * norm_w    -> bf16, or act_quant, or fp4_quant
 //
 // fp32 from the inputs to the one rounding of each output (the norm reads r
-// before it is rounded). One block of threads to a token, 8 columns to a thread
-// and vector, so that a warp reads and writes whole lines; the row stays in
-// registers from the first read to the last write. A few tokens have a block
-// each, which reads its row from memory; launch and the block-wide sums bound
-// them. More tokens than SMs go round over one block per SM: groups of its
-// threads have a token each, whose rows come into shared memory by bulk copies
-// while the group works on the one before; the columns' factors lie there too
-// (read from L2 for each token they would be as many bytes as the token's rows).
+// before it is rounded). One block of threads to a token, 16 columns to a thread
+// and unit (a quantisation block of e2m1, an eighth of one of e4m3), the row in
+// registers from the first read to the last write. HBM bounds many tokens, launch
+// and two block-wide sums a single one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <mutex>
 
 #include "block_rule.cuh"
 #include "fp4.cuh"
@@ -33,83 +27,140 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxCols = 16384;
-constexpr int kGroupThreads = 1024;       // of a block of groups
-constexpr int kMaxGroups = kGroupThreads / 32;
-constexpr int kSharedBytes = 224 * 1024;  // factors and slots of a block of groups
 
 // What h is written as.
 enum : int { kOutBf16 = 0, kOutE4m3 = 1, kOutFp4E4M3 = 2, kOutFp4UE8M0 = 3 };
 
 struct NormParams {
   const __nv_bfloat16* y;
-  const __nv_bfloat16* x;   // null: no residual
-  const float* post_w;      // null: no norm of y
-  const float* gate_col;    // null, or one factor per column
+  const __nv_bfloat16* x;         // null: no residual
+  const float* post_w;            // null: no norm of y
+  const float* gate_col;          // null, or one factor per column
   const __nv_bfloat16* gate_tok;  // null, or one factor per token and column
   const float* norm_w;
-  __nv_bfloat16* r;         // null: not written
+  __nv_bfloat16* r;               // null: not written
   void* h;
-  void* h_s;                // e4m3: fp32 scales; e2m1: scale tiles
-  float* h_g;               // e2m1 with e4m3 scales: row scales
-  int64_t rows, y_stride, x_stride, gate_stride, ktiles;
+  void* h_s;                      // e4m3: fp32 scales; e2m1: scale tiles
+  float* h_g;                     // e2m1 with e4m3 scales: row scales
+  int64_t y_stride, x_stride, gate_stride, ktiles;
   float residual_scale, eps, inv_n;
-  unsigned* err;
-  int vecs;  // columns / 8
-  int group, slots;  // blocks of groups: a group's threads and slots
+  int cols, units;                // units: ceil(cols / 16)
+  int ahead;                      // tokens between a row and the one prefetched
   int ue8m0;
 };
 
-// Columns are worked on in pairs (packed fp32 multiplies and FMAs: half the instructions).
-__device__ __forceinline__ void unpack8(const uint4& a, float2* v) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 16 columns of a bf16 row, as they are read: at once where WIDE (all rows and
+// factors aligned to 32 bytes, cols a multiple of 16), else by halves, the second
+// where it is within `cols` (a multiple of 8). Columns past the row are zeros.
+template <bool WIDE>
+__device__ __forceinline__ void read16(const __nv_bfloat16* row, int unit, int cols, bool in, uint32_t* w) {
+  const __nv_bfloat16* p = row + unit * 16;
+  if constexpr (WIDE) {
+    if (in) {
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p)
+                   : "memory");
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      for (int i = 0; i < 8; ++i) w[i] = 0;
+    }
+  } else {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 a = in ? *reinterpret_cast<const uint4*>(p) : zero;
+    const uint4 b = in && unit * 16 + 8 < cols ? *reinterpret_cast<const uint4*>(p + 8) : zero;
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
 }
 
-__device__ __forceinline__ uint4 pack8(const float2* v) {
-  uint32_t w[4];
+// The same of fp32 factors (which stay in L1: every token reads them).
+template <bool WIDE>
+__device__ __forceinline__ void read16(const float* row, int unit, int cols, float2* v) {
+  const float* p = row + unit * 16;
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int h = 0; h < 2; ++h)
+      asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=f"(v[4 * h].x), "=f"(v[4 * h].y), "=f"(v[4 * h + 1].x), "=f"(v[4 * h + 1].y), "=f"(v[4 * h + 2].x),
+            "=f"(v[4 * h + 2].y), "=f"(v[4 * h + 3].x), "=f"(v[4 * h + 3].y)
+          : "l"(p + 8 * h));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = unit * 16 + 4 * i < cols ? __ldg(reinterpret_cast<const float4*>(p) + i) : make_float4(0, 0, 0, 0);
+      v[2 * i] = make_float2(a.x, a.y);
+      v[2 * i + 1] = make_float2(a.z, a.w);
+    }
+  }
+}
+
+// Columns are worked on in pairs (packed fp32 multiplies and FMAs).
+__device__ __forceinline__ float2 pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void write16(__nv_bfloat16* row, int unit, int cols, const float2* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 b = __float22bfloat162_rn(v[i]);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  __nv_bfloat16* p = row + unit * 16;
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (unit * 16 + 8 < cols) reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
-__device__ __forceinline__ void load8(const float* row, int vec, float2* v) {
-  const float4* src = reinterpret_cast<const float4*>(row) + 2 * vec;
-  const float4 a = __ldg(src), b = __ldg(src + 1);
-  v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
-  v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+// A value combined over the block by f, the same in every thread: lanes, then
+// warps in order. `at`: a place per warp, not used before.
+template <typename T, typename F>
+__device__ __forceinline__ T block_reduce(T v, T none, T* at, F f) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if (warps == 1) return v;
+  if (lane == 0) at[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? at[lane] : none;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));  // at most 16 warps
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
 }
 
-// The threads that have a token: a block, or a group of a block's warps.
-struct Group {
-  int id, tid, n;  // which group, the thread in it, its threads
+__device__ __forceinline__ float block_sum(float v, float* at) {
+  return block_reduce(v, 0.0f, at, [](float a, float b) { return a + b; });
+}
 
-  __device__ __forceinline__ void sync() const {
-    if (n == 32) __syncwarp();
-    else named_barrier_sync(1 + id, n);
-  }
-  // Lanes, then warps in order: the same result in every thread. `at`: where the
-  // warps' values meet, not used by the sum before.
-  template <typename T, typename F>
-  __device__ __forceinline__ T reduce(T v, T none, float* at, F f) const {
+// Four sums over the block at once. In a warp each of the first two exchanges
+// halves the values that a lane goes on with: lanes 8 k .. 8 k + 7 end with sum k.
+__device__ __forceinline__ float4 block_sum4(float4 v, float* at) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, k = lane >> 3;
+  float a = k & 2 ? v.z : v.x, b = k & 2 ? v.w : v.y;
+  a += __shfl_xor_sync(0xFFFFFFFFu, k & 2 ? v.x : v.z, 16);
+  b += __shfl_xor_sync(0xFFFFFFFFu, k & 2 ? v.y : v.w, 16);
+  float s = k & 1 ? b : a;
+  s += __shfl_xor_sync(0xFFFFFFFFu, k & 1 ? a : b, 8);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    if (n == 32) return v;
-    T* w = reinterpret_cast<T*>(at);
-    if ((tid & 31) == 0) w[tid >> 5] = v;
-    sync();
-    v = (tid & 31) < (n >> 5) ? w[tid & 31] : none;
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (warps > 1) {
+    if ((lane & 7) == 0) at[(threadIdx.x >> 5) * 4 + k] = s;
+    __syncthreads();
+    const int w = lane & 7;  // and w + 8: at most 16 warps
+    s = (w < warps ? at[w * 4 + k] : 0.0f) + (w + 8 < warps ? at[(w + 8) * 4 + k] : 0.0f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   }
-  __device__ __forceinline__ float sum(float v, float* at) const {
-    return reduce(v, 0.0f, at, [](float a, float b) { return a + b; });
-  }
-};
+  return make_float4(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 8), __shfl_sync(0xFFFFFFFFu, s, 16),
+                     __shfl_sync(0xFFFFFFFFu, s, 24));
+}
 
 // 1 / sqrt(a): the hardware's estimate and one Newton step, y (1 + (1 - a y^2) / 2).
 __device__ __forceinline__ float root_inverse(float a) {
@@ -117,22 +168,27 @@ __device__ __forceinline__ float root_inverse(float a) {
   return fabsf(e) < 1.0f ? fmaf(0.5f * y, e, y) : y;  // (a = 0, infinity, NaN: as the estimate is)
 }
 
-// 1 / sqrt(mean of v^2 + eps) over the group's row. Squares that overflow fp32 (a
+// 1 / sqrt(mean of v^2 + eps) over the block's row. Squares that overflow fp32 (a
 // row near 2^60), or that vanish where eps does not hide it, are summed again
-// with v times a power of two; the sum is the same in all threads, so they turn
-// together. each(f) calls f on the thread's pairs.
-template <typename Each>
-__device__ __forceinline__ float rms_factor(const Group& g, float inv_n, float eps, float* at, Each each) {
+// with v times a power of two; the sum is the same in all threads, so they turn together.
+template <int P>
+__device__ __forceinline__ float rms_factor(const float2 (&v)[P][8], float inv_n, float eps, float* at) {
   float2 two = make_float2(0.0f, 0.0f);
-  each([&](float2 v) { two = __ffma2_rn(v, v, two); });
-  float sum = g.sum(two.x + two.y, at);
+#pragma unroll
+  for (int u = 0; u < P; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) two = __ffma2_rn(v[u][i], v[u][i], two);
+  float sum = block_sum(two.x + two.y, at);
   const bool huge = sum == __uint_as_float(0x7F800000u);
   if (huge || (sum < 7.9e-31f && eps < 8.7e-19f)) {  // 2^-100, 2^-60
     const float s = __uint_as_float(huge ? (127u - 80u) << 23 : (127u + 60u) << 23);
     sum = 0.0f;
-    each([&](float2 v) { sum = fmaf(v.x * s, v.x * s, fmaf(v.y * s, v.y * s, sum)); });
-    g.sync();  // every warp has read the first sums
-    return root_inverse(fmaf(g.sum(sum, at), inv_n, eps * s * s)) * s;
+#pragma unroll
+    for (int u = 0; u < P; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(v[u][i].x * s, v[u][i].x * s, fmaf(v[u][i].y * s, v[u][i].y * s, sum));
+    __syncthreads();  // every warp has read the first sums
+    return root_inverse(fmaf(block_sum(sum, at), inv_n, eps * s * s)) * s;
   }
   return root_inverse(fmaf(sum, inv_n, eps));
 }
@@ -157,298 +213,242 @@ __device__ __forceinline__ float scale_inverse(float s) {
   return fmaf(fmaf(-s, r, 1.0f), r, r);
 }
 
-__device__ __forceinline__ uint4 load_vec(const __nv_bfloat16* row, int vec, bool in) {
-  return in ? __ldcs(reinterpret_cast<const uint4*>(row) + vec) : make_uint4(0, 0, 0, 0);
+// A row's factor k goes onto its values after the columns' factors, where it is
+// cheaper; before them where they might not stand without it (values near the ends
+// of fp32's range).
+template <int P>
+__device__ __forceinline__ float apply_early(float2 (&v)[P][8], float k) {
+  if (k > 1e-15f && k < 1e15f) return k;
+#pragma unroll
+  for (int u = 0; u < P; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], make_float2(k, k));
+  return 1.0f;
 }
 
-// The factors of vector `vec`'s columns in z.
-__device__ __forceinline__ void z_factors(const NormParams& p, int vec, float2* c) {
+// The largest of |v| of 16 columns. KEEP_NAN: a NaN is above all.
+template <bool KEEP_NAN>
+__device__ __forceinline__ float amax16(const float2* v) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = make_float2(1.0f, 1.0f);
-  if (p.post_w) load8(p.post_w, vec, c);
-  if (p.gate_col) {
-    float2 w[4];
-    load8(p.gate_col, vec, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = __fmul2_rn(c[i], w[i]);
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (KEEP_NAN) asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v[i].x), "f"(v[i].y));
+    else asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v[i].x), "f"(v[i].y));
   }
+  return m;
 }
 
-// h of a vector (in all lanes of a warp; those with vec >= p.vecs have zeros and store nothing), written as OUT says.
-template <int OUT>
-__device__ __forceinline__ void store_h(const NormParams& p, int64_t row, int vec, const float2* h, const RowScale& rs) {
-  if constexpr (OUT == kOutBf16) {
-    if (vec < p.vecs) reinterpret_cast<uint4*>(p.h)[row * p.vecs + vec] = pack8(h);
-  } else if constexpr (OUT == kOutE4m3) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(h[i].x), fabsf(h[i].y)));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));  // 16 lanes: 128 columns
-    if (vec >= p.vecs) return;
-    const float s = e4m3_scale(m, p.ue8m0 != 0), ri = scale_inverse(s);
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 d = __fmul2_rn(h[i], make_float2(ri, ri));
-      q[i] = e4m3x2(d.x, d.y);
-    }
-    reinterpret_cast<uint2*>(p.h)[row * p.vecs + vec] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-    if ((threadIdx.x & 15) == 0) static_cast<float*>(p.h_s)[row * (p.vecs / 16) + vec / 16] = s;
-  } else {
-    fp4_store8<OUT == kOutFp4E4M3 ? kFp4E4M3 : kFp4UE8M0>(&h[0].x, amax8(&h[0].x), rs, row, vec, p.vecs,
-                                                          static_cast<uint32_t*>(p.h), static_cast<uint8_t*>(p.h_s),
-                                                          p.ktiles);
-  }
+// Asks for `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// The scale of the row whose largest |h| in this thread is `top`.
-__device__ __forceinline__ RowScale row_scale(const NormParams& p, const Group& g, int64_t row, uint32_t top, float* at) {
-  const RowScale rs = fp4_row_scale(g.reduce(top, 0u, at, [](uint32_t a, uint32_t b) { return max(a, b); }));
-  if (g.tid == 0) p.h_g[row] = rs.g;
-  return rs;
-}
-
-// A block to a token, V vectors to a thread.
-template <int OUT, int V>
-__global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(const NormParams p) {
-  __shared__ float part[3][32];
+// A block to a token, P units to a thread. EARLY: norm_w is asked for with the rows
+// (few tokens); otherwise where it is used, from L1, which keeps registers free
+// for another block to an SM (4099 x 7168 with a norm of y, into e4m3: 50.7 us with
+// two blocks of 448 threads at 72 registers, 47.6 with the next rows prefetched;
+// 55 with two units to a thread, rows through shared memory 49 to 57: the blocks'
+// arithmetic between their loads, not HBM, sets the time then).
+template <int OUT, int P, bool WIDE, bool EARLY>
+__global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(const NormParams p) {
+  constexpr int kWarps = kMaxThreads / 32;
+  __shared__ float sums[4 * kWarps], sum_y[kWarps], sum_r[kWarps], tops[kWarps];
   griddep_launch_dependents();
   griddep_wait();
-  const Group g{0, static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x)};
+  const int tid = threadIdx.x, n = blockDim.x;
   const int64_t row = blockIdx.x;
   const bool has_x = p.x != nullptr, tok = p.gate_tok != nullptr;
-  uint4 y[V], x[V], gate[V];
-  float2 v[V][4], c[V][4], nw[V][4];
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int vec = g.tid + u * g.n;
-    const bool in = vec < p.vecs;
-    y[u] = load_vec(p.y + row * p.y_stride, vec, in);
-    x[u] = load_vec(p.x + row * p.x_stride, vec, in && has_x);
-    gate[u] = load_vec(p.gate_tok + row * p.gate_stride, vec, in && tok);
-    z_factors(p, in ? vec : 0, c[u]);
-    load8(p.norm_w, in ? vec : 0, nw[u]);
+  if (!EARLY && tid == 0 && row + p.ahead < gridDim.x) {
+    // The rows that a block will read when this one's place is free again, into L2.
+    const uint32_t bytes = static_cast<uint32_t>(p.cols) * 2;
+    prefetch_l2(p.y + (row + p.ahead) * p.y_stride, bytes);
+    if (has_x) prefetch_l2(p.x + (row + p.ahead) * p.x_stride, bytes);
+    if (tok) prefetch_l2(p.gate_tok + (row + p.ahead) * p.gate_stride, bytes);
   }
-#pragma unroll
-  for (int u = 0; u < V; ++u) unpack8(y[u], v[u]);
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int u = 0; u < V; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f(v[u][i]);
-  };
-  // r = residual_scale x + v c, with c the factors of the column
-  const float k1 = p.post_w ? rms_factor(g, p.inv_n, p.eps, part[0], each) : 1.0f;
-  const float2 k1k1 = make_float2(k1, k1), scale2 = make_float2(p.residual_scale, p.residual_scale);
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int vec = g.tid + u * g.n;
-    if (vec >= p.vecs) continue;  // v is zeros
-    float2 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[u][i] = __fmul2_rn(k1k1, c[u][i]);
-    if (tok) {
-      unpack8(gate[u], w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[u][i] = __fmul2_rn(c[u][i], w[i]);
-    }
-    unpack8(x[u], w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[u][i] = __ffma2_rn(v[u][i], c[u][i], __fmul2_rn(w[i], scale2));
-    if (p.r) reinterpret_cast<uint4*>(p.r)[row * p.vecs + vec] = pack8(v[u]);
-  }
-  const float k2 = rms_factor(g, p.inv_n, p.eps, part[1], each);
-  const float2 k2k2 = make_float2(k2, k2);
-  uint32_t top = 0;
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[u][i] = __fmul2_rn(v[u][i], __fmul2_rn(k2k2, nw[u][i]));
-    if constexpr (OUT == kOutFp4E4M3) top = max(top, amax8(&v[u][0].x));
-  }
-  RowScale rs{};
-  if constexpr (OUT == kOutFp4E4M3) rs = row_scale(p, g, row, top, part[2]);
-#pragma unroll
-  for (int u = 0; u < V; ++u)
-    if ((g.tid & ~31) + u * g.n < p.vecs) store_h<OUT>(p, row, g.tid + u * g.n, v[u], rs);
-}
-
-// A block to an SM, in groups of p.group threads with a token each at a time and
-// p.slots slots of shared memory. A slot has the rows of y, x and the token's gate;
-// r takes the place of y and x in fp32. Registers hold one vector, not the row:
-// what a row of four vectors to a thread spilled went through the little L1 that
-// the slots leave, and cost more than reading it from shared memory.
-// Shared memory: [factors of z][norm_w] (each the first, then the second halves of
-// the vectors' 8 numbers, so that a warp reads whole lines), [group][slot][row][vector].
-template <int OUT>
-__global__ void __launch_bounds__(kGroupThreads, 1) residual_norm_groups_kernel(const NormParams p) {
-  __shared__ float parts[2][3][32];
-  __shared__ uint64_t full[2 * kMaxGroups];
-  extern __shared__ uint4 shared[];
-  Group g;
-  g.n = p.group;
-  g.id = threadIdx.x / p.group;
-  g.tid = threadIdx.x - g.id * g.n;
-  float* part = &parts[0][0][0] + g.id * (g.n >> 5);
-  const int64_t first = blockIdx.x + static_cast<int64_t>(g.id) * gridDim.x;
-  const int64_t step = static_cast<int64_t>(blockDim.x / p.group) * gridDim.x;
-  const bool has_x = p.x != nullptr, tok = p.gate_tok != nullptr;
-  const int slot_vecs = p.vecs * (tok ? 3 : 2);
-  float4* factors = reinterpret_cast<float4*>(shared);
-  uint4* slots = shared + 4 * p.vecs + g.id * p.slots * slot_vecs;
-  uint64_t* filled = full + g.id * p.slots;
-  if (g.tid < p.slots) {
-    mbar_init(&filled[g.tid], 1);
-    fence_barrier_init();
-    fence_proxy_async_smem();
-  }
-  griddep_launch_dependents();
-  griddep_wait();
-  const uint32_t row_bytes = static_cast<uint32_t>(p.vecs) * 16;
-  auto request = [&](int64_t row, int slot) {
-    uint4* at = slots + slot * slot_vecs;
-    mbar_arrive_expect_tx(&filled[slot], row_bytes * (1 + has_x + tok));
-    bulk_load(at, p.y + row * p.y_stride, row_bytes, &filled[slot]);
-    if (has_x) bulk_load(at + p.vecs, p.x + row * p.x_stride, row_bytes, &filled[slot]);
-    if (tok) bulk_load(at + 2 * p.vecs, p.gate_tok + row * p.gate_stride, row_bytes, &filled[slot]);
-  };
-  __syncwarp();  // the group's first warp has made its barriers
-  if (g.tid == 0)
-    for (int s = 0; s < p.slots; ++s)
-      if (first + s * step < p.rows) request(first + s * step, s);
-  for (int vec = threadIdx.x; vec < p.vecs; vec += blockDim.x) {
-    float2 c[4];
-    z_factors(p, vec, c);
-    factors[vec] = make_float4(c[0].x, c[0].y, c[1].x, c[1].y);
-    factors[p.vecs + vec] = make_float4(c[2].x, c[2].y, c[3].x, c[3].y);
-    load8(p.norm_w, vec, c);
-    factors[2 * p.vecs + vec] = make_float4(c[0].x, c[0].y, c[1].x, c[1].y);
-    factors[3 * p.vecs + vec] = make_float4(c[2].x, c[2].y, c[3].x, c[3].y);
-  }
-  __syncthreads();
-  // 8 fp32 numbers of a vector kept as two halves.
-  auto get8 = [&](const float4* halves, int vec, float2* c) {
-    const float4 a = halves[vec], b = halves[p.vecs + vec];
-    c[0] = make_float2(a.x, a.y), c[1] = make_float2(a.z, a.w);
-    c[2] = make_float2(b.x, b.y), c[3] = make_float2(b.z, b.w);
-  };
-  auto put8 = [&](float4* halves, int vec, const float2* c) {
-    halves[vec] = make_float4(c[0].x, c[0].y, c[1].x, c[1].y);
-    halves[p.vecs + vec] = make_float4(c[2].x, c[2].y, c[3].x, c[3].y);
-  };
+  uint32_t x[P][8];
+  float2 v[P][8], ne[EARLY ? P : 1][8];
   const float2 scale2 = make_float2(p.residual_scale, p.residual_scale);
-  int turn = 0, slot = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (int64_t row = first; row < p.rows; row += step, turn ^= 96) {
-    uint4* at = slots + slot * slot_vecs;
-    float4* rf = reinterpret_cast<float4*>(at);
-    // A wait that gave up (the error bit says so: the outputs are not valid) is the last one.
-    if (ok) ok = mbar_wait(&filled[slot], phase, nullptr, p.err, kDevErrTimeoutProducer);
-    float k1 = 1.0f;
-    if (p.post_w)
-      k1 = rms_factor(g, p.inv_n, p.eps, part + turn, [&](auto f) {
-#pragma unroll 4
-        for (int vec = g.tid; vec < p.vecs; vec += g.n) {
-          float2 v[4];
-          unpack8(at[vec], v);
+  float2 yy = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f(v[i]);
-        }
-      });
-    // r = residual_scale x + y c, with c the factors of the column
-    const float2 k1k1 = make_float2(k1, k1);
-    uint4* r_row = reinterpret_cast<uint4*>(p.r) + row * p.vecs;
-#pragma unroll 2
-    for (int vec = g.tid; vec < p.vecs; vec += g.n) {
-      float2 v[4], c[4], w[4];
-      unpack8(at[vec], v);
-      get8(factors, vec, c);
+  for (int u = 0; u < P; ++u) {
+    const int unit = tid + u * n;
+    const bool in = unit < p.units;
+    uint32_t y[8], g[8];
+    read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, in, y);
+    read16<WIDE>(p.x + row * p.x_stride, unit, p.cols, in && has_x, x[u]);
+    if (tok) read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, in, g);
+    if constexpr (EARLY) read16<WIDE>(p.norm_w, in ? unit : 0, p.cols, ne[u]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __fmul2_rn(k1k1, c[i]);
-      if (tok) {
-        unpack8(at[2 * p.vecs + vec], w);
+    for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
+    if (p.post_w) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = __fmul2_rn(c[i], w[i]);
-      }
-      if (has_x) {
-        unpack8(at[p.vecs + vec], w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __ffma2_rn(v[i], c[i], __fmul2_rn(w[i], scale2));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(v[i], c[i]);
-      }
-      if (p.r) r_row[vec] = pack8(v);
-      put8(rf, vec, v);
+      for (int i = 0; i < 8; ++i) yy = __ffma2_rn(v[u][i], v[u][i], yy);
     }
-    const float k2 = rms_factor(g, p.inv_n, p.eps, part + turn + 32, [&](auto f) {
-#pragma unroll 4
-      for (int vec = g.tid; vec < p.vecs; vec += g.n) {
-        float2 v[4];
-        get8(rf, vec, v);
+    // v becomes y times its columns' factors.
+    float2 w[8];
+    if (p.post_w) {
+      read16<WIDE>(p.post_w, in ? unit : 0, p.cols, w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f(v[i]);
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
+    }
+    if (p.gate_col) {
+      read16<WIDE>(p.gate_col, in ? unit : 0, p.cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
+    }
+    if (tok) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(g[i]));
+    }
+  }
+  // r = s x + k1 v, and its square sum. With k1 to be found, all that both need is
+  // summed at once, and sum r^2 = s^2 sum x^2 + 2 s k1 sum x v + k1^2 sum v^2, unless
+  // the terms cancel (to less than a quarter) or leave fp32's range.
+  auto residual = [&](float k1) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      if (k1 != 1.0f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], make_float2(k1, k1));
+      if (has_x)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = __ffma2_rn(pair(x[u][i]), scale2, v[u][i]);
+    }
+  };
+  float k2 = 0.0f;
+  bool known = false;
+  if (p.post_w) {
+    float2 vv = make_float2(0.0f, 0.0f), xv = vv, xx = vv;
+#pragma unroll
+    for (int u = 0; u < P; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 xf = pair(x[u][i]);
+        vv = __ffma2_rn(v[u][i], v[u][i], vv);
+        xv = __ffma2_rn(xf, v[u][i], xv);
+        xx = __ffma2_rn(xf, xf, xx);
       }
-    });
-    const float2 k2k2 = make_float2(k2, k2);
-    auto h_of = [&](int vec, float2* v) {
-      float2 w[4];
-      get8(rf, vec, v);
-      get8(factors + 2 * p.vecs, vec, w);
+    const float4 sum = block_sum4(make_float4(yy.x + yy.y, vv.x + vv.y, xv.x + xv.y, xx.x + xx.y), sums);
+    const float k1 = root_inverse(fmaf(sum.x, p.inv_n, p.eps)), s = p.residual_scale;
+    const float a = s * s * sum.w, b = k1 * k1 * sum.y, all = a + b;
+    const float rr = fmaf(2.0f * s * k1, sum.z, all);
+    if (sum.x > 1e-20f && sum.x < 1e30f && sum.y < 1e30f && all > 1e-20f && rr < 1e30f && rr > 0.25f * all) {
+      residual(k1);
+      k2 = root_inverse(fmaf(rr, p.inv_n, p.eps));
+      known = true;
+    } else {
+      // The long way: the row's own sums, one after the other, in the order of the formula.
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(v[i], __fmul2_rn(k2k2, w[i]));
-    };
+      for (int u = 0; u < P; ++u) {
+        const int unit = tid + u * n;
+        uint32_t y[8];
+        read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, unit < p.units, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
+      }
+      const float k = rms_factor<P>(v, p.inv_n, p.eps, sum_y);
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+        const int unit = tid + u * n < p.units ? tid + u * n : 0;
+        float2 w[8], g[8];
+        read16<WIDE>(p.post_w, unit, p.cols, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(__fmul2_rn(v[u][i], make_float2(k, k)), w[i]);
+        if (p.gate_col) {
+          read16<WIDE>(p.gate_col, unit, p.cols, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], g[i]);
+        }
+        if (tok) {
+          uint32_t t[8];
+          read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, true, t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(t[i]));
+        }
+      }
+      residual(1.0f);
+    }
+  } else {
+    residual(1.0f);
+  }
+  if (p.r) {
+#pragma unroll
+    for (int u = 0; u < P; ++u)
+      if (tid + u * n < p.units) write16<WIDE>(p.r + row * p.cols, tid + u * n, p.cols, v[u]);
+  }
+  if (!known) k2 = rms_factor<P>(v, p.inv_n, p.eps, sum_r);
+  k2 = apply_early<P>(v, k2);
+  const float2 k2k2 = make_float2(k2, k2);
+  // h / k2 = v norm_w
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int unit = tid + u * n < p.units ? tid + u * n : 0;
+    float2 w[8];
+    if constexpr (!EARLY) read16<WIDE>(p.norm_w, unit, p.cols, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], EARLY ? ne[u][i] : w[i]);
+  }
+  if constexpr (OUT == kOutBf16) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const int unit = tid + u * n;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], k2k2);
+      if (unit < p.units) write16<WIDE>(static_cast<__nv_bfloat16*>(p.h) + row * p.cols, unit, p.cols, v[u]);
+    }
+  } else if constexpr (OUT == kOutE4m3) {
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const int unit = tid + u * n;
+      if ((unit & ~31) >= p.units) continue;
+      float m = amax16<false>(v[u]);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));  // 8 lanes: 128 columns
+      if (unit >= p.units) continue;
+      const float s = e4m3_scale(m * k2, p.ue8m0 != 0), f = k2 * scale_inverse(s);
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = __fmul2_rn(v[u][2 * i], make_float2(f, f)), b = __fmul2_rn(v[u][2 * i + 1], make_float2(f, f));
+        q[i] = e4m3x2(a.x, a.y) | (static_cast<uint32_t>(e4m3x2(b.x, b.y)) << 16);
+      }
+      reinterpret_cast<uint4*>(p.h)[row * p.units + unit] = make_uint4(q[0], q[1], q[2], q[3]);
+      if ((tid & 7) == 0) static_cast<float*>(p.h_s)[row * (p.units / 8) + unit / 8] = s;
+    }
+  } else {
+    uint32_t am[P], top = 0;
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], k2k2);
+      am[u] = __float_as_uint(amax16<true>(v[u])) & 0x7FFFFFFFu;
+      top = max(top, am[u]);
+    }
     RowScale rs{};
     if constexpr (OUT == kOutFp4E4M3) {
-      uint32_t top = 0;
-#pragma unroll 2
-      for (int vec = g.tid; vec < p.vecs; vec += g.n) {
-        float2 v[4];
-        h_of(vec, v);
-        top = max(top, amax8(&v[0].x));
-      }
-      rs = row_scale(p, g, row, top, part + turn + 64);
+      rs = fp4_row_scale(block_reduce(top, 0u, reinterpret_cast<uint32_t*>(tops),
+                                      [](uint32_t a, uint32_t b) { return max(a, b); }));
+      if (tid == 0) p.h_g[row] = rs.g;
     }
-#pragma unroll 2
-    for (int vec = g.tid; (vec & ~31) < p.vecs; vec += g.n) {
-      float2 v[4] = {};
-      if (vec < p.vecs) h_of(vec, v);
-      store_h<OUT>(p, row, vec, v, rs);
-    }
-    // The slot is the copies' again: after what all of the group did with it.
-    fence_proxy_async_smem();
-    g.sync();
-    const int64_t later = row + p.slots * step;
-    if (g.tid == 0 && ok && later < p.rows) request(later, slot);
-    if (++slot == p.slots) slot = 0, phase ^= 1;
+#pragma unroll
+    for (int u = 0; u < P; ++u)
+      if ((tid & ~31) + u * n < p.units)
+        fp4_store16<OUT == kOutFp4E4M3 ? kFp4E4M3 : kFp4UE8M0>(v[u], am[u], rs, row, tid + u * n, p.units,
+                                                               static_cast<uint2*>(p.h), static_cast<uint8_t*>(p.h_s),
+                                                               p.ktiles);
   }
-  if (!ok && g.tid == 0) {  // the copies in flight land before the block ends
-    for (int s = 0; s < p.slots; ++s) {
-      mbar_wait(&filled[slot], phase, nullptr, p.err, kDevErrTimeoutDrain);
-      if (++slot == p.slots) slot = 0, phase ^= 1;
-    }
-  }
+}
+
+template <int OUT, bool WIDE>
+const void* kernel_of(int P, bool early) {
+  return P == 2  ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 2, WIDE, false>)
+         : early ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 1, WIDE, true>)
+                 : reinterpret_cast<const void*>(residual_norm_kernel<OUT, 1, WIDE, false>);
 }
 
 template <int OUT>
-const void* kernel_for(int v, bool groups) {
-  return groups   ? reinterpret_cast<const void*>(residual_norm_groups_kernel<OUT>)
-         : v == 1 ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 1>)
-         : v == 2 ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 2>)
-                  : reinterpret_cast<const void*>(residual_norm_kernel<OUT, 4>);
-}
-
-// Lets a kernel of groups have its shared memory: once per device and kind of output.
-int allow_shared(const void* kernel, int device, int which) {
-  constexpr int kMaxDevices = 64;
-  static std::once_flag once[kMaxDevices][4];
-  static cudaError_t set[kMaxDevices][4];
-  std::call_once(once[device][which], [&] {
-    set[device][which] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes);
-  });
-  return cuda_status(set[device][which]);
+const void* kernel_for(int P, bool wide, bool early) {
+  return wide ? kernel_of<OUT, true>(P, early) : kernel_of<OUT, false>(P, early);
 }
 
 }  // namespace
@@ -499,42 +499,24 @@ extern "C" int fp8blk_residual_norm(const void* y_bf16, int64_t y_stride, const 
   p.residual_scale = residual_scale;
   p.eps = eps;
   p.inv_n = 1.0f / static_cast<float>(D);
-  p.rows = T;
-  p.err = d->err_word;
-  p.vecs = static_cast<int>(D / 8);
+  p.cols = static_cast<int>(D);
+  p.ahead = d->sm_count;
+  p.units = static_cast<int>((D + 15) / 16);
   p.ue8m0 = fp8 && scale_fmt_ue8m0(scale_fmt);
-  // Up to a token per SM: as many threads as there are vectors, up to 512. More:
-  // four vectors to a thread (fewer in narrow rows), which then share the cost of
-  // the sums; as many groups as their threads and slots leave room for.
-  const bool groups = T > d->sm_count;
-  const int V = groups ? 4 : p.vecs <= kMaxThreads ? 1 : p.vecs <= 2 * kMaxThreads ? 2 : 4;
-  int threads = ((p.vecs + V - 1) / V + 31) / 32 * 32, shared = 0;
-  int64_t blocks = T;
-  if (groups) {
-    const int factors = p.vecs * 64, slot = p.vecs * 16 * (gate_tok_bf16 ? 3 : 2);
-    p.group = threads;
-    p.slots = factors + 2 * slot <= kSharedBytes ? 2 : 1;
-    int count = (kSharedBytes - factors) / (p.slots * slot);
-    if (count > kGroupThreads / threads) count = kGroupThreads / threads;
-    if (threads > 32 && count > 15) count = 15;  // a named barrier each
-    const int64_t need = (T + d->sm_count - 1) / d->sm_count;
-    if (count > need) count = static_cast<int>(need);
-    threads *= count;
-    shared = factors + count * p.slots * slot;
-    blocks = d->sm_count;
-  }
-  const int out = !fp8 && !fp4 ? kOutBf16 : fp8 ? kOutE4m3 : scale_fmt == kFp4E4M3 ? kOutFp4E4M3 : kOutFp4UE8M0;
-  const void* kernel = out == kOutBf16      ? kernel_for<kOutBf16>(V, groups)
-                       : out == kOutE4m3    ? kernel_for<kOutE4m3>(V, groups)
-                       : out == kOutFp4E4M3 ? kernel_for<kOutFp4E4M3>(V, groups)
-                                            : kernel_for<kOutFp4UE8M0>(V, groups);
-  if (groups) {
-    if (int st = allow_shared(kernel, d->device, out)) return st;
-  }
+  const auto wide_rows = [](const void* t, int64_t stride) { return !t || (is_aligned(t, 32) && stride % 16 == 0); };
+  const bool wide = D % 16 == 0 && wide_rows(y_bf16, y_stride) && wide_rows(x_bf16, x_stride) &&
+                    wide_rows(gate_tok_bf16, gate_stride) && wide_rows(r_bf16, D) && wide_rows(h, D) &&
+                    is_aligned(norm_w, 32) && is_aligned(post_w, 32) && is_aligned(gate_col, 32);
+  const int P = p.units > kMaxThreads ? 2 : 1;
+  const bool early = T <= 2 * d->sm_count;
+  const int threads = ((p.units + P - 1) / P + 31) / 32 * 32;
+  const void* kernel = !fp8 && !fp4            ? kernel_for<kOutBf16>(P, wide, early)
+                       : fp8                   ? kernel_for<kOutE4m3>(P, wide, early)
+                       : scale_fmt == kFp4E4M3 ? kernel_for<kOutFp4E4M3>(P, wide, early)
+                                               : kernel_for<kOutFp4UE8M0>(P, wide, early);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(T));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
