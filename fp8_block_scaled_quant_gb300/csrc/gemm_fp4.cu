@@ -5,15 +5,11 @@
 // The block-scaled MMA applies sa and sw itself (products of e2m1 numbers and
 // their scales, summed in fp32 in tensor memory), the epilogue the row scales.
 //
-// Kernel: 128 weight rows are the MMA's M (tensor-memory lanes), BN tokens its
-// columns, 256 of K to a stage: codes by TMA (128-byte rows, 128-byte swizzle),
-// scale tiles by bulk copies, from there into tensor memory by tcgen05.cp in the
-// order of the MMAs that use them. Few weight tiles are split over K by clusters
-// of up to 8 CTAs, whose partial sums meet in shared memory in rank order.
-//
-//   warp 0      producer: weights of the first stages before the dependency wait
-//   warp 1      MMA issuer
-//   warps 2-5   epilogue, a lane quarter each
+// Two kernels. Few tokens: 128 weight rows are the MMA's M (tensor-memory lanes), up
+// to 128 tokens its columns; memory bounds it. Many tokens: 256 x 256 tiles of CTA
+// pairs, at the tensor cores' rate (below). In both, 256 of K make a stage: codes by
+// TMA (128-byte rows, 128-byte swizzle), scale tiles in the order of their use, from
+// shared into tensor memory by tcgen05.cp in the order of the MMAs.
 //
 // Every wait is bounded; a wait that gives up sets an error bit, and the CTA
 // waits (bounded) for its own copies and MMAs, frees its tensor memory and returns.
@@ -39,7 +35,6 @@ namespace {
 
 constexpr int kStageK = 256;
 constexpr int kLaneBytes = 128 * 128;  // 128 weight rows of a stage
-constexpr int kThreads = 192;
 
 struct Fp4Params {
   const uint8_t* w_s;
@@ -48,235 +43,415 @@ struct Fp4Params {
   const float* a_g;
   __nv_bfloat16* c;
   unsigned* err;
-  int64_t M, N, ktiles;  // ktiles: scale tiles along K
-  int ksteps;            // K / 64
-  int stages_k;          // ceil(K / 256)
-  int tiles_n, tiles_m;  // weight tiles; token tiles (pairs)
-  int ksplit;            // CTAs of a tile's cluster
+  const __nv_bfloat16* x;  // few tokens: the activations themselves, quantised by every CTA
+  int64_t x_stride;
+  int64_t M, N, ktiles;    // ktiles: scale tiles along K
+  int ksteps;              // K / 64
+  int stages_k;            // ceil(K / 256)
+  int tiles_n, tiles_m;    // weight tiles; token tiles (pairs)
+  int ksplit;              // few tokens: CTAs of a tile's cluster
+  int stages;              // few tokens: slots of the ring
+  int part_cols, part_vec; // few tokens: columns that a CTA of the cluster sums, and that it is sent at once
+  uint32_t tmem_cols;      // few tokens
 };
 
-template <int BN_, int FMT_>
+// ---- few tokens ------------------------------------------------------------------------
+//
+//   warp 0      weights: requested before the dependency wait as far as the ring goes
+//   warp 1      MMA issuer: the weights' scales of those stages go to tensor memory
+//               before the tokens are there; then a stage is four copies and four MMAs,
+//               0.28 us (an MMA of 16 columns takes about 95 cycles, a copy 40)
+//   warps 2-5   epilogue, a lane quarter each
+//   warp 6      tokens, as codes; FUSE: none, warps 2-5 quantise the activations into
+//               shared memory (one launch, and 1.5 us less than a kernel of its own)
+//
+// Few weight tiles are split over K by clusters of up to 8 CTAs. A CTA sends each
+// column of its partial sums to the one that sums it (st.async on its mbarrier, no
+// barrier of the cluster on the way; up to four columns at once, a store takes 0.06 us
+// of a warp), which adds them in rank order.
+
+constexpr int kFewThreads = 224;
+constexpr int kMaxStages = 12;
+constexpr int kFuseUnits = 4;  // units of 16 numbers that a quantising thread holds
+
+template <int BN_, int FMT_, bool FUSE_>
 struct Cfg {
   static constexpr int BN = BN_, FMT = FMT_;
+  static constexpr bool FUSE = FUSE_;
   static constexpr int kTiles = FMT == kFp4E4M3 ? 4 : 2;  // scale tiles of a stage
-  static constexpr int kColBytes = BN * 128;
   static constexpr int kSfBytes = kTiles * kScaleTile;
-  static constexpr int kStageBytes = (kLaneBytes + kColBytes + 2 * kSfBytes + 1023) / 1024 * 1024;
-  // Two CTAs to an SM (113 KB each): the work of an uneven last round is then
-  // spread, and one CTA's start and end lie beside the other's stream.
-  static constexpr int kStages = 112 * 1024 / kStageBytes;
+  static constexpr int kColAt = kLaneBytes + kSfBytes;    // the tokens' part of a stage
+  static constexpr int kStageBytes = (kColAt + (FUSE ? 0 : BN * 128 + kSfBytes) + 1023) / 1024 * 1024;
+  static constexpr int kColCodesAt = (kColAt + 1023) / 1024 * 1024;  // (a swizzled tile starts at 1024 bytes)
   static constexpr int kAccCols = BN < 32 ? 32 : BN;
-  static constexpr int kSfCols = 2 * kTiles * 4;  // both operands' scales of a stage
-  static constexpr int kTmemCols = kAccCols + 2 * kSfCols <= 128 ? 128 : 256;
-  static constexpr int kBarBytes = (2 * kStages + 1) * 8 + 8;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes;
-  static_assert(kAccCols + 2 * kSfCols <= kTmemCols, "tensor memory");
-  static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the partial sums lie where the stages were");
+  static constexpr int kSfCols = kTiles * 4;              // one operand's scales of a stage
+  // FUSE: all of the CTA's tokens: codes, then scale tiles of 16 rows (256 bytes; a copy reads on into the next).
+  static constexpr int kFuseCodes = BN * 128, kFuseScales = kTiles * 256;
+  static constexpr int kBarBytes = (3 * kMaxStages + 3) * 8 + 16 + 64;
 };
 
+// Stage slots that `cols` columns of tensor memory have room for.
 template <class C>
-__global__ void __launch_bounds__(kThreads, 2)
+constexpr int most_stages(int cols) {
+  const int n = (cols - C::kAccCols) / C::kSfCols - 2;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// mbar_wait for a barrier that other CTAs arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
+                                                  unsigned code) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait_cluster(a, parity) ||
+         (mbar_wait(bar, parity, abort, err, code) && mbar_try_wait_cluster(a, parity));
+}
+
+// V numbers (1, 2 or 4) into a CTA of the cluster; they complete on its barrier.
+template <int V>
+__device__ __forceinline__ void st_async(uint32_t addr, const uint32_t* v, uint32_t bar) {
+  if constexpr (V == 4)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+                 : "memory");
+  else if constexpr (V == 2)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(bar)
+                 : "memory");
+  else
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v[0]),
+                 "r"(bar)
+                 : "memory");
+}
+
+// The columns' sums of this lane's weight row, r[0..N), to their shares' CTAs. A
+// share is `share` columns, a multiple of V; its part of this CTA: [share / V][128][V].
+template <int V, int N>
+__device__ __forceinline__ void send_columns(const uint32_t* r, int c0, int share, int ks, const float* part,
+                                             const uint64_t* bar) {
+#pragma unroll
+  for (int i = 0; i < N; i += V) {
+    const int c = c0 + i, to = c / share;
+    if (to < ks)
+      st_async<V>(map_to_rank(smem_u32(part + (c - to * share) * 128), static_cast<uint32_t>(to)), r + i,
+                  map_to_rank(smem_u32(bar), static_cast<uint32_t>(to)));
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(kFewThreads, 2)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                     const Fp4Params p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* done = empty + C::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ks = p.ksplit, rank = static_cast<int>(blockIdx.x) % ks;
   const int tile = static_cast<int>(blockIdx.x) / ks;
   const int tile_n = tile % p.tiles_n, tile_m = tile / p.tiles_n;
   const int k0 = static_cast<int>(static_cast<int64_t>(p.stages_k) * rank / ks);
-  const int k1 = static_cast<int>(static_cast<int64_t>(p.stages_k) * (rank + 1) / ks);
+  const int n = static_cast<int>(static_cast<int64_t>(p.stages_k) * (rank + 1) / ks) - k0;  // stages of this CTA
+  const int most_n = (p.stages_k + ks - 1) / ks;
+  uint8_t* fused = smem + p.stages * C::kStageBytes;  // FUSE: codes, scales
+  uint8_t* fused_s = fused + most_n * C::kFuseCodes;
+  float* parts = reinterpret_cast<float*>(C::FUSE ? fused_s + most_n * C::kFuseScales + 256 : fused);  // [rank][column][128]
+  uint64_t* full_w = reinterpret_cast<uint64_t*>(parts + (ks > 1 ? ks * p.part_cols * 128 : 0));
+  uint64_t* full_t = full_w + kMaxStages;
+  uint64_t* empty = full_t + kMaxStages;
+  uint64_t* done = empty + kMaxStages;
+  uint64_t* tokens_ready = done + 1;
+  uint64_t* parts_full = tokens_ready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* row_top = tmem_slot + 4;  // FUSE: bits of the rows' largest |x|, [16]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t m0 = static_cast<int64_t>(tile_m) * C::BN;
+  const int cols = static_cast<int>(p.M - m0 < C::BN ? p.M - m0 : C::BN);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full_w[s], 1);
+      mbar_init(&full_t[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(tokens_ready, 4);
+    mbar_init(parts_full, 1);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
+    if (ks > 1) mbar_arrive_expect_tx(parts_full, static_cast<uint32_t>(ks * p.part_cols * 512));
   }
-  if (warp == 0 && lane == 0) {
+  if (C::FUSE && threadIdx.x >= 64 && threadIdx.x < 80) row_top[threadIdx.x - 64] = 0;
+  if (warp == 6 && lane == 0) {
     tma_prefetch_desc(&map_w);
-    tma_prefetch_desc(&map_a);
+    if constexpr (!C::FUSE) tma_prefetch_desc(&map_a);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
+  if (ks > 1) cluster_sync();  // the barriers of the CTAs that sums are sent to
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   // After the allocation: a CTA of the next kernel that came first to this SM's
   // tensor memory would hold it until this kernel ends.
   griddep_launch_dependents();
 
+  const int ktiles = static_cast<int>(p.ktiles);
+  // Bytes of the scale tiles of stage k: of all of them, or those that K has left.
+  auto scale_bytes = [&](int k) {
+    const int left = ktiles - k * C::kTiles;
+    return static_cast<uint32_t>(left < C::kTiles ? left : C::kTiles) * kScaleTile;
+  };
   bool finished = true;  // epilogue warps: the accumulator is complete
-  if (warp == 0) {
+  const int q = warp & 3;  // lane quarter of an epilogue warp
+  const int64_t row = static_cast<int64_t>(tile_n) * 128 + q * 32 + lane;
+  float wg = 1.0f, ag[C::BN < 32 ? 1 : C::BN / 32];
+
+  if (warp == 0 || (!C::FUSE && warp == 6)) {
+    const bool weights = warp == 0;
+    if (!weights) griddep_wait();
+    uint64_t* full = weights ? full_w : full_t;
+    const uint8_t* scales = weights ? p.w_s + static_cast<int64_t>(tile_n) * ktiles * kScaleTile
+                                    : p.a_s + m0 / 128 * ktiles * kScaleTile;
+    const CUtensorMap* map = weights ? &map_w : &map_a;
+    const int y = weights ? tile_n * 128 : static_cast<int>(m0);
+    const uint32_t bytes = weights ? kLaneBytes : C::BN * 128;
+    auto ask = [&](int i, int st) {
+      uint8_t* at = smem + st * C::kStageBytes;
+      const uint32_t sf = scale_bytes(k0 + i);
+      mbar_arrive_expect_tx(&full[st], bytes + sf);
+      tma_load_2d(weights ? at : at + C::kColCodesAt, map, &full[st], (k0 + i) * 128, y);
+      bulk_load(weights ? at + kLaneBytes : at + C::kColCodesAt + C::BN * 128,
+                scales + static_cast<int64_t>(k0 + i) * C::kSfBytes, sf, &full[st]);
+    };
+    // The first stages by a lane each, at once; the others in their turn.
+    const int pre = n < p.stages ? n : p.stages;
+    if (lane < pre) ask(lane, lane);
+    __syncwarp();
     if (lane == 0) {
-      // Scale tiles of stage k: all of them, or those that K has left.
-      auto tiles_of = [&](int k) {
-        const int64_t left = p.ktiles - static_cast<int64_t>(k) * C::kTiles;
-        return static_cast<uint32_t>(left < C::kTiles ? left : C::kTiles);
-      };
-      auto weights = [&](int st, int k) {
-        uint8_t* at = smem + st * C::kStageBytes;
-        const uint32_t sf = tiles_of(k) * kScaleTile;
-        mbar_arrive_expect_tx(&full[st], kLaneBytes + C::kColBytes + 2 * sf);
-        tma_load_2d(at, &map_w, &full[st], k * 128, tile_n * 128);
-        bulk_load(at + kLaneBytes + C::kColBytes,
-                  p.w_s + (static_cast<int64_t>(tile_n) * p.ktiles + static_cast<int64_t>(k) * C::kTiles) * kScaleTile, sf,
-                  &full[st]);
-      };
-      auto tokens = [&](int st, int k) {
-        uint8_t* at = smem + st * C::kStageBytes;
-        tma_load_2d(at + kLaneBytes, &map_a, &full[st], k * 128, tile_m * C::BN);
-        const int64_t row_tile = static_cast<int64_t>(tile_m) * C::BN / 128;
-        bulk_load(at + kLaneBytes + C::kColBytes + C::kSfBytes,
-                  p.a_s + (row_tile * p.ktiles + static_cast<int64_t>(k) * C::kTiles) * kScaleTile,
-                  tiles_of(k) * kScaleTile, &full[st]);
-      };
-      const int n = k1 - k0, pre = n < C::kStages ? n : C::kStages;
-      for (int i = 0; i < pre; ++i) weights(i, k0 + i);
-      griddep_wait();
-      int issued = 0;
-      for (; issued < n; ++issued) {
-        const int st = issued % C::kStages;
-        if (issued >= pre) {
-          if (!mbar_wait(&empty[st], ((issued / C::kStages) & 1) ^ 1, abort_flag, p.err, kDevErrTimeoutProducer)) break;
-          weights(st, k0 + issued);
-        }
-        tokens(st, k0 + issued);
+      int st = 0, i = pre;
+      uint32_t phase = 0;
+      for (; i < n; ++i) {
+        if (!mbar_wait(&empty[st], phase, abort_flag, p.err, kDevErrTimeoutProducer)) break;
+        ask(i, st);
+        if (++st == p.stages) st = 0, phase ^= 1;
       }
-      if (issued < n) {  // gave up: the copies in flight land before the CTA ends
-        for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-          mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, nullptr, p.err, kDevErrTimeoutDrain);
+      if (i < n) {  // gave up: the copies in flight land before the CTA ends
+        for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+          mbar_wait(&full[j % p.stages], (j / p.stages) & 1, nullptr, p.err, kDevErrTimeoutDrain);
       }
     }
   } else if (warp == 1) {
     const bool leader = elect_one_sync();
-    const uint32_t sf0 = tmem + C::kAccCols;
-    bool ok = true;
-    for (int i = 0; i < k1 - k0; ++i) {
-      const int st = i % C::kStages;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[st], (i / C::kStages) & 1, abort_flag, p.err, kDevErrTimeoutMma))) {
-        ok = false;
-        break;
-      }
+    const uint32_t sf_w = tmem + C::kAccCols, sf_t = sf_w + static_cast<uint32_t>(p.stages * C::kSfCols);
+    auto all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.err, kDevErrTimeoutMma));
+    };
+    auto weight_scales = [&](int st) {
+      const uint32_t at = smem_u32(smem + st * C::kStageBytes) + kLaneBytes;
       tc_fence_after_sync();
-      const uint32_t at = smem_u32(smem + st * C::kStageBytes);
-      const uint64_t ad = sdesc_kmajor_sw128(at), bd = sdesc_kmajor_sw128(at + kLaneBytes);
-      const uint32_t sw = at + kLaneBytes + C::kColBytes;
-      const uint32_t sf = sf0 + static_cast<uint32_t>((i & 1) * C::kSfCols);
+      if (leader) {
+#pragma unroll
+        for (int t = 0; t < C::kTiles; ++t)
+          tmem_cp_scales(sf_w + st * C::kSfCols + 4 * t, sdesc_scale_tile(at + t * kScaleTile));
+      }
+      __syncwarp();
+    };
+    // Where the tokens of stage i (slot st) are.
+    auto token_codes = [&](int i, int st) {
+      return C::FUSE ? smem_u32(fused + i * C::kFuseCodes) : smem_u32(smem + st * C::kStageBytes + C::kColCodesAt);
+    };
+    auto token_scales = [&](int i, int st) {
+      const uint32_t at = C::FUSE ? smem_u32(fused_s + i * C::kFuseScales) : token_codes(i, st) + C::BN * 128;
+      tc_fence_after_sync();
+      if (leader) {
+#pragma unroll
+        for (int t = 0; t < C::kTiles; ++t)
+          tmem_cp_scales(sf_t + (i & 1) * C::kSfCols + 4 * t, sdesc_scale_tile(at + t * (C::FUSE ? 256 : kScaleTile)));
+      }
+      __syncwarp();
+    };
+    const int pre = n < p.stages ? n : p.stages;
+    bool ok = true;
+    for (int i = 0; ok && i < pre; ++i)
+      if ((ok = all(&full_w[i], 0))) weight_scales(i);
+    if (C::FUSE && ok) ok = all(tokens_ready, 0);
+    int st = 0;
+    uint32_t phase = 0;
+    for (int i = 0; ok && i < n; ++i) {
+      if (i >= pre) {
+        if (!(ok = all(&full_w[st], phase))) break;
+        weight_scales(st);
+      }
+      if (!C::FUSE && !(ok = all(&full_t[st], phase))) break;
+      token_scales(i, st);
+      const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + st * C::kStageBytes)), bd = sdesc_kmajor_sw128(token_codes(i, st));
+      const uint32_t sfa = sf_w + static_cast<uint32_t>(st * C::kSfCols), sfb = sf_t + static_cast<uint32_t>((i & 1) * C::kSfCols);
       const int left = p.ksteps - (k0 + i) * 4, steps = left < 4 ? left : 4;  // 2 or 4
       if (leader) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j >= steps) break;
           const int t = C::FMT == kFp4E4M3 ? j : j / 2;
-          const uint32_t sfa = sf + static_cast<uint32_t>(8 * t), sfb = sfa + 4;
-          if (C::FMT == kFp4E4M3 || (j & 1) == 0) {
-            tmem_cp_scales(sfa, sdesc_scale_tile(sw + t * kScaleTile));
-            tmem_cp_scales(sfb, sdesc_scale_tile(sw + C::kSfBytes + t * kScaleTile));
-          }
           mma_fp4<C::FMT>(tmem, ad + 2 * j, bd + 2 * j,
-                          idesc_fp4(128, C::BN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa, sfb,
+                          idesc_fp4(128, C::BN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa + 4 * t, sfb + 4 * t,
                           i > 0 || j > 0 ? 1u : 0u);
         }
-        mma_commit(&empty[st]);
-        if (i + 1 == k1 - k0) mma_commit(done);
+        if (i + p.stages < n) mma_commit(&empty[st]);
+        if (i + 1 == n) mma_commit(done);
       }
       __syncwarp();
+      if (++st == p.stages) st = 0, phase ^= 1;
     }
     if (leader) {
       if (!ok) mma_commit(done);
       mbar_wait(done, 0, nullptr, p.err, kDevErrTimeoutDrain);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     griddep_wait();
+    if constexpr (C::FUSE) {
+      // Units of 16 numbers, row by row over the 128 threads; the row's largest first.
+      const int t = threadIdx.x - 64, per_row = p.ksteps * 4, units = cols * per_row;
+      const __nv_bfloat16* x = p.x + m0 * p.x_stride;
+      uint32_t v[kFuseUnits][8];
+#pragma unroll
+      for (int u = 0; u < kFuseUnits; ++u) {
+        const int i = t + u * 128;
+        if (i >= units) break;
+        const int m = i / per_row, unit = i - m * per_row;
+        const uint4* src = reinterpret_cast<const uint4*>(x + m * p.x_stride + unit * 16);
+        const uint4 a = src[0], b = src[1];
+        v[u][0] = a.x, v[u][1] = a.y, v[u][2] = a.z, v[u][3] = a.w;
+        v[u][4] = b.x, v[u][5] = b.y, v[u][6] = b.z, v[u][7] = b.w;
+      }
+      uint32_t am[kFuseUnits];
+#pragma unroll
+      for (int u = 0; u < kFuseUnits; ++u) {
+        const int i = t + u * 128;
+        if (i >= units) break;
+        uint32_t m = v[u][0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = __vmaxu2(m, v[u][j] & 0x7FFF7FFFu);
+        am[u] = max(m << 16, m & 0xFFFF0000u);
+        if constexpr (C::FMT == kFp4E4M3) atomicMax(&row_top[i / per_row], am[u]);
+      }
+      __syncwarp();
+      if constexpr (C::FMT == kFp4E4M3) named_barrier_sync(1, 128);
+#pragma unroll
+      for (int u = 0; u < kFuseUnits; ++u) {
+        const int i = t + u * 128;
+        if (i >= units) break;
+        const int m = i / per_row, unit = i - m * per_row, stage = unit / 16 - k0;
+        float mul;
+        uint8_t code;
+        if constexpr (C::FMT == kFp4E4M3) {
+          code = fp4_block_scale_e4m3(am[u], fp4_row_scale(row_top[m]), &mul);
+        } else {
+          const int left = units - (i - lane);  // of this warp's units: a multiple of 8
+          am[u] = max(am[u], __shfl_xor_sync(left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u, am[u], 1));
+          code = fp4_block_scale_ue8m0(am[u], &mul);
+        }
+        if (stage < 0 || stage >= n) continue;
+        float2 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = __fmul2_rn(make_float2(__uint_as_float(v[u][j] << 16), __uint_as_float(v[u][j] & 0xFFFF0000u)),
+                            make_float2(mul, mul));
+        const uint2 codes = mul == 0.0f ? make_uint2(0, 0) : make_uint2(e2m1x8(&y[0].x), e2m1x8(&y[4].x));
+        const int in = unit & 15;  // the stage's 16 units are 128 bytes of the row, swizzled in chunks of 16
+        *reinterpret_cast<uint2*>(fused + stage * C::kFuseCodes + m * 128 + (((in >> 1) ^ (m & 7)) << 4) + (in & 1) * 8) = codes;
+        const int block = C::FMT == kFp4E4M3 ? in : in >> 1;
+        if (C::FMT == kFp4E4M3 || (in & 1) == 0)
+          fused_s[stage * C::kFuseScales + (block >> 2) * 256 + m * 16 + (block & 3)] = code;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tokens_ready);
+    }
+    // The scales of this lane's weight row and of the tokens (token 32 i + lane in ag[i]).
+    if (p.w_g) {
+      if (row < p.N) wg = __ldg(p.w_g + row);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(ag) / 4); ++i) {
+        const int m = i * 32 + lane;
+        if constexpr (C::FUSE) ag[i] = m < cols ? fp4_row_scale(row_top[m]).g : 0.0f;
+        else ag[i] = m < cols ? __ldg(p.a_g + m0 + m) : 0.0f;
+      }
+    }
     finished = mbar_wait(done, 0, nullptr, p.err, kDevErrTimeoutEpilogue);
     tc_fence_after_sync();
   }
-
   __syncwarp();
-  // The accumulator: lane = weight row, column = token.
-  const int q = warp & 3;  // lane quarter of an epilogue warp
-  const int64_t row = static_cast<int64_t>(tile_n) * 128 + q * 32 + lane;
-  const int64_t m0 = static_cast<int64_t>(tile_m) * C::BN;
-  const int cols = static_cast<int>(p.M - m0 < C::BN ? p.M - m0 : C::BN);
-  const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16);
-  float* part = reinterpret_cast<float*>(smem);  // [BN][128]
-  float wg = 1.0f;
-  if (warp >= 2 && p.w_g && row < p.N) wg = __ldg(p.w_g + row);
-  auto store = [&](int col, float v) {
-    const int64_t m = m0 + col;
-    if (p.a_g) v *= wg * __ldg(p.a_g + m);
-    if (row < p.N) p.c[m * p.N + row] = __float2bfloat16(v);
+  const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+  auto store = [&](int col, float v, float a) {
+    if (p.w_g) v *= wg * a;
+    if (row < p.N && finished) p.c[(m0 + col) * p.N + row] = __float2bfloat16(v);
   };
-  if (ks == 1) {
-    if (warp >= 2) {
-      constexpr int kStep = C::BN < 32 ? 16 : 32;
-      for (int c = 0; c < cols; c += kStep) {
-        uint32_t r[kStep];
-        if constexpr (kStep == 16) tmem_ld_32x32b_x16(at + c, r);
-        else tmem_ld_32x32b_x32(at + c, r);
+  constexpr int kStep = C::BN < 32 ? 16 : 32;
+  if (warp >= 2 && warp < 6) {
+    // The accumulator: lane = weight row, column = token.
+    const float* mine = parts + (rank * p.part_cols * 128 + (q * 32 + lane) * p.part_vec);
 #pragma unroll
-        for (int i = 0; i < kStep; ++i)
-          if (c + i < cols && finished) store(c + i, __uint_as_float(r[i]));
+    for (int c0 = 0; c0 < C::BN; c0 += kStep) {
+      if (c0 >= (ks == 1 ? cols : ks * p.part_cols)) break;
+      uint32_t r[kStep];
+      if constexpr (kStep == 16) tmem_ld_32x32b_x16(acc + c0, r);
+      else tmem_ld_32x32b_x32(acc + c0, r);
+      if (ks > 1) {
+        if (p.part_vec == 4) send_columns<4, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
+        else if (p.part_vec == 2) send_columns<2, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
+        else send_columns<1, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
+        continue;
       }
-      tc_fence_before_sync();
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const float a = __shfl_sync(0xFFFFFFFFu, ag[(c0 + i) / 32], i);
+        if (c0 + i < cols) store(c0 + i, __uint_as_float(r[i]), a);
+      }
     }
-  } else {
-    if (warp >= 2) {
-      constexpr int kStep = C::BN < 32 ? 16 : 32;
-      for (int c = 0; c < cols; c += kStep) {
-        uint32_t r[kStep];
-        if constexpr (kStep == 16) tmem_ld_32x32b_x16(at + c, r);
-        else tmem_ld_32x32b_x32(at + c, r);
-#pragma unroll
-        for (int i = 0; i < kStep; ++i) part[(c + i) * 128 + q * 32 + lane] = __uint_as_float(r[i]);
+    if (ks > 1) {  // (the shares may reach past BN)
+      const uint32_t zero[4] = {0, 0, 0, 0};
+      for (int c = C::BN; c < ks * p.part_cols; c += p.part_vec) {
+        if (p.part_vec == 4) send_columns<4, 4>(zero, c, p.part_cols, ks, mine, parts_full);
+        else if (p.part_vec == 2) send_columns<2, 2>(zero, c, p.part_cols, ks, mine, parts_full);
+        else send_columns<1, 1>(zero, c, p.part_cols, ks, mine, parts_full);
       }
-      tc_fence_before_sync();
+    }
+    tc_fence_before_sync();
+  }
+  if (ks > 1) {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // everything is sent
+    if (warp >= 2 && warp < 6) {
+      if (!mbar_wait_cluster(parts_full, 0, nullptr, p.err, kDevErrTimeoutEpilogue)) finished = false;
+      for (int c = 0; c < p.part_cols; ++c) {
+        const int col = rank * p.part_cols + c;
+        if (col >= cols) break;
+        float sum = 0.0f;
+        // [rank][group of part_vec columns][lane][column in the group]
+        const int at = (c / p.part_vec * 128 + q * 32 + lane) * p.part_vec + c % p.part_vec;
+        for (int k = 0; k < ks; ++k) sum += parts[k * p.part_cols * 128 + at];
+        float a = ag[0];
+#pragma unroll
+        for (int i = 1; i < static_cast<int>(sizeof(ag) / 4); ++i) a = col / 32 == i ? ag[i] : a;
+        store(col, sum, __shfl_sync(0xFFFFFFFFu, a, col & 31));
+      }
     }
     __syncwarp();
-    cluster_sync();
-    if (warp >= 2) {
-      // Four columns at a time, so that 4 ks loads are under way together.
-      const int c1 = cols * (rank + 1) / ks;
-      for (int c = cols * rank / ks; c < c1; c += 4) {
-        float v[4][8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i][k] = k < ks && c + i < c1
-                          ? ld_shared_cluster_f32(part + (c + i) * 128 + q * 32 + lane, static_cast<uint32_t>(k))
-                          : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float sum = v[i][0];
-#pragma unroll
-          for (int k = 1; k < 8; ++k) sum += v[i][k];
-          if (finished && c + i < c1) store(c + i, sum);
-        }
-      }
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA ends while another reads its sums
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // no CTA ends before all that is sent to it
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(tmem, p.tmem_cols);
   }
 }
 
@@ -363,14 +538,6 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 // (Relaxed: what it hands over is tensor memory, ordered by the tcgen05 fences.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// mbar_wait for a barrier that threads of both CTAs arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* err,
-                                                  unsigned code) {
-  const uint32_t a = smem_u32(bar);
-  return mbar_try_wait_cluster(a, parity) ||
-         (mbar_wait(bar, parity, abort, err, code) && mbar_try_wait_cluster(a, parity));
 }
 
 template <class C>
@@ -712,27 +879,60 @@ bool pair_fits(const Fp4Params& p) {
          (p.M + 255) / 128 * p.ktiles < int64_t{1} << 30 && (p.N + 255) / 128 * p.ktiles < int64_t{1} << 30;
 }
 
+// CTAs of a tile's cluster: up to one and a half to an SM, of two stages at least
+// (layers, us, with 1 / 2 / 4 / 8: 1 x 7168 x 18432 40 / 23.3 / 17.6 / 21.4;
+// 1 x 2112 x 7168 15.4 / 9.7 / 6.6 / 5.7; 8 x 10944 x 2048 7.0 / 6.6 / 9.3 / 12.7).
+int few_split(int64_t tiles, int stages_k, int sm_count) {
+  int64_t ks = 3 * sm_count / 2 / tiles;
+  if (ks > stages_k / 2) ks = stages_k / 2;
+  return ks < 1 ? 1 : ks > 8 ? 8 : static_cast<int>(ks);
+}
+
+// Whether a call's activations are quantised by the product's own CTAs: up to 8192
+// numbers (1 x 24576 x 1536 4.9 us, by a kernel of their own 6.6; 2 x 10944 x 2048 5.4
+// and 6.5; 8 x 10944 x 2048, 16384 numbers, 7.7 and 6.6), of which a CTA's share takes a
+// corner of its shared memory.
+bool fuses(const DevInfo* d, int64_t M, int64_t N, int64_t K) {
+  const int stages_k = static_cast<int>((K + kStageK - 1) / kStageK);
+  const int ks = few_split((N + 127) / 128, stages_k, d->sm_count);
+  return M <= 16 && M * K <= 128 * kFuseUnits * 16 && (stages_k + ks - 1) / ks <= 12;
+}
+
 template <class C>
-int launch_swapped(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, Fp4Params p, cudaStream_t stream) {
+int launch_few(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, Fp4Params p, cudaStream_t stream) {
   static std::once_flag once[kMaxDevices];
   static cudaError_t set[kMaxDevices];
   std::call_once(once[d->device], [&] {
-    set[d->device] = cudaFuncSetAttribute(fp4_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    set[d->device] = cudaFuncSetAttribute(fp4_gemm_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   });
   if (set[d->device] != cudaSuccess) return FP8BLK_ERR_CUDA;
   const int64_t tiles = p.tiles_n * ((p.M + C::BN - 1) / C::BN);
-  int ks = 1;
-#ifdef FP4_KS
-  while (ks < FP4_KS && ks < p.stages_k) ++ks;
-#else
-  while (ks < 8 && ks < p.stages_k && tiles * (ks + 1) <= 2 * d->sm_count) ++ks;
-#endif
+  const int cols = static_cast<int>(p.M < C::BN ? p.M : C::BN);
+  const int ks = few_split(tiles, p.stages_k, d->sm_count);
   if (tiles * ks >= int64_t{1} << 31) return FP8BLK_ERR_SHAPE;
   p.ksplit = ks;
+  p.part_cols = (cols + ks - 1) / ks;
+  p.part_vec = p.part_cols > 2 ? 4 : p.part_cols;
+  p.part_cols = (p.part_cols + p.part_vec - 1) / p.part_vec * p.part_vec;
+  // Two CTAs to an SM where three stages fit half of its shared memory: an uneven last
+  // round is then spread, and the next product's CTAs start beside this one's.
+  const int most_n = (p.stages_k + ks - 1) / ks;
+  const int other = 1024 + (C::FUSE ? most_n * (C::kFuseCodes + C::kFuseScales) + 256 : 0) +
+                    (ks > 1 ? ks * p.part_cols * 512 : 0) + C::kBarBytes;
+  const bool two = 113 * 1024 - other >= 3 * C::kStageBytes;
+  p.tmem_cols = two ? 256 : 512;
+  p.stages = ((two ? 113 : 226) * 1024 - other) / C::kStageBytes;
+  if (p.stages > most_stages<C>(p.tmem_cols)) p.stages = most_stages<C>(p.tmem_cols);
+  if (p.stages > most_n) p.stages = most_n;
+  if (p.stages < 1) return FP8BLK_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.blockDim = dim3(kFewThreads);
+  // (At least so much that no SM holds more CTAs than its tensor memory has columns
+  // for: one that waits for columns while its cluster waits for it could wait forever.)
+  cfg.dynamicSmemBytes = other + p.stages * C::kStageBytes;
+  const size_t least = (two ? 78 : 116) * 1024;
+  if (cfg.dynamicSmemBytes < least) cfg.dynamicSmemBytes = least;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -747,18 +947,23 @@ int launch_swapped(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& m
 
 template <int FMT>
 int run_fmt(const DevInfo* d, const void* a, const void* w, int64_t K, const Fp4Params& p, cudaStream_t stream) {
-#ifndef FP4_PAIR_MIN
-#define FP4_PAIR_MIN 256
-#endif
-  if (p.M >= FP4_PAIR_MIN && pair_fits(p)) return launch_pair<FMT>(d, a, w, K, p, stream);
-  const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   CUtensorMap mw, ma;
+  if (p.x) {
+    if (!make_code_map(&mw, w, p.N, K / 2, 128)) return FP8BLK_ERR_CUDA;
+    return launch_few<Cfg<16, FMT, true>>(d, mw, mw, p, stream);
+  }
+  // From 17 tokens on the pairs are as fast (24 x 7168 x 2048: 7.5 us, the other 7.8; 61:
+  // 7.6 and 9), but for up to 64 tokens of few weight tiles, whose K only the clusters
+  // split (32 x 1536 x 7168, 6 pairs: 7.6 us by clusters of 8).
+  const bool pairs = p.M > 64 || (p.M > 16 && (p.N + kPairN - 1) / kPairN >= 24);
+  if (pairs && pair_fits(p)) return launch_pair<FMT>(d, a, w, K, p, stream);
+  const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   if (!make_code_map(&mw, w, p.N, K / 2, 128) || !make_code_map(&ma, a, p.M, K / 2, bn)) return FP8BLK_ERR_CUDA;
   switch (bn) {
-    case 16: return launch_swapped<Cfg<16, FMT>>(d, mw, ma, p, stream);
-    case 32: return launch_swapped<Cfg<32, FMT>>(d, mw, ma, p, stream);
-    case 64: return launch_swapped<Cfg<64, FMT>>(d, mw, ma, p, stream);
-    default: return launch_swapped<Cfg<128, FMT>>(d, mw, ma, p, stream);
+    case 16: return launch_few<Cfg<16, FMT, false>>(d, mw, ma, p, stream);
+    case 32: return launch_few<Cfg<32, FMT, false>>(d, mw, ma, p, stream);
+    case 64: return launch_few<Cfg<64, FMT, false>>(d, mw, ma, p, stream);
+    default: return launch_few<Cfg<128, FMT, false>>(d, mw, ma, p, stream);  // (rows that the pair kernel cannot store)
   }
 }
 
@@ -767,9 +972,13 @@ bool gemm_shape_ok(int64_t M, int64_t N, int64_t K) {
          K <= int64_t{1} << 28;
 }
 
-int gemm_checked(const DevInfo* d, const void* a, const void* a_s, const float* a_g, const void* w, const void* w_s,
-                 const float* w_g, void* c, int64_t M, int64_t N, int64_t K, int fmt, cudaStream_t stream) {
+// x: the activations where the product quantises them itself (else null, with a, a_s, a_g).
+int gemm_checked(const DevInfo* d, const void* x, int64_t x_stride, const void* a, const void* a_s, const float* a_g,
+                 const void* w, const void* w_s, const float* w_g, void* c, int64_t M, int64_t N, int64_t K, int fmt,
+                 cudaStream_t stream) {
   Fp4Params p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.x_stride = x_stride;
   p.w_s = static_cast<const uint8_t*>(w_s);
   p.a_s = static_cast<const uint8_t*>(a_s);
   p.w_g = w_g;
@@ -816,7 +1025,7 @@ extern "C" int fp8blk_fp4_gemm(const void* a, const void* a_s, const float* a_g,
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
   if (fmt == kFp4UE8M0) a_g = w_g = nullptr;
-  return gemm_checked(d, a, a_s, a_g, w, w_s, w_g, c_bf16, M, N, K, fmt, s);
+  return gemm_checked(d, nullptr, 0, a, a_s, a_g, w, w_s, w_g, c_bf16, M, N, K, fmt, s);
 }
 
 // Workspace of the linear layer: [codes M K / 2][scale tiles][row scales 4 M], each part 256-byte aligned.
@@ -845,10 +1054,12 @@ extern "C" int fp8blk_fp4_linear(const void* x_bf16, int64_t x_stride, const voi
   if (workspace_bytes < fp8blk_fp4_linear_workspace_bytes(M, N, K, fmt)) return FP8BLK_ERR_WORKSPACE;
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
+  const bool rows = fmt == kFp4E4M3;
+  if (fuses(d, M, N, K))
+    return gemm_checked(d, x_bf16, x_stride, nullptr, nullptr, nullptr, w, w_s, rows ? w_g : nullptr, y_bf16, M, N, K, fmt, s);
   uint8_t* q = static_cast<uint8_t*>(workspace);
   uint8_t* qs = q + align256(static_cast<size_t>(M) * (K / 2));
   float* g = reinterpret_cast<float*>(qs + align256(static_cast<size_t>(fp4_scale_bytes(M, K, fmt))));
   if (int st = fp4_quant_launch(x_bf16, false, x_stride, M, K, fmt, q, qs, g, d->sm_count, s)) return st;
-  const bool rows = fmt == kFp4E4M3;
-  return gemm_checked(d, q, qs, rows ? g : nullptr, w, w_s, rows ? w_g : nullptr, y_bf16, M, N, K, fmt, s);
+  return gemm_checked(d, nullptr, 0, q, qs, rows ? g : nullptr, w, w_s, rows ? w_g : nullptr, y_bf16, M, N, K, fmt, s);
 }
