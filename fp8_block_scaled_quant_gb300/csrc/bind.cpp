@@ -6,7 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -104,7 +104,7 @@ const at::Tensor& plain(PyObject* o, at::ScalarType type, at::IntArrayRef shape,
 }
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, like.options().dtype(type));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 // The given output, or a new one.

@@ -914,12 +914,12 @@ int launch_few(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, F
   p.part_cols = (cols + ks - 1) / ks;
   p.part_vec = p.part_cols > 2 ? 4 : p.part_cols;
   p.part_cols = (p.part_cols + p.part_vec - 1) / p.part_vec * p.part_vec;
-  // Two CTAs to an SM where three stages fit half of its shared memory: an uneven last
+  // Two CTAs to an SM where three stages (two of a share of K) fit half of its shared memory: an uneven last
   // round is then spread, and the next product's CTAs start beside this one's.
   const int most_n = (p.stages_k + ks - 1) / ks;
   const int other = 1024 + (C::FUSE ? most_n * (C::kFuseCodes + C::kFuseScales) + 256 : 0) +
                     (ks > 1 ? ks * p.part_cols * 512 : 0) + C::kBarBytes;
-  const bool two = 113 * 1024 - other >= 3 * C::kStageBytes;
+  const bool two = 113 * 1024 - other >= (ks > 1 ? 2 : 3) * C::kStageBytes;
   p.tmem_cols = two ? 256 : 512;
   p.stages = ((two ? 113 : 226) * 1024 - other) / C::kStageBytes;
   if (p.stages > most_stages<C>(p.tmem_cols)) p.stages = most_stages<C>(p.tmem_cols);
