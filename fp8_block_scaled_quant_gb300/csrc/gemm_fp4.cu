@@ -728,26 +728,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, turn, abort_flag, p.err, kDevErrTimeoutEpilogue));
       if (!ok) continue;
       tc_fence_after_sync();
-      uint32_t packed[64];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(acc + c * 32, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-          if (p.a_g) {
-            const float4 g4 = *reinterpret_cast<const float4*>(factors + c * 32 + i * 4);
-            f[0] = ag * g4.x, f[1] = ag * g4.y, f[2] = ag * g4.z, f[3] = ag * g4.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[4 * i + 2 * j]) * f[2 * j],
-                                                           __uint_as_float(r[4 * i + 2 * j + 1]) * f[2 * j + 1]);
-            packed[c * 16 + i * 2 + j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-        }
-      }
+      // All 128 columns into registers and the accumulator back to the MMAs, then the rest.
+      uint32_t r[2][64];
+      tmem_ld_32x32b_x64(acc, r[0]);
+      tmem_ld_32x32b_x64(acc + 64, r[1]);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(hand_back);
@@ -757,10 +741,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < 8; ++c) {  // eight columns
+          uint32_t packed[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (p.a_g) {
+              const float4 g4 = *reinterpret_cast<const float4*>(factors + h * 64 + c * 8 + i * 4);
+              f[0] = ag * g4.x, f[1] = ag * g4.y, f[2] = ag * g4.z, f[3] = ag * g4.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int at = c * 8 + i * 4 + j * 2;
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[h][at]) * f[2 * j],
+                                                             __uint_as_float(r[h][at + 1]) * f[2 * j + 1]);
+              packed[2 * i + j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
           *reinterpret_cast<uint4*>(out + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(packed[h * 32 + c * 4], packed[h * 32 + c * 4 + 1], packed[h * 32 + c * 4 + 2],
-                         packed[h * 32 + c * 4 + 3]);
+              make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row < p.M && col0 + h * 64 < p.N) {  // (lane 0 has the box's first row)
