@@ -9,7 +9,10 @@ A prompt that all requests share is written into the cache once; then every step
     mla_absorb     the latent output into the heads' values ("v"), then the output linear
     moe_layer      gate, routed and shared experts of the step's tokens (at most 32) in one kernel
 
-    python examples/decode_step.py [--batch 4] [--prefix 300] [--steps 5] [--graph]
+With --fp4 the attention's linears have 4-bit weights and activations, and residual_norm takes the place of the torch
+norms and residual sums around them: it writes the normed hidden state in the codes that fp4_gemm reads.
+
+    python examples/decode_step.py [--batch 4] [--prefix 300] [--steps 5] [--graph] [--fp4]
 
 prints each step's hidden state norm and how far the attention is from its formula in 64 bits. With --graph one step
 is captured once and replayed: lengths, positions and slots are device tensors, so nothing in it depends on the host.
@@ -40,22 +43,30 @@ def rope_table(n, device, base=10000.0):
 
 
 class Layer:
-    """One layer's weights: FP8 linears with block scales, the gate in bf16, norms in fp32."""
+    """One layer's weights: FP8 linears with block scales (fp4: those of the attention but wkv_b in 4 bits), the gate in
+    bf16, norms in fp32."""
 
-    def __init__(self, dim=1024, heads=16, experts=32, inter=512, topk=4, shared=1, max_pos=4096, device="cuda", seed=0):
+    def __init__(self, dim=1024, heads=16, experts=32, inter=512, topk=4, shared=1, max_pos=4096, device="cuda", seed=0,
+                 fp4=False):
         g = torch.Generator(device=device).manual_seed(seed)
 
+        def weight(rows, cols):
+            return torch.randn(rows, cols, generator=g, device=device) * cols ** -0.5
+
         def fp8(rows, cols):
-            return fb.weight_quant(torch.randn(rows, cols, generator=g, device=device) * cols ** -0.5)
+            return fb.weight_quant(weight(rows, cols))
+
+        linear = (lambda rows, cols: fb.fp4_quant(weight(rows, cols))) if fp4 else fp8
+        self.fp4 = fp4
 
         self.dim, self.heads, self.topk, self.shared = dim, heads, topk, shared
         self.norm_attn = torch.ones(dim, device=device)
         self.norm_ffn = torch.ones(dim, device=device)
         self.norm_kv = torch.ones(LATENT, device=device)
-        self.wq = fp8(heads * (NOPE + ROPE), dim)
-        self.wkv_a = fp8(LATENT + ROPE, dim)
+        self.wq = linear(heads * (NOPE + ROPE), dim)
+        self.wkv_a = linear(LATENT + ROPE, dim)
         self.wkv_b = fp8(heads * (NOPE + VALUE), LATENT)
-        self.wo = fp8(dim, heads * VALUE)
+        self.wo = linear(dim, heads * VALUE)
         self.gate = (torch.randn(experts, dim, generator=g, device=device) * dim ** -0.5).to(torch.bfloat16)
         n = experts + shared
         self.w1, self.w3, self.w2 = fp8(n * inter, dim), fp8(n * inter, dim), fp8(n * dim, inter)
@@ -88,7 +99,10 @@ class Cache:
 
 def write_prompt(layer, cache, x):
     """The prompt's rows, once: x bf16 [prefix, dim]."""
-    kv = fb.linear(rms_norm(x, layer.norm_attn), *layer.wkv_a)
+    if layer.fp4:
+        kv = fb.fp4_gemm(*fb.residual_norm(x, None, layer.norm_attn, quant="fp4")[1], *layer.wkv_a)
+    else:
+        kv = fb.linear(rms_norm(x, layer.norm_attn), *layer.wkv_a)
     pos = torch.arange(x.shape[0], device=x.device)
     fb.mla_append(kv, layer.norm_kv, layer.rope, pos, cache.prefix_slots(), cache.rows)
 
@@ -96,9 +110,13 @@ def write_prompt(layer, cache, x):
 def step(layer, cache, x):
     """One token per request: x bf16 [batch, dim] -> the layer's output and the attention's operands and output."""
     b = x.shape[0]
-    h = rms_norm(x, layer.norm_attn)
-    q = fb.linear(h, *layer.wq).view(b, layer.heads, NOPE + ROPE)
-    kv = fb.linear(h, *layer.wkv_a)
+    if layer.fp4:
+        _, h = fb.residual_norm(x, None, layer.norm_attn, quant="fp4")
+        q, kv = fb.fp4_gemm(*h, *layer.wq), fb.fp4_gemm(*h, *layer.wkv_a)
+    else:
+        h = rms_norm(x, layer.norm_attn)
+        q, kv = fb.linear(h, *layer.wq), fb.linear(h, *layer.wkv_a)
+    q = q.view(b, layer.heads, NOPE + ROPE)
     q_nope, q_pe = fb.mla_append(kv, layer.norm_kv, layer.rope, cache.prefix + cache.lens.long(), cache.slots(),
                                  cache.rows, q=q)
     cache.lens += 1
@@ -106,8 +124,13 @@ def step(layer, cache, x):
     o = fb.mla_attention(q_lat, q_pe, cache.rows, cache.table, cache.lens, layer.scale,
                          prefix_pages=cache.prefix_pages, prefix_len=cache.prefix)
     v = fb.mla_absorb(o, *layer.wkv_b, "v")
-    x = x + fb.linear(v.view(b, layer.heads * VALUE), *layer.wo)
-    y = fb.moe_layer(rms_norm(x, layer.norm_ffn), layer.gate, *layer.w1, *layer.w3, *layer.w2, layer.topk,
+    v = v.view(b, layer.heads * VALUE)
+    if layer.fp4:
+        x, h = fb.residual_norm(fb.fp4_linear(v, *layer.wo), x, layer.norm_ffn)
+    else:
+        x = x + fb.linear(v, *layer.wo)
+        h = rms_norm(x, layer.norm_ffn)
+    y = fb.moe_layer(h, layer.gate, *layer.w1, *layer.w3, *layer.w2, layer.topk,
                      n_shared=layer.shared)
     return x + y, q_lat, q_pe, o
 
@@ -132,10 +155,11 @@ def main(argv=None):
     a.add_argument("--prefix", type=int, default=300)
     a.add_argument("--steps", type=int, default=5)
     a.add_argument("--graph", action="store_true")
+    a.add_argument("--fp4", action="store_true")
     a = a.parse_args(argv)
     if not 1 <= a.batch <= fb.MOE_LAYER_MAX_TOKENS:
         raise SystemExit(f"--batch: 1 to {fb.MOE_LAYER_MAX_TOKENS}")
-    layer, cache = Layer(), Cache(a.batch, a.prefix, a.steps + 2)
+    layer, cache = Layer(fp4=a.fp4), Cache(a.batch, a.prefix, a.steps + 2)
     g = torch.Generator(device="cuda").manual_seed(1)
     write_prompt(layer, cache, torch.randn(a.prefix, layer.dim, generator=g, device="cuda").to(torch.bfloat16))
     first = torch.randn(a.batch, layer.dim, generator=g, device="cuda").to(torch.bfloat16)

@@ -29,6 +29,7 @@ struct QuantParams {
   int units;    // K / 16
   int threads;  // of a row
   int wide;     // rows aligned to 32 bytes
+  int early;    // the next kernel may start beside this one (inside a layer: what it reads ahead are weights)
 };
 
 __device__ __forceinline__ void load32(const void* p, bool wide, uint32_t* w) {
@@ -95,7 +96,7 @@ __device__ __forceinline__ void store_unit(const QuantParams& p, int64_t row, in
 template <typename T, int FMT, int P>
 __global__ void __launch_bounds__(kMaxThreads) fp4_quant_kernel(const QuantParams p) {
   __shared__ uint32_t part[kMaxThreads / 32];
-  griddep_launch_dependents();
+  if (p.early) griddep_launch_dependents();
   griddep_wait();
   const int n = p.threads, lane = threadIdx.x & 31;
   // (n is 32 where a block has several rows; a warp leaves as a whole)
@@ -162,7 +163,6 @@ struct DequantParams {
 // blockDim.x units of a row, blockDim.y rows.
 template <int FMT>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantParams p) {
-  griddep_launch_dependents();
   griddep_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;
@@ -219,8 +219,9 @@ bool fp4_fmt_valid(int fmt) { return fmt == kFp4E4M3 || fmt == kFp4UE8M0; }
 
 // Arguments checked by the caller.
 int fp4_quant_launch(const void* x, bool fp32, int64_t x_stride, int64_t M, int64_t K, int fmt, void* q, void* s, float* g,
-                     int sm_count, cudaStream_t stream) {
+                     int sm_count, bool early, cudaStream_t stream) {
   QuantParams p{};
+  p.early = early;
   p.x = x;
   p.q = static_cast<uint2*>(q);
   p.s = static_cast<uint8_t*>(s);
@@ -268,7 +269,7 @@ extern "C" int fp8blk_fp4_quant(const void* x, int is_fp32, int64_t x_stride, in
     return FP8BLK_ERR_ALIGN;
   const DevInfo* d;
   if (int st = current_device(&d)) return st;
-  return fp4_quant_launch(x, is_fp32 == 1, x_stride, M, K, fmt, q, s, g, d->sm_count,
+  return fp4_quant_launch(x, is_fp32 == 1, x_stride, M, K, fmt, q, s, g, d->sm_count, false,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 

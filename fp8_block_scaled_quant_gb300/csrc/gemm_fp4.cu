@@ -29,7 +29,7 @@ namespace fp8blk {
 
 bool fp4_fmt_valid(int fmt);
 int fp4_quant_launch(const void* x, bool fp32, int64_t x_stride, int64_t M, int64_t K, int fmt, void* q, void* s, float* g,
-                     int sm_count, cudaStream_t stream);
+                     int sm_count, bool early, cudaStream_t stream);
 
 namespace {
 
@@ -1060,6 +1060,6 @@ extern "C" int fp8blk_fp4_linear(const void* x_bf16, int64_t x_stride, const voi
   uint8_t* q = static_cast<uint8_t*>(workspace);
   uint8_t* qs = q + align256(static_cast<size_t>(M) * (K / 2));
   float* g = reinterpret_cast<float*>(qs + align256(static_cast<size_t>(fp4_scale_bytes(M, K, fmt))));
-  if (int st = fp4_quant_launch(x_bf16, false, x_stride, M, K, fmt, q, qs, g, d->sm_count, s)) return st;
+  if (int st = fp4_quant_launch(x_bf16, false, x_stride, M, K, fmt, q, qs, g, d->sm_count, true, s)) return st;
   return gemm_checked(d, nullptr, 0, q, qs, rows ? g : nullptr, w, w_s, rows ? w_g : nullptr, y_bf16, M, N, K, fmt, s);
 }

@@ -109,7 +109,14 @@ def operands(M, N, K, fmt, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     a = torch.randn(M, K, generator=g, device="cuda").bfloat16()
     w = torch.randn(N, K, generator=g, device="cuda") * 0.05
-    return fb.fp4_quant(a, fmt), fb.fp4_quant(w, fmt)
+    return quantised(a, w, fmt)
+
+
+def quantised(a, w, fmt):
+    """Both operands, finished: a weight may be read before the calls just before the product have ended."""
+    both = fb.fp4_quant(a, fmt), fb.fp4_quant(w, fmt)
+    torch.cuda.synchronize()
+    return both
 
 
 def dense(op, fmt):
@@ -169,7 +176,7 @@ def test_gemm_keeps_bad_rows_apart(M, fmt):
     x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
     wt = torch.randn(N, K, generator=g, device="cuda")
     x[1, 5], wt[17, 600] = float("inf"), float("nan")
-    a, w = fb.fp4_quant(x, fmt), fb.fp4_quant(wt, fmt)
+    a, w = quantised(x, wt, fmt)
     for op, rows in ((a, M), (w, N)):
         flat = op[1].permute(0, 3, 2, 1, 4).reshape(-1, op[1].shape[1] * 4)      # a copy [rows, blocks]
         flat[rows:] = 255
@@ -189,7 +196,7 @@ def test_gemm_large_and_small_numbers(fmt):
     g = torch.Generator(device="cuda").manual_seed(4)
     x = torch.randn(M, K, generator=g, device="cuda") * torch.exp2(torch.linspace(-60, 60, M, device="cuda"))[:, None]
     wt = torch.randn(N, K, generator=g, device="cuda") * torch.exp2(torch.linspace(-50, 50, N, device="cuda"))[:, None]
-    a, w = fb.fp4_quant(x.bfloat16(), fmt), fb.fp4_quant(wt, fmt)
+    a, w = quantised(x.bfloat16(), wt, fmt)
     check_product(fb.fp4_gemm(*a, *w, fmt), dense(a, fmt), dense(w, fmt), K)
 
 
@@ -208,7 +215,7 @@ def test_linear_is_quant_and_gemm(M, N, K, fmt):
 
 
 def test_empty_sizes():
-    w = fb.fp4_quant(torch.randn(64, 256, device="cuda"))
+    _, w = operands(1, 64, 256, fb.FP4_E4M3, 0)
     x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
     assert fb.fp4_linear(x, *w).shape == (0, 64)
     q, s, g = fb.fp4_quant(x)
@@ -291,3 +298,31 @@ def test_refusals():
         with pytest.raises(fb.Fp8BlkError):
             f()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(3, 300, 640), (1, 2112, 7168), (5, 128, 1536)])
+def test_linear_keeps_bad_tokens_apart(M, N, K, fmt):
+    """Few tokens are quantised by the product's own blocks: zeros, a NaN, an infinity and far scales as by fp4_quant."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    _, w = quantised(x, torch.randn(N, K, generator=g, device="cuda"), fmt)
+    bad = []
+    for i, what in enumerate(["zero", "nan", "inf", "small", "large"]):
+        y = x.clone()
+        row = i % M
+        if what == "zero":
+            y[row] = 0
+        elif what == "nan":
+            y[row, K // 2] = float("nan")
+        elif what == "inf":
+            y[row, 3] = -float("inf")
+        else:
+            y[row] *= 2.0 ** (-110 if what == "small" else 100)
+        y = y.bfloat16()
+        got, want = fb.fp4_linear(y, *w, fmt), fb.fp4_gemm(*fb.fp4_quant(y, fmt), *w, fmt)
+        if not (torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))):
+            bad.append(what)
+        if what in ("nan", "inf"):
+            assert bool(got[row].isnan().all()) and int(got.isnan().any(1).sum()) == 1
+    assert not bad

@@ -199,6 +199,7 @@ def test_the_seam_feeds_the_products(T, fmt):
     up = fb.fp4_quant(torch.randn(N, D, generator=g, device="cuda") * D ** -0.5, fmt)
     down = fb.weight_quant(torch.randn(D, N, generator=g, device="cuda") * N ** -0.5)
     w2 = 1 + torch.randn(N, generator=g, device="cuda") * 0.1
+    torch.cuda.synchronize()
 
     def layer(sync=lambda: None):
         r, h = fb.residual_norm(**a, quant="fp4", scale_fmt=fmt)
