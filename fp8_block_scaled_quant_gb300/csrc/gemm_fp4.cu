@@ -190,13 +190,20 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     tma_prefetch_desc(&map_w);
     if constexpr (!C::FUSE) tma_prefetch_desc(&map_a);
   }
+  if (ks > 1) {
+    // This CTA's barrier of partial sums is there (waited for before they are sent).
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  // No CTA waits for another of its cluster while it holds tensor memory or waits for
+  // it (the arrival above is before the allocation, the release before the wait for the
+  // sums): its columns may be another kernel's, whose cluster waits for this SM's.
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (ks > 1) cluster_sync();  // the barriers of the CTAs that sums are sent to
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   // After the allocation: a CTA of the next kernel that came first to this SM's
@@ -399,6 +406,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (warp >= 2 && warp < 6) {
     // The accumulator: lane = weight row, column = token.
     const float* mine = parts + (rank * p.part_cols * 128 + (q * 32 + lane) * p.part_vec);
+    if (ks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
     for (int c0 = 0; c0 < C::BN; c0 += kStep) {
       if (c0 >= (ks == 1 ? cols : ks * p.part_cols)) break;
@@ -426,9 +434,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
     }
     tc_fence_before_sync();
+    named_barrier_arrive(2, 160);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    named_barrier_sync(2, 160);  // the accumulator has been read
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, p.tmem_cols);
   }
   if (ks > 1) {
-    __syncwarp();
+    if (warp < 2 || warp == 6) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // everything is sent
     if (warp >= 2 && warp < 6) {
       if (!mbar_wait_cluster(parts_full, 0, nullptr, p.err, kDevErrTimeoutEpilogue)) finished = false;
@@ -447,11 +462,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // no CTA ends before all that is sent to it
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after_sync();
-    tmem_dealloc(tmem, p.tmem_cols);
   }
 }
 
@@ -888,14 +898,16 @@ int few_split(int64_t tiles, int stages_k, int sm_count) {
   return ks < 1 ? 1 : ks > 8 ? 8 : static_cast<int>(ks);
 }
 
-// Whether a call's activations are quantised by the product's own CTAs: up to 8192
-// numbers (1 x 24576 x 1536 4.9 us, by a kernel of their own 6.6; 2 x 10944 x 2048 5.4
-// and 6.5; 8 x 10944 x 2048, 16384 numbers, 7.7 and 6.6), of which a CTA's share takes a
-// corner of its shared memory.
+// Whether a call's activations are quantised by the product's own CTAs (us, and by a
+// kernel of their own): a token of up to 8192 numbers (1 x 24576 x 1536 4.9 and 6.6; 1 x
+// 2112 x 7168 5.8 and 5.9; 1 x 1536 x 7168 5.1 and 5.5), or up to 4096 numbers of more
+// (2 x 24576 x 1536 5.4 and 6.7; 2 x 10944 x 2048 5.4 and 5.9; 4 x 10944 x 2048, 8192
+// numbers, 6.4 and 5.9; 5 x 7168 x 1536 5.6 and 5.1), where a CTA's share takes a corner
+// of its shared memory.
 bool fuses(const DevInfo* d, int64_t M, int64_t N, int64_t K) {
   const int stages_k = static_cast<int>((K + kStageK - 1) / kStageK);
   const int ks = few_split((N + 127) / 128, stages_k, d->sm_count);
-  return M <= 16 && M * K <= 128 * kFuseUnits * 16 && (stages_k + ks - 1) / ks <= 12;
+  return M <= 16 && M * K <= 128 * kFuseUnits * 16 / (M == 1 ? 1 : 2) && (stages_k + ks - 1) / ks <= 12;
 }
 
 template <class C>
@@ -928,8 +940,7 @@ int launch_few(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, F
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks));
   cfg.blockDim = dim3(kFewThreads);
-  // (At least so much that no SM holds more CTAs than its tensor memory has columns
-  // for: one that waits for columns while its cluster waits for it could wait forever.)
+  // (At least so much that no SM is given more CTAs than its tensor memory has columns for.)
   cfg.dynamicSmemBytes = other + p.stages * C::kStageBytes;
   const size_t least = (two ? 78 : 116) * 1024;
   if (cfg.dynamicSmemBytes < least) cfg.dynamicSmemBytes = least;

@@ -477,7 +477,7 @@ FP8BLK_API int fp8blk_moe_layer(const void *x_bf16, const void *gate_w_bf16, con
  *   s[row / 128][block / 4][row % 32][row % 128 / 32][block % 4]
  * of ceil(rows / 128) x (blocks / 4) tiles, fp8blk_fp4_scale_bytes in all. The
  * bytes of rows past the last one may hold anything.
- * K is a multiple of 128 throughout (FP8BLK_ERR_SHAPE).
+ * K is a multiple of 128 throughout (FP8BLK_ERR_SHAPE). No output may overlap an input.
  */
 #define FP8BLK_FP4_E4M3 0
 #define FP8BLK_FP4_UE8M0 1
@@ -511,12 +511,12 @@ FP8BLK_API int fp8blk_fp4_dequant(const void *q, const void *s, const float *g, 
  *   C[m, n] = bf16( a_g[m] * w_g[n] * sum over blocks b of
  *                   a_s[m, b] * w_s[n, b] * sum_{k in b} a[m, k] * w[n, k] )
  * (UE8M0: without a_g and w_g, which may be NULL). The block-scaled MMA applies
- * the block scales and sums in fp32. a [M, K/2], w [N, K/2] and scale tiles
- * 16-byte aligned, c bf16 [M, N] of any alignment of its elements, row scales
- * 4-byte aligned; any M and N up to 2^28. K == 0 writes zeros. The result does
- * not vary from run to run. No workspace. Weights (w, w_s) may be read before
- * the previous kernel on the stream has ended (the overlap rule above); w_g may
- * not.
+ * the block scales and sums in fp32; a_g * w_g is one fp32 product. a [M, K/2],
+ * w [N, K/2] and scale tiles 16-byte aligned, c bf16 [M, N] of any alignment of
+ * its elements, row scales 4-byte aligned; any M and N up to 2^28. K == 0 writes
+ * zeros. The result does not vary from run to run. No workspace. Weights (w, w_s)
+ * may be read before the previous kernel on the stream has ended (the overlap rule
+ * above); w_g may not.
  */
 FP8BLK_API int fp8blk_fp4_gemm(const void *a, const void *a_s, const float *a_g, const void *w, const void *w_s,
                                const float *w_g, void *c_bf16, int64_t M, int64_t N, int64_t K, int fmt,

@@ -326,3 +326,41 @@ def test_linear_keeps_bad_tokens_apart(M, N, K, fmt):
         if what in ("nan", "inf"):
             assert bool(got[row].isnan().all()) and int(got.isnan().any(1).sum()) == 1
     assert not bad
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", [(1, 8192), (1, 8320), (2, 2048), (2, 2176), (16, 256), (16, 384), (17, 256)])
+def test_linear_on_both_sides_of_the_fused_sizes(M, K, fmt):
+    """Where the activations stop being quantised inside the product, the numbers stay the same."""
+    x = random_rows(M, K, M * K).cuda()
+    _, w = operands(1, 333, K, fmt, 5)
+    want = fb.fp4_gemm(*fb.fp4_quant(x, fmt), *w, fmt)
+    assert torch.equal(fb.fp4_linear(x, *w, fmt), want)
+
+
+def test_two_streams():
+    """Products split over clusters, of every size of tensor memory, and an FP8 linear, from two streams at once: they
+    share SMs (and columns of tensor memory), and each gives what it gives alone."""
+    fmt = fb.FP4_E4M3
+    shapes = [(8, 2112, 7168), (100, 1533, 1536), (1, 2112, 7168), (40, 640, 7168), (100, 333, 7168), (600, 1536, 512)]
+    pairs = [operands(m, n, k, fmt, i) for i, (m, n, k) in enumerate(shapes)]
+    x8 = torch.randn(4, 2048, device="cuda").bfloat16()
+    w8 = fb.weight_quant(torch.randn(1408, 2048, device="cuda"))
+    torch.cuda.synchronize()
+    want = [fb.fp4_gemm(*a, *w, fmt) for a, w in pairs]
+    want8 = fb.linear(x8, *w8)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for turn in range(12):
+        for side, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                for i in range(len(pairs)):
+                    j = (i + turn + 3 * side) % len(pairs)
+                    got[side].append((want[j], fb.fp4_gemm(*pairs[j][0], *pairs[j][1], fmt)))
+                got[side].append((want8, fb.linear(x8, *w8)))
+    torch.cuda.synchronize()
+    for side in got:
+        for a, b in side:
+            assert torch.equal(a, b)
+    assert fb.last_device_error() == 0
