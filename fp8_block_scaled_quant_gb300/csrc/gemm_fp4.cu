@@ -5,8 +5,8 @@
 // The block-scaled MMA applies sa and sw itself (products of e2m1 numbers and
 // their scales, summed in fp32 in tensor memory), the epilogue the row scales.
 //
-// Two kernels. Few tokens: 128 weight rows are the MMA's M (tensor-memory lanes), up
-// to 128 tokens its columns; memory bounds it. Many tokens: 256 x 256 tiles of CTA
+// Two kernels. Few tokens: 128 weight rows are the MMA's M (tensor-memory lanes), 16,
+// 32 or 64 tokens its columns; memory and latency bound it. Many tokens: tiles of CTA
 // pairs, at the tensor cores' rate (below). In both, 256 of K make a stage: codes by
 // TMA (128-byte rows, 128-byte swizzle), scale tiles in the order of their use, from
 // shared into tensor memory by tcgen05.cp in the order of the MMAs.
@@ -52,7 +52,6 @@ struct Fp4Params {
   int ksplit;              // few tokens: CTAs of a tile's cluster
   int stages;              // few tokens: slots of the ring
   int part_cols, part_vec; // few tokens: columns that a CTA of the cluster sums, and that it is sent at once
-  uint32_t tmem_cols;      // few tokens
 };
 
 // ---- few tokens ------------------------------------------------------------------------
@@ -90,12 +89,12 @@ struct Cfg {
   static constexpr int kBarBytes = (3 * kMaxStages + 3) * 8 + 16 + 64;
 };
 
-// Stage slots that `cols` columns of tensor memory have room for.
+// Stage slots that half of tensor memory has room for.
+constexpr int kFewTmemCols = 256;
 template <class C>
-constexpr int most_stages(int cols) {
-  const int n = (cols - C::kAccCols) / C::kSfCols - 2;
-  return n < kMaxStages ? n : kMaxStages;
-}
+constexpr int kMostStages = (kFewTmemCols - C::kAccCols) / C::kSfCols - 2 < kMaxStages
+                                ? (kFewTmemCols - C::kAccCols) / C::kSfCols - 2
+                                : kMaxStages;
 
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -139,6 +138,27 @@ __device__ __forceinline__ void send_columns(const uint32_t* r, int c0, int shar
     if (to < ks)
       st_async<V>(map_to_rank(smem_u32(part + (c - to * share) * 128), static_cast<uint32_t>(to)), r + i,
                   map_to_rank(smem_u32(bar), static_cast<uint32_t>(to)));
+  }
+}
+
+// The sums of a share's columns, parts [rank][share / V][128][V] in rank order, to
+// put(column, sum).
+template <int V, typename Put>
+__device__ __forceinline__ void sum_columns(const float* parts, int ks, int share, int lane, const Put& put) {
+  struct alignas(4 * V) Part {
+    float v[V];
+  };
+  const Part* at = reinterpret_cast<const Part*>(parts) + lane;
+  for (int g = 0; g < share; g += V, at += 128) {
+    float sum[V] = {};
+#pragma unroll 4
+    for (int k = 0; k < ks; ++k) {
+      const Part part = at[k * (share / V) * 128];
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += part.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) put(g + i, sum[i]);
   }
 }
 
@@ -199,7 +219,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   // it (the arrival above is before the allocation, the release before the wait for the
   // sums): its columns may be another kernel's, whose cluster waits for this SM's.
   if (warp == 1) {
-    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_alloc(tmem_slot, kFewTmemCols);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -258,6 +278,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   } else if (warp == 1) {
     const bool leader = elect_one_sync();
     const uint32_t sf_w = tmem + C::kAccCols, sf_t = sf_w + static_cast<uint32_t>(p.stages * C::kSfCols);
+    const uint32_t sf_first = static_cast<uint32_t>(m0 >> 5) & 3;  // a column holds the scales of 32 tokens
     auto all = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.err, kDevErrTimeoutMma));
     };
@@ -300,7 +321,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if (!C::FUSE && !(ok = all(&full_t[st], phase))) break;
       token_scales(i, st);
       const uint64_t ad = sdesc_kmajor_sw128(smem_u32(smem + st * C::kStageBytes)), bd = sdesc_kmajor_sw128(token_codes(i, st));
-      const uint32_t sfa = sf_w + static_cast<uint32_t>(st * C::kSfCols), sfb = sf_t + static_cast<uint32_t>((i & 1) * C::kSfCols);
+      const uint32_t sfa = sf_w + static_cast<uint32_t>(st * C::kSfCols), sfb = sf_t + static_cast<uint32_t>((i & 1) * C::kSfCols) + sf_first;
       const int left = p.ksteps - (k0 + i) * 4, steps = left < 4 ? left : 4;  // 2 or 4
       if (leader) {
 #pragma unroll
@@ -440,25 +461,24 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   if (warp == 1) {
     named_barrier_sync(2, 160);  // the accumulator has been read
     tc_fence_after_sync();
-    tmem_dealloc(tmem, p.tmem_cols);
+    tmem_dealloc(tmem, kFewTmemCols);
   }
   if (ks > 1) {
     if (warp < 2 || warp == 6) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // everything is sent
     if (warp >= 2 && warp < 6) {
       if (!mbar_wait_cluster(parts_full, 0, nullptr, p.err, kDevErrTimeoutEpilogue)) finished = false;
-      for (int c = 0; c < p.part_cols; ++c) {
+      auto put = [&](int c, float sum) {
         const int col = rank * p.part_cols + c;
-        if (col >= cols) break;
-        float sum = 0.0f;
-        // [rank][group of part_vec columns][lane][column in the group]
-        const int at = (c / p.part_vec * 128 + q * 32 + lane) * p.part_vec + c % p.part_vec;
-        for (int k = 0; k < ks; ++k) sum += parts[k * p.part_cols * 128 + at];
         float a = ag[0];
 #pragma unroll
         for (int i = 1; i < static_cast<int>(sizeof(ag) / 4); ++i) a = col / 32 == i ? ag[i] : a;
-        store(col, sum, __shfl_sync(0xFFFFFFFFu, a, col & 31));
-      }
+        a = __shfl_sync(0xFFFFFFFFu, a, col & 31);
+        if (col < cols) store(col, sum, a);
+      };
+      if (p.part_vec == 4) sum_columns<4>(parts, ks, p.part_cols, q * 32 + lane, put);
+      else if (p.part_vec == 2) sum_columns<2>(parts, ks, p.part_cols, q * 32 + lane, put);
+      else sum_columns<1>(parts, ks, p.part_cols, q * 32 + lane, put);
     }
     __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // no CTA ends before all that is sent to it
@@ -467,35 +487,39 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 // ---- CTA pairs -----------------------------------------------------------------------
 //
-// Many tokens: 256 tokens x 256 weight rows to a pair of CTAs (cta_group::2), tokens
-// as tensor-memory lanes. Each CTA has 128 tokens and half of the weight rows, so a
-// byte of either operand is fetched once per 256 products; both have the scales of
-// all 256 weight rows. One accumulator of 256 columns: the epilogue's eight warps
-// take it out in bf16 registers, hand it back, and store from there while the next
-// tile is summed.
+// Many tokens: 256 tokens x 256 weight rows (128 where those are few tiles) to a pair
+// of CTAs (cta_group::2), tokens as tensor-memory lanes. Each CTA has 128 tokens and
+// half of the weight rows, so a byte of either operand is fetched once per 256
+// products; both have the scales of all the tile's weight rows. The accumulator is
+// single: the epilogue's eight warps take it out into registers, hand it back, and
+// convert and store from there while the next tile is summed. A stage brings 38 KB to
+// each SM in 0.35 us, 0.9 of what an SM takes from L2, while the tensor pipe is 82 %
+// active at 1.85 GHz (4096 x 18432 x 7168: 155 us, 7.0 PFLOP/s; power-of-two scales 150).
 //
 //   warps 0, 2   producers: this CTA's codes and scales, completing on the leader's barriers
 //   warp 1       MMA issuer (leader CTA); both allocate tensor memory
-//   warps 4-11   epilogue: lane quarter warp % 4, columns 128 (warp >= 8) on
+//   warps 4-11   epilogue: lane quarter warp % 4, the tile's second half from warp 8 on
 
 constexpr int kPairThreads = 384;
-constexpr int kPairN = 256;
 
-template <int FMT_>
+template <int BN_, int FMT_>
 struct PairCfg {
-  static constexpr int FMT = FMT_;
+  static constexpr int BN = BN_, FMT = FMT_;
+  static constexpr int kHalf = BN / 2;                           // weight rows of a CTA; columns of an epilogue half
+  static constexpr int kSfRows = BN / 128;                       // scale tile rows of the weights
   static constexpr int kTiles = FMT == kFp4E4M3 ? 4 : 2;
   static constexpr int kSfBytes = kTiles * kScaleTile;           // 128 rows of a stage
-  static constexpr int kSfaAt = 2 * kLaneBytes, kSfbAt = kSfaAt + kSfBytes;
-  static constexpr int kTxBytes = kSfbAt + 2 * kSfBytes;         // of one CTA
+  static constexpr int kSfaAt = kLaneBytes + kHalf * 128, kSfbAt = kSfaAt + kSfBytes;
+  static constexpr int kTxBytes = kSfbAt + kSfRows * kSfBytes;   // of one CTA
   static constexpr int kStageBytes = (kTxBytes + 1023) / 1024 * 1024;
-  static constexpr int kStages = 5;
-  static constexpr int kSfCols = kTiles * 12;                    // 4 for the tokens, 8 for the weights
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kSfStep = 4 + 4 * kSfRows;                // columns of 4 blocks' scales: tokens', weights'
+  static constexpr int kSfCols = kTiles * kSfStep;
   static constexpr int kOutAt = kStages * kStageBytes;           // 8 warps x 4 KB
-  static constexpr int kFactorsAt = kOutAt + 8 * 4096;           // the tile's 256 weight row scales
-  static constexpr int kBarsAt = kFactorsAt + kPairN * 4;
+  static constexpr int kFactorsAt = kOutAt + 8 * 4096;           // the tile's weight row scales
+  static constexpr int kBarsAt = kFactorsAt + BN * 4;
   static constexpr int kSmem = 1024 + kBarsAt + (2 * kStages + 3) * 8 + 8;
-  static_assert(kPairN + 2 * kSfCols <= 512, "tensor memory");
+  static_assert(BN + 2 * kSfCols <= 512, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const int tm = c.tile % p.tiles_m, tn = c.tile / p.tiles_m;
         c.k = 0;
         c.y_a = codes ? tm * 256 + rank * 128 : (tm * 2 + rank) * ktiles;
-        c.y_w = codes ? tn * kPairN + rank * 128 : tn * 2 * ktiles;
+        c.y_w = codes ? tn * C::BN + rank * C::kHalf : tn * C::kSfRows * ktiles;
       };
       auto advance = [&](Cursor& c) {
         if (++c.st == C::kStages) c.st = 0, c.at = smem0, c.bar = bar0;
@@ -632,8 +656,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[c.st], 2 * C::kTxBytes);
           tma_load_pair(c.at + kLaneBytes, &map_w, c.bar, c.k * 128, c.y_w);
         } else {
-          tma_load_pair(c.at + C::kSfbAt, &map_ws, c.bar, 0, c.y_w + c.k * C::kTiles);
-          tma_load_pair(c.at + C::kSfbAt + C::kSfBytes, &map_ws, c.bar, 0, c.y_w + ktiles + c.k * C::kTiles);
+#pragma unroll
+          for (int r = 0; r < C::kSfRows; ++r)
+            tma_load_pair(c.at + C::kSfbAt + r * C::kSfBytes, &map_ws, c.bar, 0, c.y_w + r * ktiles + c.k * C::kTiles);
         }
       };
       auto tokens = [&](const Cursor& c) {
@@ -666,7 +691,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1 && rank == 0) {
     const bool leader = elect_one_sync();
-    const uint32_t sf0 = tmem + kPairN;
+    const uint32_t sf0 = tmem + C::BN;
     bool ok = true;
     int st = 0;
     uint32_t turn = 0, phase = 0, sf_turn = 0;
@@ -688,14 +713,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           for (int j = 0; j < 4; ++j) {
             if (j >= left) break;
             const int t = C::FMT == kFp4E4M3 ? j : j / 2;
-            const uint32_t sfa = sf + static_cast<uint32_t>(12 * t), sfb = sfa + 4;
+            const uint32_t sfa = sf + static_cast<uint32_t>(C::kSfStep * t), sfb = sfa + 4;
             if (C::FMT == kFp4E4M3 || (j & 1) == 0) {
               tmem_cp_scales_pair(sfa, sdesc_scale_tile(at + C::kSfaAt + t * kScaleTile));
-              tmem_cp_scales_pair(sfb, sdesc_scale_tile(at + C::kSfbAt + t * kScaleTile));
-              tmem_cp_scales_pair(sfb + 4, sdesc_scale_tile(at + C::kSfbAt + C::kSfBytes + t * kScaleTile));
+#pragma unroll
+              for (int r = 0; r < C::kSfRows; ++r)
+                tmem_cp_scales_pair(sfb + 4 * r, sdesc_scale_tile(at + C::kSfbAt + r * C::kSfBytes + t * kScaleTile));
             }
             mma_fp4_pair<C::FMT>(tmem, ad + 2 * j, bd + 2 * j,
-                                 idesc_fp4(256, kPairN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa, sfb,
+                                 idesc_fp4(256, C::BN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa, sfb,
                                  k > 0 || j > 0 ? 1u : 0u);
           }
           mma_commit_pair(&empty[st]);
@@ -715,39 +741,39 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     griddep_wait();  // row scales of the tokens; the output may be the previous kernel's to read
     const int w = warp - 4, q = warp & 3, half = w >> 2;
     uint8_t* out = smem + C::kOutAt + w * 4096;
-    float* factors = reinterpret_cast<float*>(smem + C::kFactorsAt + half * 512);
-    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
+    float* factors = reinterpret_cast<float*>(smem + C::kFactorsAt + half * C::kHalf * 4);
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * C::kHalf);
     const uint32_t hand_back = pair_leader_addr(acc_empty);
     uint32_t turn = 0;
     bool ok = true;
     for (int tile = pair; tile < tiles; tile += pairs, turn ^= 1) {
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
       const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32 + lane;
-      const int64_t col0 = static_cast<int64_t>(tn) * kPairN + half * 128;
+      const int64_t col0 = static_cast<int64_t>(tn) * C::BN + half * C::kHalf;
       float ag = 1.0f;
       if (p.a_g) {
-        // The four warps of these columns bring 32 of their scales each.
-        const int64_t c = col0 + q * 32 + lane;
-        const float wg = c < p.N ? __ldg(p.w_g + c) : 0.0f;
+        // The four warps of these columns bring up to 32 of their scales each.
+        const int in = q * 32 + lane;
+        const float wg = in < C::kHalf && col0 + in < p.N ? __ldg(p.w_g + col0 + in) : 0.0f;
         if (row < p.M) ag = __ldg(p.a_g + row);
         named_barrier_sync(1 + half, 128);  // the tile before has been multiplied
-        factors[q * 32 + lane] = wg;
+        if (in < C::kHalf) factors[in] = wg;
         named_barrier_sync(1 + half, 128);
       }
       // (After a wait that gave up the warps still meet at their barriers, and store nothing.)
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, turn, abort_flag, p.err, kDevErrTimeoutEpilogue));
       if (!ok) continue;
       tc_fence_after_sync();
-      // All 128 columns into registers and the accumulator back to the MMAs, then the rest.
-      uint32_t r[2][64];
-      tmem_ld_32x32b_x64(acc, r[0]);
-      tmem_ld_32x32b_x64(acc + 64, r[1]);
+      // All columns into registers and the accumulator back to the MMAs, then the rest.
+      uint32_t r[C::kHalf / 64][64];
+#pragma unroll
+      for (int h = 0; h < C::kHalf / 64; ++h) tmem_ld_32x32b_x64(acc + h * 64, r[h]);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(hand_back);
       // 64 columns at a time through a swizzled box of 32 rows.
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < C::kHalf / 64; ++h) {
         if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
         __syncwarp();
 #pragma unroll
@@ -850,9 +876,8 @@ bool make_out_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols) {
 
 constexpr int kMaxDevices = 64;
 
-template <int FMT>
+template <class C>
 int launch_pair(const DevInfo* d, const void* a, const void* w, int64_t K, Fp4Params p, cudaStream_t stream) {
-  using C = PairCfg<FMT>;
   static std::once_flag once[kMaxDevices];
   static cudaError_t set[kMaxDevices];
   std::call_once(once[d->device], [&] {
@@ -861,12 +886,12 @@ int launch_pair(const DevInfo* d, const void* a, const void* w, int64_t K, Fp4Pa
   if (set[d->device] != cudaSuccess) return FP8BLK_ERR_CUDA;
   CUtensorMap ma, mw, mas, mws, mc;
   const uint64_t at = static_cast<uint64_t>((p.M + 127) / 128 * p.ktiles), wt = static_cast<uint64_t>((p.N + 127) / 128 * p.ktiles);
-  if (!make_code_map(&ma, a, p.M, K / 2, 128) || !make_code_map(&mw, w, p.N, K / 2, 128) ||
+  if (!make_code_map(&ma, a, p.M, K / 2, 128) || !make_code_map(&mw, w, p.N, K / 2, C::kHalf) ||
       !make_scale_map(&mas, p.a_s, at, C::kTiles) || !make_scale_map(&mws, p.w_s, wt, C::kTiles) ||
       !make_out_map(&mc, p.c, p.M, p.N))
     return FP8BLK_ERR_CUDA;
   p.tiles_m = static_cast<int>((p.M + 255) / 256);
-  p.tiles_n = static_cast<int>((p.N + kPairN - 1) / kPairN);
+  p.tiles_n = static_cast<int>((p.N + C::BN - 1) / C::BN);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n, pairs = d->sm_count / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
@@ -884,18 +909,42 @@ int launch_pair(const DevInfo* d, const void* a, const void* w, int64_t K, Fp4Pa
 // Whether a product's sizes fit the pair kernel's 32-bit tile coordinates and its
 // output the vector stores.
 bool pair_fits(const Fp4Params& p) {
-  const int64_t tiles = (p.M + 255) / 256 * ((p.N + kPairN - 1) / kPairN);
+  const int64_t tiles = (p.M + 255) / 256 * ((p.N + 127) / 128);
   return p.N % 8 == 0 && is_aligned(p.c, 16) && tiles * p.stages_k < int64_t{1} << 30 &&
          (p.M + 255) / 128 * p.ktiles < int64_t{1} << 30 && (p.N + 255) / 128 * p.ktiles < int64_t{1} << 30;
 }
 
-// CTAs of a tile's cluster: up to one and a half to an SM, of two stages at least
-// (layers, us, with 1 / 2 / 4 / 8: 1 x 7168 x 18432 40 / 23.3 / 17.6 / 21.4;
-// 1 x 2112 x 7168 15.4 / 9.7 / 6.6 / 5.7; 8 x 10944 x 2048 7.0 / 6.6 / 9.3 / 12.7).
+// Tiles of 128 weight rows where all of them run at once: twice the SMs then bring the
+// operands (128 x 2112 x 7168 9.8 us, of 256 rows 11.3; 200 x 5120 x 7168 10.7 and 11.6;
+// in two rounds against one of 256 rows, 517 x 5120 x 7168, 17.7 and 12.9; in three
+// against two, 700 x 7168 x 2048, 10.0 and 9.1).
+bool narrow_tiles(const DevInfo* d, const Fp4Params& p) {
+  return (p.M + 255) / 256 * ((p.N + 127) / 128) <= d->sm_count / 2;
+}
+
+// CTAs of a tile's cluster, of two stages of K at least: as many as give every SM one,
+// or one and a half where a CTA would have eight stages or more (8 tokens, us: 4096 x
+// 4096 4.0 at one, 5.8 at one and a half; 4096 x 7168 5.6 and 5.9; 7168 x 7168 8.9 and
+// 7.2; 7168 x 18432 20.7 and 15.6; without a split 8.8, 13.9, 14.6 and 35.2).
 int few_split(int64_t tiles, int stages_k, int sm_count) {
-  int64_t ks = 3 * sm_count / 2 / tiles;
+  int64_t ks = sm_count / tiles;
+  if (stages_k >= 8 * (ks < 1 ? 1 : ks)) ks = 3 * sm_count / 2 / tiles;
   if (ks > stages_k / 2) ks = stages_k / 2;
   return ks < 1 ? 1 : ks > 8 ? 8 : static_cast<int>(ks);
+}
+
+// Whether pairs multiply. Up to 32 tokens, where K is four stages or less and the weight
+// rows are few (us: 32 x 2112 x 1024 3.8 and 4.7, but 32 x 2112 x 2048 4.9 and 4.2, 32 x
+// 18432 x 1536 6.9 and 6.1). With more, unless splitting K saves more than the longer
+// rows of partial sums cost (33 x 2112 x 7168 9.6 and 6.6, 48 x 5120 x 2048 5.7 and 6.1)
+// and, from 49 on, the clusters take a part of the SMs, more of it the longer K is (128 x
+// 1024 x 7168 9.9 and 7.0, 256 x 2112 x 7168 10.2 and 12.3, 100 x 1536 x 4096 7.1 and 7.1).
+bool takes_pairs(const DevInfo* d, const Fp4Params& p) {
+  if (p.M <= 32) return p.M > 16 && p.stages_k <= 4 && p.tiles_n <= 32;
+  const int64_t tiles = p.tiles_n * ((p.M + 63) / 64);
+  const int ks = few_split(tiles, p.stages_k, d->sm_count);
+  if (6 * (p.stages_k - (p.stages_k + ks - 1) / ks) < (p.M < 64 ? p.M : 64) + 4) return true;
+  return p.M > 48 && (5 * tiles > 2 * d->sm_count || 3 * tiles > 5 * p.stages_k);
 }
 
 // Whether a call's activations are quantised by the product's own CTAs (us, and by a
@@ -926,15 +975,13 @@ int launch_few(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, F
   p.part_cols = (cols + ks - 1) / ks;
   p.part_vec = p.part_cols > 2 ? 4 : p.part_cols;
   p.part_cols = (p.part_cols + p.part_vec - 1) / p.part_vec * p.part_vec;
-  // Two CTAs to an SM where three stages (two of a share of K) fit half of its shared memory: an uneven last
-  // round is then spread, and the next product's CTAs start beside this one's.
+  // Two CTAs to an SM: an uneven last round is then spread, and the next product's CTAs
+  // start beside this one's.
   const int most_n = (p.stages_k + ks - 1) / ks;
   const int other = 1024 + (C::FUSE ? most_n * (C::kFuseCodes + C::kFuseScales) + 256 : 0) +
                     (ks > 1 ? ks * p.part_cols * 512 : 0) + C::kBarBytes;
-  const bool two = 113 * 1024 - other >= (ks > 1 ? 2 : 3) * C::kStageBytes;
-  p.tmem_cols = two ? 256 : 512;
-  p.stages = ((two ? 113 : 226) * 1024 - other) / C::kStageBytes;
-  if (p.stages > most_stages<C>(p.tmem_cols)) p.stages = most_stages<C>(p.tmem_cols);
+  p.stages = (113 * 1024 - other) / C::kStageBytes;
+  if (p.stages > kMostStages<C>) p.stages = kMostStages<C>;
   if (p.stages > most_n) p.stages = most_n;
   if (p.stages < 1) return FP8BLK_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
@@ -942,8 +989,7 @@ int launch_few(const DevInfo* d, const CUtensorMap& mw, const CUtensorMap& ma, F
   cfg.blockDim = dim3(kFewThreads);
   // (At least so much that no SM is given more CTAs than its tensor memory has columns for.)
   cfg.dynamicSmemBytes = other + p.stages * C::kStageBytes;
-  const size_t least = (two ? 78 : 116) * 1024;
-  if (cfg.dynamicSmemBytes < least) cfg.dynamicSmemBytes = least;
+  if (cfg.dynamicSmemBytes < 78 * 1024) cfg.dynamicSmemBytes = 78 * 1024;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -963,18 +1009,15 @@ int run_fmt(const DevInfo* d, const void* a, const void* w, int64_t K, const Fp4
     if (!make_code_map(&mw, w, p.N, K / 2, 128)) return FP8BLK_ERR_CUDA;
     return launch_few<Cfg<16, FMT, true>>(d, mw, mw, p, stream);
   }
-  // From 17 tokens on the pairs are as fast (24 x 7168 x 2048: 7.5 us, the other 7.8; 61:
-  // 7.6 and 9), but for up to 64 tokens of few weight tiles, whose K only the clusters
-  // split (32 x 1536 x 7168, 6 pairs: 7.6 us by clusters of 8).
-  const bool pairs = p.M > 64 || (p.M > 16 && (p.N + kPairN - 1) / kPairN >= 24);
-  if (pairs && pair_fits(p)) return launch_pair<FMT>(d, a, w, K, p, stream);
-  const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  if (takes_pairs(d, p) && pair_fits(p))
+    return narrow_tiles(d, p) ? launch_pair<PairCfg<128, FMT>>(d, a, w, K, p, stream)
+                              : launch_pair<PairCfg<256, FMT>>(d, a, w, K, p, stream);
+  const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
   if (!make_code_map(&mw, w, p.N, K / 2, 128) || !make_code_map(&ma, a, p.M, K / 2, bn)) return FP8BLK_ERR_CUDA;
   switch (bn) {
     case 16: return launch_few<Cfg<16, FMT, false>>(d, mw, ma, p, stream);
     case 32: return launch_few<Cfg<32, FMT, false>>(d, mw, ma, p, stream);
-    case 64: return launch_few<Cfg<64, FMT, false>>(d, mw, ma, p, stream);
-    default: return launch_few<Cfg<128, FMT, false>>(d, mw, ma, p, stream);  // (rows that the pair kernel cannot store)
+    default: return launch_few<Cfg<64, FMT, false>>(d, mw, ma, p, stream);
   }
 }
 

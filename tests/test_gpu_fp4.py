@@ -339,7 +339,7 @@ def test_linear_on_both_sides_of_the_fused_sizes(M, K, fmt):
 
 
 def test_two_streams():
-    """Products split over clusters, of every size of tensor memory, and an FP8 linear, from two streams at once: they
+    """Products split over clusters, of pairs, and an FP8 linear, from two streams at once: they
     share SMs (and columns of tensor memory), and each gives what it gives alone."""
     fmt = fb.FP4_E4M3
     shapes = [(8, 2112, 7168), (100, 1533, 1536), (1, 2112, 7168), (40, 640, 7168), (100, 333, 7168), (600, 1536, 512)]
