@@ -1,7 +1,7 @@
 // The Python binding of the calls that a decode step issues between its large
 // kernels: tensors checked, outputs allocated and the C ABI called without a line
-// of Python in between (a norm of one token runs in 2.3 us, and took 12 to issue
-// through ctypes; 5 from here). Marshalling only, as in the package's ctypes calls; the
+// of Python in between (a norm of one token runs in 2.1 us, and took 12 to issue
+// through ctypes; 3.4 to 4.5 from here). Marshalling only, as in the package's ctypes calls; the
 // computation is in libfp8blk, whose functions are handed over by setup().
 #include <Python.h>
 
