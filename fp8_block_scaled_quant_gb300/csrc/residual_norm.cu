@@ -7,8 +7,8 @@
 //   h = r * rsqrt(mean(r^2) + eps) * norm_w    -> bf16, or act_quant, or fp4_quant
 //
 // fp32 from the inputs to the one rounding of each output (the norm reads r
-// before it is rounded). One block of threads to a token, 16 columns to a thread
-// and unit (a quantisation block of e2m1, an eighth of one of e4m3), the row in
+// before it is rounded). One block of threads to a token (or to token after token,
+// below), 16 columns to a thread and unit (a quantisation block of e2m1, an eighth of one of e4m3), the row in
 // registers from the first read to the last write. HBM bounds many tokens, launch
 // and two block-wide sums a single one.
 #include <cuda_bf16.h>
@@ -47,6 +47,8 @@ struct NormParams {
   int cols, units;                // units: ceil(cols / 16)
   int ahead;                      // tokens between a row and the one prefetched
   int ue8m0;
+  int64_t rows;
+  unsigned* err;
 };
 
 // 16 columns of a bf16 row, as they are read: at once where WIDE (all rows and
@@ -139,10 +141,10 @@ __device__ __forceinline__ float block_sum(float v, float* at) {
   return block_reduce(v, 0.0f, at, [](float a, float b) { return a + b; });
 }
 
-// Four sums over the block at once. In a warp each of the first two exchanges
-// halves the values that a lane goes on with: lanes 8 k .. 8 k + 7 end with sum k.
-__device__ __forceinline__ float4 block_sum4(float4 v, float* at) {
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5, k = lane >> 3;
+// Four sums over a warp at once: each of the first two exchanges halves the values
+// that a lane goes on with, so lanes 8 k .. 8 k + 7 end with sum k.
+__device__ __forceinline__ float warp_sum4(float4 v) {
+  const int k = (threadIdx.x & 31) >> 3;
   float a = k & 2 ? v.z : v.x, b = k & 2 ? v.w : v.y;
   a += __shfl_xor_sync(0xFFFFFFFFu, k & 2 ? v.x : v.z, 16);
   b += __shfl_xor_sync(0xFFFFFFFFu, k & 2 ? v.y : v.w, 16);
@@ -150,14 +152,15 @@ __device__ __forceinline__ float4 block_sum4(float4 v, float* at) {
   s += __shfl_xor_sync(0xFFFFFFFFu, k & 1 ? a : b, 8);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (warps > 1) {
-    if ((lane & 7) == 0) at[(threadIdx.x >> 5) * 4 + k] = s;
-    __syncthreads();
-    const int w = lane & 7;  // and w + 8: at most 16 warps
-    s = (w < warps ? at[w * 4 + k] : 0.0f) + (w + 8 < warps ? at[(w + 8) * 4 + k] : 0.0f);
+  return s;
+}
+
+// The block's sums from those of its warps (at[4 warp + k], at most 16 warps).
+__device__ __forceinline__ float4 warps_sum4(const float* at) {
+  const int warps = blockDim.x >> 5, k = (threadIdx.x & 31) >> 3, w = threadIdx.x & 7;
+  float s = (w < warps ? at[w * 4 + k] : 0.0f) + (w + 8 < warps ? at[(w + 8) * 4 + k] : 0.0f);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  }
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   return make_float4(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 8), __shfl_sync(0xFFFFFFFFu, s, 16),
                      __shfl_sync(0xFFFFFFFFu, s, 24));
 }
@@ -243,151 +246,100 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// A block to a token, P units to a thread. EARLY: norm_w is asked for with the rows
-// (few tokens); otherwise where it is used, from L1, which keeps registers free
-// for another block to an SM (4099 x 7168 with a norm of y, into e4m3: 50.7 us with
-// two blocks of 448 threads at 72 registers, 47.6 with the next rows prefetched;
-// 55 with two units to a thread, rows through shared memory 49 to 57: the blocks'
-// arithmetic between their loads, not HBM, sets the time then).
-template <int OUT, int P, bool WIDE, bool EARLY>
-__global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(const NormParams p) {
-  constexpr int kWarps = kMaxThreads / 32;
-  __shared__ float sums[4 * kWarps], sum_y[kWarps], sum_r[kWarps], tops[kWarps];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int tid = threadIdx.x, n = blockDim.x;
-  const int64_t row = blockIdx.x;
-  const bool has_x = p.x != nullptr, tok = p.gate_tok != nullptr;
-  if (!EARLY && tid == 0 && row + p.ahead < gridDim.x) {
-    // The rows that a block will read when this one's place is free again, into L2.
-    const uint32_t bytes = static_cast<uint32_t>(p.cols) * 2;
-    prefetch_l2(p.y + (row + p.ahead) * p.y_stride, bytes);
-    if (has_x) prefetch_l2(p.x + (row + p.ahead) * p.x_stride, bytes);
-    if (tok) prefetch_l2(p.gate_tok + (row + p.ahead) * p.gate_stride, bytes);
-  }
-  uint32_t x[P][8];
-  float2 v[P][8], ne[EARLY ? P : 1][8];
+// r = s x + k1 v, in place of v.
+template <int P>
+__device__ __forceinline__ void add_residual(const NormParams& p, const uint32_t (&x)[P][8], float k1, float2 (&v)[P][8]) {
   const float2 scale2 = make_float2(p.residual_scale, p.residual_scale);
-  float2 yy = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    if (k1 != 1.0f)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], make_float2(k1, k1));
+    if (p.x)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __ffma2_rn(pair(x[u][i]), scale2, v[u][i]);
+  }
+}
+
+// A thread's parts of the sums of y^2 (given), v^2, x v and x^2.
+template <int P>
+__device__ __forceinline__ float4 row_sums(float2 yy, const float2 (&v)[P][8], const uint32_t (&x)[P][8]) {
+  float2 vv = make_float2(0.0f, 0.0f), xv = vv, xx = vv;
+#pragma unroll
+  for (int u = 0; u < P; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 xf = pair(x[u][i]);
+      vv = __ffma2_rn(v[u][i], v[u][i], vv);
+      xv = __ffma2_rn(xf, v[u][i], xv);
+      xx = __ffma2_rn(xf, xf, xx);
+    }
+  return make_float4(yy.x + yy.y, vv.x + vv.y, xv.x + xv.y, xx.x + xx.y);
+}
+
+// From the row's sums its residual, in place of v (y times its columns' factors, P units
+// to a thread), and the factor of its norm: sum r^2 = s^2 sum x^2 + 2 s k1 sum x v +
+// k1^2 sum v^2, unless the terms cancel (to less than a quarter) or leave fp32's range;
+// then false, and r comes the long way, in the order of the formula.
+template <int P, bool WIDE>
+__device__ __forceinline__ bool both_norms(const NormParams& p, int64_t row, float4 sum, const uint32_t (&x)[P][8],
+                                           float2 (&v)[P][8], float* k2, float* sum_y) {
+  const int tid = threadIdx.x, n = blockDim.x;
+  const float k1 = root_inverse(fmaf(sum.x, p.inv_n, p.eps)), s = p.residual_scale;
+  const float a = s * s * sum.w, b = k1 * k1 * sum.y, all = a + b;
+  const float rr = fmaf(2.0f * s * k1, sum.z, all);
+  if (sum.x > 1e-20f && sum.x < 1e30f && sum.y < 1e30f && all > 1e-20f && rr < 1e30f && rr > 0.25f * all) {
+    add_residual<P>(p, x, k1, v);
+    *k2 = root_inverse(fmaf(rr, p.inv_n, p.eps));
+    return true;
+  }
 #pragma unroll
   for (int u = 0; u < P; ++u) {
     const int unit = tid + u * n;
-    const bool in = unit < p.units;
-    uint32_t y[8], g[8];
-    read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, in, y);
-    read16<WIDE>(p.x + row * p.x_stride, unit, p.cols, in && has_x, x[u]);
-    if (tok) read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, in, g);
-    if constexpr (EARLY) read16<WIDE>(p.norm_w, in ? unit : 0, p.cols, ne[u]);
+    uint32_t y[8];
+    read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, unit < p.units, y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
-    if (p.post_w) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) yy = __ffma2_rn(v[u][i], v[u][i], yy);
-    }
-    // v becomes y times its columns' factors.
-    float2 w[8];
-    if (p.post_w) {
-      read16<WIDE>(p.post_w, in ? unit : 0, p.cols, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
-    }
-    if (p.gate_col) {
-      read16<WIDE>(p.gate_col, in ? unit : 0, p.cols, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
-    }
-    if (tok) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(g[i]));
-    }
   }
-  // r = s x + k1 v, and its square sum. With k1 to be found, all that both need is
-  // summed at once, and sum r^2 = s^2 sum x^2 + 2 s k1 sum x v + k1^2 sum v^2, unless
-  // the terms cancel (to less than a quarter) or leave fp32's range.
-  auto residual = [&](float k1) {
-#pragma unroll
-    for (int u = 0; u < P; ++u) {
-      if (k1 != 1.0f)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], make_float2(k1, k1));
-      if (has_x)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = __ffma2_rn(pair(x[u][i]), scale2, v[u][i]);
-    }
-  };
-  float k2 = 0.0f;
-  bool known = false;
-  if (p.post_w) {
-    float2 vv = make_float2(0.0f, 0.0f), xv = vv, xx = vv;
-#pragma unroll
-    for (int u = 0; u < P; ++u)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 xf = pair(x[u][i]);
-        vv = __ffma2_rn(v[u][i], v[u][i], vv);
-        xv = __ffma2_rn(xf, v[u][i], xv);
-        xx = __ffma2_rn(xf, xf, xx);
-      }
-    const float4 sum = block_sum4(make_float4(yy.x + yy.y, vv.x + vv.y, xv.x + xv.y, xx.x + xx.y), sums);
-    const float k1 = root_inverse(fmaf(sum.x, p.inv_n, p.eps)), s = p.residual_scale;
-    const float a = s * s * sum.w, b = k1 * k1 * sum.y, all = a + b;
-    const float rr = fmaf(2.0f * s * k1, sum.z, all);
-    if (sum.x > 1e-20f && sum.x < 1e30f && sum.y < 1e30f && all > 1e-20f && rr < 1e30f && rr > 0.25f * all) {
-      residual(k1);
-      k2 = root_inverse(fmaf(rr, p.inv_n, p.eps));
-      known = true;
-    } else {
-      // The long way: the row's own sums, one after the other, in the order of the formula.
-#pragma unroll
-      for (int u = 0; u < P; ++u) {
-        const int unit = tid + u * n;
-        uint32_t y[8];
-        read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, unit < p.units, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
-      }
-      const float k = rms_factor<P>(v, p.inv_n, p.eps, sum_y);
-#pragma unroll
-      for (int u = 0; u < P; ++u) {
-        const int unit = tid + u * n < p.units ? tid + u * n : 0;
-        float2 w[8], g[8];
-        read16<WIDE>(p.post_w, unit, p.cols, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(__fmul2_rn(v[u][i], make_float2(k, k)), w[i]);
-        if (p.gate_col) {
-          read16<WIDE>(p.gate_col, unit, p.cols, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], g[i]);
-        }
-        if (tok) {
-          uint32_t t[8];
-          read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, true, t);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(t[i]));
-        }
-      }
-      residual(1.0f);
-    }
-  } else {
-    residual(1.0f);
-  }
-  if (p.r) {
-#pragma unroll
-    for (int u = 0; u < P; ++u)
-      if (tid + u * n < p.units) write16<WIDE>(p.r + row * p.cols, tid + u * n, p.cols, v[u]);
-  }
-  if (!known) k2 = rms_factor<P>(v, p.inv_n, p.eps, sum_r);
-  k2 = apply_early<P>(v, k2);
-  const float2 k2k2 = make_float2(k2, k2);
-  // h / k2 = v norm_w
+  const float k = rms_factor<P>(v, p.inv_n, p.eps, sum_y);
 #pragma unroll
   for (int u = 0; u < P; ++u) {
     const int unit = tid + u * n < p.units ? tid + u * n : 0;
-    float2 w[8];
-    if constexpr (!EARLY) read16<WIDE>(p.norm_w, unit, p.cols, w);
+    float2 w[8], g[8];
+    read16<WIDE>(p.post_w, unit, p.cols, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], EARLY ? ne[u][i] : w[i]);
+    for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(__fmul2_rn(v[u][i], make_float2(k, k)), w[i]);
+    if (p.gate_col) {
+      read16<WIDE>(p.gate_col, unit, p.cols, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], g[i]);
+    }
+    if (p.gate_tok) {
+      uint32_t t[8];
+      read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, true, t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(t[i]));
+    }
   }
+  add_residual<P>(p, x, 1.0f, v);
+  return false;
+}
+
+template <int P, bool WIDE>
+__device__ __forceinline__ void write_residual(const NormParams& p, int64_t row, const float2 (&v)[P][8]) {
+  if (!p.r) return;
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int unit = static_cast<int>(threadIdx.x + u * blockDim.x);
+    if (unit < p.units) write16<WIDE>(p.r + row * p.cols, unit, p.cols, v[u]);
+  }
+}
+
+// h = k2 v, v being r times norm_w, in its type. `tops`: a place per warp.
+template <int OUT, int P, bool WIDE>
+__device__ __forceinline__ void write_h(const NormParams& p, int64_t row, float2 (&v)[P][8], float k2, uint32_t* tops) {
+  const int tid = threadIdx.x, n = blockDim.x;
+  const float2 k2k2 = make_float2(k2, k2);
   if constexpr (OUT == kOutBf16) {
 #pragma unroll
     for (int u = 0; u < P; ++u) {
@@ -426,7 +378,7 @@ __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(cons
     }
     RowScale rs{};
     if constexpr (OUT == kOutFp4E4M3) {
-      rs = fp4_row_scale(block_reduce(top, 0u, reinterpret_cast<uint32_t*>(tops),
+      rs = fp4_row_scale(block_reduce(top, 0u, tops,
                                       [](uint32_t a, uint32_t b) { return max(a, b); }));
       if (tid == 0) p.h_g[row] = rs.g;
     }
@@ -439,11 +391,179 @@ __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(cons
   }
 }
 
+// A block to a token, P units to a thread. EARLY: norm_w is asked for with the rows
+// (few tokens); otherwise where it is used, from L1, which keeps registers free
+// for another block to an SM (4099 x 7168 with a norm of y, into e4m3: 50.7 us with
+// two blocks of 448 threads, 47.4 with the next rows prefetched; 55 with two units to
+// a thread, rows through shared memory 49 to 57: the blocks' arithmetic between their
+// loads, not HBM, sets the time then).
+template <int OUT, int P, bool WIDE, bool EARLY>
+__global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(const NormParams p) {
+  constexpr int kWarps = kMaxThreads / 32;
+  __shared__ float sums[4 * kWarps], sum_y[kWarps], sum_r[kWarps];
+  __shared__ uint32_t tops[kWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, n = blockDim.x;
+  const int64_t row = blockIdx.x;
+  const bool has_x = p.x != nullptr, tok = p.gate_tok != nullptr;
+  if (!EARLY && tid == 0 && row + p.ahead < gridDim.x) {
+    // The rows that a block will read when this one's place is free again, into L2.
+    const uint32_t bytes = static_cast<uint32_t>(p.cols) * 2;
+    prefetch_l2(p.y + (row + p.ahead) * p.y_stride, bytes);
+    if (has_x) prefetch_l2(p.x + (row + p.ahead) * p.x_stride, bytes);
+    if (tok) prefetch_l2(p.gate_tok + (row + p.ahead) * p.gate_stride, bytes);
+  }
+  uint32_t x[P][8];
+  float2 v[P][8], ne[EARLY ? P : 1][8];
+  float2 yy = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int unit = tid + u * n;
+    const bool in = unit < p.units;
+    uint32_t y[8], g[8];
+    read16<WIDE>(p.y + row * p.y_stride, unit, p.cols, in, y);
+    read16<WIDE>(p.x + row * p.x_stride, unit, p.cols, in && has_x, x[u]);
+    if (tok) read16<WIDE>(p.gate_tok + row * p.gate_stride, unit, p.cols, in, g);
+    if constexpr (EARLY) read16<WIDE>(p.norm_w, in ? unit : 0, p.cols, ne[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
+    if (p.post_w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) yy = __ffma2_rn(v[u][i], v[u][i], yy);
+    }
+    // v becomes y times its columns' factors.
+    float2 w[8];
+    if (p.post_w) {
+      read16<WIDE>(p.post_w, in ? unit : 0, p.cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
+    }
+    if (p.gate_col) {
+      read16<WIDE>(p.gate_col, in ? unit : 0, p.cols, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], w[i]);
+    }
+    if (tok) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], pair(g[i]));
+    }
+  }
+  float k2 = 0.0f;
+  bool known = false;
+  if (p.post_w) {
+    const float sum = warp_sum4(row_sums<P>(yy, v, x));
+    if ((tid & 7) == 0) sums[(tid >> 5) * 4 + ((tid & 31) >> 3)] = sum;
+    __syncthreads();
+    known = both_norms<P, WIDE>(p, row, warps_sum4(sums), x, v, &k2, sum_y);
+  } else {
+    add_residual<P>(p, x, 1.0f, v);
+  }
+  write_residual<P, WIDE>(p, row, v);
+  if (!known) k2 = rms_factor<P>(v, p.inv_n, p.eps, sum_r);
+  k2 = apply_early<P>(v, k2);
+#pragma unroll
+  for (int u = 0; u < P; ++u) {
+    const int unit = tid + u * n < p.units ? tid + u * n : 0;
+    float2 w[8];
+    if constexpr (!EARLY) read16<WIDE>(p.norm_w, unit, p.cols, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = __fmul2_rn(v[u][i], EARLY ? ne[u][i] : w[i]);
+  }
+  write_h<OUT, P, WIDE>(p, row, v, k2, tops);
+}
+
+// Many tokens whose y is normed, without a gate by token, into types that need nothing
+// else of the whole row: a block keeps its columns' factors in registers and goes from row to row. The sums of the next row are under way
+// (its warps arrive on a barrier per row, of four in turn: a warp that writes a row's
+// sums has seen all warps' next but two, so they have read the ones four rows before)
+// while this one is finished, and the one after it is being read.
+template <int OUT>
+__global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(const NormParams p) {
+  constexpr int kWarps = kMaxThreads / 32;
+  __shared__ float sums[4][4 * kWarps], sum_y[kWarps], sum_r[kWarps];
+  __shared__ uint64_t summed[4];
+  const int tid = threadIdx.x, lane = tid & 31;
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&summed[i], blockDim.x >> 5);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  const bool in = tid < p.units;
+  const int unit = in ? tid : 0;
+  float2 norm[8], factor[8];
+  read16<true>(p.norm_w, unit, p.cols, norm);
+  read16<true>(p.post_w, unit, p.cols, factor);
+  if (p.gate_col) {
+    float2 w[8];
+    read16<true>(p.gate_col, unit, p.cols, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) factor[i] = __fmul2_rn(factor[i], w[i]);
+  }
+  const int64_t step = gridDim.x;
+  uint32_t y[8], x_new[1][8], x[1][8];
+  float2 v[1][8];
+  auto load = [&](int64_t row) {
+    read16<true>(p.y + row * p.y_stride, tid, p.cols, in && row < p.rows, y);
+    read16<true>(p.x + row * p.x_stride, tid, p.cols, in && row < p.rows && p.x, x_new[0]);
+    if (tid == 0 && row + step < p.rows) {
+      prefetch_l2(p.y + (row + step) * p.y_stride, static_cast<uint32_t>(p.cols) * 2);
+      if (p.x) prefetch_l2(p.x + (row + step) * p.x_stride, static_cast<uint32_t>(p.cols) * 2);
+    }
+  };
+  // A row that has been read: v, x, and its warps' sums.
+  auto begin = [&](float2 (&to)[1][8], uint32_t (&x_to)[1][8], int turn) {
+    float2 yy = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      to[0][i] = pair(y[i]);
+      yy = __ffma2_rn(to[0][i], to[0][i], yy);
+      to[0][i] = __fmul2_rn(to[0][i], factor[i]);
+      x_to[0][i] = x_new[0][i];
+    }
+    const float sum = warp_sum4(row_sums<1>(yy, to, x_to));
+    if ((lane & 7) == 0) sums[turn & 3][(tid >> 5) * 4 + (lane >> 3)] = sum;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&summed[turn & 3]);
+  };
+  int64_t row = blockIdx.x;
+  load(row);
+  begin(v, x, 0);
+  load(row + step);
+  for (int turn = 0; row < p.rows; row += step, ++turn) {
+    float2 v_next[1][8];
+    uint32_t x_next[1][8];
+    if (row + step < p.rows) {
+      begin(v_next, x_next, turn + 1);
+      load(row + 2 * step);
+    }
+    mbar_wait(&summed[turn & 3], (turn >> 2) & 1, nullptr, p.err, kDevErrTimeoutEpilogue);
+    float k2;
+    const bool known = both_norms<1, true>(p, row, warps_sum4(sums[turn & 3]), x, v, &k2, sum_y);
+    write_residual<1, true>(p, row, v);
+    if (!known) k2 = rms_factor<1>(v, p.inv_n, p.eps, sum_r);
+    k2 = apply_early<1>(v, k2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[0][i] = __fmul2_rn(v[0][i], norm[i]);
+    write_h<OUT, 1, true>(p, row, v, k2, nullptr);  // (no OUT that needs the places)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[0][i] = v_next[0][i], x[0][i] = x_next[0][i];
+  }
+}
+
 template <int OUT, bool WIDE>
 const void* kernel_of(int P, bool early) {
   return P == 2  ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 2, WIDE, false>)
          : early ? reinterpret_cast<const void*>(residual_norm_kernel<OUT, 1, WIDE, true>)
                  : reinterpret_cast<const void*>(residual_norm_kernel<OUT, 1, WIDE, false>);
+}
+
+const void* rows_kernel(int out) {
+  return out == kOutBf16   ? reinterpret_cast<const void*>(residual_norm_rows_kernel<kOutBf16>)
+         : out == kOutE4m3 ? reinterpret_cast<const void*>(residual_norm_rows_kernel<kOutE4m3>)
+                           : reinterpret_cast<const void*>(residual_norm_rows_kernel<kOutFp4UE8M0>);
 }
 
 template <int OUT>
@@ -501,6 +621,8 @@ extern "C" int fp8blk_residual_norm(const void* y_bf16, int64_t y_stride, const 
   p.inv_n = 1.0f / static_cast<float>(D);
   p.cols = static_cast<int>(D);
   p.ahead = d->sm_count;
+  p.rows = T;
+  p.err = d->err_word;
   p.units = static_cast<int>((D + 15) / 16);
   p.ue8m0 = fp8 && scale_fmt_ue8m0(scale_fmt);
   const auto wide_rows = [](const void* t, int64_t stride) { return !t || (is_aligned(t, 32) && stride % 16 == 0); };
@@ -510,12 +632,21 @@ extern "C" int fp8blk_residual_norm(const void* y_bf16, int64_t y_stride, const 
   const int P = p.units > kMaxThreads ? 2 : 1;
   const bool early = T <= 2 * d->sm_count;
   const int threads = ((p.units + P - 1) / P + 31) / 32 * 32;
-  const void* kernel = !fp8 && !fp4            ? kernel_for<kOutBf16>(P, wide, early)
+  // Blocks that go from row to row: where y is normed, the factors are the columns' alone,
+  // nothing but the norms needs the whole row, and blocks of 128 registers to a thread
+  // leave an SM twelve warps (us: 4099 x 7168 into e4m3 42.6, a block to a token 47.4; into
+  // bf16 40.1 and 41.5; 4099 x 8192 into e4m3 43.0 and 52.8; 500 x 7168 7.9 and 8.3; with
+  // ten warps, 8000 x 5120, 69.7 and 59.9; into e2m1 with row scales 55.0 and 48.5).
+  const int64_t places = kMaxThreads / threads;
+  const bool rows = !early && post_w && !gate_tok_bf16 && wide && P == 1 && !(fp4 && scale_fmt == kFp4E4M3) &&
+                    places * threads >= 384;
+  const void* kernel = rows                    ? rows_kernel(fp8 ? kOutE4m3 : fp4 ? kOutFp4UE8M0 : kOutBf16)
+                       : !fp8 && !fp4          ? kernel_for<kOutBf16>(P, wide, early)
                        : fp8                   ? kernel_for<kOutE4m3>(P, wide, early)
                        : scale_fmt == kFp4E4M3 ? kernel_for<kOutFp4E4M3>(P, wide, early)
                                                : kernel_for<kOutFp4UE8M0>(P, wide, early);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T));
+  cfg.gridDim = dim3(static_cast<unsigned>(rows && T > places * d->sm_count ? places * d->sm_count : T));
   cfg.blockDim = dim3(threads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
