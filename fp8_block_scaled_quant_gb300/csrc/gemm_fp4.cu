@@ -487,14 +487,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 // ---- CTA pairs -----------------------------------------------------------------------
 //
-// Many tokens: 256 tokens x 256 weight rows (128 where those are few tiles) to a pair
-// of CTAs (cta_group::2), tokens as tensor-memory lanes. Each CTA has 128 tokens and
-// half of the weight rows, so a byte of either operand is fetched once per 256
-// products; both have the scales of all the tile's weight rows. The accumulator is
-// single: the epilogue's eight warps take it out into registers, hand it back, and
-// convert and store from there while the next tile is summed. A stage brings 38 KB to
-// each SM in 0.35 us, 0.9 of what an SM takes from L2, while the tensor pipe is 82 %
-// active at 1.85 GHz (4096 x 18432 x 7168: 155 us, 7.0 PFLOP/s; power-of-two scales 150).
+// Many tokens: 256 tokens x 256 weight rows (128 or 384 where that makes better
+// rounds) to a pair of CTAs (cta_group::2), tokens as tensor-memory lanes. Each CTA has
+// 128 tokens and half of the weight rows, so a byte of either operand is fetched once
+// per 256 products; both have the scales of all the tile's weight rows. The accumulator
+// is single: the epilogue's eight warps take it out into registers, hand it back, and
+// store from there while the next tile is summed. The MMAs bound it: 147 cycles for each
+// 256 x 256 x 64 (128 by the nominal rate), tensor pipe 81 % active, the clock at 1.86
+// GHz by power (4096 x 18432 x 7168: 155 us, 7.0 PFLOP/s; power-of-two scales, half the
+// scale copies, 149). An SM takes 38 KB a stage from L2, 57 bytes a clock; tiles of 384
+// rows, which take a sixth less for a product, need the same time for it.
 //
 //   warps 0, 2   producers: this CTA's codes and scales, completing on the leader's barriers
 //   warp 1       MMA issuer (leader CTA); both allocate tensor memory
@@ -506,13 +508,15 @@ template <int BN_, int FMT_>
 struct PairCfg {
   static constexpr int BN = BN_, FMT = FMT_;
   static constexpr int kHalf = BN / 2;                           // weight rows of a CTA; columns of an epilogue half
+  static constexpr int kMmas = BN > 256 ? 2 : 1;                 // side by side: an MMA has 256 columns at most
+  static constexpr int kMmaN = BN / kMmas, kBox = kMmaN / 2;     // an MMA's columns, and its weight rows in a CTA
   static constexpr int kSfRows = BN / 128;                       // scale tile rows of the weights
   static constexpr int kTiles = FMT == kFp4E4M3 ? 4 : 2;
   static constexpr int kSfBytes = kTiles * kScaleTile;           // 128 rows of a stage
   static constexpr int kSfaAt = kLaneBytes + kHalf * 128, kSfbAt = kSfaAt + kSfBytes;
   static constexpr int kTxBytes = kSfbAt + kSfRows * kSfBytes;   // of one CTA
   static constexpr int kStageBytes = (kTxBytes + 1023) / 1024 * 1024;
-  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kStages = BN == 128 ? 6 : BN == 256 ? 5 : 4;
   static constexpr int kSfStep = 4 + 4 * kSfRows;                // columns of 4 blocks' scales: tokens', weights'
   static constexpr int kSfCols = kTiles * kSfStep;
   static constexpr int kOutAt = kStages * kStageBytes;           // 8 warps x 4 KB
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const int tm = c.tile % p.tiles_m, tn = c.tile / p.tiles_m;
         c.k = 0;
         c.y_a = codes ? tm * 256 + rank * 128 : (tm * 2 + rank) * ktiles;
-        c.y_w = codes ? tn * C::BN + rank * C::kHalf : tn * C::kSfRows * ktiles;
+        c.y_w = codes ? tn * C::BN + rank * C::kBox : tn * C::kSfRows * ktiles;
       };
       auto advance = [&](Cursor& c) {
         if (++c.st == C::kStages) c.st = 0, c.at = smem0, c.bar = bar0;
@@ -654,7 +658,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       auto weights = [&](const Cursor& c) {
         if (codes) {
           if (rank == 0) mbar_arrive_expect_tx(&full[c.st], 2 * C::kTxBytes);
-          tma_load_pair(c.at + kLaneBytes, &map_w, c.bar, c.k * 128, c.y_w);
+#pragma unroll
+          for (int m = 0; m < C::kMmas; ++m)
+            tma_load_pair(c.at + kLaneBytes + m * C::kBox * 128, &map_w, c.bar, c.k * 128, c.y_w + m * C::kMmaN);
         } else {
 #pragma unroll
           for (int r = 0; r < C::kSfRows; ++r)
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         tc_fence_after_sync();
         const uint32_t at = smem_u32(smem + st * C::kStageBytes);
-        const uint64_t ad = sdesc_kmajor_sw128(at), bd = sdesc_kmajor_sw128(at + kLaneBytes);
+        const uint64_t ad = sdesc_kmajor_sw128(at);
         const uint32_t sf = sf0 + sf_turn * C::kSfCols;
         const int left = p.ksteps - k * 4;
         if (leader) {
@@ -720,9 +726,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
               for (int r = 0; r < C::kSfRows; ++r)
                 tmem_cp_scales_pair(sfb + 4 * r, sdesc_scale_tile(at + C::kSfbAt + r * C::kSfBytes + t * kScaleTile));
             }
-            mma_fp4_pair<C::FMT>(tmem, ad + 2 * j, bd + 2 * j,
-                                 idesc_fp4(256, C::BN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa, sfb,
-                                 k > 0 || j > 0 ? 1u : 0u);
+#pragma unroll
+            for (int m = 0; m < C::kMmas; ++m)
+              mma_fp4_pair<C::FMT>(tmem + m * C::kMmaN, ad + 2 * j,
+                                   sdesc_kmajor_sw128(at + kLaneBytes + m * C::kBox * 128) + 2 * j,
+                                   idesc_fp4(256, C::kMmaN, C::FMT, C::FMT == kFp4E4M3 ? 0 : 2 * (j & 1)), sfa,
+                                   sfb + m * (C::kMmaN / 32), k > 0 || j > 0 ? 1u : 0u);
           }
           mma_commit_pair(&empty[st]);
           if (k + 1 == p.stages_k) mma_commit_pair(acc_full);
@@ -752,26 +761,47 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t col0 = static_cast<int64_t>(tn) * C::BN + half * C::kHalf;
       float ag = 1.0f;
       if (p.a_g) {
-        // The four warps of these columns bring up to 32 of their scales each.
-        const int in = q * 32 + lane;
-        const float wg = in < C::kHalf && col0 + in < p.N ? __ldg(p.w_g + col0 + in) : 0.0f;
-        if (row < p.M) ag = __ldg(p.a_g + row);
+        // The four warps of these columns bring their scales.
         named_barrier_sync(1 + half, 128);  // the tile before has been multiplied
-        if (in < C::kHalf) factors[in] = wg;
+        for (int in = q * 32 + lane; in < C::kHalf; in += 128) factors[in] = col0 + in < p.N ? __ldg(p.w_g + col0 + in) : 0.0f;
+        if (row < p.M) ag = __ldg(p.a_g + row);
         named_barrier_sync(1 + half, 128);
       }
       // (After a wait that gave up the warps still meet at their barriers, and store nothing.)
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, turn, abort_flag, p.err, kDevErrTimeoutEpilogue));
       if (!ok) continue;
       tc_fence_after_sync();
-      // All columns into registers and the accumulator back to the MMAs, then the rest.
-      uint32_t r[C::kHalf / 64][64];
+      // Two columns of this lane's row, times their scales, as bf16.
+      auto two = [&](int col, uint32_t a, uint32_t b) {
+        float2 v = make_float2(__uint_as_float(a), __uint_as_float(b));
+        if (p.a_g) {
+          const float2 g = *reinterpret_cast<const float2*>(factors + col);
+          v.x *= ag * g.x, v.y *= ag * g.y;
+        }
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t*>(&t);
+      };
+      // All columns into registers (as bf16 where fp32 would take too many) and the
+      // accumulator back to the MMAs, then 64 columns at a time through a swizzled box of 32 rows.
+      constexpr bool kPack = C::kHalf > 128;
+      uint32_t r[C::kHalf / 64][kPack ? 32 : 64];
 #pragma unroll
-      for (int h = 0; h < C::kHalf / 64; ++h) tmem_ld_32x32b_x64(acc + h * 64, r[h]);
+      for (int h = 0; h < C::kHalf / 64; ++h) {
+        if constexpr (kPack) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t t[32];
+            tmem_ld_32x32b_x32(acc + h * 64 + c, t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[h][c / 2 + i] = two(h * 64 + c + 2 * i, t[2 * i], t[2 * i + 1]);
+          }
+        } else {
+          tmem_ld_32x32b_x64(acc + h * 64, r[h]);
+        }
+      }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(hand_back);
-      // 64 columns at a time through a swizzled box of 32 rows.
 #pragma unroll
       for (int h = 0; h < C::kHalf / 64; ++h) {
         if (lane == 0) bulk_wait_group_read0();  // the box's last store has read it
@@ -780,19 +810,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         for (int c = 0; c < 8; ++c) {  // eight columns
           uint32_t packed[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float f[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-            if (p.a_g) {
-              const float4 g4 = *reinterpret_cast<const float4*>(factors + h * 64 + c * 8 + i * 4);
-              f[0] = ag * g4.x, f[1] = ag * g4.y, f[2] = ag * g4.z, f[3] = ag * g4.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int at = c * 8 + i * 4 + j * 2;
-              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[h][at]) * f[2 * j],
-                                                             __uint_as_float(r[h][at + 1]) * f[2 * j + 1]);
-              packed[2 * i + j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (kPack) packed[i] = r[h][c * 4 + i];
+            else packed[i] = two(h * 64 + c * 8 + 2 * i, r[h][c * 8 + 2 * i], r[h][c * 8 + 2 * i + 1]);
           }
           *reinterpret_cast<uint4*>(out + lane * 128 + ((c ^ (lane & 7)) << 4)) =
               make_uint4(packed[0], packed[1], packed[2], packed[3]);
@@ -886,7 +906,7 @@ int launch_pair(const DevInfo* d, const void* a, const void* w, int64_t K, Fp4Pa
   if (set[d->device] != cudaSuccess) return FP8BLK_ERR_CUDA;
   CUtensorMap ma, mw, mas, mws, mc;
   const uint64_t at = static_cast<uint64_t>((p.M + 127) / 128 * p.ktiles), wt = static_cast<uint64_t>((p.N + 127) / 128 * p.ktiles);
-  if (!make_code_map(&ma, a, p.M, K / 2, 128) || !make_code_map(&mw, w, p.N, K / 2, C::kHalf) ||
+  if (!make_code_map(&ma, a, p.M, K / 2, 128) || !make_code_map(&mw, w, p.N, K / 2, C::kBox) ||
       !make_scale_map(&mas, p.a_s, at, C::kTiles) || !make_scale_map(&mws, p.w_s, wt, C::kTiles) ||
       !make_out_map(&mc, p.c, p.M, p.N))
     return FP8BLK_ERR_CUDA;
@@ -914,12 +934,18 @@ bool pair_fits(const Fp4Params& p) {
          (p.M + 255) / 128 * p.ktiles < int64_t{1} << 30 && (p.N + 255) / 128 * p.ktiles < int64_t{1} << 30;
 }
 
-// Tiles of 128 weight rows where all of them run at once: twice the SMs then bring the
-// operands (128 x 2112 x 7168 9.8 us, of 256 rows 11.3; 200 x 5120 x 7168 10.7 and 11.6;
-// in two rounds against one of 256 rows, 517 x 5120 x 7168, 17.7 and 12.9; in three
-// against two, 700 x 7168 x 2048, 10.0 and 9.1).
-bool narrow_tiles(const DevInfo* d, const Fp4Params& p) {
-  return (p.M + 255) / 256 * ((p.N + 127) / 128) <= d->sm_count / 2;
+// Weight rows of a pair's tile. 128 where all tiles then run at once: twice the SMs
+// bring the operands (us, 128 x 2112 x 7168 9.8, by 256 rows 11.3; 200 x 5120 x 7168 10.7
+// and 11.6; in two rounds against one, 517 x 5120 x 7168, 17.7 and 12.9). Else 256, or 384
+// where that leaves so many rounds fewer that they are shorter in all: a round of 256 is
+// 0.35 us a stage and 0.55 to hand the accumulator over, of 384 0.51 and 1.3 (1024 x 7168 x
+// 7168 19.4, by 256 22.4; 4096 x 7168 x 18432 140 and 143; 900 x 5120 x 1536 8.3 and 7.7;
+// 4096 x 18432 x 7168 156 and 154).
+int pair_columns(const DevInfo* d, const Fp4Params& p) {
+  const int64_t pairs = d->sm_count / 2, tm = (p.M + 255) / 256, s = p.stages_k;
+  auto rounds = [&](int bn) { return (tm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
+  if (rounds(128) == 1) return 128;
+  return rounds(384) * (51 * s + 130) + 100 < rounds(256) * (35 * s + 55) ? 384 : 256;
 }
 
 // CTAs of a tile's cluster, of two stages of K at least: as many as give every SM one,
@@ -1010,8 +1036,11 @@ int run_fmt(const DevInfo* d, const void* a, const void* w, int64_t K, const Fp4
     return launch_few<Cfg<16, FMT, true>>(d, mw, mw, p, stream);
   }
   if (takes_pairs(d, p) && pair_fits(p))
-    return narrow_tiles(d, p) ? launch_pair<PairCfg<128, FMT>>(d, a, w, K, p, stream)
-                              : launch_pair<PairCfg<256, FMT>>(d, a, w, K, p, stream);
+    switch (pair_columns(d, p)) {
+      case 128: return launch_pair<PairCfg<128, FMT>>(d, a, w, K, p, stream);
+      case 256: return launch_pair<PairCfg<256, FMT>>(d, a, w, K, p, stream);
+      default: return launch_pair<PairCfg<384, FMT>>(d, a, w, K, p, stream);
+    }
   const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
   if (!make_code_map(&mw, w, p.N, K / 2, 128) || !make_code_map(&ma, a, p.M, K / 2, bn)) return FP8BLK_ERR_CUDA;
   switch (bn) {

@@ -364,3 +364,13 @@ def test_two_streams():
         for a, b in side:
             assert torch.equal(a, b)
     assert fb.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1024, 7168, 2048), (700, 7168, 2432), (600, 7000, 2176), (1000, 7272, 2560), (2000, 3400, 2176),
+                                   (769, 6920, 2176)])
+def test_gemm_by_wide_tiles(M, N, K, fmt):
+    """Products whose tiles go a round less where they are wider, with last tiles of every width."""
+    a, w = operands(M, N, K, fmt, M + N)
+    check_product(fb.fp4_gemm(*a, *w, fmt), dense(a, fmt), dense(w, fmt), K)
+    assert fb.last_device_error() == 0
