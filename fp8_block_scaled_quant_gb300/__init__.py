@@ -9,6 +9,16 @@ Names follow the DeepSeek-V3 inference kernels ("Administrator & Developer
 Guide", 8.5 The Triton kernels): act_quant, weight_dequant, fp8_gemm, plus
 the FP8 linear layer of 6.3 and the block weight quantisation of the README's
 weight_scale_inv section.
+
+Calls on a stream overlap. Those that end in a GEMM, mla_absorb, mla_append,
+mla_attention and residual_norm let the next call start early, which then
+reads its weight operands (w, w1, w3, w2, wkv_b and their block scales)
+at once, any number of such calls in a row. So between the call that writes a
+weight and the one that multiplies by it there has to be a synchronisation or
+an ordering call (act_quant, weight_quant, weight_dequant, fp4_quant,
+fp4_dequant, a moe_* call, or any kernel or copy of torch's) that is neither
+of the two. Weights quantised when a model is loaded need nothing more;
+``linear(x, *weight_quant(w))`` does: synchronise in between.
 """
 from __future__ import annotations
 
@@ -395,7 +405,8 @@ def _native():
 def fp4_quant(x: torch.Tensor, fmt: int = FP4_E4M3):
     """x bf16 or float32 [M, K] (rows may be strided) -> (q uint8 [M, K/2], s uint8 scale tiles of fp4_scale_shape,
     g float32 [M]; g is None for FP4_UE8M0): e2m1 codes, low half first, with their block and row scales. The scale
-    bytes of rows past M are not written."""
+    bytes of rows past M are not written. Before a product takes these as its weight (w, w_s, w_g), synchronise or issue
+    another ordering call (the module's rule on overlap); as activations they may go straight into fp4_gemm."""
     return (_bind or _native()).fp4_quant(x, fmt)
 
 
@@ -407,7 +418,9 @@ def fp4_dequant(q: torch.Tensor, s: torch.Tensor, g: torch.Tensor | None, fmt: i
 
 def fp4_gemm(a: torch.Tensor, a_s: torch.Tensor, a_g: torch.Tensor | None, w: torch.Tensor, w_s: torch.Tensor,
              w_g: torch.Tensor | None, fmt: int = FP4_E4M3, out: torch.Tensor | None = None) -> torch.Tensor:
-    """Two 4-bit matrices as fp4_quant gives them, a [M, K] and w [N, K] -> bf16 [M, N] = a w^T."""
+    """Two 4-bit matrices as fp4_quant gives them, a [M, K] and w [N, K] -> bf16 [M, N] = a w^T. w and w_s are read at
+    once: they must not come from the call just before, nor from residual_norm without an ordering call since (the
+    module's rule on overlap). a, a_s, a_g may come from any call."""
     return (_bind or _native()).fp4_gemm(a, a_s, a_g, w, w_s, w_g, fmt, out)
 
 
@@ -418,7 +431,8 @@ def fp4_linear_workspace_bytes(M: int, N: int, K: int, fmt: int = FP4_E4M3) -> i
 def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, w_g: torch.Tensor | None, fmt: int = FP4_E4M3,
                out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """FP4 linear layer: fp4_gemm(fp4_quant(x), w). x bf16 [M, K] (rows may be strided) -> bf16 [M, N]. ws: a workspace
-    of fp4_linear_workspace_bytes, 256-byte aligned, any contents, used by one stream at a time."""
+    of fp4_linear_workspace_bytes, 256-byte aligned, any contents, used by one stream at a time. w and w_s are read at
+    once, as in fp4_gemm: a weight that fp4_quant has just made needs a synchronisation in between."""
     return (_bind or _native()).fp4_linear(x, w, w_s, w_g, fmt, out, ws)
 
 
@@ -429,7 +443,8 @@ def residual_norm(y: torch.Tensor, x: torch.Tensor | None, norm_w: torch.Tensor,
     h = RMSNorm(r) * norm_w. y, x bf16 [T, D] (rows may be strided; x None: r = gate * z), norm_w and post_w float32
     [D], gate float32 [D] or bf16 [T, D]. Returns (r bf16 [T, D], h): h is bf16 [T, D], or with quant="fp8"
     act_quant's (q, s) of it (scale_fmt SCALE_*), or with quant="fp4" fp4_quant's (q, s, g) of it (scale_fmt FP4_*).
-    r may be given; it may be x or y itself. fp32 until each output's one rounding."""
+    r may be given; it may be x or y itself. fp32 until each output's one rounding. h is the next product's activation at
+    once; to multiply by it as a weight needs an ordering call in between (the module's rule on overlap)."""
     return (_bind or _native()).residual_norm(y, x, norm_w, post_w, gate, residual_scale, eps, quant, scale_fmt, r)
 
 

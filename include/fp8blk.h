@@ -29,19 +29,28 @@
  *   - Sizes of 0 are valid and launch nothing (except where noted).
  *   - Not thread-safe per workspace: calls that share a workspace must be
  *     ordered on one stream.
- *   - Overlap on a stream: the GEMM kernels, the MLA absorb kernels,
- *     fp8blk_residual_norm (and act_quant inside fp8blk_linear / fp8blk_ffn,
- *     fp4_quant inside fp8blk_fp4_linear) let the next kernel of
- *     this library on the same stream start early (programmatic dependent
- *     launch). That kernel may begin loading its WEIGHT operands (w, w1, w3,
- *     w2; wkv_b and its scales for the MLA absorb; w and w_s of the FP4 GEMM)
- *     before the previous one has finished; it reads activations and activation
- *     scales, and writes anything, only after. Inside fp8blk_linear /
- *     fp8blk_ffn / fp8blk_fp4_linear the GEMM's
- *     weight loads may even start while the library call before is still
- *     running. So a weight operand must not be the output of either of the
- *     two library calls issued just before it on the same stream. Kernels of
- *     other libraries are ordered as usual.
+ *   - Overlap on a stream: early calls let the next call of this library on the
+ *     same stream start before they have ended (programmatic dependent launch):
+ *       fp8blk_gemm, fp8blk_gemm_noalloc, fp8blk_linear, fp8blk_linear_host,
+ *       fp8blk_swiglu_gemm, fp8blk_ffn, fp8blk_mla_absorb_qk,
+ *       fp8blk_mla_absorb_v, fp8blk_mla_append, fp8blk_mla_attention,
+ *       fp8blk_fp4_gemm, fp8blk_fp4_linear, fp8blk_residual_norm.
+ *     A call that starts so reads activations and their scales, and writes
+ *     anything, only after all calls before it have ended. But the GEMMs, the
+ *     linears and the MLA absorb read their WEIGHT operands at once (w, w1, w3,
+ *     w2 and their block scales; wkv_b and its scales; w and w_s of the FP4
+ *     calls, not w_g), and any number of early calls in a row may be running
+ *     then beside the one before them. So between the call that writes a
+ *     weight operand and a call that reads it there has to be, on the stream,
+ *     a synchronisation, or one ordering call at least: one of
+ *       fp8blk_act_quant, fp8blk_weight_quant, fp8blk_weight_dequant,
+ *       fp8blk_moe_gate, fp8blk_moe_route, fp8blk_moe_permute,
+ *       fp8blk_moe_grouped_gemm, fp8blk_moe_layer, fp8blk_fp4_quant,
+ *       fp8blk_fp4_dequant
+ *     that launches something, or a kernel or a copy of another library. The
+ *     call that writes the weight is not counted, whatever it is. (Weights that
+ *     are made when a model is loaded need nothing; a matrix that was just
+ *     quantised, or that fp8blk_residual_norm wrote, and is multiplied as w does.)
  */
 #ifndef FP8BLK_H
 #define FP8BLK_H
@@ -515,8 +524,8 @@ FP8BLK_API int fp8blk_fp4_dequant(const void *q, const void *s, const float *g, 
  * w [N, K/2] and scale tiles 16-byte aligned, c bf16 [M, N] of any alignment of
  * its elements, row scales 4-byte aligned; any M and N up to 2^28. K == 0 writes
  * zeros. The result does not vary from run to run. No workspace. Weights (w, w_s)
- * may be read before the previous kernel on the stream has ended (the overlap rule
- * above); w_g may not.
+ * are read at once (the overlap rule above: they may not be the output of the call
+ * just before); a, a_s, a_g and w_g are not.
  */
 FP8BLK_API int fp8blk_fp4_gemm(const void *a, const void *a_s, const float *a_g, const void *w, const void *w_s,
                                const float *w_g, void *c_bf16, int64_t M, int64_t N, int64_t K, int fmt,
