@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       __syncwarp();
       if (++st == p.stages) st = 0, phase ^= 1;
     }
+    if (!ok) __threadfence_block();  // the abort flag, before the epilogue is let go
+    __syncwarp();
     if (leader) {
       if (!ok) mma_commit(done);
       mbar_wait(done, 0, nullptr, p.err, kDevErrTimeoutDrain);
@@ -414,7 +416,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         else ag[i] = m < cols ? __ldg(p.a_g + m0 + m) : 0.0f;
       }
     }
-    finished = mbar_wait(done, 0, nullptr, p.err, kDevErrTimeoutEpilogue);
+    // (After a wait that gave up the MMA warp commits what it has: not all of K.)
+    finished = mbar_wait(done, 0, nullptr, p.err, kDevErrTimeoutEpilogue) && *abort_flag == 0;
     tc_fence_after_sync();
   }
   __syncwarp();
@@ -435,6 +438,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if constexpr (kStep == 16) tmem_ld_32x32b_x16(acc + c0, r);
       else tmem_ld_32x32b_x32(acc + c0, r);
       if (ks > 1) {
+        if (!finished) {  // the CTAs that sum this part wait for it, and must not take it for a sum
+#pragma unroll
+          for (int i = 0; i < kStep; ++i) r[i] = 0x7FFFFFFFu;
+        }
         if (p.part_vec == 4) send_columns<4, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
         else if (p.part_vec == 2) send_columns<2, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
         else send_columns<1, kStep>(r, c0, p.part_cols, ks, mine, parts_full);
