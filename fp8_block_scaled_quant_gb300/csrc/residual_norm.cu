@@ -483,11 +483,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(cons
   constexpr int kWarps = kMaxThreads / 32;
   __shared__ float sums[4][4 * kWarps], sum_y[kWarps], sum_r[kWarps];
   __shared__ uint64_t summed[4];
+  __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31;
   griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&summed[i], blockDim.x >> 5);
     fence_barrier_init();
+    abort_flag = 0;
   }
   __syncthreads();
   griddep_wait();
@@ -539,7 +541,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(cons
       begin(v_next, x_next, turn + 1);
       load(row + 2 * step);
     }
-    mbar_wait(&summed[turn & 3], (turn >> 2) & 1, nullptr, p.err, kDevErrTimeoutEpilogue);
+    // A warp whose wait gave up ends here: its row's sums are not all there. (The block's barriers
+    // count the threads that have not ended; the other warps' waits see the flag.)
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&summed[turn & 3], (turn >> 2) & 1, &abort_flag, p.err, kDevErrTimeoutEpilogue)))
+      return;
     float k2;
     const bool known = both_norms<1, true>(p, row, warps_sum4(sums[turn & 3]), x, v, &k2, sum_y);
     write_residual<1, true>(p, row, v);
