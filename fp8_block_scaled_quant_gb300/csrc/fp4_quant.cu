@@ -36,9 +36,10 @@ __device__ __forceinline__ void load32(const void* p, bool wide, uint32_t* w) {
   if (wide) {
     asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
   } else {
-    const uint4 a = __ldcs(static_cast<const uint4*>(p)), b = __ldcs(static_cast<const uint4*>(p) + 1);
+    const uint4 a = load_once16(p), b = load_once16(static_cast<const uint4*>(p) + 1);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
     w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
@@ -167,14 +168,14 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantParams p)
   const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;
   float g = 1.0f;
-  if constexpr (FMT == kFp4E4M3) g = __ldg(p.g + row);
+  if constexpr (FMT == kFp4E4M3) g = p.g[row];
   for (int unit = blockIdx.y * blockDim.x + threadIdx.x; unit < p.units; unit += gridDim.y * blockDim.x) {
-    const uint2 codes = __ldcs(p.q + row * p.units + unit);
+    const uint2 codes = load_once8(p.q + row * p.units + unit);
     float s;
     if constexpr (FMT == kFp4E4M3) {
-      s = e4m3_value(__ldg(p.s + fp4_scale_at(row, unit, p.ktiles)));
+      s = e4m3_value(p.s[fp4_scale_at(row, unit, p.ktiles)]);
     } else {
-      const uint32_t e = __ldg(p.s + fp4_scale_at(row, unit / 2, p.ktiles));
+      const uint32_t e = p.s[fp4_scale_at(row, unit / 2, p.ktiles)];
       // 2^(e - 127): a subnormal for e = 0, NaN for e = 255
       s = e == 255 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float(e ? e << 23 : 1u << 22);
     }

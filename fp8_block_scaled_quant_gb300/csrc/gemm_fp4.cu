@@ -408,12 +408,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     // The scales of this lane's weight row and of the tokens (token 32 i + lane in ag[i]).
     if (p.w_g) {
-      if (row < p.N) wg = __ldg(p.w_g + row);
+      if (row < p.N) wg = p.w_g[row];
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(ag) / 4); ++i) {
         const int m = i * 32 + lane;
         if constexpr (C::FUSE) ag[i] = m < cols ? fp4_row_scale(row_top[m]).g : 0.0f;
-        else ag[i] = m < cols ? __ldg(p.a_g + m0 + m) : 0.0f;
+        else ag[i] = m < cols ? p.a_g[m0 + m] : 0.0f;
       }
     }
     // (After a wait that gave up the MMA warp commits what it has: not all of K.)
@@ -770,8 +770,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (p.a_g) {
         // The four warps of these columns bring their scales.
         named_barrier_sync(1 + half, 128);  // the tile before has been multiplied
-        for (int in = q * 32 + lane; in < C::kHalf; in += 128) factors[in] = col0 + in < p.N ? __ldg(p.w_g + col0 + in) : 0.0f;
-        if (row < p.M) ag = __ldg(p.a_g + row);
+        for (int in = q * 32 + lane; in < C::kHalf; in += 128) factors[in] = col0 + in < p.N ? p.w_g[col0 + in] : 0.0f;
+        if (row < p.M) ag = p.a_g[row];
         named_barrier_sync(1 + half, 128);
       }
       // (After a wait that gave up the warps still meet at their barriers, and store nothing.)

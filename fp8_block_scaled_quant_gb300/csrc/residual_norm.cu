@@ -83,14 +83,15 @@ __device__ __forceinline__ void read16(const float* row, int unit, int cols, flo
   if constexpr (WIDE) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-          : "=f"(v[4 * h].x), "=f"(v[4 * h].y), "=f"(v[4 * h + 1].x), "=f"(v[4 * h + 1].y), "=f"(v[4 * h + 2].x),
-            "=f"(v[4 * h + 2].y), "=f"(v[4 * h + 3].x), "=f"(v[4 * h + 3].y)
-          : "l"(p + 8 * h));
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[4 * h].x), "=f"(v[4 * h].y), "=f"(v[4 * h + 1].x), "=f"(v[4 * h + 1].y), "=f"(v[4 * h + 2].x),
+                     "=f"(v[4 * h + 2].y), "=f"(v[4 * h + 3].x), "=f"(v[4 * h + 3].y)
+                   : "l"(p + 8 * h)
+                   : "memory");
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 a = unit * 16 + 4 * i < cols ? __ldg(reinterpret_cast<const float4*>(p) + i) : make_float4(0, 0, 0, 0);
+      const float4 a = unit * 16 + 4 * i < cols ? reinterpret_cast<const float4*>(p)[i] : make_float4(0, 0, 0, 0);
       v[2 * i] = make_float2(a.x, a.y);
       v[2 * i + 1] = make_float2(a.z, a.w);
     }
