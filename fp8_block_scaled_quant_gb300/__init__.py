@@ -393,6 +393,12 @@ def _native():
             raise Fp8BlkError(f"{path} is missing: build it with __graft_entry__.build() "
                               "or python fp8_block_scaled_quant_gb300/_build.py")
         import importlib.util
+        from . import _build
+        if os.path.exists(_build.BIND_FOR):
+            with open(_build.BIND_FOR) as f:
+                made = f.read()
+            if made != _build.bind_for():
+                raise Fp8BlkError(f"{path} was compiled for {made}: build it again for {_build.bind_for()}")
         spec = importlib.util.spec_from_file_location(__name__ + "._bind", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

@@ -9,6 +9,7 @@ the library does not link libcuda either.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -20,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8blk.so")
 BIND = os.path.join(PKG, "_bind.so")
 BUILD = os.path.join(PKG, "_build")
+BIND_FOR = os.path.join(BUILD, "bind.for")   # what BIND was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -50,6 +52,25 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+class BindError(RuntimeError):
+    """The native part of the Python binding could not be compiled; the C library is there."""
+
+
+def bind_for() -> str:
+    """The torch and the interpreter that the native part of the binding is compiled against."""
+    import sys
+
+    import torch
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, python {sys.version}"
+
+
+def _bind_is_stale() -> bool:
+    if _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "fp8blk.h")]) or not os.path.exists(BIND_FOR):
+        return True
+    with open(BIND_FOR) as f:
+        return f.read() != bind_for()
+
+
 def bind_command(out: str) -> list[str]:
     """Compiles the native part of the Python binding against the installed torch."""
     import sysconfig
@@ -65,6 +86,8 @@ def bind_command(out: str) -> list[str]:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compiles what is out of date: the C library, which needs nvcc alone, and, where torch is installed, the native part
+    of the Python binding. Where that fails BindError is raised after the library has been linked."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     hdrs = _headers()
@@ -85,28 +108,40 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     def compile_bind():
-        if force or _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "fp8blk.h")]):
+        if importlib.util.find_spec("torch") is None:
+            return
+        try:
+            if not force and not _bind_is_stale():
+                return
             tmp = BIND + f".tmp{os.getpid()}"
             r = subprocess.run(bind_command(tmp), capture_output=True, text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stdout}\n{r.stderr}")
-            os.replace(tmp, BIND)
+        except (OSError, ImportError) as e:
+            raise BindError(f"bind.cpp was not compiled ({e}); {LIB} does not need it") from e
+        if r.returncode != 0:
+            raise BindError(f"g++ failed on bind.cpp ({LIB} does not need it):\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BIND)
+        with open(BIND_FOR, "w") as f:
+            f.write(bind_for())
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         bind = ex.submit(compile_bind)
         list(ex.map(compile_one, zip(srcs, objs)))
+        if force or _stale(LIB, objs):
+            tmp = LIB + f".tmp{os.getpid()}"
+            cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, LIB)
         bind.result()
-    if force or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
     return LIB
 
 
 if __name__ == "__main__":
     import sys
 
-    print(build(force="--force" in sys.argv, verbose=True))
+    try:
+        print(build(force="--force" in sys.argv, verbose=True))
+    except BindError as e:
+        print(LIB)
+        print(f"{e}\nwithout it the Python binding has no 4-bit calls and no residual_norm", file=sys.stderr)
