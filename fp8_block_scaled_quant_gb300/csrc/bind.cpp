@@ -138,11 +138,20 @@ void make_together(std::initializer_list<Piece> pieces, const at::Tensor& like) 
   }
 }
 
-// The given output, or a new one.
-at::Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like, const char* name) {
-  if (o != Py_None) return plain(o, type, shape, like.get_device(), name);
-  return make(shape, type, like);
+// The given output, or none.
+at::Tensor given_output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like,
+                        const char* name) {
+  return o != Py_None ? plain(o, type, shape, like.get_device(), name) : at::Tensor();
 }
+
+// The interpreter's lock is not held while tensors are allocated and kernels
+// launched: either may wait (for memory, for room in the launch queue).
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
@@ -201,7 +210,7 @@ Operand operand(PyObject* q, PyObject* s, PyObject* g, int fmt, int dev, const c
 
 const void* data(const at::Tensor& t) { return t.const_data_ptr(); }
 
-// Makes a call on the device and the current stream of `like`.
+// Makes a call on the device and the current stream of `like` (without the interpreter's lock).
 template <typename F>
 void call(const at::Tensor& like, const char* what, F f) {
   const auto dev = like.device();
@@ -240,13 +249,16 @@ PyObject* fp4_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const std::array<int64_t, 2> qs = {x.rows, x.cols / 2};
     const auto ss = scale_shape(x.rows, x.cols, fmt);
     const std::array<int64_t, 1> gs = {x.rows};
-    if (fmt == FP8BLK_FP4_E4M3)
-      make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *x.t);
-    else make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}}, *x.t);
-    call(*x.t, "fp4_quant", [&](fp8blk_stream_t st) {
-      return lib.fp4_quant(data(*x.t), fp32, x.stride, x.rows, x.cols, fmt, q.mutable_data_ptr(), s.mutable_data_ptr(),
-                           g.defined() ? g.mutable_data_ptr<float>() : nullptr, st);
-    });
+    {
+      const Unlocked unlocked;
+      if (fmt == FP8BLK_FP4_E4M3)
+        make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *x.t);
+      else make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}}, *x.t);
+      call(*x.t, "fp4_quant", [&](fp8blk_stream_t st) {
+        return lib.fp4_quant(data(*x.t), fp32, x.stride, x.rows, x.cols, fmt, q.mutable_data_ptr(), s.mutable_data_ptr(),
+                             g.defined() ? g.mutable_data_ptr<float>() : nullptr, st);
+      });
+    }
     return tuple({&q, &s, &g});
   });
 }
@@ -257,10 +269,14 @@ PyObject* fp4_dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     count(n, 5);
     const int fmt = format(a[3]);
     const Operand q = operand(a[0], a[1], a[2], fmt, -1, "q");
-    const at::Tensor out = output(a[4], {q.rows, q.K}, at::kBFloat16, *q.q, "out");
-    call(*q.q, "fp4_dequant", [&](fp8blk_stream_t st) {
-      return lib.fp4_dequant(data(*q.q), q.s, q.g, q.rows, q.K, fmt, out.mutable_data_ptr(), st);
-    });
+    at::Tensor out = given_output(a[4], {q.rows, q.K}, at::kBFloat16, *q.q, "out");
+    {
+      const Unlocked unlocked;
+      if (!out.defined()) out = make({q.rows, q.K}, at::kBFloat16, *q.q);
+      call(*q.q, "fp4_dequant", [&](fp8blk_stream_t st) {
+        return lib.fp4_dequant(data(*q.q), q.s, q.g, q.rows, q.K, fmt, out.mutable_data_ptr(), st);
+      });
+    }
     return THPVariable_Wrap(out);
   });
 }
@@ -273,10 +289,15 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Operand x = operand(a[0], a[1], a[2], fmt, -1, "a");
     const Operand w = operand(a[3], a[4], a[5], fmt, x.q->get_device(), "w");
     if (x.K != w.K) refuse("a and w must share K");
-    const at::Tensor out = output(a[7], {x.rows, w.rows}, at::kBFloat16, *x.q, "out");
-    call(*x.q, "fp4_gemm", [&](fp8blk_stream_t st) {
-      return lib.fp4_gemm(data(*x.q), x.s, x.g, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.K, fmt, st);
-    });
+    at::Tensor out = given_output(a[7], {x.rows, w.rows}, at::kBFloat16, *x.q, "out");
+    {
+      const Unlocked unlocked;
+      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16, *x.q);
+      call(*x.q, "fp4_gemm", [&](fp8blk_stream_t st) {
+        return lib.fp4_gemm(data(*x.q), x.s, x.g, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.K, fmt,
+                            st);
+      });
+    }
     return THPVariable_Wrap(out);
   });
 }
@@ -294,7 +315,7 @@ PyObject* fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int dev = x.t->get_device(), fmt = format(a[4]);
     const Operand w = operand(a[1], a[2], a[3], fmt, dev, "w");
     if (x.cols != w.K) refuse("x and w must share K");
-    const at::Tensor out = output(a[5], {x.rows, w.rows}, at::kBFloat16, *x.t, "out");
+    at::Tensor out = given_output(a[5], {x.rows, w.rows}, at::kBFloat16, *x.t, "out");
     // The caller's workspace, or the one that the package keeps for the device and stream.
     uintptr_t at;
     size_t room;
@@ -324,10 +345,14 @@ PyObject* fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
       at = (reinterpret_cast<uintptr_t>(held.mutable_data_ptr()) + 255) & ~uintptr_t{255};
     }
-    call(*x.t, "fp4_linear", [&](fp8blk_stream_t st) {
-      return lib.fp4_linear(data(*x.t), x.stride, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.cols, fmt,
-                            reinterpret_cast<void*>(at), room, st);
-    });
+    {
+      const Unlocked unlocked;
+      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16, *x.t);
+      call(*x.t, "fp4_linear", [&](fp8blk_stream_t st) {
+        return lib.fp4_linear(data(*x.t), x.stride, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.cols,
+                              fmt, reinterpret_cast<void*>(at), room, st);
+      });
+    }
     return THPVariable_Wrap(out);
   });
 }
@@ -378,21 +403,25 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // (an empty piece takes no room)
     const std::array<int64_t, 1> none = {0};
     const Piece rp = given ? Piece{none, at::kBFloat16, &unused} : Piece{rs, at::kBFloat16, &r};
-    if (kind == FP8BLK_NORM_BF16) {
-      make_together({rp, {rs, at::kBFloat16, &h}}, *y.t);
-    } else if (kind == FP8BLK_NORM_E4M3) {
-      make_together({rp, {rs, at::kFloat8_e4m3fn, &h}, {bs, at::kFloat, &s}}, *y.t);
-    } else {
-      const auto ss = scale_shape(T, D, fmt);
-      if (fmt == FP8BLK_FP4_E4M3) make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *y.t);
-      else make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}}, *y.t);
+    {
+      const Unlocked unlocked;
+      if (kind == FP8BLK_NORM_BF16) {
+        make_together({rp, {rs, at::kBFloat16, &h}}, *y.t);
+      } else if (kind == FP8BLK_NORM_E4M3) {
+        make_together({rp, {rs, at::kFloat8_e4m3fn, &h}, {bs, at::kFloat, &s}}, *y.t);
+      } else {
+        const auto ss = scale_shape(T, D, fmt);
+        if (fmt == FP8BLK_FP4_E4M3)
+          make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *y.t);
+        else make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}}, *y.t);
+      }
+      call(*y.t, "residual_norm", [&](fp8blk_stream_t st) {
+        return lib.residual_norm(data(*y.t), y.stride, x, x_stride, post, col, tok, tok_stride, residual_scale, norm, eps, T,
+                                 D, kind, fmt, r.mutable_data_ptr(), h.mutable_data_ptr(),
+                                 s.defined() ? s.mutable_data_ptr() : nullptr,
+                                 g.defined() ? g.mutable_data_ptr<float>() : nullptr, st);
+      });
     }
-    call(*y.t, "residual_norm", [&](fp8blk_stream_t st) {
-      return lib.residual_norm(data(*y.t), y.stride, x, x_stride, post, col, tok, tok_stride, residual_scale, norm, eps, T, D,
-                               kind, fmt, r.mutable_data_ptr(), h.mutable_data_ptr(),
-                               s.defined() ? s.mutable_data_ptr() : nullptr,
-                               g.defined() ? g.mutable_data_ptr<float>() : nullptr, st);
-    });
     PyObject* out = kind == FP8BLK_NORM_BF16   ? THPVariable_Wrap(h)
                     : kind == FP8BLK_NORM_E4M3 ? tuple({&h, &s})
                                                : tuple({&h, &s, &g});
