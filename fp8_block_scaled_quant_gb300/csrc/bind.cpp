@@ -1,12 +1,12 @@
 // The Python binding of the calls that a decode step issues between its large
 // kernels: tensors checked, outputs allocated and the C ABI called without a line
 // of Python in between (a norm of one token runs in 2.1 us, and took 12 to issue
-// through ctypes; 3.4 to 4.5 from here). Marshalling only, as in the package's ctypes calls; the
+// through ctypes; 3.1 to 5.4 from here, by its outputs). Marshalling only, as in the ctypes calls; the
 // computation is in libfp8blk, whose functions are handed over by setup().
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -103,39 +103,18 @@ const at::Tensor& plain(PyObject* o, at::ScalarType type, at::IntArrayRef shape,
   return t;
 }
 
-at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-}
-
-// Several tensors, small ones in one allocation, each at a multiple of 256 bytes (an
-// allocation takes 0.7 us of the host, a piece of one 0.1; large ones do not
-// keep each other's memory).
-struct Piece {
-  at::IntArrayRef shape;
-  at::ScalarType type;
-  at::Tensor* out;
-};
-
-void make_together(std::initializer_list<Piece> pieces, const at::Tensor& like) {
-  size_t bytes = 0;
-  for (const Piece& p : pieces) {
-    size_t n = c10::elementSize(p.type);
-    for (int64_t d : p.shape) n *= static_cast<size_t>(d);
-    bytes += (n + 255) & ~size_t{255};
-  }
-  if (bytes > size_t{1} << 20) {
-    for (const Piece& p : pieces) *p.out = make(p.shape, p.type, like);
-    return;
-  }
-  const at::Tensor all = make({static_cast<int64_t>(bytes)}, at::kByte, like);
-  size_t at = 0;
-  for (const Piece& p : pieces) {
-    const size_t size = c10::elementSize(p.type);
-    *p.out = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(p.type));
-    p.out->unsafeGetTensorImpl()->set_storage_offset(static_cast<int64_t>(at / size));
-    p.out->unsafeGetTensorImpl()->set_sizes_contiguous(p.shape);
-    at += (static_cast<size_t>(p.out->numel()) * size + 255) & ~size_t{255};
-  }
+// A new tensor of the current device (Issue, below), with memory of its own: straight
+// from the allocator, 0.3 us of the host where at::empty takes 0.7.
+at::Tensor make(at::IntArrayRef shape, at::ScalarType type) {
+  size_t bytes = c10::elementSize(type);
+  for (int64_t d : shape) bytes *= static_cast<size_t>(d);
+  c10::Allocator* from = c10::cuda::CUDACachingAllocator::get();
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, from->allocate(bytes),
+                                                         from, /*resizable=*/true)),
+      c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
 }
 
 // The given output, or none.
@@ -144,13 +123,22 @@ at::Tensor given_output(PyObject* o, at::IntArrayRef shape, at::ScalarType type,
   return o != Py_None ? plain(o, type, shape, like.get_device(), name) : at::Tensor();
 }
 
-// The interpreter's lock is not held while tensors are allocated and kernels
-// launched: either may wait (for memory, for room in the launch queue).
-struct Unlocked {
-  PyThreadState* state = PyEval_SaveThread();
-  Unlocked() = default;
-  Unlocked(const Unlocked&) = delete;
-  ~Unlocked() { PyEval_RestoreThread(state); }
+// While tensors are allocated and kernels launched, on the device of `like`: the
+// interpreter's lock is not held (either may wait, for memory or for room in the
+// launch queue).
+struct Issue {
+  PyThreadState* state;
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit Issue(const at::Tensor& like) : state(PyEval_SaveThread()) {
+    try {
+      if (c10::cuda::current_device() != like.get_device()) guard.set_device(like.device());
+    } catch (...) {
+      PyEval_RestoreThread(state);
+      throw;
+    }
+  }
+  Issue(const Issue&) = delete;
+  ~Issue() { PyEval_RestoreThread(state); }
 };
 
 int64_t integer(PyObject* o) {
@@ -210,13 +198,10 @@ Operand operand(PyObject* q, PyObject* s, PyObject* g, int fmt, int dev, const c
 
 const void* data(const at::Tensor& t) { return t.const_data_ptr(); }
 
-// Makes a call on the device and the current stream of `like` (without the interpreter's lock).
+// Makes a call on the current stream of the device of `like`.
 template <typename F>
 void call(const at::Tensor& like, const char* what, F f) {
-  const auto dev = like.device();
-  c10::cuda::OptionalCUDAGuard guard;
-  if (c10::cuda::current_device() != dev.index()) guard.set_device(dev);
-  const int status = f(reinterpret_cast<fp8blk_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+  const int status = f(reinterpret_cast<fp8blk_stream_t>(c10::cuda::getCurrentCUDAStream(like.get_device()).stream()));
   if (status) refuse(std::string(what) + ": " + lib.status_string(status) + " (status " + std::to_string(status) + ")");
 }
 
@@ -250,10 +235,9 @@ PyObject* fp4_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto ss = scale_shape(x.rows, x.cols, fmt);
     const std::array<int64_t, 1> gs = {x.rows};
     {
-      const Unlocked unlocked;
-      if (fmt == FP8BLK_FP4_E4M3)
-        make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *x.t);
-      else make_together({{qs, at::kByte, &q}, {ss, at::kByte, &s}}, *x.t);
+      const Issue issue(*x.t);
+      q = make(qs, at::kByte), s = make(ss, at::kByte);
+      if (fmt == FP8BLK_FP4_E4M3) g = make(gs, at::kFloat);
       call(*x.t, "fp4_quant", [&](fp8blk_stream_t st) {
         return lib.fp4_quant(data(*x.t), fp32, x.stride, x.rows, x.cols, fmt, q.mutable_data_ptr(), s.mutable_data_ptr(),
                              g.defined() ? g.mutable_data_ptr<float>() : nullptr, st);
@@ -271,8 +255,8 @@ PyObject* fp4_dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Operand q = operand(a[0], a[1], a[2], fmt, -1, "q");
     at::Tensor out = given_output(a[4], {q.rows, q.K}, at::kBFloat16, *q.q, "out");
     {
-      const Unlocked unlocked;
-      if (!out.defined()) out = make({q.rows, q.K}, at::kBFloat16, *q.q);
+      const Issue issue(*q.q);
+      if (!out.defined()) out = make({q.rows, q.K}, at::kBFloat16);
       call(*q.q, "fp4_dequant", [&](fp8blk_stream_t st) {
         return lib.fp4_dequant(data(*q.q), q.s, q.g, q.rows, q.K, fmt, out.mutable_data_ptr(), st);
       });
@@ -291,8 +275,8 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.K != w.K) refuse("a and w must share K");
     at::Tensor out = given_output(a[7], {x.rows, w.rows}, at::kBFloat16, *x.q, "out");
     {
-      const Unlocked unlocked;
-      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16, *x.q);
+      const Issue issue(*x.q);
+      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16);
       call(*x.q, "fp4_gemm", [&](fp8blk_stream_t st) {
         return lib.fp4_gemm(data(*x.q), x.s, x.g, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.K, fmt,
                             st);
@@ -346,8 +330,8 @@ PyObject* fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
       at = (reinterpret_cast<uintptr_t>(held.mutable_data_ptr()) + 255) & ~uintptr_t{255};
     }
     {
-      const Unlocked unlocked;
-      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16, *x.t);
+      const Issue issue(*x.t);
+      if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16);
       call(*x.t, "fp4_linear", [&](fp8blk_stream_t st) {
         return lib.fp4_linear(data(*x.t), x.stride, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.cols,
                               fmt, reinterpret_cast<void*>(at), room, st);
@@ -395,25 +379,20 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check_columns(D);
       if (kind == FP8BLK_NORM_E2M1) fmt = format(a[8]);
     }
-    at::Tensor r, h, s, g, unused;
-    const std::array<int64_t, 2> rs = {T, D}, qs = {T, D / 2}, bs = {T, D / 128};
+    at::Tensor r, h, s, g;
+    const std::array<int64_t, 2> rs = {T, D}, bs = {T, D / 128};
     const std::array<int64_t, 1> gs = {T};
-    const bool given = a[9] != Py_None;
-    if (given) r = plain(a[9], at::kBFloat16, rs, dev, "r");
-    // (an empty piece takes no room)
-    const std::array<int64_t, 1> none = {0};
-    const Piece rp = given ? Piece{none, at::kBFloat16, &unused} : Piece{rs, at::kBFloat16, &r};
+    if (a[9] != Py_None) r = plain(a[9], at::kBFloat16, rs, dev, "r");
     {
-      const Unlocked unlocked;
+      const Issue issue(*y.t);
+      if (!r.defined()) r = make(rs, at::kBFloat16);
       if (kind == FP8BLK_NORM_BF16) {
-        make_together({rp, {rs, at::kBFloat16, &h}}, *y.t);
+        h = make(rs, at::kBFloat16);
       } else if (kind == FP8BLK_NORM_E4M3) {
-        make_together({rp, {rs, at::kFloat8_e4m3fn, &h}, {bs, at::kFloat, &s}}, *y.t);
+        h = make(rs, at::kFloat8_e4m3fn), s = make(bs, at::kFloat);
       } else {
-        const auto ss = scale_shape(T, D, fmt);
-        if (fmt == FP8BLK_FP4_E4M3)
-          make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}, {gs, at::kFloat, &g}}, *y.t);
-        else make_together({rp, {qs, at::kByte, &h}, {ss, at::kByte, &s}}, *y.t);
+        h = make({T, D / 2}, at::kByte), s = make(scale_shape(T, D, fmt), at::kByte);
+        if (fmt == FP8BLK_FP4_E4M3) g = make(gs, at::kFloat);
       }
       call(*y.t, "residual_norm", [&](fp8blk_stream_t st) {
         return lib.residual_norm(data(*y.t), y.stride, x, x_stride, post, col, tok, tok_stride, residual_scale, norm, eps, T,
