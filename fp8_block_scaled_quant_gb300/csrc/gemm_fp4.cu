@@ -33,6 +33,19 @@ int fp4_quant_launch(const void* x, bool fp32, int64_t x_stride, int64_t M, int6
 
 namespace {
 
+// A sum is multiplied by its two row scales one after the other: their own product may
+// leave fp32's range where the result does not (rows of small numbers: 0; rows of large
+// ones and a sum of 0: NaN). Of the lane's scale, `first` is multiplied before the other
+// scale and `last` after it, and one of them is 1: a scale below 1 goes first, where a sum
+// (2^-20 at least) keeps 18 bits with the smallest of fp4_quant's scales, 2^-112; one
+// above 1 goes last, when the product is as large only as the result. A NaN stays.
+struct LaneScale {
+  float first = 1.0f, last = 1.0f;
+  __device__ __forceinline__ LaneScale() {}
+  __device__ __forceinline__ explicit LaneScale(float g)
+      : first(fabsf(g) <= 1.0f ? g : 1.0f), last(fabsf(g) <= 1.0f ? 1.0f : g) {}
+};
+
 constexpr int kStageK = 256;
 constexpr int kLaneBytes = 128 * 128;  // 128 weight rows of a stage
 
@@ -239,7 +252,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   bool finished = true;  // epilogue warps: the accumulator is complete
   const int q = warp & 3;  // lane quarter of an epilogue warp
   const int64_t row = static_cast<int64_t>(tile_n) * 128 + q * 32 + lane;
-  float wg = 1.0f, ag[C::BN < 32 ? 1 : C::BN / 32];
+  LaneScale wg;
+  float ag[C::BN < 32 ? 1 : C::BN / 32];
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(ag) / 4); ++i) ag[i] = 1.0f;
 
   if (warp == 0 || (!C::FUSE && warp == 6)) {
     const bool weights = warp == 0;
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     // The scales of this lane's weight row and of the tokens (token 32 i + lane in ag[i]).
     if (p.w_g) {
-      if (row < p.N) wg = p.w_g[row];
+      if (row < p.N) wg = LaneScale(p.w_g[row]);
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(ag) / 4); ++i) {
         const int m = i * 32 + lane;
@@ -423,7 +439,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncwarp();
   const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
   auto store = [&](int col, float v, float a) {
-    if (p.w_g) v *= wg * a;
+    v = v * wg.first * a * wg.last;  // (without row scales: all 1)
     if (row < p.N && finished) p.c[(m0 + col) * p.N + row] = __float2bfloat16(v);
   };
   constexpr int kStep = C::BN < 32 ? 16 : 32;
@@ -766,12 +782,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
       const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + q * 32 + lane;
       const int64_t col0 = static_cast<int64_t>(tn) * C::BN + half * C::kHalf;
-      float ag = 1.0f;
+      LaneScale ag;
       if (p.a_g) {
         // The four warps of these columns bring their scales.
         named_barrier_sync(1 + half, 128);  // the tile before has been multiplied
         for (int in = q * 32 + lane; in < C::kHalf; in += 128) factors[in] = col0 + in < p.N ? p.w_g[col0 + in] : 0.0f;
-        if (row < p.M) ag = p.a_g[row];
+        if (row < p.M) ag = LaneScale(p.a_g[row]);
         named_barrier_sync(1 + half, 128);
       }
       // (After a wait that gave up the warps still meet at their barriers, and store nothing.)
@@ -782,8 +798,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       auto two = [&](int col, uint32_t a, uint32_t b) {
         float2 v = make_float2(__uint_as_float(a), __uint_as_float(b));
         if (p.a_g) {
-          const float2 g = *reinterpret_cast<const float2*>(factors + col);
-          v.x *= ag * g.x, v.y *= ag * g.y;
+          v = __fmul2_rn(v, make_float2(ag.first, ag.first));
+          v = __fmul2_rn(v, *reinterpret_cast<const float2*>(factors + col));
+          v = __fmul2_rn(v, make_float2(ag.last, ag.last));
         }
         const __nv_bfloat162 t = __floats2bfloat162_rn(v.x, v.y);
         return *reinterpret_cast<const uint32_t*>(&t);

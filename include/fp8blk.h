@@ -520,8 +520,9 @@ FP8BLK_API int fp8blk_fp4_dequant(const void *q, const void *s, const float *g, 
  *   C[m, n] = bf16( a_g[m] * w_g[n] * sum over blocks b of
  *                   a_s[m, b] * w_s[n, b] * sum_{k in b} a[m, k] * w[n, k] )
  * (UE8M0: without a_g and w_g, which may be NULL). The block-scaled MMA applies
- * the block scales and sums in fp32; a_g * w_g is one fp32 product. a [M, K/2],
- * w [N, K/2] and scale tiles 16-byte aligned, c bf16 [M, N] of any alignment of
+ * the block scales and sums in fp32; the sum is multiplied by a_g and w_g one after
+ * the other, in fp32, in an order that leaves fp32's range only where the result
+ * does (for scales as fp8blk_fp4_quant gives them). a [M, K/2], w [N, K/2] and scale tiles 16-byte aligned, c bf16 [M, N] of any alignment of
  * its elements, row scales 4-byte aligned; any M and N up to 2^28. K == 0 writes
  * zeros. The result does not vary from run to run. No workspace. Weights (w, w_s)
  * are read at once (the overlap rule above: they may not be the output of the call
