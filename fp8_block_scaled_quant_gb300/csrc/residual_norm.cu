@@ -175,22 +175,29 @@ __device__ __forceinline__ float root_inverse(float a) {
 // 1 / sqrt(mean of v^2 + eps) over the block's row. Squares that overflow fp32 (a
 // row near 2^60), or that vanish where eps does not hide it, are summed again
 // with v times a power of two; the sum is the same in all threads, so they turn together.
+// Not `in`: the thread's last unit is past the row and does not count (a zero there
+// that was multiplied by an infinite factor is a NaN).
 template <int P>
-__device__ __forceinline__ float rms_factor(const float2 (&v)[P][8], float inv_n, float eps, float* at) {
+__device__ __forceinline__ float rms_factor(const float2 (&v)[P][8], bool in, float inv_n, float eps, float* at) {
   float2 two = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int u = 0; u < P; ++u)
+  for (int u = 0; u < P; ++u) {
+    const float2 before = two;
 #pragma unroll
     for (int i = 0; i < 8; ++i) two = __ffma2_rn(v[u][i], v[u][i], two);
+    if (u == P - 1 && !in) two = before;
+  }
   float sum = block_sum(two.x + two.y, at);
   const bool huge = sum == __uint_as_float(0x7F800000u);
   if (huge || (sum < 7.9e-31f && eps < 8.7e-19f)) {  // 2^-100, 2^-60
     const float s = __uint_as_float(huge ? (127u - 80u) << 23 : (127u + 60u) << 23);
     sum = 0.0f;
 #pragma unroll
-    for (int u = 0; u < P; ++u)
+    for (int u = 0; u < P; ++u) {
+      if (u == P - 1 && !in) break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(v[u][i].x * s, v[u][i].x * s, fmaf(v[u][i].y * s, v[u][i].y * s, sum));
+    }
     __syncthreads();  // every warp has read the first sums
     return root_inverse(fmaf(block_sum(sum, at), inv_n, eps * s * s)) * s;
   }
@@ -262,12 +269,13 @@ __device__ __forceinline__ void add_residual(const NormParams& p, const uint32_t
   }
 }
 
-// A thread's parts of the sums of y^2 (given), v^2, x v and x^2.
+// A thread's parts of the sums of y^2 (given), v^2, x v and x^2 (`in`: as above).
 template <int P>
-__device__ __forceinline__ float4 row_sums(float2 yy, const float2 (&v)[P][8], const uint32_t (&x)[P][8]) {
+__device__ __forceinline__ float4 row_sums(float2 yy, const float2 (&v)[P][8], const uint32_t (&x)[P][8], bool in) {
   float2 vv = make_float2(0.0f, 0.0f), xv = vv, xx = vv;
 #pragma unroll
-  for (int u = 0; u < P; ++u)
+  for (int u = 0; u < P; ++u) {
+    const float2 vv_before = vv, xv_before = xv;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 xf = pair(x[u][i]);
@@ -275,6 +283,8 @@ __device__ __forceinline__ float4 row_sums(float2 yy, const float2 (&v)[P][8], c
       xv = __ffma2_rn(xf, v[u][i], xv);
       xx = __ffma2_rn(xf, xf, xx);
     }
+    if (u == P - 1 && !in) vv = vv_before, xv = xv_before;
+  }
   return make_float4(yy.x + yy.y, vv.x + vv.y, xv.x + xv.y, xx.x + xx.y);
 }
 
@@ -302,7 +312,7 @@ __device__ __forceinline__ bool both_norms(const NormParams& p, int64_t row, flo
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[u][i] = pair(y[i]);
   }
-  const float k = rms_factor<P>(v, p.inv_n, p.eps, sum_y);
+  const float k = rms_factor<P>(v, true, p.inv_n, p.eps, sum_y);  // (zeros past the row)
 #pragma unroll
   for (int u = 0; u < P; ++u) {
     const int unit = tid + u * n < p.units ? tid + u * n : 0;
@@ -415,6 +425,7 @@ __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(cons
     if (has_x) prefetch_l2(p.x + (row + p.ahead) * p.x_stride, bytes);
     if (tok) prefetch_l2(p.gate_tok + (row + p.ahead) * p.gate_stride, bytes);
   }
+  const bool last_in = tid + (P - 1) * n < p.units;
   uint32_t x[P][8];
   float2 v[P][8], ne[EARLY ? P : 1][8];
   float2 yy = make_float2(0.0f, 0.0f);
@@ -453,7 +464,7 @@ __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(cons
   float k2 = 0.0f;
   bool known = false;
   if (p.post_w) {
-    const float sum = warp_sum4(row_sums<P>(yy, v, x));
+    const float sum = warp_sum4(row_sums<P>(yy, v, x, last_in));
     if ((tid & 7) == 0) sums[(tid >> 5) * 4 + ((tid & 31) >> 3)] = sum;
     __syncthreads();
     known = both_norms<P, WIDE>(p, row, warps_sum4(sums), x, v, &k2, sum_y);
@@ -461,7 +472,7 @@ __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(cons
     add_residual<P>(p, x, 1.0f, v);
   }
   write_residual<P, WIDE>(p, row, v);
-  if (!known) k2 = rms_factor<P>(v, p.inv_n, p.eps, sum_r);
+  if (!known) k2 = rms_factor<P>(v, last_in, p.inv_n, p.eps, sum_r);
   k2 = apply_early<P>(v, k2);
 #pragma unroll
   for (int u = 0; u < P; ++u) {
@@ -505,6 +516,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) factor[i] = __fmul2_rn(factor[i], w[i]);
   }
+  // (zeros past the row times infinity would be none)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) factor[i] = in ? factor[i] : make_float2(0.0f, 0.0f);
   const int64_t step = gridDim.x;
   uint32_t y[8], x_new[1][8], x[1][8];
   float2 v[1][8];
@@ -526,7 +540,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(cons
       to[0][i] = __fmul2_rn(to[0][i], factor[i]);
       x_to[0][i] = x_new[0][i];
     }
-    const float sum = warp_sum4(row_sums<1>(yy, to, x_to));
+    const float sum = warp_sum4(row_sums<1>(yy, to, x_to, true));
     if ((lane & 7) == 0) sums[turn & 3][(tid >> 5) * 4 + (lane >> 3)] = sum;
     __syncwarp();
     if (lane == 0) mbar_arrive(&summed[turn & 3]);
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_rows_kernel(cons
     float k2;
     const bool known = both_norms<1, true>(p, row, warps_sum4(sums[turn & 3]), x, v, &k2, sum_y);
     write_residual<1, true>(p, row, v);
-    if (!known) k2 = rms_factor<1>(v, p.inv_n, p.eps, sum_r);
+    if (!known) k2 = rms_factor<1>(v, in, p.inv_n, p.eps, sum_r);
     k2 = apply_early<1>(v, k2);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[0][i] = __fmul2_rn(v[0][i], norm[i]);
