@@ -448,7 +448,8 @@ def residual_norm(y: torch.Tensor, x: torch.Tensor | None, norm_w: torch.Tensor,
     """The seam between two blocks, per token: z = post_w ? RMSNorm(y) * post_w : y; r = residual_scale * x + gate * z;
     h = RMSNorm(r) * norm_w. y, x bf16 [T, D] (rows may be strided; x None: r = gate * z), norm_w and post_w float32
     [D], gate float32 [D] or bf16 [T, D]. Returns (r bf16 [T, D], h): h is bf16 [T, D], or with quant="fp8"
-    act_quant's (q, s) of it (scale_fmt SCALE_*), or with quant="fp4" fp4_quant's (q, s, g) of it (scale_fmt FP4_*).
+    (q, s) of it as act_quant gives them (scale_fmt SCALE_*; from h in fp32, the codes by the scale's reciprocal), or with
+    quant="fp4" (q, s, g) of it as fp4_quant gives them (scale_fmt FP4_*).
     r may be given; it may be x or y itself. fp32 until each output's one rounding. h is the next product's activation at
     once; to multiply by it as a weight needs an ordering call in between (the module's rule on overlap)."""
     return (_bind or _native()).residual_norm(y, x, norm_w, post_w, gate, residual_scale, eps, quant, scale_fmt, r)

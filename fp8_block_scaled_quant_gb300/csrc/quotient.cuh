@@ -40,4 +40,26 @@ __device__ __forceinline__ float2 div2_by_scale(float2 x, float2 sn2, float2 r2)
                      __uint_as_float(__float_as_uint(q.y) | (__float_as_uint(q0.y) & 0x80000000u)));
 }
 
+// ---- reciprocals that are not exact ------------------------------------------
+//
+// For numbers that have passed fp32 roundings already: the hardware's estimate and one
+// step of Newton's iteration, whose error is the square of the estimate's (2^-22) and
+// the roundings of the step itself. tests/test_gpu_inverse.py checks the bounds over
+// every fp32 input of the range.
+
+// 1 / s by r + r (1 - s r), for 2^-126 <= s < 2^126: within 2^-24 (1 + 2^-10) of it.
+__device__ __forceinline__ float inverse(float s) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return fmaf(fmaf(-s, r, 1.0f), r, r);
+}
+
+// 1 / sqrt(a) by y + y (1 - a y^2) / 2, for positive a: within 1.5 x 2^-24 (1 + 2^-8) of
+// it (a y is rounded, by 2^-24, which reaches the result by half). a = 0, infinity and
+// NaN give what the estimate gives.
+__device__ __forceinline__ float inverse_root(float a) {
+  const float y = rsqrtf(a), e = fmaf(-a * y, y, 1.0f);
+  return fabsf(e) < 1.0f ? fmaf(0.5f * y, e, y) : y;
+}
+
 }  // namespace fp8blk

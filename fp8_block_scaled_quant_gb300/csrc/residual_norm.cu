@@ -166,12 +166,6 @@ __device__ __forceinline__ float4 warps_sum4(const float* at) {
                      __shfl_sync(0xFFFFFFFFu, s, 24));
 }
 
-// 1 / sqrt(a): the hardware's estimate and one Newton step, y (1 + (1 - a y^2) / 2).
-__device__ __forceinline__ float root_inverse(float a) {
-  const float y = rsqrtf(a), e = fmaf(-a * y, y, 1.0f);
-  return fabsf(e) < 1.0f ? fmaf(0.5f * y, e, y) : y;  // (a = 0, infinity, NaN: as the estimate is)
-}
-
 // 1 / sqrt(mean of v^2 + eps) over the block's row. Squares that overflow fp32 (a
 // row near 2^60), or that vanish where eps does not hide it, are summed again
 // with v times a power of two; the sum is the same in all threads, so they turn together.
@@ -199,15 +193,17 @@ __device__ __forceinline__ float rms_factor(const float2 (&v)[P][8], bool in, fl
       for (int i = 0; i < 8; ++i) sum = fmaf(v[u][i].x * s, v[u][i].x * s, fmaf(v[u][i].y * s, v[u][i].y * s, sum));
     }
     __syncthreads();  // every warp has read the first sums
-    return root_inverse(fmaf(block_sum(sum, at), inv_n, eps * s * s)) * s;
+    return inverse_root(fmaf(block_sum(sum, at), inv_n, eps * s * s)) * s;
   }
-  return root_inverse(fmaf(sum, inv_n, eps));
+  return inverse_root(fmaf(sum, inv_n, eps));
 }
 
 // The act_quant scale of a block (block_scale's value: max(amax, 1e-4) / 448 by
-// Markstein's correction, exact), and its reciprocal to half a step or a little more.
-// h has passed several fp32 roundings, so the product with the reciprocal takes
-// the place of act_quant's exact quotient.
+// Markstein's correction: the IEEE quotient for every fp32 amax from 1e-4 on). h has
+// passed several fp32 roundings, so its product with the scale's reciprocal takes the
+// place of act_quant's exact quotient of a bf16 number: three more roundings, 2^-22 in
+// all, and a value as near as that to a border between two codes may take either one
+// (1 code in 1.5 million, as often as by the formula in fp32).
 __device__ __forceinline__ float e4m3_scale(float amax, bool ue8m0) {
   float s = div_by_scale(fmaxf(amax, 1e-4f), 448.0f, 1.0f / 448.0f);
   if (ue8m0) {
@@ -216,12 +212,6 @@ __device__ __forceinline__ float e4m3_scale(float amax, bool ue8m0) {
     s = __uint_as_float(b);
   }
   return s;
-}
-
-__device__ __forceinline__ float scale_inverse(float s) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return fmaf(fmaf(-s, r, 1.0f), r, r);
 }
 
 // A row's factor k goes onto its values after the columns' factors, where it is
@@ -296,12 +286,12 @@ template <int P, bool WIDE>
 __device__ __forceinline__ bool both_norms(const NormParams& p, int64_t row, float4 sum, const uint32_t (&x)[P][8],
                                            float2 (&v)[P][8], float* k2, float* sum_y) {
   const int tid = threadIdx.x, n = blockDim.x;
-  const float k1 = root_inverse(fmaf(sum.x, p.inv_n, p.eps)), s = p.residual_scale;
+  const float k1 = inverse_root(fmaf(sum.x, p.inv_n, p.eps)), s = p.residual_scale;
   const float a = s * s * sum.w, b = k1 * k1 * sum.y, all = a + b;
   const float rr = fmaf(2.0f * s * k1, sum.z, all);
   if (sum.x > 1e-20f && sum.x < 1e30f && sum.y < 1e30f && all > 1e-20f && rr < 1e30f && rr > 0.25f * all) {
     add_residual<P>(p, x, k1, v);
-    *k2 = root_inverse(fmaf(rr, p.inv_n, p.eps));
+    *k2 = inverse_root(fmaf(rr, p.inv_n, p.eps));
     return true;
   }
 #pragma unroll
@@ -368,7 +358,7 @@ __device__ __forceinline__ void write_h(const NormParams& p, int64_t row, float2
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));  // 8 lanes: 128 columns
       if (unit >= p.units) continue;
-      const float s = e4m3_scale(m * k2, p.ue8m0 != 0), f = k2 * scale_inverse(s);
+      const float s = e4m3_scale(m * k2, p.ue8m0 != 0), f = k2 * inverse(s);
       uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -554,7 +554,10 @@ FP8BLK_API int fp8blk_fp4_linear(const void *x_bf16, int64_t x_stride, const voi
  * fp32 from the inputs to one rounding of each output: r as bf16 (r NULL: not
  * written), and h by out_kind as
  *   FP8BLK_NORM_BF16  bf16 [T, D];
- *   FP8BLK_NORM_E4M3  act_quant of h (scale_fmt as there): e4m3 [T, D], h_s fp32 [T, D/128];
+ *   FP8BLK_NORM_E4M3  h by act_quant's rule (scale_fmt as there): e4m3 [T, D], h_s fp32
+ *                     [T, D/128]. The scale is the rule's, of h in fp32; the codes are those
+ *                     of h times the scale's reciprocal in fp32, within 2^-22 of the exact
+ *                     quotient that act_quant rounds (of a bf16 input);
  *   FP8BLK_NORM_E2M1  fp4_quant of h (scale_fmt FP8BLK_FP4_*): codes [T, D/2], scale
  *                     tiles h_s, row scales h_g [T] (E4M3 format).
  * y, x: bf16 [T, D], rows y_stride / x_stride elements apart. The gate is one of
