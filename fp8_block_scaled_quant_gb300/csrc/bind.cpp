@@ -16,6 +16,7 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <array>
+#include <mutex>
 #include <string>
 
 #include "fp8blk.h"
@@ -286,6 +287,10 @@ PyObject* fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Two threads may call fp4_linear on one stream, whose workspace then holds the one's
+// activations after the other's: the launches of a call go out together.
+std::mutex linear_launches;
+
 bool capturing(cudaStream_t stream) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   return cudaStreamIsCapturing(stream, &status) != cudaSuccess || status != cudaStreamCaptureStatusNone;
@@ -332,6 +337,7 @@ PyObject* fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const Issue issue(*x.t);
       if (!out.defined()) out = make({x.rows, w.rows}, at::kBFloat16);
+      const std::lock_guard<std::mutex> together(linear_launches);
       call(*x.t, "fp4_linear", [&](fp8blk_stream_t st) {
         return lib.fp4_linear(data(*x.t), x.stride, data(*w.q), w.s, w.g, out.mutable_data_ptr(), x.rows, w.rows, x.cols,
                               fmt, reinterpret_cast<void*>(at), room, st);
