@@ -1002,7 +1002,9 @@ bool takes_pairs(const DevInfo* d, const Fp4Params& p) {
 // 2112 x 7168 5.8 and 5.9; 1 x 1536 x 7168 5.1 and 5.5), or up to 4096 numbers of more
 // (2 x 24576 x 1536 5.4 and 6.7; 2 x 10944 x 2048 5.4 and 5.9; 4 x 10944 x 2048, 8192
 // numbers, 6.4 and 5.9; 5 x 7168 x 1536 5.6 and 5.1), where a CTA's share takes a corner
-// of its shared memory.
+// of its shared memory. (In both formats each CTA converts all of K, with the 128 threads
+// of its epilogue, and keeps its share. Powers of two need no more than the share, row
+// scales the rows' maxima besides; neither is built.)
 bool fuses(const DevInfo* d, int64_t M, int64_t N, int64_t K) {
   const int stages_k = static_cast<int>((K + kStageK - 1) / kStageK);
   const int ks = few_split((N + 127) / 128, stages_k, d->sm_count);

@@ -394,10 +394,13 @@ __device__ __forceinline__ void write_h(const NormParams& p, int64_t row, float2
 
 // A block to a token, P units to a thread. EARLY: norm_w is asked for with the rows
 // (few tokens); otherwise where it is used, from L1, which keeps registers free
-// for another block to an SM (4099 x 7168 with a norm of y, into e4m3: 50.7 us with
-// two blocks of 448 threads, 47.4 with the next rows prefetched; 55 with two units to
-// a thread, rows through shared memory 49 to 57: the blocks' arithmetic between their
-// loads, not HBM, sets the time then).
+// for another block to an SM. It has what does not go from token to token, below: few
+// tokens, y that is not normed (4099 x 7168 into bf16 36.1 us, HBM's rate), a gate by
+// token (4099 x 7168 into e4m3 46.6, 4099 x 8192 into e2m1 58.2), e2m1 with row scales
+// (4099 x 7168 48.5): with a post norm the blocks' arithmetic between their loads, not
+// HBM, sets the time. (Tried on such a case, 4099 x 7168 into e4m3: next rows not
+// prefetched 50.7 against 47.4; two units to a thread 55; rows through shared memory 49
+// to 57.)
 template <int OUT, int P, bool WIDE, bool EARLY>
 __global__ void __maxnreg__(EARLY || P > 1 ? 128 : 72) residual_norm_kernel(const NormParams p) {
   constexpr int kWarps = kMaxThreads / 32;
@@ -644,9 +647,11 @@ extern "C" int fp8blk_residual_norm(const void* y_bf16, int64_t y_stride, const 
   const int threads = ((p.units + P - 1) / P + 31) / 32 * 32;
   // Blocks that go from row to row: where y is normed, the factors are the columns' alone,
   // nothing but the norms needs the whole row, and blocks of 128 registers to a thread
-  // leave an SM twelve warps (us: 4099 x 7168 into e4m3 42.6, a block to a token 47.4; into
-  // bf16 40.1 and 41.5; 4099 x 8192 into e4m3 43.0 and 52.8; 500 x 7168 7.9 and 8.3; with
-  // ten warps, 8000 x 5120, 69.7 and 59.9; into e2m1 with row scales 55.0 and 48.5).
+  // leave an SM twelve warps (with a gate by column, us: 4099 x 7168 into e4m3 42.1, a block
+  // to a token 46.3; into bf16 38.0 and 46.4; into e2m1 with powers of two 44.4 and 46.4;
+  // 4099 x 8192 into e4m3 42.1 and 51.9; 500 x 7168 8.2 and 8.5; 16000 x 1536 35.2 and 34.6;
+  // with ten warps, 8000 x 5120 into e4m3, 69.0 and 58.7). E2m1 with row scales needs the
+  // row's maximum besides (built so, 55.0 against 48.5).
   const int64_t places = kMaxThreads / threads;
   const bool rows = !early && post_w && !gate_tok_bf16 && wide && P == 1 && !(fp4 && scale_fmt == kFp4E4M3) &&
                     places * threads >= 384;
